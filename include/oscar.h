@@ -312,6 +312,199 @@ oscar_status oscar_decode_attention_noalloc(oscar_cache* cache, int32_t n_seqs, 
                                             const void* q, int32_t num_q_heads, float softmax_scale,
                                             void* out, void* stream);
 
+/*
+ * The calls below prepare, choose, attend and read back parts of the cache.
+ * Element types of their float buffers:
+ */
+enum {
+  OSCAR_BF16 = 0,
+  OSCAR_F32 = 1
+};
+
+/* How rotary frequencies are scaled for contexts longer than the model was
+ * trained for (oscar_rotary_config.scaling). */
+enum {
+  OSCAR_ROTARY_NONE = 0,
+  OSCAR_ROTARY_LINEAR = 1, /* every frequency divided by `factor`            */
+  OSCAR_ROTARY_BANDED = 2, /* by wavelength: with t = original_length f /
+                              (2 pi) turns over the original context, f / factor
+                              below `low` turns, f above `high`, between them
+                              (1 - r) f / factor + r f, r = (t - low) / (high - low) */
+  OSCAR_ROTARY_YARN = 3    /* by pair index: with c(t) = rotary_dim ln(
+                              original_length / (2 pi t)) / (2 ln base), l =
+                              max(floor(c(high)), 0), h = min(ceil(c(low)),
+                              rotary_dim - 1) (h = l + 0.001 when equal), r =
+                              clamp((i - l) / (h - l), 0, 1): f / factor r +
+                              f (1 - r)                                       */
+};
+
+typedef struct oscar_rotary_config {
+  int32_t head_dim;        /* must be 128                                     */
+  int32_t rotary_dim;      /* rotated channels, the first of the head: a
+                              multiple of 16 up to 128                        */
+  int32_t interleaved;     /* 0: pair i is channels (i, i + rotary_dim / 2);
+                              1: channels (2 i, 2 i + 1)                      */
+  int32_t scaling;         /* OSCAR_ROTARY_*                                  */
+  double base;             /* frequency of pair i: base^(-2 i / rotary_dim);
+                              > 1                                             */
+  double factor;           /* >= 1 (scaling other than NONE)                  */
+  double original_length;  /* tokens of the original context (BANDED, YARN)   */
+  double low, high;        /* BANDED: turns, 0 and 0 mean 1 and 4; YARN: slow
+                              and fast turns, 0 and 0 mean 1 and 32           */
+  double attention_factor; /* multiplies the rotated channels; 0 means 1, for
+                              YARN 0.1 ln(factor) + 1                         */
+} oscar_rotary_config;
+
+/* Frequencies (radians per position, rotary_dim / 2 of them) and the factor
+ * on the rotated channels that `cfg` stands for.  Pure host arithmetic. */
+oscar_status oscar_rotary_frequencies(const oscar_rotary_config* cfg, double* frequencies,
+                                      double* attention_factor);
+
+/* Rows of one tensor [n_tokens, heads, 128]: strides in elements, channels
+ * contiguous.  `out` may be `in` with the same strides (in place); otherwise
+ * the rows written must not overlap any rows read. */
+typedef struct oscar_rotary_rows {
+  const void* in;
+  void* out;
+  int64_t in_token_stride, in_head_stride;
+  int64_t out_token_stride, out_head_stride;
+  int32_t heads;
+} oscar_rotary_rows;
+
+/*
+ * Rotary positions of queries and keys, before the keys are appended and the
+ * queries attend: with t = positions[token] * frequency (evaluated to 2^-32
+ * of a turn at any int32 position) and m the attention factor,
+ *   (y_a, y_b) = m (x_a cos t - x_b sin t, x_a sin t + x_b cos t)
+ * for every pair (a, b); channels from rotary_dim on are copied.
+ *   positions  int32 [n_tokens], device or page-locked host memory, may be
+ *              negative
+ *   type       OSCAR_BF16 or OSCAR_F32 (q and k, in and out)
+ *   q, k       rows on the current device; k may be NULL; 16-byte aligned
+ *              pointers, strides of 16-byte multiples; inputs may have any
+ *              strides (0 broadcasts), output rows must be distinct: either
+ *              the heads of a token or the tokens of a head side by side.
+ *              Zero heads or zero tokens: nothing is done.
+ *   transpose  0, or 1 for the transposed rotation (t -> -t, the same m): the
+ *              gradient, and with m = 1 the inverse
+ * float32 arithmetic, one rounding to the output type.
+ */
+oscar_status oscar_rotary(const oscar_rotary_config* cfg, int64_t n_tokens, const int32_t* positions,
+                          int32_t type, const oscar_rotary_rows* q, const oscar_rotary_rows* k,
+                          int32_t transpose, void* stream);
+
+/*
+ * Read tokens back: for each i, tokens start[i] .. end[i] - 1 of slot
+ * seq_ids[i], packed one range after the other.
+ *   seq_ids, start, end  host int32 [n_seqs]; 0 <= start <= end <= length; a
+ *                        slot may appear more than once
+ *   type                 OSCAR_BF16 or OSCAR_F32
+ *   k_out, v_out         [sum(end - start), Hkv, 128], 16-byte aligned device
+ *                        memory (bf16 keys are written faster when both are
+ *                        32-byte aligned); either may be NULL
+ * A quantised key is H_d (n (code s + z)) (back in the basis in which it was
+ * appended), a quantised value code s + z, both in float32 and rounded once to
+ * the output type; window tokens are their stored bf16 rows.
+ */
+oscar_status oscar_cache_read(oscar_cache* cache, int32_t n_seqs, const int32_t* seq_ids,
+                              const int32_t* start, const int32_t* end, int32_t type, void* k_out,
+                              void* v_out, void* stream);
+
+/*
+ * Move a sequence's packed state out of the cache and back in (swapping a
+ * sequence to host memory, sending it to another cache of the same head count
+ * and meta_bits).  With L tokens, g = L / 128 and w = L % 128:
+ *   blocks  Hkv x g x B bytes: the group blocks, KV head by KV head (B = 13,824
+ *           or 11,008)
+ *   window  bf16 [Hkv, 2, 128, 128]: key rows, then value rows; the first w
+ *           rows of each are read or written, the others left as they are
+ *   maxima  float32 [2, Hkv]: the largest value scale, the largest |value zero|
+ * Device or page-locked host memory, 16-byte aligned; blocks may be NULL when
+ * g = 0 and window when w = 0.  Plain copies on `stream`.
+ * oscar_cache_import replaces what the slot holds by `length` tokens.
+ */
+oscar_status oscar_cache_export(oscar_cache* cache, int32_t seq, void* blocks, void* window,
+                                float* maxima, void* stream);
+oscar_status oscar_cache_import(oscar_cache* cache, int32_t seq, int32_t length, const void* blocks,
+                                const void* window, const float* maxima, void* stream);
+
+/*
+ * Choosing the groups worth attending.  An index holds an 8-bit summary of
+ * every quantised group, 264 bytes per (slot, KV head, group):
+ *   +0            int8 [slot][Hkv][max_groups][32][2][4]: for channels 4 l .. 4 l + 3
+ *                 the lowest values lo8 (4), then the highest hi8 (4) of the
+ *                 group's unit keys, in steps of 2^e
+ *   +256 S H max_groups   float32 [slot][Hkv][max_groups][2]: w_max, w_min, the
+ *                 largest and the smallest token norm times 2^e
+ * with lo = z, hi = fl32(z + 3 s), lo8 = rne(lo / 2^e), hi8 = rne(hi / 2^e), e
+ * the smallest exponent >= -100 with |lo|, |hi| <= 127 2^e over the channels
+ * (e = -100 for an all-zero group); values that are not finite count as 0.
+ * The caller owns the index buffer (256-byte aligned device memory), attaches
+ * it once, and brings it up to date after groups have closed.
+ */
+oscar_status oscar_index_required_bytes(const oscar_cache* cache, size_t* out_bytes);
+
+/* Attach an index buffer of at least oscar_index_required_bytes (nothing in
+ * it is valid yet); NULL detaches. */
+oscar_status oscar_index_attach(oscar_cache* cache, void* index, size_t index_bytes);
+
+/* Summarise the groups of each slot that are not in the index yet (rebuild =
+ * 0) or all of them (rebuild = 1).  Enqueues nothing when there are none.
+ * At most 1,024 sequences per call. */
+oscar_status oscar_index_update(oscar_cache* cache, int32_t n_seqs, const int32_t* seq_ids,
+                                int32_t rebuild, void* stream);
+
+/*
+ * For each (sequence, KV head), the n_select groups with the largest scores
+ * for its query heads, in ascending order; -1 behind them when there are fewer
+ * groups.  With E the smallest exponent >= -100 such that |q| < 2^E for the
+ * query heads of the KV head (elements that are not finite count as 0),
+ *   a = rne(q 2^(22 - E)),  b = Hu a (Hu = sqrt(128) H_d; whole numbers),
+ *   q8 = floor(b / 2^B + 1/2), B >= 0 the smallest with |b| <= 127 2^B (no 1/2
+ *        for B = 0),
+ *   S = max over the heads of sum_c max(q8_c lo8_c, q8_c hi8_c),
+ *   score = S w_max if S >= 0, else S w_min, exactly;
+ * up to its 8-bit steps, the largest score any key within the group's box
+ * could reach.  Equal scores: the lower group first.
+ *   seq_ids     host int32 [n_seqs], distinct, at most 1,024; every group of
+ *               each must be in the index (OSCAR_ERR_INVALID_ARG otherwise)
+ *   q           bf16 [n_seqs, num_q_heads, 128], 16-byte aligned, device or
+ *               page-locked host memory; num_q_heads a multiple of Hkv, at most
+ *               64 per KV head
+ *   n_select    >= 1
+ *   keep_first, keep_last  that many first and last groups of each sequence are
+ *               always chosen (attention sinks, recent tokens); >= 0, together
+ *               <= n_select
+ *   groups      int32 [n_seqs, Hkv, n_select], device memory
+ * Sequences without a group get -1s.  A sequence of more than about 25,000
+ * groups that does not fit n_select fails with OSCAR_ERR_UNSUPPORTED.
+ */
+oscar_status oscar_select_groups(oscar_cache* cache, int32_t n_seqs, const int32_t* seq_ids, const void* q,
+                                 int32_t num_q_heads, int32_t n_select, int32_t keep_first,
+                                 int32_t keep_last, int32_t* groups, void* stream);
+
+/*
+ * Single-query decode attention over listed groups: oscar_decode_attention
+ * restricted, for each (sequence, KV head), to the groups listed for it and
+ * the sequence's window.
+ *   groups    int32 [n_seqs, Hkv, n_select] in device memory, read on
+ *             `stream` (oscar_select_groups may produce it); an entry outside
+ *             [0, length / 128) is empty, a group listed twice counts twice
+ *   n_select  >= 1
+ *   type      OSCAR_BF16 or OSCAR_F32: type of out
+ *   lse       float32 [n_seqs, num_q_heads] or NULL: ln sum exp(score) over the
+ *             attended tokens (natural log, scores times softmax_scale)
+ * A row with nothing to attend (no valid entry, empty window) gets zeros and
+ * an lse of -infinity.  q, out and lse may be device or page-locked host
+ * memory; every other argument, the workspace and the stream order are those
+ * of oscar_decode_attention.
+ */
+oscar_status oscar_sparse_decode_attention(oscar_cache* cache, int32_t n_seqs, const int32_t* seq_ids,
+                                           const void* q, int32_t num_q_heads, float softmax_scale,
+                                           const int32_t* groups, int32_t n_select, int32_t type,
+                                           void* out, float* lse, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
 /* Footprint: kind = OSCAR_BYTES_USED / _BF16_EQUIVALENT for slot `seq`
  * (or all slots if seq == -1), or OSCAR_BYTES_ARENA.  Host arithmetic:
  * a full group costs 13,824 B per KV head (108 B per token) versus 65,536 B

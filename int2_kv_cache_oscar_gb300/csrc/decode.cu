@@ -33,6 +33,7 @@
 //   * online softmax in the log2 domain; tensor-core accumulators restart at
 //     every group and are added into fp32 registers on the CUDA cores.
 #include <cstddef>
+#include <type_traits>
 
 #include "decode_common.cuh"
 
@@ -79,6 +80,7 @@ struct DecSmemT {
   uint32_t issued[kStages];   // uses of each stage issued so far (producer -> consumers)
   uint64_t qready;            // consumers have requested their first queries (-> producer)
   int abort_flag;
+  uint32_t skip[kStages];     // listed groups: the stage's use is an empty entry
 };
 static_assert(kPbStride >= kHeadDim, "output rows must fit in the probability rows");
 static_assert((kPbStride * 4) % 16 == 0, "pbuf rows must keep 16-byte alignment");
@@ -168,7 +170,7 @@ __device__ __forceinline__ float fast_exp2(float x) {
 // programmatic dependency).
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-template <int MAXS, bool M16, bool PAIRS>
+template <int MAXS, bool M16, bool PAIRS, bool SPARSE>
 __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
     decode_int2_kernel(const __grid_constant__ DecodeParams<MAXS> p, const uint8_t* __restrict__ arena) {
   using DecSmem = DecSmemT<M16>;
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
 
   if (warp == kConsumers) {
     // ------------------------------------------------------------ producer
-    if (lane != 0) return;
+    if (!SPARSE && lane != 0) return;
     int64_t k = 0;
     int64_t u = u0;
     // Use k of the ring: stage ks = k mod kStages, its use ku = k / kStages,
@@ -212,7 +214,10 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
     int ks = 0;
     uint32_t ku = 0;
     auto issue = [&](const uint8_t* src) {
-      if (!(cta == 0 && k == p.h.fault_unit)) {
+      if constexpr (SPARSE) S.skip[ks] = src == nullptr;
+      if (SPARSE && src == nullptr) {
+        mbar_arrive(&S.full[ks]);       // an empty entry: nothing to copy
+      } else if (!(cta == 0 && k == p.h.fault_unit)) {
         mbar_arrive_expect_tx(&S.full[ks], kStageBytes);
         bulk_g2s(S.stage[ks], src, kStageBytes, &S.full[ks]);
       }
@@ -228,9 +233,9 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
     // previous kernel finishes, and these copies overlap its tail.
     // a CTA with at most one unit per consumer fills all of them
     const int64_t pre = (u1 - u0) <= kConsumers ? kConsumers : kPreWaitStages;
-    while (u < u1 && k < pre) {
+    while (!SPARSE && u < u1 && k < pre) {
       int b, j, g, ng;
-      locate_unit(p, u, b, j, g, ng);
+      locate_unit<SPARSE>(p, u, b, j, g, ng);
       const int64_t row_end = p.seq[b].ubase + (int64_t)(j + 1) * ng;
       const int64_t seg_end = row_end < u1 ? row_end : u1;
       const int settled = p.seq[b].settled;
@@ -240,10 +245,45 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
     }
     grid_dependency_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if constexpr (SPARSE) {
+      // The listed groups are an output of the kernels before this one, so
+      // nothing is copied early.  The warp looks up 32 entries at a time (the
+      // next 32 while lane 0 issues these); an entry outside the sequence's
+      // groups is passed on as empty.
+      auto entry = [&](int64_t v) -> int64_t {
+        if (v >= u1) return -1;
+        int b, j, g, ng;
+        locate_unit<SPARSE>(p, v, b, j, g, ng);
+        const int gi = p.h.groups[((int64_t)b * hkv + j) * ng + g];
+        if (gi < 0 || gi >= p.seq[b].len / kGroup) return -1;
+        return (((int64_t)p.seq[b].slot * hkv + j) * p.h.max_groups + gi) * kStageBytes;
+      };
+      int64_t next = entry(u + lane);
+      bool stop = lane == 0 && !mbar_wait_bounded(&S.qready, 0, &S.abort_flag, p.h.err_word, p.h.spin_limit);
+      while (u < u1 && !__shfl_sync(0xffffffffu, (int)stop, 0)) {
+        const int64_t at = next;
+        const int n = (int)(u1 - u < 32 ? u1 - u : 32);
+        u += n;
+        next = entry(u + lane);
+        for (int i = 0; i < n; ++i) {
+          const int64_t off = __shfl_sync(0xffffffffu, at, i);
+          if (lane == 0 && !stop) {
+            stop = ku > 0 && !mbar_wait_bounded(&S.empty[ks], (ku - 1) & 1, &S.abort_flag, p.h.err_word, p.h.spin_limit);
+            if (!stop) {
+              issue(off < 0 ? nullptr : blocks + off);
+              ++k;
+            }
+          }
+          __syncwarp();
+        }
+      }
+      if (lane != 0) return;
+      goto drain;
+    }
     if (!mbar_wait_bounded(&S.qready, 0, &S.abort_flag, p.h.err_word, p.h.spin_limit)) goto drain;
     while (u < u1) {
       int b, j, g, ng;
-      locate_unit(p, u, b, j, g, ng);
+      locate_unit<SPARSE>(p, u, b, j, g, ng);
       const int64_t row_end = p.seq[b].ubase + (int64_t)(j + 1) * ng;
       const int64_t seg_end = row_end < u1 ? row_end : u1;
       const uint8_t* src = blocks + (((int64_t)p.seq[b].slot * hkv + j) * p.h.max_groups + g) * kStageBytes;
@@ -308,7 +348,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
     for (int i = 0; i < 2; ++i) {
       if (uu < u1) {
         int b, j, gg, ng;
-        locate_unit(p, uu, b, j, gg, ng);
+        locate_unit<SPARSE>(p, uu, b, j, gg, ng);
         uint2 qr = make_uint2(0u, 0u);
         if (warp < gqa)
           qr = *reinterpret_cast<const uint2*>(p.h.q + ((int64_t)b * p.h.hq + j * p.h.q_group + p.h.q_head0 + warp) * kHeadDim + 4 * lane);
@@ -327,7 +367,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
   int seg_idx = 0;
   while (u < u1) {
     int b, j, g0, ng;
-    locate_unit(p, u, b, j, g0, ng);
+    locate_unit<SPARSE>(p, u, b, j, g0, ng);
     const int64_t row_end = p.seq[b].ubase + (int64_t)(j + 1) * ng;
     const int64_t seg_end = row_end < u1 ? row_end : u1;
     const int64_t k_begin = k;
@@ -445,6 +485,13 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
       }
       if (!wait_issued(&S.issued[s], use, &S.abort_flag, p.h.err_word, p.h.spin_limit)) continue;
       if (!mbar_wait_bounded(&S.full[s], use & 1, &S.abort_flag, p.h.err_word, p.h.spin_limit)) continue;
+      if constexpr (SPARSE) {
+        if (S.skip[s]) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.empty[s]);
+          continue;
+        }
+      }
       const uint8_t* blk = S.stage[s];
       const uint8_t* ksc = blk + B::kKScale;
       const uint8_t* kze = blk + B::kKZero;
@@ -712,7 +759,7 @@ __global__ void __launch_bounds__(kCombineThreads)
   const DecodeSeq sq = p.seq[b];
   const int hkv = p.h.hkv, gqa = p.h.gqa;
   const bool active = h < gqa;
-  const int ng = units_of_len(sq.len, p.h.bf16_mode);
+  const int ng = p.h.groups != nullptr ? row_units<true>(p, b) : units_of_len(sq.len, p.h.bf16_mode);
   const int wlen = p.h.bf16_mode ? 0 : (sq.len % kGroup);
   // fused append: the newest window row comes from the input (the host only
   // fuses when no group closes, so wlen >= 1); the others from the arena
@@ -877,7 +924,12 @@ __global__ void __launch_bounds__(kCombineThreads)
     }
   }
   if (active) {
-    const float ov = Oh / Lh;
+    // listed groups can leave a row without a token: zeros, log-sum-exp -inf
+    const bool none = p.h.groups != nullptr && Mh == -INFINITY;
+    const float ov = none ? 0.0f : Oh / Lh;
+    if (p.h.lse != nullptr && c == 0)
+      p.h.lse[(int64_t)b * p.h.hq + j * p.h.q_group + p.h.q_head0 + h] =
+          none ? -INFINITY : fmaf(Mh, 0.693147180559945309f, logf(Lh));
     const int64_t oi = ((int64_t)b * p.h.hq + j * p.h.q_group + p.h.q_head0 + h) * kHeadDim + c;
     if (p.h.out_f32)
       reinterpret_cast<float*>(p.h.out)[oi] = ov;
@@ -896,13 +948,13 @@ int num_sms(int device) {
   return n;
 }
 
-template <int MAXS, bool M16, bool PAIRS>
+template <int MAXS, bool M16, bool PAIRS, bool SPARSE>
 cudaError_t launch_decode_int2_t(const DecodeParams<MAXS>& p, const uint8_t* arena, cudaStream_t stream,
                                  cudaEvent_t ev_start, cudaEvent_t ev_stop) {
   if (p.h.n_units <= 0) return cudaSuccess;
   const int smem = (int)sizeof(DecSmemT<M16>);
   static bool attr_done[64] = {};
-  cudaError_t e = ensure_smem_attr(decode_int2_kernel<MAXS, M16, PAIRS>, smem, attr_done);
+  cudaError_t e = ensure_smem_attr(decode_int2_kernel<MAXS, M16, PAIRS, SPARSE>, smem, attr_done);
   if (e != cudaSuccess) return e;
   if (ev_start) cudaEventRecord(ev_start, stream);
   // programmatic dependent launch: the grid may start while the previous
@@ -917,7 +969,7 @@ cudaError_t launch_decode_int2_t(const DecodeParams<MAXS>& p, const uint8_t* are
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, decode_int2_kernel<MAXS, M16, PAIRS>, p, arena);
+  e = cudaLaunchKernelEx(&cfg, decode_int2_kernel<MAXS, M16, PAIRS, SPARSE>, p, arena);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (ev_stop) cudaEventRecord(ev_stop, stream);
   return e;
@@ -927,11 +979,18 @@ template <int MAXS>
 cudaError_t launch_decode_int2(const DecodeParams<MAXS>& p, const uint8_t* arena, bool meta16, cudaStream_t stream,
                                cudaEvent_t ev_start, cudaEvent_t ev_stop) {
   // more than kMaxGqa query heads per KV head: two head sets on the same blocks
-  if (p.h.gqa > kMaxGqa)
-    return meta16 ? launch_decode_int2_t<MAXS, true, true>(p, arena, stream, ev_start, ev_stop)
-                  : launch_decode_int2_t<MAXS, false, true>(p, arena, stream, ev_start, ev_stop);
-  return meta16 ? launch_decode_int2_t<MAXS, true, false>(p, arena, stream, ev_start, ev_stop)
-                : launch_decode_int2_t<MAXS, false, false>(p, arena, stream, ev_start, ev_stop);
+  auto launch = [&](auto m16, auto pairs, auto sparse) {
+    return launch_decode_int2_t<MAXS, decltype(m16)::value, decltype(pairs)::value, decltype(sparse)::value>(
+        p, arena, stream, ev_start, ev_stop);
+  };
+  using T = std::true_type;
+  using F = std::false_type;
+  if (p.h.groups != nullptr) {
+    if (p.h.gqa > kMaxGqa) return meta16 ? launch(T{}, T{}, T{}) : launch(F{}, T{}, T{});
+    return meta16 ? launch(T{}, F{}, T{}) : launch(F{}, F{}, T{});
+  }
+  if (p.h.gqa > kMaxGqa) return meta16 ? launch(T{}, T{}, F{}) : launch(F{}, T{}, F{});
+  return meta16 ? launch(T{}, F{}, F{}) : launch(F{}, F{}, F{});
 }
 
 template <int MAXS>

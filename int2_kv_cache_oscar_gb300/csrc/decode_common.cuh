@@ -28,9 +28,17 @@ __device__ __forceinline__ int units_of_len(int len, int bf16_mode) {
   return bf16_mode ? (len + 63) / 64 : len / kGroup;
 }
 
+// Units of sequence b's rows; with listed groups (SPARSE) the entries of the
+// list, none for a sequence without groups.
+template <bool SPARSE, int MAXS>
+__device__ __forceinline__ int row_units(const DecodeParams<MAXS>& p, int b) {
+  if constexpr (SPARSE) return p.seq[b].len >= kGroup ? p.h.n_sel : 0;
+  return units_of_len(p.seq[b].len, p.h.bf16_mode);
+}
+
 // Locate unit u: sequence b (the largest with ubase <= u; it is never empty),
 // KV head j and unit index g within the row.
-template <int MAXS>
+template <bool SPARSE = false, int MAXS>
 __device__ __forceinline__ void locate_unit(const DecodeParams<MAXS>& p, int64_t u, int& b, int& j, int& g,
                                             int& ng) {
   int lo = 0, hi = p.h.n_seqs - 1;
@@ -39,7 +47,7 @@ __device__ __forceinline__ void locate_unit(const DecodeParams<MAXS>& p, int64_t
     if (p.seq[mid].ubase <= u) lo = mid; else hi = mid - 1;
   }
   b = lo;
-  ng = units_of_len(p.seq[b].len, p.h.bf16_mode);
+  ng = row_units<SPARSE>(p, b);
   const int64_t off = u - p.seq[b].ubase;
   j = (int)(off / ng);
   g = (int)(off - (int64_t)j * ng);

@@ -4,6 +4,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "common.cuh"
+
 namespace oscar {
 
 // One 128-token group of one sequence that fills during an append (all KV
@@ -127,6 +129,12 @@ struct DecodeHeader {
   // unit's copy unissued (its consumer's wait runs out), and a small limit
   uint32_t spin_limit;
   int32_t fault_unit;
+  // INT2 over listed groups: a row's units are the n_sel entries of
+  // groups[(sequence * hkv + head) * n_sel], an entry outside [0, groups of
+  // the sequence) is skipped (NULL: a row's units are its groups)
+  const int32_t* groups;
+  int32_t n_sel;
+  float* lse;            // [n_seqs, hq] natural-log log-sum-exp of the rows, or NULL
 };
 
 template <int MAXS>
@@ -140,6 +148,115 @@ constexpr int kDecodeSeqsLarge = 1024;
 
 // Floats of one partial record (o[128], m, l, 2 pad) per query head.
 constexpr int kPartialFloats = 132;
+
+// ------------------------------------------------------------------ rotary
+
+// Rows of one tensor [n, heads, 128]: strides in bytes, in and out.
+struct RotaryRows {
+  const uint8_t* in;
+  uint8_t* out;
+  int64_t in_token, in_head;
+  int64_t out_token, out_head;
+  int32_t heads;
+};
+
+struct RotaryParams {
+  RotaryRows q, k;            // heads 0: absent
+  const int32_t* positions;   // [n]
+  int64_t n;
+  int32_t dim;                // rotated channels
+  int32_t block_tokens;       // set by the launch
+  int32_t transpose;
+  float factor;
+  uint64_t freq[kHeadDim / 2];   // turns per position, 2^64 to the turn
+};
+
+cudaError_t launch_rotary(const RotaryParams& p, bool f32, bool interleaved, int sms, cudaStream_t stream);
+
+// -------------------------------------------------------------------- read
+
+// Tokens [start, end) of one sequence; its output rows begin at row0.  Tiles
+// of 128 tokens (the last one may be the window) times KV heads, head fastest,
+// are numbered from ubase.
+struct ReadSeq {
+  int32_t slot;
+  int32_t len;
+  int32_t start;
+  int32_t end;
+  int64_t row0;
+  int64_t ubase;
+};
+
+constexpr int kReadSeqsLarge = 512;   // sequences of one launch (within the kernel parameter limit)
+
+template <int MAXS>
+struct ReadParams {
+  int32_t n_seqs;      // sequences with a non-empty range
+  int32_t hkv;
+  int32_t max_groups;
+  int32_t wide;        // 1: both outputs are 32-byte aligned
+  int64_t blocks_off;
+  int64_t windows_off;
+  int64_t n_tiles;
+  void* k_out;         // [rows, hkv, 128], or NULL
+  void* v_out;
+  ReadSeq seq[MAXS];
+};
+
+template <int MAXS>
+cudaError_t launch_read(const ReadParams<MAXS>& p, const uint8_t* arena, bool meta16, bool f32, int sms,
+                        cudaStream_t stream);
+
+// ------------------------------------------------------------------ select
+
+struct IndexSeq {
+  int32_t slot;
+  int32_t first;   // groups [first, end) are summarised
+  int32_t end;
+};
+
+template <int MAXS>
+struct IndexParams {
+  int32_t n_seqs;
+  int32_t hkv;
+  int32_t max_groups;
+  int64_t blocks_off;
+  uint2* codes;        // [slot][KV head][group][lane]: 4 channels' lowest and highest values
+  float2* weights;     // [slot][KV head][group]: largest and smallest norm, times the step
+  IndexSeq seq[MAXS];
+};
+
+struct SelectSeq {
+  int32_t slot;
+  int32_t ng;
+};
+
+template <int MAXS>
+struct SelectParams {
+  int32_t n_seqs;
+  int32_t hkv;
+  int32_t hq;
+  int32_t q_group;
+  int32_t max_groups;
+  int32_t n_select;
+  int32_t keep_first;
+  int32_t keep_last;
+  const uint2* codes;
+  const float2* weights;
+  const uint16_t* q;   // [n_seqs, hq, 128]
+  int32_t* out;        // [n_seqs, hkv, n_select]
+  SelectSeq seq[MAXS];
+};
+
+constexpr int kSelectMaxSmem = 200 * 1024;
+constexpr int kSelectMaxHeads = 64;   // query heads per KV head
+// dynamic shared memory of the selection among `groups` groups
+size_t select_smem_bytes(int q_group, int groups);
+
+template <int MAXS>
+cudaError_t launch_index(const IndexParams<MAXS>& p, const uint8_t* arena, bool meta16, cudaStream_t stream);
+template <int MAXS>
+cudaError_t launch_select(const SelectParams<MAXS>& p, cudaStream_t stream);
 
 // ----------------------------------------------------------------- prefill
 

@@ -1,9 +1,11 @@
 // C ABI of the OScaR INT2 KV-cache library: host-side validation, planning
 // and launches.  Every argument is checked before anything is enqueued; on
 // error nothing is enqueued and no host state changes.
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 #include <exception>
 #include <string>
@@ -35,6 +37,11 @@ struct oscar_cache {
   std::vector<int32_t> fresh_from;
   bool decoded = false;          // a decode was enqueued on last_stream
   cudaStream_t last_stream = nullptr;
+  // Group summaries (caller's buffer): codes, then weights; per slot the
+  // leading groups that an update has been enqueued for.
+  uint2* index_codes = nullptr;
+  float2* index_weights = nullptr;
+  std::vector<int32_t> indexed;
 };
 
 namespace {
@@ -176,15 +183,22 @@ oscar_status run_quant_plan(oscar_cache* c, const std::vector<QuantTask>& tasks,
 
 size_t partial_bytes(int64_t slots, int gqa) { return (size_t)slots * gqa * kPartialFloats * sizeof(float); }
 
+// Work units of one row: 64-token tiles (BF16 reference), groups, or (n_sel >
+// 0) the entries of its group list.
+int units_of_row(int len, int bf16_mode, int32_t n_sel) {
+  if (n_sel > 0) return len >= kGroup ? n_sel : 0;
+  return bf16_mode ? (len + 63) / 64 : len / kGroup;
+}
+
 // Fill the per-sequence table and unit counts of one decode launch.
 template <int MAXS>
 void fill_decode(DecodeParams<MAXS>& P, int32_t n, const int32_t* slots, const int32_t* lens, int hkv,
-                 int bf16_mode, int64_t& rows_nonempty) {
+                 int bf16_mode, int32_t n_sel, int64_t& rows_nonempty) {
   int64_t ubase = 0;
   int32_t rank = 0;
   for (int32_t i = 0; i < n; ++i) {
     const int len = lens[i];
-    const int units = bf16_mode ? (len + 63) / 64 : len / kGroup;
+    const int units = units_of_row(len, bf16_mode, n_sel);
     P.seq[i].slot = slots[i];
     P.seq[i].len = len;
     P.seq[i].ubase = ubase;
@@ -203,11 +217,15 @@ oscar_status run_decode(int device, int sms, int ctas_per_sm, int32_t n, const i
                         int64_t windows_off, const uint8_t* arena, uint32_t* err_word, const uint16_t* kc,
                         const uint16_t* vc, const void* q, void* out, void* ws, size_t ws_bytes,
                         cudaStream_t stream, const void* k_new = nullptr, const void* v_new = nullptr,
-                        bool meta16 = false, bool out_f32 = false, const int32_t* settled = nullptr) {
+                        bool meta16 = false, bool out_f32 = false, const int32_t* settled = nullptr,
+                        const int32_t* groups = nullptr, int32_t n_sel = 0, float* lse = nullptr) {
   DecodeParams<MAXS> P;
   std::memset(&P, 0, sizeof(P));
   int64_t rows = 0;
-  fill_decode(P, n, slots, lens, hkv, bf16_mode, rows);
+  fill_decode(P, n, slots, lens, hkv, bf16_mode, n_sel, rows);
+  P.h.groups = groups;
+  P.h.n_sel = n_sel;
+  P.h.lse = lse;
   if (settled)
     for (int32_t i = 0; i < n; ++i) P.seq[i].settled = settled[i];
   const int q_group = hq / hkv;
@@ -259,7 +277,7 @@ oscar_status run_decode(int device, int sms, int ctas_per_sm, int32_t n, const i
   int64_t max_count = 1;
   for (int32_t i = 0; i < n; ++i) {
     if (!bf16_mode) wrows = std::max(wrows, lens[i] % kGroup);
-    const int64_t units = bf16_mode ? (lens[i] + 63) / 64 : lens[i] / kGroup;
+    const int64_t units = units_of_row(lens[i], bf16_mode, n_sel);
     if (units == 0 || T == 0) continue;
     for (int j = 0; j < hkv; ++j) {
       const int64_t U = P.seq[i].ubase + (int64_t)j * units;
@@ -338,6 +356,7 @@ oscar_status oscar_cache_create(const oscar_cache_config* cfg, void* device_aren
     c->layout = L;
     c->len.assign(cfg->max_batch, 0);
     c->fresh_from.assign(cfg->max_batch, 0);
+    c->indexed.assign(cfg->max_batch, 0);
     c->sms = sms;
     *out = c;
     return ok();
@@ -372,9 +391,11 @@ oscar_status oscar_cache_reset(oscar_cache* c, int32_t seq, void* stream) {
   if (seq < 0) {
     std::fill(c->len.begin(), c->len.end(), 0);
     std::fill(c->fresh_from.begin(), c->fresh_from.end(), 0);
+    std::fill(c->indexed.begin(), c->indexed.end(), 0);
   } else {
     c->len[seq] = 0;
     c->fresh_from[seq] = 0;
+    c->indexed[seq] = 0;
   }
   return ok();
 }
@@ -514,10 +535,11 @@ void note_decode(oscar_cache* c, int32_t n, const int32_t* ids, cudaStream_t st)
   c->last_stream = st;
 }
 
-// oscar_decode_attention and oscar_decode_attention_f32 (out_f32: float32 outputs).
+// oscar_decode_attention and oscar_decode_attention_f32 (out_f32: float32 outputs);
+// with `groups`, oscar_sparse_decode_attention.
 oscar_status decode_call(oscar_cache* c, int32_t n_seqs, const int32_t* seq_ids, const void* q, int32_t num_q_heads,
                          float softmax_scale, void* out, bool out_f32, void* workspace, size_t workspace_bytes,
-                         void* stream) {
+                         void* stream, const int32_t* groups = nullptr, int32_t n_sel = 0, float* lse = nullptr) {
   try {
     if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
     if (n_seqs < 1) return fail(OSCAR_ERR_INVALID_ARG, "n_seqs must be >= 1");
@@ -544,21 +566,24 @@ oscar_status decode_call(oscar_cache* c, int32_t n_seqs, const int32_t* seq_ids,
     if ((s = device_view_as(q, "q", c->cfg.device, &q)) != OSCAR_OK) return s;
     if ((s = device_view_as(out, "out", c->cfg.device, &out)) != OSCAR_OK) return s;
     if ((s = device_view_as(workspace, "workspace", c->cfg.device, &workspace, false)) != OSCAR_OK) return s;
+    if (groups && (s = device_view_as(groups, "groups", c->cfg.device, &groups, false)) != OSCAR_OK) return s;
+    if (lse && (s = device_view_as(lse, "lse", c->cfg.device, &lse)) != OSCAR_OK) return s;
     uint32_t* err_word = reinterpret_cast<uint32_t*>(c->arena);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const std::vector<int32_t> settled = settled_groups(c, n_seqs, seq_ids, st);
+    // (listed groups are device data: none of their blocks is copied early)
+    const std::vector<int32_t> settled = groups ? std::vector<int32_t>(n_seqs, 0) : settled_groups(c, n_seqs, seq_ids, st);
     if (n_seqs <= kDecodeSeqsSmall)
       s = run_decode<kDecodeSeqsSmall>(c->cfg.device, c->sms, decode_int2_ctas_per_sm(), n_seqs, seq_ids,
                                        lens.data(), hkv, num_q_heads, scale, 0, c->layout.max_groups,
                                        c->layout.blocks_off, c->layout.windows_off, c->arena, err_word, nullptr,
                                        nullptr, q, out, workspace, workspace_bytes, st, nullptr, nullptr,
-                                       c->meta16, out_f32, settled.data());
+                                       c->meta16, out_f32, settled.data(), groups, n_sel, lse);
     else
       s = run_decode<kDecodeSeqsLarge>(c->cfg.device, c->sms, decode_int2_ctas_per_sm(), n_seqs, seq_ids,
                                        lens.data(), hkv, num_q_heads, scale, 0, c->layout.max_groups,
                                        c->layout.blocks_off, c->layout.windows_off, c->arena, err_word, nullptr,
                                        nullptr, q, out, workspace, workspace_bytes, st, nullptr, nullptr,
-                                       c->meta16, out_f32, settled.data());
+                                       c->meta16, out_f32, settled.data(), groups, n_sel, lse);
     if (s != OSCAR_OK) return s;
     note_decode(c, n_seqs, seq_ids, st);
     return ok();
@@ -904,6 +929,475 @@ oscar_status oscar_bf16_decode_attention(int32_t n_seqs, const int32_t* seq_ids,
   } catch (const std::exception& ex) {
     return fail(OSCAR_ERR_INVALID_ARG, "host allocation failed: %s", ex.what());
   }
+}
+
+}  // extern "C"
+
+namespace {
+
+// Checks shared by the calls over a batch of at most 1,024 sequences.
+oscar_status check_batch(const oscar_cache* c, int32_t n_seqs, const int32_t* seq_ids) {
+  if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
+  if (n_seqs < 0) return fail(OSCAR_ERR_INVALID_ARG, "n_seqs < 0");
+  if (n_seqs > kDecodeSeqsLarge) return fail(OSCAR_ERR_CAPACITY, "at most %d sequences per call", kDecodeSeqsLarge);
+  if (n_seqs > 0 && !seq_ids) return fail(OSCAR_ERR_INVALID_ARG, "seq_ids is NULL");
+  return OSCAR_OK;
+}
+
+oscar_status check_type(int32_t type) {
+  if (type != OSCAR_BF16 && type != OSCAR_F32)
+    return fail(OSCAR_ERR_UNSUPPORTED, "type must be OSCAR_BF16 or OSCAR_F32 (got %d)", type);
+  return OSCAR_OK;
+}
+
+// Frequencies and factor of a rotary configuration.
+oscar_status rotary_frequencies(const oscar_rotary_config* c, double* f, double* m) {
+  if (!c) return fail(OSCAR_ERR_INVALID_ARG, "config is NULL");
+  if (c->head_dim != kHeadDim) return fail(OSCAR_ERR_UNSUPPORTED, "head_dim must be 128 (got %d)", c->head_dim);
+  if (c->rotary_dim < 16 || c->rotary_dim > kHeadDim || c->rotary_dim % 16 != 0)
+    return fail(OSCAR_ERR_UNSUPPORTED, "rotary_dim must be a multiple of 16 up to 128 (got %d)", c->rotary_dim);
+  if (c->interleaved != 0 && c->interleaved != 1) return fail(OSCAR_ERR_INVALID_ARG, "interleaved must be 0 or 1");
+  if (c->scaling < OSCAR_ROTARY_NONE || c->scaling > OSCAR_ROTARY_YARN)
+    return fail(OSCAR_ERR_UNSUPPORTED, "unknown rotary scaling %d", c->scaling);
+  if (!(c->base > 1.0) || std::isinf(c->base)) return fail(OSCAR_ERR_INVALID_ARG, "base must be finite and > 1");
+  if (!std::isfinite(c->attention_factor)) return fail(OSCAR_ERR_INVALID_ARG, "attention_factor must be finite");
+  const bool scaled = c->scaling != OSCAR_ROTARY_NONE;
+  if (scaled && (!(c->factor >= 1.0) || std::isinf(c->factor)))
+    return fail(OSCAR_ERR_INVALID_ARG, "factor must be finite and >= 1");
+  double low = c->low, high = c->high;
+  const bool by_length = c->scaling == OSCAR_ROTARY_BANDED || c->scaling == OSCAR_ROTARY_YARN;
+  if (by_length) {
+    if (!(c->original_length > 0.0) || std::isinf(c->original_length))
+      return fail(OSCAR_ERR_INVALID_ARG, "original_length must be finite and > 0");
+    if (low == 0.0 && high == 0.0) {
+      low = 1.0;
+      high = c->scaling == OSCAR_ROTARY_BANDED ? 4.0 : 32.0;
+    }
+    if (!(low > 0.0) || !(high > low) || std::isinf(high))
+      return fail(OSCAR_ERR_INVALID_ARG, "low and high must be finite with 0 < low < high");
+  }
+  const double two_pi = 6.283185307179586476925286766559;
+  const int dim = c->rotary_dim;
+  double l = 0.0, h = 0.0;
+  if (c->scaling == OSCAR_ROTARY_YARN) {
+    const auto at = [&](double turns) {
+      return dim * std::log(c->original_length / (two_pi * turns)) / (2.0 * std::log(c->base));
+    };
+    l = std::max(std::floor(at(high)), 0.0);
+    h = std::min(std::ceil(at(low)), (double)(dim - 1));
+    if (l == h) h += 0.001;
+  }
+  for (int i = 0; i < dim / 2; ++i) {
+    const double x = std::pow(c->base, -2.0 * i / dim);
+    double y = x;
+    if (c->scaling == OSCAR_ROTARY_LINEAR) {
+      y = x / c->factor;
+    } else if (by_length) {
+      const double keep = c->scaling == OSCAR_ROTARY_BANDED
+                              ? (c->original_length * x / two_pi - low) / (high - low)
+                              : 1.0 - (i - l) / (h - l);
+      const double r = std::min(1.0, std::max(0.0, keep));
+      y = (1.0 - r) * x / c->factor + r * x;
+    }
+    f[i] = y;
+  }
+  *m = c->attention_factor != 0.0 ? c->attention_factor
+       : c->scaling == OSCAR_ROTARY_YARN ? 0.1 * std::log(c->factor) + 1.0
+                                         : 1.0;
+  return OSCAR_OK;
+}
+
+// One tensor's rows of a rotary call.
+oscar_status rotary_rows(const oscar_rotary_rows* x, const char* name, int64_t n, int elem, int device,
+                         RotaryRows* out) {
+  std::memset(out, 0, sizeof(*out));
+  if (x == nullptr || x->heads == 0) return OSCAR_OK;
+  if (x->heads < 0 || x->heads > (1 << 16))
+    return fail(OSCAR_ERR_INVALID_ARG, "%s: heads must be in [0, 65536]", name);
+  if (!x->in || !x->out) return fail(OSCAR_ERR_INVALID_ARG, "%s: NULL rows", name);
+  const int64_t unit = 16 / elem;
+  const int64_t strides[4] = {x->in_token_stride, x->in_head_stride, x->out_token_stride, x->out_head_stride};
+  for (int i = 0; i < 4; ++i) {
+    if (strides[i] % unit != 0 || std::llabs(strides[i]) > (INT64_MAX >> 8) / (std::max<int64_t>(n, 1 << 16)))
+      return fail(OSCAR_ERR_INVALID_ARG, "%s: strides must be multiples of 16 bytes", name);
+  }
+  if (!aligned(x->in, 16) || !aligned(x->out, 16))
+    return fail(OSCAR_ERR_INVALID_ARG, "%s: rows must be 16-byte aligned", name);
+  if (x->in == x->out && (x->in_token_stride != x->out_token_stride || x->in_head_stride != x->out_head_stride))
+    return fail(OSCAR_ERR_INVALID_ARG, "%s: in-place rows need the same strides in and out", name);
+  // distinct output rows: heads side by side within a token, or tokens within a head
+  const int64_t ts = std::llabs(x->out_token_stride), hs = std::llabs(x->out_head_stride), H = x->heads;
+  const bool heads_inner = (H == 1 || hs >= kHeadDim) && (n == 1 || ts >= (H - 1) * hs + kHeadDim);
+  const bool tokens_inner = (n == 1 || ts >= kHeadDim) && (H == 1 || hs >= (n - 1) * ts + kHeadDim);
+  if (!heads_inner && !tokens_inner) return fail(OSCAR_ERR_INVALID_ARG, "%s: output rows overlap", name);
+  const void* in = nullptr;
+  const void* dst = nullptr;
+  oscar_status s = device_view(x->in, name, device, &in, false);
+  if (s == OSCAR_OK) s = device_view(x->out, name, device, &dst, false);
+  if (s != OSCAR_OK) return s;
+  out->in = static_cast<const uint8_t*>(in);
+  out->out = static_cast<uint8_t*>(const_cast<void*>(dst));
+  out->in_token = x->in_token_stride * elem;
+  out->in_head = x->in_head_stride * elem;
+  out->out_token = x->out_token_stride * elem;
+  out->out_head = x->out_head_stride * elem;
+  out->heads = x->heads;
+  return OSCAR_OK;
+}
+
+template <int CAP>
+oscar_status run_read(oscar_cache* c, const std::vector<ReadSeq>& seqs, size_t first, size_t n, bool f32, void* k,
+                      void* v, cudaStream_t st) {
+  ReadParams<CAP> P;
+  std::memset(&P, 0, sizeof(P));
+  P.n_seqs = (int32_t)n;
+  P.hkv = c->cfg.num_kv_heads;
+  P.max_groups = c->layout.max_groups;
+  P.wide = (aligned(k, 32) && aligned(v, 32)) ? 1 : 0;
+  P.blocks_off = c->layout.blocks_off;
+  P.windows_off = c->layout.windows_off;
+  P.k_out = k;
+  P.v_out = v;
+  int64_t ubase = 0;
+  for (size_t i = 0; i < n; ++i) {
+    P.seq[i] = seqs[first + i];
+    P.seq[i].ubase = ubase;
+    ubase += (int64_t)((P.seq[i].end - 1) / kGroup - P.seq[i].start / kGroup + 1) * P.hkv;
+  }
+  P.n_tiles = ubase;
+  const cudaError_t e = launch_read(P, c->arena, c->meta16, f32, c->sms, st);
+  return e == cudaSuccess ? OSCAR_OK : cuda_fail(e, "read launch");
+}
+
+template <int CAP>
+oscar_status run_index(oscar_cache* c, const std::vector<IndexSeq>& seqs, cudaStream_t st) {
+  IndexParams<CAP> P;
+  std::memset(&P, 0, sizeof(P));
+  P.n_seqs = (int32_t)seqs.size();
+  P.hkv = c->cfg.num_kv_heads;
+  P.max_groups = c->layout.max_groups;
+  P.blocks_off = c->layout.blocks_off;
+  P.codes = c->index_codes;
+  P.weights = c->index_weights;
+  std::copy(seqs.begin(), seqs.end(), P.seq);
+  const cudaError_t e = launch_index(P, c->arena, c->meta16, st);
+  return e == cudaSuccess ? OSCAR_OK : cuda_fail(e, "index launch");
+}
+
+template <int CAP>
+oscar_status run_select(const oscar_cache* c, const std::vector<SelectSeq>& seqs, const void* q, int32_t hq,
+                        int32_t n_select, int32_t keep_first, int32_t keep_last, int32_t* out, cudaStream_t st) {
+  SelectParams<CAP> P;
+  std::memset(&P, 0, sizeof(P));
+  P.n_seqs = (int32_t)seqs.size();
+  P.hkv = c->cfg.num_kv_heads;
+  P.hq = hq;
+  P.q_group = hq / P.hkv;
+  P.max_groups = c->layout.max_groups;
+  P.n_select = n_select;
+  P.keep_first = keep_first;
+  P.keep_last = keep_last;
+  P.codes = c->index_codes;
+  P.weights = c->index_weights;
+  P.q = static_cast<const uint16_t*>(q);
+  P.out = out;
+  std::copy(seqs.begin(), seqs.end(), P.seq);
+  const cudaError_t e = launch_select(P, st);
+  return e == cudaSuccess ? OSCAR_OK : cuda_fail(e, "select launch");
+}
+
+// Addresses and byte counts of one slot's state for the copies of export and import.
+struct SlotCopies {
+  uint8_t *blocks, *window, *smax, *zmax;
+  size_t block_row, block_pitch, window_row;
+};
+
+SlotCopies slot_copies(const oscar_cache* c, int32_t seq, int32_t length) {
+  SlotCopies r;
+  const int64_t row = (int64_t)seq * c->cfg.num_kv_heads;
+  r.block_pitch = (size_t)c->layout.max_groups * c->block_bytes;
+  r.block_row = (size_t)(length / kGroup) * c->block_bytes;
+  r.blocks = c->arena + c->layout.blocks_off + row * (int64_t)r.block_pitch;
+  r.window = c->arena + c->layout.windows_off + row * kWindowBytes;
+  r.window_row = (size_t)(length % kGroup) * kHeadDim * 2;
+  r.smax = c->arena + kMetaHeader + row * 4;
+  r.zmax = c->arena + c->layout.zmax_off + row * 4;
+  return r;
+}
+
+oscar_status check_slot_buffers(const oscar_cache* c, int32_t length, const void* blocks, const void* window,
+                                const float* maxima) {
+  if ((length >= kGroup && !blocks) || (length % kGroup != 0 && !window) || !maxima)
+    return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
+  if (!aligned(blocks, 16) || !aligned(window, 16) || !aligned(maxima, 16))
+    return fail(OSCAR_ERR_INVALID_ARG, "blocks, window and maxima must be 16-byte aligned");
+  const void* v = nullptr;
+  oscar_status s = OSCAR_OK;
+  if (length >= kGroup) s = device_view(blocks, "blocks", c->cfg.device, &v);
+  if (s == OSCAR_OK && length % kGroup != 0) s = device_view(window, "window", c->cfg.device, &v);
+  if (s == OSCAR_OK) s = device_view(maxima, "maxima", c->cfg.device, &v);
+  return s;
+}
+
+}  // namespace
+
+extern "C" {
+
+oscar_status oscar_rotary_frequencies(const oscar_rotary_config* cfg, double* frequencies, double* attention_factor) {
+  double f[kHeadDim / 2], m = 0.0;
+  const oscar_status s = rotary_frequencies(cfg, f, &m);
+  if (s != OSCAR_OK) return s;
+  if (!frequencies || !attention_factor) return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
+  std::copy(f, f + cfg->rotary_dim / 2, frequencies);
+  *attention_factor = m;
+  return ok();
+}
+
+oscar_status oscar_rotary(const oscar_rotary_config* cfg, int64_t n_tokens, const int32_t* positions, int32_t type,
+                          const oscar_rotary_rows* q, const oscar_rotary_rows* k, int32_t transpose, void* stream) {
+  double f[kHeadDim / 2], m = 0.0;
+  oscar_status s = rotary_frequencies(cfg, f, &m);
+  if (s == OSCAR_OK) s = check_type(type);
+  if (s != OSCAR_OK) return s;
+  if (n_tokens < 0 || n_tokens > INT32_MAX) return fail(OSCAR_ERR_INVALID_ARG, "n_tokens out of range");
+  if (transpose != 0 && transpose != 1) return fail(OSCAR_ERR_INVALID_ARG, "transpose must be 0 or 1");
+  if (n_tokens == 0) return ok();
+  if (!positions) return fail(OSCAR_ERR_INVALID_ARG, "positions is NULL");
+  if (!aligned(positions, 4)) return fail(OSCAR_ERR_INVALID_ARG, "positions must be 4-byte aligned");
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  RotaryParams P;
+  std::memset(&P, 0, sizeof(P));
+  const int elem = type == OSCAR_F32 ? 4 : 2;
+  if ((s = rotary_rows(q, "q", n_tokens, elem, dev, &P.q)) != OSCAR_OK) return s;
+  if ((s = rotary_rows(k, "k", n_tokens, elem, dev, &P.k)) != OSCAR_OK) return s;
+  if (P.q.heads + P.k.heads == 0) return ok();
+  if ((s = device_view_as(positions, "positions", dev, &positions)) != OSCAR_OK) return s;
+  P.positions = positions;
+  P.n = n_tokens;
+  P.dim = cfg->rotary_dim;
+  P.transpose = transpose;
+  P.factor = (float)m;
+  // turns per position (below 1/6: frequencies are at most 1 radian), 2^64 to
+  // the turn: the quotient by 2 pi (as a sum of two float64) and its remainder
+  const double two_pi_hi = 6.283185307179586, two_pi_lo = 2.4492935982947064e-16;
+  for (int i = 0; i < cfg->rotary_dim / 2; ++i) {
+    const double t = f[i] / two_pi_hi;
+    const double rest = std::fma(-t, two_pi_lo, std::fma(-t, two_pi_hi, f[i])) / two_pi_hi;
+    P.freq[i] = (uint64_t)std::ldexp(t, 64) + (uint64_t)(int64_t)std::rint(std::ldexp(rest, 64));
+  }
+  e = launch_rotary(P, type == OSCAR_F32, cfg->interleaved != 0, num_sms(dev), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rotary launch");
+  return ok();
+}
+
+oscar_status oscar_cache_read(oscar_cache* c, int32_t n_seqs, const int32_t* seq_ids, const int32_t* start,
+                              const int32_t* end, int32_t type, void* k_out, void* v_out, void* stream) {
+  try {
+    if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
+    if (n_seqs < 0) return fail(OSCAR_ERR_INVALID_ARG, "n_seqs < 0");
+    oscar_status s = check_type(type);
+    if (s != OSCAR_OK) return s;
+    if (n_seqs > 0 && (!seq_ids || !start || !end)) return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
+    std::vector<ReadSeq> seqs;
+    int64_t rows = 0;
+    for (int32_t i = 0; i < n_seqs; ++i) {
+      if (seq_ids[i] < 0 || seq_ids[i] >= c->cfg.max_batch)
+        return fail(OSCAR_ERR_INVALID_ARG, "seq_ids[%d] = %d out of range", i, seq_ids[i]);
+      const int32_t len = c->len[seq_ids[i]];
+      if (start[i] < 0 || start[i] > end[i] || end[i] > len)
+        return fail(OSCAR_ERR_INVALID_ARG, "range %d: [%d, %d) outside the %d tokens of sequence %d", i, start[i],
+                    end[i], len, seq_ids[i]);
+      if (start[i] < end[i]) seqs.push_back(ReadSeq{seq_ids[i], len, start[i], end[i], rows, 0});
+      rows += end[i] - start[i];
+    }
+    if (!aligned(k_out, 16) || !aligned(v_out, 16))
+      return fail(OSCAR_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
+    if (rows == 0 || (!k_out && !v_out)) return ok();
+    if (k_out == v_out) return fail(OSCAR_ERR_INVALID_ARG, "k_out and v_out are the same buffer");
+    DeviceGuard dg(c->cfg.device);
+    if (dg.err != cudaSuccess) return cuda_fail(dg.err, "cudaSetDevice");
+    if (k_out && (s = device_view_as(k_out, "k_out", c->cfg.device, &k_out, false)) != OSCAR_OK) return s;
+    if (v_out && (s = device_view_as(v_out, "v_out", c->cfg.device, &v_out, false)) != OSCAR_OK) return s;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    for (size_t b = 0; b < seqs.size(); b += kReadSeqsLarge) {
+      const size_t n = std::min(seqs.size() - b, (size_t)kReadSeqsLarge);
+      s = n <= (size_t)kDecodeSeqsSmall ? run_read<kDecodeSeqsSmall>(c, seqs, b, n, type == OSCAR_F32, k_out, v_out, st)
+                                        : run_read<kReadSeqsLarge>(c, seqs, b, n, type == OSCAR_F32, k_out, v_out, st);
+      if (s != OSCAR_OK) return s;   // earlier parts may already be enqueued
+    }
+    return ok();
+  } catch (const std::exception& ex) {
+    return fail(OSCAR_ERR_INVALID_ARG, "host allocation failed: %s", ex.what());
+  }
+}
+
+oscar_status oscar_cache_export(oscar_cache* c, int32_t seq, void* blocks, void* window, float* maxima, void* stream) {
+  if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
+  if (seq < 0 || seq >= c->cfg.max_batch) return fail(OSCAR_ERR_INVALID_ARG, "seq %d out of range", seq);
+  const int32_t length = c->len[seq];
+  DeviceGuard dg(c->cfg.device);
+  if (dg.err != cudaSuccess) return cuda_fail(dg.err, "cudaSetDevice");
+  const oscar_status s = check_slot_buffers(c, length, blocks, window, maxima);
+  if (s != OSCAR_OK) return s;
+  const SlotCopies r = slot_copies(c, seq, length);
+  const size_t hkv = (size_t)c->cfg.num_kv_heads;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  if (r.block_row > 0)
+    e = cudaMemcpy2DAsync(blocks, r.block_row, r.blocks, r.block_pitch, r.block_row, hkv, cudaMemcpyDefault, st);
+  if (e == cudaSuccess && r.window_row > 0)
+    e = cudaMemcpy2DAsync(window, kWindowBytes / 2, r.window, kWindowBytes / 2, r.window_row, 2 * hkv,
+                          cudaMemcpyDefault, st);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(maxima, r.smax, hkv * 4, cudaMemcpyDefault, st);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(maxima + hkv, r.zmax, hkv * 4, cudaMemcpyDefault, st);
+  if (e != cudaSuccess) return cuda_fail(e, "export copy");
+  return ok();
+}
+
+oscar_status oscar_cache_import(oscar_cache* c, int32_t seq, int32_t length, const void* blocks, const void* window,
+                                const float* maxima, void* stream) {
+  if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
+  if (seq < 0 || seq >= c->cfg.max_batch) return fail(OSCAR_ERR_INVALID_ARG, "seq %d out of range", seq);
+  if (length < 0) return fail(OSCAR_ERR_INVALID_ARG, "length < 0");
+  if (length > c->cfg.max_seq_len)
+    return fail(OSCAR_ERR_CAPACITY, "length %d > max_seq_len %d", length, c->cfg.max_seq_len);
+  DeviceGuard dg(c->cfg.device);
+  if (dg.err != cudaSuccess) return cuda_fail(dg.err, "cudaSetDevice");
+  const oscar_status s = check_slot_buffers(c, length, blocks, window, maxima);
+  if (s != OSCAR_OK) return s;
+  const SlotCopies r = slot_copies(c, seq, length);
+  const size_t hkv = (size_t)c->cfg.num_kv_heads;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  // until a copy is known to be enqueued the slot is empty
+  c->len[seq] = 0;
+  c->fresh_from[seq] = 0;
+  c->indexed[seq] = 0;
+  if (r.block_row > 0)
+    e = cudaMemcpy2DAsync(r.blocks, r.block_pitch, blocks, r.block_row, r.block_row, hkv, cudaMemcpyDefault, st);
+  if (e == cudaSuccess && r.window_row > 0)
+    e = cudaMemcpy2DAsync(r.window, kWindowBytes / 2, window, kWindowBytes / 2, r.window_row, 2 * hkv,
+                          cudaMemcpyDefault, st);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(r.smax, maxima, hkv * 4, cudaMemcpyDefault, st);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(r.zmax, maxima + hkv, hkv * 4, cudaMemcpyDefault, st);
+  if (e != cudaSuccess) return cuda_fail(e, "import copy");
+  c->len[seq] = length;
+  return ok();
+}
+
+oscar_status oscar_index_required_bytes(const oscar_cache* c, size_t* out_bytes) {
+  if (!c || !out_bytes) return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
+  *out_bytes = (size_t)c->cfg.max_batch * c->cfg.num_kv_heads * c->layout.max_groups * 264;
+  return ok();
+}
+
+oscar_status oscar_index_attach(oscar_cache* c, void* index, size_t index_bytes) {
+  if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
+  if (index) {
+    size_t need = 0;
+    oscar_status s = oscar_index_required_bytes(c, &need);
+    if (s != OSCAR_OK) return s;
+    if (!aligned(index, 256)) return fail(OSCAR_ERR_INVALID_ARG, "index must be 256-byte aligned");
+    if (index_bytes < need) return fail(OSCAR_ERR_CAPACITY, "index too small: %zu < %zu bytes", index_bytes, need);
+    DeviceGuard dg(c->cfg.device);
+    if (dg.err != cudaSuccess) return cuda_fail(dg.err, "cudaSetDevice");
+    if ((s = device_view_as(index, "index", c->cfg.device, &index, false)) != OSCAR_OK) return s;
+  }
+  const int64_t records = (int64_t)c->cfg.max_batch * c->cfg.num_kv_heads * c->layout.max_groups;
+  c->index_codes = static_cast<uint2*>(index);
+  c->index_weights = index ? reinterpret_cast<float2*>(c->index_codes + records * 32) : nullptr;
+  std::fill(c->indexed.begin(), c->indexed.end(), 0);
+  return ok();
+}
+
+oscar_status oscar_index_update(oscar_cache* c, int32_t n_seqs, const int32_t* seq_ids, int32_t rebuild,
+                                void* stream) {
+  try {
+    oscar_status s = check_batch(c, n_seqs, seq_ids);
+    if (s != OSCAR_OK) return s;
+    if (rebuild != 0 && rebuild != 1) return fail(OSCAR_ERR_INVALID_ARG, "rebuild must be 0 or 1");
+    if (!c->index_codes) return fail(OSCAR_ERR_INVALID_ARG, "no index attached");
+    std::vector<char> seen;
+    if ((s = check_slots(c, n_seqs, seq_ids, seen)) != OSCAR_OK) return s;
+    std::vector<IndexSeq> seqs;
+    for (int32_t i = 0; i < n_seqs; ++i) {
+      const int32_t slot = seq_ids[i], ng = c->len[slot] / kGroup, first = rebuild ? 0 : c->indexed[slot];
+      if (first < ng) seqs.push_back(IndexSeq{slot, first, ng});
+    }
+    if (seqs.empty()) return ok();
+    DeviceGuard dg(c->cfg.device);
+    if (dg.err != cudaSuccess) return cuda_fail(dg.err, "cudaSetDevice");
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    s = seqs.size() <= (size_t)kDecodeSeqsSmall ? run_index<kDecodeSeqsSmall>(c, seqs, st)
+                                                : run_index<kDecodeSeqsLarge>(c, seqs, st);
+    if (s != OSCAR_OK) return s;
+    for (const IndexSeq& x : seqs) c->indexed[x.slot] = x.end;
+    return ok();
+  } catch (const std::exception& ex) {
+    return fail(OSCAR_ERR_INVALID_ARG, "host allocation failed: %s", ex.what());
+  }
+}
+
+oscar_status oscar_select_groups(oscar_cache* c, int32_t n_seqs, const int32_t* seq_ids, const void* q,
+                                 int32_t num_q_heads, int32_t n_select, int32_t keep_first, int32_t keep_last,
+                                 int32_t* groups, void* stream) {
+  try {
+    oscar_status s = check_batch(c, n_seqs, seq_ids);
+    if (s != OSCAR_OK) return s;
+    if (!c->index_codes) return fail(OSCAR_ERR_INVALID_ARG, "no index attached");
+    const int hkv = c->cfg.num_kv_heads;
+    if (num_q_heads < hkv || num_q_heads % hkv != 0)
+      return fail(OSCAR_ERR_INVALID_ARG, "num_q_heads must be a positive multiple of Hkv");
+    if (num_q_heads / hkv > kSelectMaxHeads)
+      return fail(OSCAR_ERR_UNSUPPORTED, "at most %d query heads per KV head", kSelectMaxHeads);
+    if (n_select < 1) return fail(OSCAR_ERR_INVALID_ARG, "n_select must be >= 1");
+    if (keep_first < 0 || keep_last < 0 || (int64_t)keep_first + keep_last > n_select)
+      return fail(OSCAR_ERR_INVALID_ARG, "keep_first and keep_last must be >= 0, together <= n_select");
+    if (n_seqs == 0) return ok();
+    if (!q || !groups) return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
+    if (!aligned(q, 16) || !aligned(groups, 4))
+      return fail(OSCAR_ERR_INVALID_ARG, "q must be 16-byte aligned, groups 4-byte aligned");
+    std::vector<char> seen;
+    if ((s = check_slots(c, n_seqs, seq_ids, seen)) != OSCAR_OK) return s;
+    std::vector<SelectSeq> seqs(n_seqs);
+    for (int32_t i = 0; i < n_seqs; ++i) {
+      const int32_t ng = c->len[seq_ids[i]] / kGroup;
+      if (c->indexed[seq_ids[i]] < ng)
+        return fail(OSCAR_ERR_INVALID_ARG, "sequence %d: %d of %d groups in the index (oscar_index_update)", seq_ids[i],
+                    c->indexed[seq_ids[i]], ng);
+      if (ng > n_select && select_smem_bytes(num_q_heads / hkv, ng) > (size_t)kSelectMaxSmem)
+        return fail(OSCAR_ERR_UNSUPPORTED, "sequence %d: %d groups are too many to choose from", seq_ids[i], ng);
+      seqs[i] = SelectSeq{seq_ids[i], ng};
+    }
+    DeviceGuard dg(c->cfg.device);
+    if (dg.err != cudaSuccess) return cuda_fail(dg.err, "cudaSetDevice");
+    if ((s = device_view_as(q, "q", c->cfg.device, &q)) != OSCAR_OK) return s;
+    if ((s = device_view_as(groups, "groups", c->cfg.device, &groups, false)) != OSCAR_OK) return s;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    s = n_seqs <= kDecodeSeqsSmall
+            ? run_select<kDecodeSeqsSmall>(c, seqs, q, num_q_heads, n_select, keep_first, keep_last, groups, st)
+            : run_select<kDecodeSeqsLarge>(c, seqs, q, num_q_heads, n_select, keep_first, keep_last, groups, st);
+    if (s != OSCAR_OK) return s;
+    return ok();
+  } catch (const std::exception& ex) {
+    return fail(OSCAR_ERR_INVALID_ARG, "host allocation failed: %s", ex.what());
+  }
+}
+
+oscar_status oscar_sparse_decode_attention(oscar_cache* c, int32_t n_seqs, const int32_t* seq_ids, const void* q,
+                                           int32_t num_q_heads, float softmax_scale, const int32_t* groups,
+                                           int32_t n_select, int32_t type, void* out, float* lse, void* workspace,
+                                           size_t workspace_bytes, void* stream) {
+  if (!groups) return fail(OSCAR_ERR_INVALID_ARG, "groups is NULL");
+  if (n_select < 1) return fail(OSCAR_ERR_INVALID_ARG, "n_select must be >= 1");
+  if (!aligned(groups, 4) || !aligned(lse, 4))
+    return fail(OSCAR_ERR_INVALID_ARG, "groups and lse must be 4-byte aligned");
+  const oscar_status s = check_type(type);
+  if (s != OSCAR_OK) return s;
+  return decode_call(c, n_seqs, seq_ids, q, num_q_heads, softmax_scale, out, type == OSCAR_F32, workspace,
+                     workspace_bytes, stream, groups, n_select, lse);
 }
 
 // ------------------------------------------------------------------------

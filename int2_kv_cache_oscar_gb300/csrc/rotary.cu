@@ -1,0 +1,190 @@
+// Rotary positions of queries and keys (sm_103a): one launch turns the query
+// and the key rows of a run of tokens, half or interleaved layout, over the
+// first rotary_dim channels of the 128-channel heads.
+//
+//   (y_a, y_b) = m (x_a cos t - x_b sin t, x_a sin t + x_b cos t),
+//   t = position * frequency(pair); the transpose (the gradient) takes -t.
+//
+// Angles.  A float32 angle of position 131,072 is off by up to 4e-3 rad, and
+// float64 products are slow on this chip, so the angle is kept as a phase, in
+// turns modulo one, in 64-bit fixed point: phase = position * F mod 2^64 with
+// F = frequency / (2 pi) * 2^64, exact integer arithmetic (off by 2^-33 of a
+// turn at position 2^31).  Its top 32 bits give the quadrant and the remainder
+// (at most an eighth of a turn) for sincospif.
+//
+// What bounds it: every element is read and written once, so HBM for long
+// runs and the launch for one token.  A block computes the cosines and sines
+// of its few tokens once for all heads (shared memory) after it has requested
+// its rows, so the loads and that arithmetic overlap.
+#include <algorithm>
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace oscar {
+namespace {
+
+constexpr int kRotThreads = 256;
+constexpr int kRotItems = 4;        // row pieces in flight per thread
+constexpr int kRotMaxTokens = 32;   // tokens of one block
+
+// cos and sin of a phase (turns, 2^64 to the turn)
+__device__ __forceinline__ float2 phase_cos_sin(uint64_t phase) {
+  const uint32_t x = (uint32_t)(phase >> 32) + 0x20000000u;   // + 1/8 turn: quadrant by rounding
+  const int32_t r = (int32_t)(x & 0x3fffffffu) - 0x20000000;  // remainder, 2^-32 turns
+  float s, c;
+  sincospif((float)r * 0x1p-31f, &s, &c);
+  switch (x >> 30) {
+    case 0: return make_float2(c, s);
+    case 1: return make_float2(-s, c);
+    case 2: return make_float2(-c, -s);
+    default: return make_float2(s, -c);
+  }
+}
+
+template <bool F32>
+struct Row;   // 16 bytes of a row, as float32 values
+template <>
+struct Row<false> {
+  static constexpr int kVec = 8;
+  static __device__ __forceinline__ void widen(const uint4& u, float* f) {
+    f[0] = bf16_lo(u.x); f[1] = bf16_hi(u.x); f[2] = bf16_lo(u.y); f[3] = bf16_hi(u.y);
+    f[4] = bf16_lo(u.z); f[5] = bf16_hi(u.z); f[6] = bf16_lo(u.w); f[7] = bf16_hi(u.w);
+  }
+  static __device__ __forceinline__ uint4 narrow(const float* f) {   // nearest even: the output type
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+  }
+};
+template <>
+struct Row<true> {
+  static constexpr int kVec = 4;
+  static __device__ __forceinline__ void widen(const uint4& u, float* f) {
+    f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
+    f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
+  }
+  static __device__ __forceinline__ uint4 narrow(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+
+// A row is cut into items of two 16-byte pieces: in the half layout piece i of
+// the first half and of the second half of the rotated channels, in the
+// interleaved layout (and behind the rotated channels) two neighbours.
+template <bool F32, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
+  using R = Row<F32>;
+  constexpr int V = R::kVec;
+  constexpr int kRowItems = kHeadDim / (2 * V);
+  __shared__ __align__(16) float2 table[kRotMaxTokens][kHeadDim / 2];
+  const int64_t t0 = (int64_t)blockIdx.x * p.block_tokens;
+  const int tokens = (int)min((int64_t)p.block_tokens, (int64_t)p.n - t0);
+  const int rows = p.q.heads + p.k.heads;
+  const int items = tokens * rows * kRowItems;
+  const int rot_items = p.dim / (2 * V);
+  const int half = p.dim / 2;
+
+  auto place = [&](int idx, const uint8_t*& src, uint8_t*& dst, int& a, int& b, int& tok) {
+    const int j = idx % kRowItems;
+    const int row = idx / kRowItems;
+    tok = row / rows;
+    const int h = row - tok * rows;
+    const bool isq = h < p.q.heads;
+    const RotaryRows& x = isq ? p.q : p.k;
+    const int head = isq ? h : h - p.q.heads;
+    src = x.in + (t0 + tok) * x.in_token + head * x.in_head;
+    dst = x.out + (t0 + tok) * x.out_token + head * x.out_head;
+    if (INTERLEAVED || j >= rot_items) {
+      a = 2 * V * j;
+      b = a + V;
+    } else {
+      a = V * j;
+      b = half + V * j;
+    }
+  };
+
+  for (int base = 0; base < items; base += kRotThreads * kRotItems) {
+    uint4 xa[kRotItems], xb[kRotItems];
+#pragma unroll
+    for (int i = 0; i < kRotItems; ++i) {
+      const int idx = base + i * kRotThreads + threadIdx.x;
+      if (idx < items) {
+        const uint8_t* src;
+        uint8_t* dst;
+        int a, b, tok;
+        place(idx, src, dst, a, b, tok);
+        xa[i] = *reinterpret_cast<const uint4*>(src + a * (16 / V));
+        xb[i] = *reinterpret_cast<const uint4*>(src + b * (16 / V));
+      }
+    }
+    if (base == 0) {
+      for (int i = threadIdx.x; i < tokens * half; i += kRotThreads) {
+        const int tok = i / half, pair = i - tok * half;
+        const uint64_t pos = (uint64_t)(int64_t)p.positions[t0 + tok];
+        const float2 cs = phase_cos_sin(pos * p.freq[pair]);
+        table[tok][pair] = make_float2(cs.x * p.factor, cs.y * (p.transpose ? -p.factor : p.factor));
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kRotItems; ++i) {
+      const int idx = base + i * kRotThreads + threadIdx.x;
+      if (idx < items) {
+        const uint8_t* src;
+        uint8_t* dst;
+        int a, b, tok;
+        place(idx, src, dst, a, b, tok);
+        const int j = idx % kRowItems;
+        uint4 ya = xa[i], yb = xb[i];
+        if (j < rot_items) {
+          float u[2 * V];
+          R::widen(ya, u);
+          R::widen(yb, u + V);
+          const float4* cs = reinterpret_cast<const float4*>(&table[tok][V * j]);
+#pragma unroll
+          for (int e = 0; e < V; e += 2) {
+            const float4 w = cs[e / 2];   // (cos, sin) of two pairs
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+              const float c = o ? w.z : w.x, s = o ? w.w : w.y;
+              const int ia = INTERLEAVED ? 2 * (e + o) : e + o;
+              const int ib = INTERLEAVED ? ia + 1 : V + e + o;
+              const float x0 = u[ia], x1 = u[ib];
+              u[ia] = fmaf(x0, c, -(x1 * s));
+              u[ib] = fmaf(x0, s, x1 * c);
+            }
+          }
+          ya = R::narrow(u);
+          yb = R::narrow(u + V);
+        }
+        *reinterpret_cast<uint4*>(dst + a * (16 / V)) = ya;
+        *reinterpret_cast<uint4*>(dst + b * (16 / V)) = yb;
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const RotaryParams& params, bool f32, bool interleaved, int sms, cudaStream_t stream) {
+  RotaryParams p = params;
+  const int rows = p.q.heads + p.k.heads;
+  if (p.n <= 0 || rows <= 0) return cudaSuccess;
+  const int per_token = rows * (kHeadDim / (2 * (f32 ? Row<true>::kVec : Row<false>::kVec)));
+  // as many tokens as give every thread its kRotItems pieces, but no fewer
+  // blocks than two per SM
+  int64_t tokens = std::min<int64_t>(kRotThreads * kRotItems / per_token, (p.n + 2 * sms - 1) / (2 * sms));
+  tokens = std::max<int64_t>(1, std::min<int64_t>(tokens, kRotMaxTokens));
+  p.block_tokens = (int32_t)tokens;
+  const unsigned grid = (unsigned)((p.n + tokens - 1) / tokens);
+  if (f32) {
+    if (interleaved) rotary_kernel<true, true><<<grid, kRotThreads, 0, stream>>>(p);
+    else rotary_kernel<true, false><<<grid, kRotThreads, 0, stream>>>(p);
+  } else {
+    if (interleaved) rotary_kernel<false, true><<<grid, kRotThreads, 0, stream>>>(p);
+    else rotary_kernel<false, false><<<grid, kRotThreads, 0, stream>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace oscar

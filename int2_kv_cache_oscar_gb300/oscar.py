@@ -8,6 +8,7 @@ CPU fallback: importing this module fails loudly if the library is missing.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -26,6 +27,11 @@ OSCAR_ERR_DEVICE_TIMEOUT = 5
 OSCAR_BYTES_USED = 0
 OSCAR_BYTES_BF16_EQUIVALENT = 1
 OSCAR_BYTES_ARENA = 2
+
+OSCAR_BF16 = 0
+OSCAR_F32 = 1
+
+ROTARY_SCALING = {"none": 0, "linear": 1, "banded": 2, "yarn": 3}
 
 HEAD_DIM = 128
 GROUP = 128
@@ -46,6 +52,20 @@ class oscar_cache_config(ctypes.Structure):
                 ("head_dim", ctypes.c_int32), ("max_seq_len", ctypes.c_int32),
                 ("group_size", ctypes.c_int32), ("value_group", ctypes.c_int32),
                 ("device", ctypes.c_int32), ("meta_bits", ctypes.c_int32)]
+
+
+class oscar_rotary_config(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_length", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("attention_factor", ctypes.c_double)]
+
+
+class oscar_rotary_rows(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p),
+                ("src_token_stride", ctypes.c_int64), ("src_head_stride", ctypes.c_int64),
+                ("dst_token_stride", ctypes.c_int64), ("dst_head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32)]
 
 
 def _load() -> ctypes.CDLL:
@@ -80,6 +100,18 @@ def _load() -> ctypes.CDLL:
         "oscar_append_decode": [P, I32, I32P, P, P, P, I32, ctypes.c_float, P, P, SZ, P],
         "oscar_prefill_attention": [P, I32, I32, P, I32, ctypes.c_float, P, P, P, SZ, P],
         "oscar_prefill_workspace_bytes": [P, I32, I32, I32, ctypes.POINTER(SZ)],
+        "oscar_rotary_frequencies": [ctypes.POINTER(oscar_rotary_config), ctypes.POINTER(ctypes.c_double),
+                                     ctypes.POINTER(ctypes.c_double)],
+        "oscar_rotary": [ctypes.POINTER(oscar_rotary_config), ctypes.c_int64, P, I32,
+                         ctypes.POINTER(oscar_rotary_rows), ctypes.POINTER(oscar_rotary_rows), I32, P],
+        "oscar_cache_read": [P, I32, I32P, I32P, I32P, I32, P, P, P],
+        "oscar_cache_export": [P, I32, P, P, P, P],
+        "oscar_cache_import": [P, I32, I32, P, P, P, P],
+        "oscar_index_required_bytes": [P, ctypes.POINTER(SZ)],
+        "oscar_index_attach": [P, P, SZ],
+        "oscar_index_update": [P, I32, I32P, I32, P],
+        "oscar_select_groups": [P, I32, I32P, P, I32, I32, I32, I32, P, P],
+        "oscar_sparse_decode_attention": [P, I32, I32P, P, I32, ctypes.c_float, P, I32, I32, P, P, P, SZ, P],
     }
     for name, args in sigs.items():
         f = getattr(lib, name)
@@ -276,6 +308,148 @@ def oscar_prefill_attention(handle, seq: int, q: torch.Tensor, num_q_heads: int,
                                         ctypes.c_size_t(ws_bytes), _stream(stream)))
 
 
+def _float_type(dtype, name: str) -> int:
+    if dtype == torch.bfloat16:
+        return OSCAR_BF16
+    if dtype == torch.float32:
+        return OSCAR_F32
+    raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {dtype}")
+
+
+def make_rotary_config(rotary_dim: int = HEAD_DIM, base: float = 10000.0, interleaved: bool = False,
+                       scaling: str = "none", factor: float = 1.0, original_length: float = 0.0,
+                       low: float = 0.0, high: float = 0.0, attention_factor: float = 0.0,
+                       head_dim: int = HEAD_DIM) -> oscar_rotary_config:
+    """Rotary positions of 128-channel heads: layout, rotated channels and the
+    scaling for long contexts ("none", "linear", "banded", "yarn"; see
+    include/oscar.h)."""
+    if scaling not in ROTARY_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALING)}, got {scaling!r}")
+    return oscar_rotary_config(head_dim, rotary_dim, int(bool(interleaved)), ROTARY_SCALING[scaling], base, factor,
+                               original_length, low, high, attention_factor)
+
+
+def oscar_rotary_frequencies(cfg: oscar_rotary_config):
+    """(frequencies in radians per position, factor on the rotated channels)."""
+    f = (ctypes.c_double * (HEAD_DIM // 2))()
+    m = ctypes.c_double(0.0)
+    _check(_lib.oscar_rotary_frequencies(ctypes.byref(cfg), f, ctypes.byref(m)))
+    return [f[i] for i in range(cfg.rotary_dim // 2)], m.value
+
+
+def _rotary_rows(x, out, n: int, dtype, name: str):
+    if x is None:
+        return None
+    if out is None:
+        out = x
+    for t, what in ((x, name), (out, name + "_out")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{what} must be a torch.Tensor")
+        if t.dtype != dtype:
+            raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+        if t.dim() != 3 or t.shape[2] != HEAD_DIM or t.shape[0] != n or t.shape[1] != x.shape[1]:
+            raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {(n, x.shape[1], HEAD_DIM)}")
+        if t.stride(2) != 1:
+            raise ValueError(f"{what} must have contiguous channels")
+    return oscar_rotary_rows(x.data_ptr(), out.data_ptr(), x.stride(0), x.stride(1), out.stride(0), out.stride(1),
+                             x.shape[1])
+
+
+def oscar_rotary(cfg: oscar_rotary_config, positions: torch.Tensor, q: torch.Tensor,
+                 k: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, transpose: bool = False, stream=None) -> None:
+    """Rotates q [n, heads, 128] and k [n, kv heads, 128] (bf16 or float32, any
+    strides with contiguous channels) by their tokens' positions (int32 [n])
+    into q_out and k_out, or in place without them.  transpose: the transposed
+    rotation (the gradient)."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    kind = _float_type(q.dtype, "q")
+    n = q.shape[0]
+    pos = _buf(positions, torch.int32, (n,), "positions")
+    rq = _rotary_rows(q, q_out, n, q.dtype, "q")
+    rk = _rotary_rows(k, k_out, n, q.dtype, "k")
+    _check(_lib.oscar_rotary(ctypes.byref(cfg), n, pos, kind, ctypes.byref(rq),
+                             None if rk is None else ctypes.byref(rk), int(bool(transpose)), _stream(stream)))
+
+
+def oscar_cache_read(handle, seq_ids: Sequence[int], start: Sequence[int], end: Sequence[int],
+                     k_out: Optional[torch.Tensor], v_out: Optional[torch.Tensor], stream=None) -> None:
+    """Tokens start[i] .. end[i] - 1 of each slot seq_ids[i] as rows of k_out
+    and v_out [rows, kv heads, 128] (bf16 or float32; either may be None)."""
+    if not (len(start) == len(end) == len(seq_ids)):
+        raise ValueError("seq_ids, start and end must have the same length")
+    rows = sum(max(0, int(e) - int(s)) for s, e in zip(start, end))
+    given = [t for t in (k_out, v_out) if t is not None]
+    kind = OSCAR_BF16
+    ptr = {}
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None:
+            kind = _float_type(given[0].dtype, name)
+            ptr[name] = _buf(t, given[0].dtype, (rows,) + tuple(given[0].shape[1:2]) + (HEAD_DIM,), name)
+    _check(_lib.oscar_cache_read(handle, len(seq_ids), _i32(seq_ids), _i32(start), _i32(end), kind,
+                                 ptr.get("k_out"), ptr.get("v_out"), _stream(stream)))
+
+
+def oscar_cache_export(handle, seq: int, blocks: Optional[torch.Tensor], window: Optional[torch.Tensor],
+                       maxima: torch.Tensor, stream=None) -> None:
+    _check(_lib.oscar_cache_export(handle, seq, _buf(blocks, torch.uint8, None, "blocks", optional=True),
+                                   _buf(window, torch.bfloat16, (None, 2, GROUP, HEAD_DIM), "window", optional=True),
+                                   _buf(maxima, torch.float32, (2, None), "maxima"), _stream(stream)))
+
+
+def oscar_cache_import(handle, seq: int, length: int, blocks: Optional[torch.Tensor],
+                       window: Optional[torch.Tensor], maxima: torch.Tensor, stream=None) -> None:
+    _check(_lib.oscar_cache_import(handle, seq, length, _buf(blocks, torch.uint8, None, "blocks", optional=True),
+                                   _buf(window, torch.bfloat16, (None, 2, GROUP, HEAD_DIM), "window", optional=True),
+                                   _buf(maxima, torch.float32, (2, None), "maxima"), _stream(stream)))
+
+
+def oscar_index_required_bytes(handle) -> int:
+    out = ctypes.c_size_t(0)
+    _check(_lib.oscar_index_required_bytes(handle, ctypes.byref(out)))
+    return out.value
+
+
+def oscar_index_attach(handle, index: Optional[torch.Tensor]) -> None:
+    _check(_lib.oscar_index_attach(handle, _buf(index, torch.uint8, (None,), "index", optional=True),
+                                   0 if index is None else index.numel()))
+
+
+def oscar_index_update(handle, seq_ids: Sequence[int], rebuild: bool = False, stream=None) -> None:
+    _check(_lib.oscar_index_update(handle, len(seq_ids), _i32(seq_ids), int(bool(rebuild)), _stream(stream)))
+
+
+def oscar_select_groups(handle, seq_ids: Sequence[int], q: torch.Tensor, num_q_heads: int, groups: torch.Tensor,
+                        keep_first: int = 0, keep_last: int = 0, stream=None) -> None:
+    """The groups with the largest scores of each (sequence, KV head), into
+    groups int32 [n_seqs, kv heads, n_select]."""
+    gp = _buf(groups, torch.int32, (len(seq_ids), None, None), "groups")
+    _check(_lib.oscar_select_groups(handle, len(seq_ids), _i32(seq_ids),
+                                    _buf(q, torch.bfloat16, (len(seq_ids), num_q_heads, HEAD_DIM), "q"), num_q_heads,
+                                    groups.shape[2], keep_first, keep_last, gp, _stream(stream)))
+
+
+def oscar_sparse_decode_attention(handle, seq_ids: Sequence[int], q: torch.Tensor, num_q_heads: int,
+                                  softmax_scale: float, groups: torch.Tensor, out: torch.Tensor,
+                                  workspace: torch.Tensor, lse: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Decode attention over the listed groups (int32 [n_seqs, kv heads,
+    n_select], entries outside a sequence's groups are empty) and the window;
+    out bf16 or float32."""
+    n = len(seq_ids)
+    shape = (n, num_q_heads, HEAD_DIM)
+    gp = _buf(groups, torch.int32, (n, None, None), "groups")
+    if not isinstance(out, torch.Tensor):
+        raise TypeError("out must be a torch.Tensor")
+    kind = _float_type(out.dtype, "out")
+    _check(_lib.oscar_sparse_decode_attention(
+        handle, n, _i32(seq_ids), _buf(q, torch.bfloat16, shape, "q"), num_q_heads, ctypes.c_float(softmax_scale), gp,
+        groups.shape[2], kind, _buf(out, out.dtype, shape, "out"),
+        _buf(lse, torch.float32, (n, num_q_heads), "lse", optional=True),
+        _buf(workspace, torch.uint8, None, "workspace"), workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+
+
 def oscar_cache_bytes(handle, seq: int, kind: int) -> int:
     out = ctypes.c_size_t(0)
     _check(_lib.oscar_cache_bytes(handle, seq, kind, ctypes.byref(out)))
@@ -396,3 +570,61 @@ class OscarCache:
             raise ValueError(f"k_new has {k_new.shape[1]} KV heads, the cache {self.num_kv_heads}")
         oscar_append_decode(self.handle, seq_ids, k_new, v_new, q, num_q_heads, softmax_scale, out, workspace,
                             stream)
+
+    def _heads(self, t, dim: int, name: str):
+        """A buffer's KV-head dimension against the cache's (the C ABI cannot see it)."""
+        if isinstance(t, torch.Tensor) and t.dim() > dim and t.shape[dim] != self.num_kv_heads:
+            raise ValueError(f"{name} has {t.shape[dim]} KV heads, the cache {self.num_kv_heads}")
+
+    def read(self, seq_ids, start, end, k_out=None, v_out=None, stream=None):
+        self._heads(k_out, 1, "k_out")
+        self._heads(v_out, 1, "v_out")
+        oscar_cache_read(self.handle, seq_ids, start, end, k_out, v_out, stream)
+
+    @property
+    def block_bytes(self) -> int:
+        return BLOCK_BYTES_META16 if self.meta_bits == 16 else BLOCK_BYTES
+
+    def _slot_buffers(self, length: int, blocks, window, maxima):
+        g = length // GROUP
+        if isinstance(blocks, torch.Tensor) and tuple(blocks.shape) != (self.num_kv_heads, g, self.block_bytes):
+            raise ValueError(f"blocks has shape {tuple(blocks.shape)}, expected "
+                             f"{(self.num_kv_heads, g, self.block_bytes)}")
+        self._heads(window, 0, "window")
+        self._heads(maxima, 1, "maxima")
+
+    def export_sequence(self, seq: int, pinned: bool = False, stream=None):
+        """The packed state of a slot, (length, blocks, window, maxima), in new
+        tensors on the cache's device or in page-locked host memory."""
+        n = self.length(seq)
+        where = dict(pin_memory=True) if pinned else dict(device=self.arena.device)
+        # device tensors belong to the stream that fills them
+        with torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext():
+            blocks = torch.empty((self.num_kv_heads, n // GROUP, self.block_bytes), dtype=torch.uint8, **where)
+            window = torch.empty((self.num_kv_heads, 2, GROUP, HEAD_DIM), dtype=torch.bfloat16, **where)
+            maxima = torch.empty((2, self.num_kv_heads), dtype=torch.float32, **where)
+        oscar_cache_export(self.handle, seq, blocks, window, maxima, stream)
+        return n, blocks, window, maxima
+
+    def import_sequence(self, seq: int, length: int, blocks, window, maxima, stream=None):
+        self._slot_buffers(length, blocks, window, maxima)
+        oscar_cache_import(self.handle, seq, length, blocks, window, maxima, stream)
+
+    def enable_index(self):
+        """Allocates and attaches the group index (kept with the cache)."""
+        n = oscar_index_required_bytes(self.handle)
+        self.index = torch.empty(n, dtype=torch.uint8, device=self.arena.device)
+        oscar_index_attach(self.handle, self.index)
+
+    def update_index(self, seq_ids, rebuild: bool = False, stream=None):
+        oscar_index_update(self.handle, seq_ids, rebuild, stream)
+
+    def select_groups(self, seq_ids, q, num_q_heads, groups, keep_first=0, keep_last=0, stream=None):
+        self._heads(groups, 1, "groups")
+        oscar_select_groups(self.handle, seq_ids, q, num_q_heads, groups, keep_first, keep_last, stream)
+
+    def sparse_decode(self, seq_ids, q, num_q_heads, groups, out, workspace, lse=None, softmax_scale=0.0,
+                      stream=None):
+        self._heads(groups, 1, "groups")
+        oscar_sparse_decode_attention(self.handle, seq_ids, q, num_q_heads, softmax_scale, groups, out, workspace,
+                                      lse, stream)

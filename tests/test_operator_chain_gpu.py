@@ -1,0 +1,66 @@
+"""The operators as a serving loop uses them: rotate the step's queries and
+keys, append, bring the index up to date, choose groups, attend over them, and
+read the sequence back; against the same steps in float64 on the library's own
+intermediate results."""
+import numpy as np
+import pytest
+import torch
+
+from int2_kv_cache_oscar_gb300 import workloads as W
+from oracle import oscar_oracle as OR
+from tests import gpu_util as U
+from tests import test_read_gpu as R
+from tests import test_rotary_gpu as ROT
+from tests import test_select_gpu as SEL
+from tests import test_sparse_gpu as SP
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("meta", [32, 16])
+def test_serving_loop(meta):
+    O = U.lib()
+    hkv, hq, keep = 2, 8, 6
+    lens = [1500, 383, 90]
+    gen = torch.Generator().manual_seed(81)
+    cfg = O.make_rotary_config(128, base=500000.0, scaling="banded", factor=8.0, original_length=8192)
+    cache = O.OscarCache(3, hkv, 2000, meta_bits=meta)
+    cache.enable_index()
+    for i, n in enumerate(lens):           # prefill: rotated keys, appended
+        k, v = W.make_sequence_kv(n, hkv, W.LLAMA_RECIPE, gen)
+        k = k.cuda()
+        O.oscar_rotary(cfg, torch.arange(n, dtype=torch.int32).cuda(), k)
+        cache.append([i], [0, n], k, v.cuda())
+    ids = [0, 1, 2]
+    ws = cache.workspace(3, hq)
+    for step in range(3):                  # the second sequence closes a group at the first step
+        qkv = torch.randn((3, hq + 2 * hkv, 128), generator=gen).bfloat16().cuda()
+        raw = qkv.clone()
+        q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+        pos = torch.tensor([cache.length(i) for i in ids], dtype=torch.int32).cuda()
+        qr = torch.empty((3, hq, 128), dtype=torch.bfloat16, device="cuda")
+        kr = torch.empty((3, hkv, 128), dtype=torch.bfloat16, device="cuda")
+        O.oscar_rotary(cfg, pos, q, k, qr, kr)
+        ROT.check(cfg, pos, raw[:, :hq], qr)
+        ROT.check(cfg, pos, raw[:, hq:hq + hkv], kr)
+        cache.append(ids, [0, 1, 2, 3], kr, v.contiguous())
+        cache.update_index(ids)
+        groups = torch.empty((3, hkv, keep), dtype=torch.int32, device="cuda")
+        cache.select_groups(ids, qr, hq, groups, keep_first=1, keep_last=1)
+        out = torch.empty((3, hq, 128), dtype=torch.bfloat16, device="cuda")
+        cache.sparse_decode(ids, qr, hq, groups, out, ws)
+        torch.cuda.synchronize()
+        SEL.check(cache, ids, qr, keep, 1, 1)
+        again, _ = SP.check(cache, ids, qr, groups, torch.bfloat16)
+        assert torch.equal(again, out)
+    R.check(cache, ids, [0, 100, 0], [cache.length(i) for i in ids], torch.bfloat16)
+    # attention over the read-back rows is the attention over the packed cache
+    n = cache.length(0)
+    k, v = (torch.empty((n, hkv, 128), device="cuda") for _ in range(2))
+    cache.read([0], [0], [n], k, v)
+    full = torch.empty((1, hq, 128), device="cuda")
+    cache.decode_f32([0], qr[:1].contiguous(), hq, full, ws)
+    for j in range(hkv):
+        s = U.f64(qr)[0, 4 * j:4 * j + 4] @ U.f64(k)[:, j].T / np.sqrt(128)
+        ref = OR.softmax_attend(s.T, U.f64(v)[:, j])
+        assert np.abs(ref - U.f64(full)[0, 4 * j:4 * j + 4]).max() <= 2e-3     # the decode's own bound
