@@ -360,6 +360,18 @@ typedef struct oscar_rotary_config {
 oscar_status oscar_rotary_frequencies(const oscar_rotary_config* cfg, double* frequencies,
                                       double* attention_factor);
 
+/* A configuration made ready for oscar_rotary, by oscar_rotary_prepare (which
+ * checks it): keep it beside the model and pass it to every call. */
+typedef struct oscar_rotary_table {
+  int32_t rotary_dim;
+  int32_t interleaved;
+  float factor;            /* on the rotated channels                         */
+  int32_t reserved;
+  uint64_t phase[64];      /* turns per position of pair i, 2^64 to the turn  */
+} oscar_rotary_table;
+
+oscar_status oscar_rotary_prepare(const oscar_rotary_config* cfg, oscar_rotary_table* table);
+
 /* Rows of one tensor [n_tokens, heads, 128]: strides in elements, channels
  * contiguous.  `out` may be `in` with the same strides (in place); otherwise
  * the rows written must not overlap any rows read. */
@@ -373,7 +385,7 @@ typedef struct oscar_rotary_rows {
 
 /*
  * Rotary positions of queries and keys, before the keys are appended and the
- * queries attend: with t = positions[token] * frequency (evaluated to 2^-32
+ * queries attend: with t = positions[token] * frequency (evaluated to 2^-31
  * of a turn at any int32 position) and m the attention factor,
  *   (y_a, y_b) = m (x_a cos t - x_b sin t, x_a sin t + x_b cos t)
  * for every pair (a, b); channels from rotary_dim on are copied.
@@ -389,7 +401,7 @@ typedef struct oscar_rotary_rows {
  *              gradient, and with m = 1 the inverse
  * float32 arithmetic, one rounding to the output type.
  */
-oscar_status oscar_rotary(const oscar_rotary_config* cfg, int64_t n_tokens, const int32_t* positions,
+oscar_status oscar_rotary(const oscar_rotary_table* table, int64_t n_tokens, const int32_t* positions,
                           int32_t type, const oscar_rotary_rows* q, const oscar_rotary_rows* k,
                           int32_t transpose, void* stream);
 

@@ -117,22 +117,23 @@ __device__ __forceinline__ int range_exponent(float bound) {
 }
 
 // A fragment of k-step kk (= ks & 3) from the words of rows g and g+8.
-template <int KK>
+template <int KK, bool HIGH>
 __device__ __forceinline__ void frag_a(uint32_t w0, uint32_t w1, uint32_t& a0, uint32_t& a1, uint32_t& a2,
                                        uint32_t& a3) {
-  a0 = frag_extract<2 * KK>(w0);
-  a1 = frag_extract<2 * KK>(w1);
-  a2 = frag_extract<2 * KK + 1>(w0);
-  a3 = frag_extract<2 * KK + 1>(w1);
+  a0 = frag_extract<2 * KK, HIGH>(w0);
+  a1 = frag_extract<2 * KK, HIGH>(w1);
+  a2 = frag_extract<2 * KK + 1, HIGH>(w0);
+  a3 = frag_extract<2 * KK + 1, HIGH>(w1);
 }
 
+template <bool HIGH>
 __device__ __forceinline__ void frag_a_dyn(int kk, uint32_t w0, uint32_t w1, uint32_t& a0, uint32_t& a1,
                                            uint32_t& a2, uint32_t& a3) {
   switch (kk) {
-    case 0: frag_a<0>(w0, w1, a0, a1, a2, a3); break;
-    case 1: frag_a<1>(w0, w1, a0, a1, a2, a3); break;
-    case 2: frag_a<2>(w0, w1, a0, a1, a2, a3); break;
-    default: frag_a<3>(w0, w1, a0, a1, a2, a3); break;
+    case 0: frag_a<0, HIGH>(w0, w1, a0, a1, a2, a3); break;
+    case 1: frag_a<1, HIGH>(w0, w1, a0, a1, a2, a3); break;
+    case 2: frag_a<2, HIGH>(w0, w1, a0, a1, a2, a3); break;
+    default: frag_a<3, HIGH>(w0, w1, a0, a1, a2, a3); break;
   }
 }
 
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
         const int c = 16 * ks + 2 * tig + 8 * half;
-        const int pp = half ? frag_p(2 * (ks & 3) + 1) : frag_p(2 * (ks & 3));
+        const int pp = half ? frag_p<SPARSE>(2 * (ks & 3) + 1) : frag_p<SPARSE>(2 * (ks & 3));
         const float f = pow2f(Fk_b - pp);
         q2[2 * ks] = S.qrot[h0 + hb][c] * f;
         q2[2 * ks + 1] = S.qrot[h0 + hb][c + 1] * f;
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
     const int vzl0 = 16 * g, vzl1 = 16 * ((g + 8) ^ 1);               //        tokens g, g + 8
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
-      const int pp = half ? frag_p(2 * kk + 1) : frag_p(2 * kk);
+      const int pp = half ? frag_p<SPARSE>(2 * kk + 1) : frag_p<SPARSE>(2 * kk);
       zwk[kk] = pow2f(pp);
       fsc[kk] = fv * pow2f(-pp);
     }
@@ -549,7 +550,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
               const uint32_t w0 = (ks < 4) ? w[m].x : w[m].z;
               const uint32_t w1 = (ks < 4) ? w[m].y : w[m].w;
               uint32_t a0, a1, a2, a3;
-              frag_a_dyn(ks & 3, w0, w1, a0, a1, a2, a3);
+              frag_a_dyn<SPARSE>(ks & 3, w0, w1, a0, a1, a2, a3);
               mma_f16_16816(acc[m], a0, a1, a2, a3, bk[ks][0], bk[ks][1]);
             }
           }
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
               for (int h2 = 0; h2 < 2; ++h2) {
                 const int mt = 2 * gr + h2;
                 uint32_t a0, a1, a2, a3;
-                frag_a_dyn(kk2, vw[mt].x, vw[mt].y, a0, a1, a2, a3);
+                frag_a_dyn<SPARSE>(kk2, vw[mt].x, vw[mt].y, a0, a1, a2, a3);
                 mma_f16_16816(pacc[mt], a0, a1, a2, a3, b0, b1);
               }
             }

@@ -1153,11 +1153,32 @@ oscar_status oscar_rotary_frequencies(const oscar_rotary_config* cfg, double* fr
   return ok();
 }
 
-oscar_status oscar_rotary(const oscar_rotary_config* cfg, int64_t n_tokens, const int32_t* positions, int32_t type,
-                          const oscar_rotary_rows* q, const oscar_rotary_rows* k, int32_t transpose, void* stream) {
+oscar_status oscar_rotary_prepare(const oscar_rotary_config* cfg, oscar_rotary_table* table) {
   double f[kHeadDim / 2], m = 0.0;
-  oscar_status s = rotary_frequencies(cfg, f, &m);
-  if (s == OSCAR_OK) s = check_type(type);
+  const oscar_status s = rotary_frequencies(cfg, f, &m);
+  if (s != OSCAR_OK) return s;
+  if (!table) return fail(OSCAR_ERR_INVALID_ARG, "table is NULL");
+  std::memset(table, 0, sizeof(*table));
+  table->rotary_dim = cfg->rotary_dim;
+  table->interleaved = cfg->interleaved;
+  table->factor = (float)m;
+  // turns per position (below 1/6: frequencies are at most 1 radian), 2^64 to
+  // the turn: the quotient by 2 pi (as a sum of two float64) and its remainder
+  const double two_pi_hi = 6.283185307179586, two_pi_lo = 2.4492935982947064e-16;
+  for (int i = 0; i < cfg->rotary_dim / 2; ++i) {
+    const double t = f[i] / two_pi_hi;
+    const double rest = std::fma(-t, two_pi_lo, std::fma(-t, two_pi_hi, f[i])) / two_pi_hi;
+    table->phase[i] = (uint64_t)std::ldexp(t, 64) + (uint64_t)(int64_t)std::rint(std::ldexp(rest, 64));
+  }
+  return ok();
+}
+
+oscar_status oscar_rotary(const oscar_rotary_table* table, int64_t n_tokens, const int32_t* positions, int32_t type,
+                          const oscar_rotary_rows* q, const oscar_rotary_rows* k, int32_t transpose, void* stream) {
+  if (!table) return fail(OSCAR_ERR_INVALID_ARG, "table is NULL");
+  if (table->rotary_dim < 16 || table->rotary_dim > kHeadDim || table->rotary_dim % 16 != 0)
+    return fail(OSCAR_ERR_INVALID_ARG, "table not made by oscar_rotary_prepare");
+  oscar_status s = check_type(type);
   if (s != OSCAR_OK) return s;
   if (n_tokens < 0 || n_tokens > INT32_MAX) return fail(OSCAR_ERR_INVALID_ARG, "n_tokens out of range");
   if (transpose != 0 && transpose != 1) return fail(OSCAR_ERR_INVALID_ARG, "transpose must be 0 or 1");
@@ -1168,7 +1189,6 @@ oscar_status oscar_rotary(const oscar_rotary_config* cfg, int64_t n_tokens, cons
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   RotaryParams P;
-  std::memset(&P, 0, sizeof(P));
   const int elem = type == OSCAR_F32 ? 4 : 2;
   if ((s = rotary_rows(q, "q", n_tokens, elem, dev, &P.q)) != OSCAR_OK) return s;
   if ((s = rotary_rows(k, "k", n_tokens, elem, dev, &P.k)) != OSCAR_OK) return s;
@@ -1176,18 +1196,12 @@ oscar_status oscar_rotary(const oscar_rotary_config* cfg, int64_t n_tokens, cons
   if ((s = device_view_as(positions, "positions", dev, &positions)) != OSCAR_OK) return s;
   P.positions = positions;
   P.n = n_tokens;
-  P.dim = cfg->rotary_dim;
+  P.dim = table->rotary_dim;
+  P.block_tokens = 1;
   P.transpose = transpose;
-  P.factor = (float)m;
-  // turns per position (below 1/6: frequencies are at most 1 radian), 2^64 to
-  // the turn: the quotient by 2 pi (as a sum of two float64) and its remainder
-  const double two_pi_hi = 6.283185307179586, two_pi_lo = 2.4492935982947064e-16;
-  for (int i = 0; i < cfg->rotary_dim / 2; ++i) {
-    const double t = f[i] / two_pi_hi;
-    const double rest = std::fma(-t, two_pi_lo, std::fma(-t, two_pi_hi, f[i])) / two_pi_hi;
-    P.freq[i] = (uint64_t)std::ldexp(t, 64) + (uint64_t)(int64_t)std::rint(std::ldexp(rest, 64));
-  }
-  e = launch_rotary(P, type == OSCAR_F32, cfg->interleaved != 0, num_sms(dev), static_cast<cudaStream_t>(stream));
+  P.factor = table->factor;
+  std::copy(table->phase, table->phase + kHeadDim / 2, P.freq);
+  e = launch_rotary(P, type == OSCAR_F32, table->interleaved != 0, num_sms(dev), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rotary launch");
   return ok();
 }

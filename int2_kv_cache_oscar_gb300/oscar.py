@@ -11,6 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -61,11 +62,13 @@ class oscar_rotary_config(ctypes.Structure):
                 ("attention_factor", ctypes.c_double)]
 
 
-class oscar_rotary_rows(ctypes.Structure):
-    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p),
-                ("src_token_stride", ctypes.c_int64), ("src_head_stride", ctypes.c_int64),
-                ("dst_token_stride", ctypes.c_int64), ("dst_head_stride", ctypes.c_int64),
-                ("heads", ctypes.c_int32)]
+class oscar_rotary_table(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("factor", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("phase", ctypes.c_uint64 * (128 // 2))]
+
+
+# oscar_rotary_rows: in, out, four strides (elements), heads
+_rotary_rows_pack = struct.Struct("@PPqqqqi4x").pack
 
 
 def _load() -> ctypes.CDLL:
@@ -102,8 +105,8 @@ def _load() -> ctypes.CDLL:
         "oscar_prefill_workspace_bytes": [P, I32, I32, I32, ctypes.POINTER(SZ)],
         "oscar_rotary_frequencies": [ctypes.POINTER(oscar_rotary_config), ctypes.POINTER(ctypes.c_double),
                                      ctypes.POINTER(ctypes.c_double)],
-        "oscar_rotary": [ctypes.POINTER(oscar_rotary_config), ctypes.c_int64, P, I32,
-                         ctypes.POINTER(oscar_rotary_rows), ctypes.POINTER(oscar_rotary_rows), I32, P],
+        "oscar_rotary_prepare": [ctypes.POINTER(oscar_rotary_config), ctypes.POINTER(oscar_rotary_table)],
+        "oscar_rotary": [P, ctypes.c_int64, P, I32, ctypes.c_char_p, ctypes.c_char_p, I32, P],
         "oscar_cache_read": [P, I32, I32P, I32P, I32P, I32, P, P, P],
         "oscar_cache_export": [P, I32, P, P, P, P],
         "oscar_cache_import": [P, I32, I32, P, P, P, P],
@@ -123,6 +126,10 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
+
+# The current stream's handle without building a Stream object (3 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def library_path() -> str:
@@ -149,10 +156,20 @@ def _i32(seq: Sequence[int]):
 
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return ctypes.c_void_p(_raw_stream(_raw_device()))
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
+
+
+def _dense(t, dtype, shape, name: str) -> Optional[int]:
+    """Address of a caller buffer, checked as by _buf; the exact shape is
+    accepted at once."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
+    return _buf(t, dtype, shape, name).value
 
 
 def _ptr(t: Optional[torch.Tensor]) -> ctypes.c_void_p:
@@ -316,46 +333,68 @@ def _float_type(dtype, name: str) -> int:
     raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {dtype}")
 
 
+class RotaryConfig:
+    """A rotary configuration and its prepared table (keep it beside the model)."""
+
+    def __init__(self, cfg: oscar_rotary_config):
+        self.cfg = cfg
+        self.rotary_dim = cfg.rotary_dim
+        self.interleaved = bool(cfg.interleaved)
+        self._table = oscar_rotary_table()
+        _check(_lib.oscar_rotary_prepare(ctypes.byref(cfg), ctypes.byref(self._table)))
+        self.address = ctypes.addressof(self._table)
+
+
 def make_rotary_config(rotary_dim: int = HEAD_DIM, base: float = 10000.0, interleaved: bool = False,
                        scaling: str = "none", factor: float = 1.0, original_length: float = 0.0,
                        low: float = 0.0, high: float = 0.0, attention_factor: float = 0.0,
-                       head_dim: int = HEAD_DIM) -> oscar_rotary_config:
+                       head_dim: int = HEAD_DIM) -> RotaryConfig:
     """Rotary positions of 128-channel heads: layout, rotated channels and the
     scaling for long contexts ("none", "linear", "banded", "yarn"; see
     include/oscar.h)."""
     if scaling not in ROTARY_SCALING:
         raise ValueError(f"scaling must be one of {sorted(ROTARY_SCALING)}, got {scaling!r}")
-    return oscar_rotary_config(head_dim, rotary_dim, int(bool(interleaved)), ROTARY_SCALING[scaling], base, factor,
-                               original_length, low, high, attention_factor)
+    return RotaryConfig(oscar_rotary_config(head_dim, rotary_dim, int(bool(interleaved)), ROTARY_SCALING[scaling], base,
+                                            factor, original_length, low, high, attention_factor))
 
 
-def oscar_rotary_frequencies(cfg: oscar_rotary_config):
+def oscar_rotary_frequencies(config: RotaryConfig):
     """(frequencies in radians per position, factor on the rotated channels)."""
     f = (ctypes.c_double * (HEAD_DIM // 2))()
     m = ctypes.c_double(0.0)
-    _check(_lib.oscar_rotary_frequencies(ctypes.byref(cfg), f, ctypes.byref(m)))
-    return [f[i] for i in range(cfg.rotary_dim // 2)], m.value
+    _check(_lib.oscar_rotary_frequencies(ctypes.byref(config.cfg), f, ctypes.byref(m)))
+    return [f[i] for i in range(config.rotary_dim // 2)], m.value
 
 
-def _rotary_rows(x, out, n: int, dtype, name: str):
+def _rotary_rows(x, out, n: int, dtype, name: str) -> Optional[bytes]:
     if x is None:
         return None
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != n or shape[2] != HEAD_DIM:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {(n, 'heads', HEAD_DIM)}")
+    if x.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
+    token, head, channel = x.stride()
+    if channel != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    src = x.data_ptr()
     if out is None:
-        out = x
-    for t, what in ((x, name), (out, name + "_out")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{what} must be a torch.Tensor")
-        if t.dtype != dtype:
-            raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
-        if t.dim() != 3 or t.shape[2] != HEAD_DIM or t.shape[0] != n or t.shape[1] != x.shape[1]:
-            raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {(n, x.shape[1], HEAD_DIM)}")
-        if t.stride(2) != 1:
-            raise ValueError(f"{what} must have contiguous channels")
-    return oscar_rotary_rows(x.data_ptr(), out.data_ptr(), x.stride(0), x.stride(1), out.stride(0), out.stride(1),
-                             x.shape[1])
+        return _rotary_rows_pack(src, src, token, head, token, head, shape[1])
+    if not isinstance(out, torch.Tensor):
+        raise TypeError(f"{name}_out must be a torch.Tensor")
+    if out.dtype is not dtype:
+        raise ValueError(f"{name}_out must be {dtype}, got {out.dtype}")
+    if out.shape != shape:
+        raise ValueError(f"{name}_out has shape {tuple(out.shape)}, expected {tuple(shape)}")
+    out_token, out_head, channel = out.stride()
+    if channel != 1:
+        raise ValueError(f"{name}_out must have contiguous channels")
+    return _rotary_rows_pack(src, out.data_ptr(), token, head, out_token, out_head, shape[1])
 
 
-def oscar_rotary(cfg: oscar_rotary_config, positions: torch.Tensor, q: torch.Tensor,
+def oscar_rotary(config: RotaryConfig, positions: torch.Tensor, q: torch.Tensor,
                  k: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
                  k_out: Optional[torch.Tensor] = None, transpose: bool = False, stream=None) -> None:
     """Rotates q [n, heads, 128] and k [n, kv heads, 128] (bf16 or float32, any
@@ -364,31 +403,35 @@ def oscar_rotary(cfg: oscar_rotary_config, positions: torch.Tensor, q: torch.Ten
     rotation (the gradient)."""
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
-    kind = _float_type(q.dtype, "q")
+    dtype = q.dtype
+    kind = _float_type(dtype, "q")
     n = q.shape[0]
-    pos = _buf(positions, torch.int32, (n,), "positions")
-    rq = _rotary_rows(q, q_out, n, q.dtype, "q")
-    rk = _rotary_rows(k, k_out, n, q.dtype, "k")
-    _check(_lib.oscar_rotary(ctypes.byref(cfg), n, pos, kind, ctypes.byref(rq),
-                             None if rk is None else ctypes.byref(rk), int(bool(transpose)), _stream(stream)))
+    _check(_lib.oscar_rotary(config.address, n, _dense(positions, torch.int32, (n,), "positions"), kind,
+                             _rotary_rows(q, q_out, n, dtype, "q"), _rotary_rows(k, k_out, n, dtype, "k"),
+                             1 if transpose else 0, _stream(stream)))
 
 
 def oscar_cache_read(handle, seq_ids: Sequence[int], start: Sequence[int], end: Sequence[int],
                      k_out: Optional[torch.Tensor], v_out: Optional[torch.Tensor], stream=None) -> None:
     """Tokens start[i] .. end[i] - 1 of each slot seq_ids[i] as rows of k_out
     and v_out [rows, kv heads, 128] (bf16 or float32; either may be None)."""
-    if not (len(start) == len(end) == len(seq_ids)):
+    n = len(seq_ids)
+    if len(start) != n or len(end) != n:
         raise ValueError("seq_ids, start and end must have the same length")
-    rows = sum(max(0, int(e) - int(s)) for s, e in zip(start, end))
-    given = [t for t in (k_out, v_out) if t is not None]
-    kind = OSCAR_BF16
-    ptr = {}
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is not None:
-            kind = _float_type(given[0].dtype, name)
-            ptr[name] = _buf(t, given[0].dtype, (rows,) + tuple(given[0].shape[1:2]) + (HEAD_DIM,), name)
-    _check(_lib.oscar_cache_read(handle, len(seq_ids), _i32(seq_ids), _i32(start), _i32(end), kind,
-                                 ptr.get("k_out"), ptr.get("v_out"), _stream(stream)))
+    rows = sum(end) - sum(start)     # the library refuses a range that runs backwards
+    first = v_out if k_out is None else k_out
+    kind, kp, vp = OSCAR_BF16, None, None
+    if first is not None:
+        if not isinstance(first, torch.Tensor):
+            raise TypeError("k_out and v_out must be torch.Tensors")
+        dtype = first.dtype
+        kind = _float_type(dtype, "k_out" if first is k_out else "v_out")
+        shape = (rows, first.shape[1] if first.dim() == 3 else -1, HEAD_DIM)
+        if k_out is not None:
+            kp = _dense(k_out, dtype, shape, "k_out")
+        if v_out is not None:
+            vp = _dense(v_out, dtype, shape, "v_out")
+    _check(_lib.oscar_cache_read(handle, n, _i32(seq_ids), _i32(start), _i32(end), kind, kp, vp, _stream(stream)))
 
 
 def oscar_cache_export(handle, seq: int, blocks: Optional[torch.Tensor], window: Optional[torch.Tensor],
@@ -420,14 +463,24 @@ def oscar_index_update(handle, seq_ids: Sequence[int], rebuild: bool = False, st
     _check(_lib.oscar_index_update(handle, len(seq_ids), _i32(seq_ids), int(bool(rebuild)), _stream(stream)))
 
 
+def _groups(groups, n: int):
+    """Address and entries per row of a group list [n, kv heads, entries]."""
+    if isinstance(groups, torch.Tensor) and groups.dim() == 3:
+        shape = groups.shape
+        return _dense(groups, torch.int32, (n, shape[1], shape[2]), "groups"), shape[2]
+    _buf(groups, torch.int32, (n, None, None), "groups")
+    raise AssertionError
+
+
 def oscar_select_groups(handle, seq_ids: Sequence[int], q: torch.Tensor, num_q_heads: int, groups: torch.Tensor,
                         keep_first: int = 0, keep_last: int = 0, stream=None) -> None:
     """The groups with the largest scores of each (sequence, KV head), into
     groups int32 [n_seqs, kv heads, n_select]."""
-    gp = _buf(groups, torch.int32, (len(seq_ids), None, None), "groups")
-    _check(_lib.oscar_select_groups(handle, len(seq_ids), _i32(seq_ids),
-                                    _buf(q, torch.bfloat16, (len(seq_ids), num_q_heads, HEAD_DIM), "q"), num_q_heads,
-                                    groups.shape[2], keep_first, keep_last, gp, _stream(stream)))
+    n = len(seq_ids)
+    gp, n_select = _groups(groups, n)
+    _check(_lib.oscar_select_groups(handle, n, _i32(seq_ids),
+                                    _dense(q, torch.bfloat16, (n, num_q_heads, HEAD_DIM), "q"), num_q_heads,
+                                    n_select, keep_first, keep_last, gp, _stream(stream)))
 
 
 def oscar_sparse_decode_attention(handle, seq_ids: Sequence[int], q: torch.Tensor, num_q_heads: int,
@@ -438,16 +491,15 @@ def oscar_sparse_decode_attention(handle, seq_ids: Sequence[int], q: torch.Tenso
     out bf16 or float32."""
     n = len(seq_ids)
     shape = (n, num_q_heads, HEAD_DIM)
-    gp = _buf(groups, torch.int32, (n, None, None), "groups")
+    gp, n_select = _groups(groups, n)
     if not isinstance(out, torch.Tensor):
         raise TypeError("out must be a torch.Tensor")
-    kind = _float_type(out.dtype, "out")
+    dtype = out.dtype
     _check(_lib.oscar_sparse_decode_attention(
-        handle, n, _i32(seq_ids), _buf(q, torch.bfloat16, shape, "q"), num_q_heads, ctypes.c_float(softmax_scale), gp,
-        groups.shape[2], kind, _buf(out, out.dtype, shape, "out"),
-        _buf(lse, torch.float32, (n, num_q_heads), "lse", optional=True),
-        _buf(workspace, torch.uint8, None, "workspace"), workspace.numel() * workspace.element_size(),
-        _stream(stream)))
+        handle, n, _i32(seq_ids), _dense(q, torch.bfloat16, shape, "q"), num_q_heads, softmax_scale, gp, n_select,
+        _float_type(dtype, "out"), _dense(out, dtype, shape, "out"),
+        None if lse is None else _dense(lse, torch.float32, (n, num_q_heads), "lse"),
+        _dense(workspace, torch.uint8, None, "workspace"), workspace.numel(), _stream(stream)))
 
 
 def oscar_cache_bytes(handle, seq: int, kind: int) -> int:

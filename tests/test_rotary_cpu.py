@@ -79,23 +79,26 @@ def test_attention_factor_given(O):
     (dict(attention_factor=float("inf")), 1)])
 def test_bad_configurations(O, change, status):
     with pytest.raises(O.OscarError) as e:
-        O.oscar_rotary_frequencies(O.make_rotary_config(**change))
+        O.make_rotary_config(**change)
     assert e.value.status == status
 
 
 def test_refusals_before_any_gpu_call(O):
     lib = O.raw_library()
     cfg = O.make_rotary_config()
-    rows = O.oscar_rotary_rows(4096, 4096, 128, 128, 128, 128, 1)
+    rows = O._rotary_rows_pack(4096, 4096, 128, 128, 128, 128, 1)
     pos = ctypes.c_void_p(4096)
-    call = lambda n=1, p=pos, t=0, tr=0: lib.oscar_rotary(ctypes.byref(cfg), n, p, t, ctypes.byref(rows), None, tr, None)  # noqa: E731
+    call = lambda n=1, p=pos, t=0, tr=0: lib.oscar_rotary(cfg.address, n, p, t, rows, None, tr, None)  # noqa: E731
     assert call(n=-1) == O.OSCAR_ERR_INVALID_ARG
     assert call(p=None) == O.OSCAR_ERR_INVALID_ARG
     assert call(p=ctypes.c_void_p(4097)) == O.OSCAR_ERR_INVALID_ARG
     assert call(t=2) == O.OSCAR_ERR_UNSUPPORTED
     assert call(tr=2) == O.OSCAR_ERR_INVALID_ARG
     assert call(n=0) == O.OSCAR_OK
-    assert lib.oscar_rotary(None, 1, pos, 0, ctypes.byref(rows), None, 0, None) == O.OSCAR_ERR_INVALID_ARG
+    assert lib.oscar_rotary(None, 1, pos, 0, rows, None, 0, None) == O.OSCAR_ERR_INVALID_ARG
+    assert lib.oscar_rotary(ctypes.addressof(O.oscar_rotary_table()), 1, pos, 0, rows, None, 0,
+                            None) == O.OSCAR_ERR_INVALID_ARG          # never prepared
+    assert lib.oscar_rotary_prepare(ctypes.byref(cfg.cfg), None) == O.OSCAR_ERR_INVALID_ARG
     for fn, args in [("oscar_cache_read", (None, 0, None, None, None, 0, None, None, None)),
                      ("oscar_cache_export", (None, 0, None, None, None, None)),
                      ("oscar_cache_import", (None, 0, 0, None, None, None, None)),

@@ -145,22 +145,21 @@ def test_rows_with_nothing():
 
 
 def test_all_groups_listed_is_the_full_decode():
-    """Every group in order, each once: the units, their split and the merge
-    are the full decode's, so the bits are too."""
+    """Every group in order, each once, against the full decode: each is
+    within 2e-3 of the oracle (the full decode's own bound; the sparse one's is
+    tighter, see check)."""
     for lens, hkv, hq in ([[5000], 2, 8], [[3000, 3000], 1, 7]):
         cache = make(lens, hkv, seed=41)
         n, ng = len(lens), lens[0] // 128
         q = W.make_q(n, hq, seed=2).cuda()
         groups = torch.arange(ng, dtype=torch.int32).expand(n, hkv, ng).contiguous().cuda()
         ids = list(range(n))
-        ws = cache.workspace(n, hq)
         a = torch.empty((n, hq, 128), device="cuda")
-        b, c = torch.empty_like(a), torch.empty((n, hq, 128), dtype=torch.bfloat16, device="cuda")
-        cache.decode_f32(ids, q, hq, a, ws)
-        cache.sparse_decode(ids, q, hq, groups, b, ws)
-        assert torch.equal(a, b)
-        cache.sparse_decode(ids, q, hq, groups, c, ws)
-        assert torch.equal(c, a.bfloat16())
+        cache.decode_f32(ids, q, hq, a, cache.workspace(n, hq))
+        b, _ = check(cache, ids, q, groups)
+        c, _ = check(cache, ids, q, groups, torch.bfloat16)
+        assert (a - b).abs().max().item() <= 4e-3
+        assert torch.equal(c, b.bfloat16())
 
 
 def test_lse_merges_two_parts():
