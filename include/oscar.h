@@ -488,8 +488,8 @@ oscar_status oscar_index_update(oscar_cache* cache, int32_t n_seqs, const int32_
  *               always chosen (attention sinks, recent tokens); >= 0, together
  *               <= n_select
  *   groups      int32 [n_seqs, Hkv, n_select], device memory
- * Sequences without a group get -1s.  A sequence of more than about 25,000
- * groups that does not fit n_select fails with OSCAR_ERR_UNSUPPORTED.
+ * Sequences without a group get -1s.  A sequence of more than 12,000 groups
+ * (1,536,000 tokens) and more than n_select fails with OSCAR_ERR_UNSUPPORTED.
  */
 oscar_status oscar_select_groups(oscar_cache* cache, int32_t n_seqs, const int32_t* seq_ids, const void* q,
                                  int32_t num_q_heads, int32_t n_select, int32_t keep_first,

@@ -166,11 +166,6 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-// Waits until the kernels this grid depends on have completed and their
-// writes are visible (returns at once when it was launched without a
-// programmatic dependency).
-__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 template <int MAXS, bool M16, bool PAIRS, bool SPARSE>
 __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
     decode_int2_kernel(const __grid_constant__ DecodeParams<MAXS> p, const uint8_t* __restrict__ arena) {

@@ -241,6 +241,9 @@ struct SelectParams {
   int32_t n_select;
   int32_t keep_first;
   int32_t keep_last;
+  int32_t blocks;      // of a row (a cluster), set by the launch
+  int32_t stages;      // copies in flight, set by the launch
+  uint32_t* err_word;
   const uint2* codes;
   const float2* weights;
   const uint16_t* q;   // [n_seqs, hq, 128]
@@ -248,15 +251,15 @@ struct SelectParams {
   SelectSeq seq[MAXS];
 };
 
-constexpr int kSelectMaxSmem = 200 * 1024;
-constexpr int kSelectMaxHeads = 64;   // query heads per KV head
-// dynamic shared memory of the selection among `groups` groups
-size_t select_smem_bytes(int q_group, int groups);
+constexpr int kSelectMaxSmem = 224 * 1024;
+constexpr int kSelectMaxHeads = 64;       // query heads per KV head
+constexpr int kSelectMaxGroups = 12000;   // groups of a sequence to choose among (their keys in shared memory)
+constexpr int kSelMaxBlocks = 8;          // blocks of a row
 
 template <int MAXS>
 cudaError_t launch_index(const IndexParams<MAXS>& p, const uint8_t* arena, bool meta16, cudaStream_t stream);
 template <int MAXS>
-cudaError_t launch_select(const SelectParams<MAXS>& p, cudaStream_t stream);
+cudaError_t launch_select(const SelectParams<MAXS>& p, int sms, cudaStream_t stream);
 
 // ----------------------------------------------------------------- prefill
 

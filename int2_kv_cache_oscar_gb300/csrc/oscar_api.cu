@@ -1097,12 +1097,13 @@ oscar_status run_select(const oscar_cache* c, const std::vector<SelectSeq>& seqs
   P.n_select = n_select;
   P.keep_first = keep_first;
   P.keep_last = keep_last;
+  P.err_word = reinterpret_cast<uint32_t*>(c->arena);
   P.codes = c->index_codes;
   P.weights = c->index_weights;
   P.q = static_cast<const uint16_t*>(q);
   P.out = out;
   std::copy(seqs.begin(), seqs.end(), P.seq);
-  const cudaError_t e = launch_select(P, st);
+  const cudaError_t e = launch_select(P, c->sms, st);
   return e == cudaSuccess ? OSCAR_OK : cuda_fail(e, "select launch");
 }
 
@@ -1381,8 +1382,9 @@ oscar_status oscar_select_groups(oscar_cache* c, int32_t n_seqs, const int32_t* 
       if (c->indexed[seq_ids[i]] < ng)
         return fail(OSCAR_ERR_INVALID_ARG, "sequence %d: %d of %d groups in the index (oscar_index_update)", seq_ids[i],
                     c->indexed[seq_ids[i]], ng);
-      if (ng > n_select && select_smem_bytes(num_q_heads / hkv, ng) > (size_t)kSelectMaxSmem)
-        return fail(OSCAR_ERR_UNSUPPORTED, "sequence %d: %d groups are too many to choose from", seq_ids[i], ng);
+      if (ng > n_select && ng > kSelectMaxGroups)
+        return fail(OSCAR_ERR_UNSUPPORTED, "sequence %d: more than %d groups to choose from (%d)", seq_ids[i],
+                    kSelectMaxGroups, ng);
       seqs[i] = SelectSeq{seq_ids[i], ng};
     }
     DeviceGuard dg(c->cfg.device);

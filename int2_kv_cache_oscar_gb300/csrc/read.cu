@@ -106,6 +106,8 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
     fence_mbar_init();
   }
   __syncthreads();
+  grid_dependency_wait();
+  allow_dependents();
   uint32_t* err = reinterpret_cast<uint32_t*>(const_cast<uint8_t*>(arena));
 
   // requests the block of tile u (window tiles need none)
@@ -294,8 +296,7 @@ cudaError_t launch_read_t(const ReadParams<MAXS>& p, const uint8_t* arena, int s
   cudaError_t e = ensure_smem_attr(read_kernel<MAXS, M16, F32>, smem, attr_done);
   if (e != cudaSuccess) return e;
   const unsigned grid = (unsigned)std::min<int64_t>(p.n_tiles, 3 * (int64_t)sms);
-  read_kernel<MAXS, M16, F32><<<grid, kReadThreads, smem, stream>>>(p, arena);
-  return cudaGetLastError();
+  return launch_dependent(read_kernel<MAXS, M16, F32>, dim3(grid), dim3(kReadThreads), (size_t)smem, stream, 1, p, arena);
 }
 
 }  // namespace

@@ -103,6 +103,8 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
     }
   };
 
+  grid_dependency_wait();
+  allow_dependents();
   for (int base = 0; base < items; base += kRotThreads * kRotItems) {
     uint4 xa[kRotItems], xb[kRotItems];
 #pragma unroll
@@ -177,14 +179,9 @@ cudaError_t launch_rotary(const RotaryParams& params, bool f32, bool interleaved
   tokens = std::max<int64_t>(1, std::min<int64_t>(tokens, kRotMaxTokens));
   p.block_tokens = (int32_t)tokens;
   const unsigned grid = (unsigned)((p.n + tokens - 1) / tokens);
-  if (f32) {
-    if (interleaved) rotary_kernel<true, true><<<grid, kRotThreads, 0, stream>>>(p);
-    else rotary_kernel<true, false><<<grid, kRotThreads, 0, stream>>>(p);
-  } else {
-    if (interleaved) rotary_kernel<false, true><<<grid, kRotThreads, 0, stream>>>(p);
-    else rotary_kernel<false, false><<<grid, kRotThreads, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  const auto kernel = f32 ? (interleaved ? rotary_kernel<true, true> : rotary_kernel<true, false>)
+                          : (interleaved ? rotary_kernel<false, true> : rotary_kernel<false, false>);
+  return launch_dependent(kernel, dim3(grid), dim3(kRotThreads), 0, stream, 1, p);
 }
 
 }  // namespace oscar

@@ -20,9 +20,18 @@
 // does not depend on how the sums are split, and ties are true ties (the
 // lowest group wins).
 //
-// Bound by latency for a few rows (a score pass over 264 bytes a group, then a
-// radix selection in shared memory), by HBM / L2 for many.
+// Selection: a cluster of 1 to 8 blocks per (sequence, KV head) row, each
+// scoring a contiguous slice of its groups and storing the scores' keys into
+// the first block's shared memory; that block then chooses.  A slice's codes
+// come by bulk copies of 128 groups (32 KB), up to four in flight, requested
+// before the queries are turned.  Four lanes score a group: each holds a
+// quarter of the query bytes of four heads in registers, so a group costs a
+// warp 12 instructions (a warp per group, with a warp sum per head, took 51).
+// The m-th largest key is found by a radix histogram, starting at the first
+// bit in which the row's keys differ, and, once at most 32 keys share a digit,
+// by ranking those.  Everything is latency and, for many rows, instructions.
 #include <algorithm>
+#include <cstddef>
 
 #include "common.cuh"
 #include "launch.h"
@@ -30,8 +39,13 @@
 namespace oscar {
 namespace {
 
-constexpr int kSelThreads = 512;
-constexpr int kSelBatch = 4;   // groups in flight per warp
+constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelHeads = 4;      // query heads scored at once
+constexpr int kSelChunk = 128;    // groups of one bulk copy
+constexpr int kSelStages = 4;     // copies in flight
+constexpr int kSelRank = 32;      // keys ranked directly
+static_assert(kSelThreads == 256, "one thread per digit of the histogram");
 constexpr int kIdxThreads = 256;
 constexpr int kIdxMinExp = -100;
 
@@ -47,6 +61,8 @@ __global__ void __launch_bounds__(kIdxThreads)
     index_kernel(const __grid_constant__ IndexParams<MAXS> p, const uint8_t* __restrict__ arena) {
   using B = Blk<M16>;
   using MR = Meta<M16>;
+  grid_dependency_wait();
+  allow_dependents();
   const IndexSeq sq = p.seq[blockIdx.z];
   const int g = sq.first + (int)(blockIdx.x * (kIdxThreads / 32) + (threadIdx.x >> 5));
   if (g >= sq.end) return;
@@ -95,43 +111,81 @@ __device__ __forceinline__ uint64_t order_key(double x) {
 }
 
 struct SelSmem {
-  uint32_t red[kSelThreads / 32];
-  uint64_t red64[2][kSelThreads / 32];
-  uint32_t hist[256];
-  uint32_t cnt[2][kSelThreads / 32];
+  alignas(8) uint64_t full[kSelStages];
+  uint64_t cand[kSelRank];         // keys to rank
+  int32_t cand_group[kSelRank];
+  uint64_t limit_key;
+  alignas(16) uint32_t hist[256];   // read as uint4
+  uint32_t red[4][kSelWarps];
+  uint32_t cnt[2][2][kSelWarps];
+  uint32_t n_cand;
   uint32_t digit, above, inbin;
+  int32_t limit_group;
+  int abort_flag;
 };
+static_assert(offsetof(SelSmem, hist) % 16 == 0 && offsetof(SelSmem, full) % 8 == 0 && alignof(SelSmem) >= 16,
+              "vector loads of the histogram, 8-byte barriers");
 
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
-  v = __reduce_max_sync(0xffffffffu, v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < kSelThreads / 32; ++i) m = max(m, red[i]);
-  return m;
+// Address of a shared variable in block `rank` of the cluster.
+template <typename T>
+__device__ __forceinline__ T* in_block(T* p, int rank) {
+  uint64_t a;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(a) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+  return reinterpret_cast<T*>(a);
 }
 
 template <int MAXS>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_constant__ SelectParams<MAXS> p) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
+__global__ void __launch_bounds__(kSelThreads)
+    select_kernel(const __grid_constant__ SelectParams<MAXS> p) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ SelSmem S;
-  const int b = blockIdx.x / p.hkv, j = blockIdx.x % p.hkv;
+  const int blocks = p.blocks;
+  const int rank = blocks > 1 ? (int)(blockIdx.x % (unsigned)blocks) : 0;
+  const int row_id = blocks > 1 ? (int)(blockIdx.x / (unsigned)blocks) : (int)blockIdx.x;
+  const int b = row_id / p.hkv, j = row_id - b * p.hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int ng = p.seq[b].ng, gqa = p.q_group;
   int32_t* out = p.out + ((int64_t)b * p.hkv + j) * p.n_select;
   const int m = min(p.n_select, ng);
-  for (int i = m + tid; i < p.n_select; i += kSelThreads) out[i] = -1;
-  if (ng <= p.n_select) {
-    for (int i = tid; i < ng; i += kSelThreads) out[i] = i;
-    return;
-  }
-  // dynamic shared memory: [gqa][32] rotated queries (4 channels a lane), [gqa][32] their bytes (parts above and
-  // below zero), [ng] score keys
-  int4* turned = reinterpret_cast<int4*>(smem_raw);
+  const int slice = blocks > 1 ? (ng + blocks - 1) / blocks : ng;
+  const int first = min(ng, rank * slice), n = min(ng, first + slice) - first;   // this block's groups
+  // dynamic shared memory: staged codes, [gqa][32] rotated queries (4 channels
+  // a lane), [gqa][32] their bytes (parts below and above zero), [ng] score
+  // keys (the first block's; the others use it for their weights)
+  uint8_t* stages = smem_raw;
+  int4* turned = reinterpret_cast<int4*>(stages + (size_t)p.stages * kSelChunk * 256);
   int2* q8 = reinterpret_cast<int2*>(turned + (size_t)gqa * 32);
   uint64_t* keys = reinterpret_cast<uint64_t*>(q8 + (size_t)gqa * 32);
+  if (tid == 0) {
+    for (int s = 0; s < kSelStages; ++s) mbar_init(&S.full[s], 1);
+    S.n_cand = 0;
+    S.abort_flag = 0;
+    fence_mbar_init();
+  }
+  S.hist[tid] = 0;
+  __syncthreads();
+  // every block of the cluster runs before another one stores into it
+  if (blocks > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  grid_dependency_wait();      // q and the index are outputs of earlier kernels, `out` may be read by one
+  allow_dependents();
+  if (rank == 0)
+    for (int i = m + tid; i < p.n_select; i += kSelThreads) out[i] = -1;
+  if (ng <= p.n_select) {
+    for (int i = tid; i < n; i += kSelThreads) out[first + i] = first + i;
+    if (blocks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    return;
+  }
+
+  const int64_t row = ((int64_t)p.seq[b].slot * p.hkv + j) * p.max_groups + first;
+  const int chunks = (n + kSelChunk - 1) / kSelChunk;
+  auto request = [&](int c) {      // chunk c into its stage
+    const int s = c % p.stages;
+    const uint32_t bytes = (uint32_t)min(kSelChunk, n - c * kSelChunk) * 256;
+    mbar_arrive_expect_tx(&S.full[s], bytes);
+    bulk_g2s(stages + (size_t)s * kSelChunk * 256, p.codes + (row + c * kSelChunk) * 32, bytes, &S.full[s]);
+  };
+  if (tid == 0)
+    for (int c = 0; c < min(chunks, p.stages); ++c) request(c);
 
   // ---- the queries in 8 bits, one step size for the heads of the KV head
   const uint16_t* q = p.q + ((int64_t)b * p.hq + (int64_t)j * gqa) * kHeadDim;
@@ -142,16 +196,27 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     f[2] = finite_or_zero(bf16_lo(raw.y));
     f[3] = finite_or_zero(bf16_hi(raw.y));
   };
+  auto block_max = [&](uint32_t v, uint32_t* red) {
+    v = __reduce_max_sync(0xffffffffu, v);
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    uint32_t r = red[0];
+#pragma unroll
+    for (int i = 1; i < kSelWarps; ++i) r = max(r, red[i]);
+    return r;
+  };
   uint32_t top = 0;
-  for (int h = warp; h < gqa; h += kSelThreads / 32) {
+  for (int h = warp; h < gqa; h += kSelWarps) {
     float f[4];
     load_q(h, f);
     top = max(top, __float_as_uint(fmaxf(fmaxf(fabsf(f[0]), fabsf(f[1])), fmaxf(fabsf(f[2]), fabsf(f[3])))));
   }
-  top = block_max(top, S.red);
+  // this block's weights, in place of its keys (block 0) or at the front
+  for (int i = tid; i < n; i += kSelThreads) keys[i] = reinterpret_cast<const uint64_t*>(p.weights)[row + i];
+  top = block_max(top, S.red[0]);
   const float up = exp2i(22 - max((int)(top >> 23) - 126, kIdxMinExp));
   uint32_t big = 0;
-  for (int h = warp; h < gqa; h += kSelThreads / 32) {
+  for (int h = warp; h < gqa; h += kSelWarps) {
     float f[4];
     load_q(h, f);
     int v[4];
@@ -175,11 +240,11 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     for (int i = 0; i < 4; ++i) big = max(big, (uint32_t)abs(v[i]));
     turned[h * 32 + lane] = make_int4(v[0], v[1], v[2], v[3]);
   }
-  big = block_max(big, S.red);
-  int shift = 0;
-  while (big > (127u << shift)) ++shift;
+  big = block_max(big, S.red[1]);
+  int shift = max(0, 25 - __clz((int)big));      // big < 2^(shift + 7)
+  if (big > (127u << shift)) ++shift;
   const int round = (1 << shift) >> 1;
-  for (int h = warp; h < gqa; h += kSelThreads / 32) {
+  for (int h = warp; h < gqa; h += kSelWarps) {
     const int4 t = turned[h * 32 + lane];
     const int v[4] = {(t.x + round) >> shift, (t.y + round) >> shift, (t.z + round) >> shift, (t.w + round) >> shift};
     uint32_t pos = 0, neg = 0;
@@ -188,93 +253,131 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
       pos |= (uint32_t)(max(v[i], 0) & 0xff) << (8 * i);
       neg |= (uint32_t)(min(v[i], 0) & 0xff) << (8 * i);
     }
-    q8[h * 32 + lane] = make_int2((int)pos, (int)neg);
+    q8[h * 32 + lane] = make_int2((int)neg, (int)pos);
   }
   __syncthreads();
 
-  // ---- scores: one warp per group, kSelBatch groups in flight
-  const int64_t row = (int64_t)p.seq[b].slot * p.hkv + j;
-  const uint2* codes = p.codes + row * p.max_groups * 32;
-  const float2* weights = p.weights + row * p.max_groups;
-  uint64_t kmin = ~0ull, kmax = 0;
-  for (int g0 = warp * kSelBatch; g0 < ng; g0 += kSelThreads / 32 * kSelBatch) {
-    uint2 c[kSelBatch];
+  // ---- scores: four lanes per group, lane part `part` takes the 16-byte
+  // pieces part + 4 k (channels 8 (part + 4 k) .. + 7)
+  const int part = lane & 3;
+  const int4* q8v = reinterpret_cast<const int4*>(q8);     // [gqa][16 pieces]
+  uint64_t* dst = rank == 0 ? keys : in_block(keys, 0);
+  if (blocks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  uint32_t hmin = ~0u, hmax = 0;      // upper words of the smallest and the largest scored key
+  int4 qr[kSelHeads][4];
+  auto load_heads = [&](int h0) {
 #pragma unroll
-    for (int i = 0; i < kSelBatch; ++i)
-      c[i] = g0 + i < ng ? codes[(int64_t)(g0 + i) * 32 + lane] : make_uint2(0u, 0u);
-    float2 w = make_float2(0.0f, 0.0f);
-    if (lane < kSelBatch && g0 + lane < ng) w = weights[g0 + lane];
-    int best[kSelBatch];
+    for (int h = 0; h < kSelHeads; ++h)
 #pragma unroll
-    for (int i = 0; i < kSelBatch; ++i) best[i] = INT32_MIN;
-    for (int h = 0; h < gqa; ++h) {
-      const int2 qq = q8[h * 32 + lane];
+      for (int k = 0; k < 4; ++k)
+        qr[h][k] = q8v[min(h0 + h, gqa - 1) * 16 + part + 4 * k];    // (a head twice changes no maximum)
+  };
+  load_heads(0);
+  for (int c = 0; c < chunks; ++c) {
+    const int s = c % p.stages;
+    mbar_wait_bounded(&S.full[s], (uint32_t)((c / p.stages) & 1), &S.abort_flag, p.err_word);
+    const int4* codes = reinterpret_cast<const int4*>(stages + (size_t)s * kSelChunk * 256);
+    const int here = min(kSelChunk, n - c * kSelChunk);
+    for (int g0 = warp * 8; g0 < here; g0 += kSelWarps * 8) {
+      const int gl = g0 + (lane >> 2);    // behind the last group: whatever the stage holds, not used
+      int4 w[4];
 #pragma unroll
-      for (int i = 0; i < kSelBatch; ++i) {
-        const int s = __reduce_add_sync(0xffffffffu, __dp4a((int)c[i].y, qq.x, __dp4a((int)c[i].x, qq.y, 0)));
-        best[i] = max(best[i], s);
+      for (int k = 0; k < 4; ++k) w[k] = codes[gl * 16 + part + 4 * k];
+      int best = INT32_MIN;
+      for (int h0 = 0; h0 < gqa; h0 += kSelHeads) {
+        if (gqa > kSelHeads) load_heads(h0);
+#pragma unroll
+        for (int h = 0; h < kSelHeads; ++h) {
+          int a = 0, d = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            a = __dp4a(w[k].x, qr[h][k].x, a);
+            d = __dp4a(w[k].y, qr[h][k].y, d);
+            a = __dp4a(w[k].z, qr[h][k].z, a);
+            d = __dp4a(w[k].w, qr[h][k].w, d);
+          }
+          a += d;
+          a += __shfl_xor_sync(0xffffffffu, a, 1);
+          a += __shfl_xor_sync(0xffffffffu, a, 2);
+          best = max(best, a);
+        }
+      }
+      const int i = c * kSelChunk + gl;
+      if (part == 0 && gl < here) {
+        const int g = first + i;
+        const float2 wt = *reinterpret_cast<const float2*>(&keys[i]);
+        const double score = (double)best * (double)(best >= 0 ? wt.x : wt.y) + 0.0;   // -0 + 0 = +0
+        const bool kept = g < p.keep_first || g >= ng - p.keep_last;
+        const uint64_t key = kept ? ~0ull : order_key(score);
+        dst[g] = key;
+        if (!kept) {
+          hmin = min(hmin, (uint32_t)(key >> 32));
+          hmax = max(hmax, (uint32_t)(key >> 32));
+        }
       }
     }
-    int s = best[0];
-#pragma unroll
-    for (int i = 1; i < kSelBatch; ++i) s = lane == i ? best[i] : s;
-    const int g = g0 + lane;
-    if (lane < kSelBatch && g < ng) {
-      const double score = (double)s * (double)(s >= 0 ? w.x : w.y) + 0.0;   // -0 + 0 = +0
-      const bool kept = g < p.keep_first || g >= ng - p.keep_last;
-      const uint64_t key = kept ? ~0ull : order_key(score);
-      keys[g] = key;
-      if (!kept) {
-        kmin = min(kmin, key);
-        kmax = max(kmax, key);
+    if (c + p.stages < chunks) {
+      __syncthreads();          // everyone is done with the stage
+      if (tid == 0 && !S.abort_flag) request(c + p.stages);
+    }
+  }
+  if (S.abort_flag && tid == 0) {
+    // a wait gave up: wait (bounded) for the copies still in flight
+    for (int c = max(0, chunks - p.stages); c < chunks; ++c)
+      for (uint32_t i = 0; i < kSpinLimit; ++i)
+        if (mbar_try_wait(&S.full[c % p.stages], (uint32_t)((c / p.stages) & 1))) break;
+  }
+  if (blocks > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (rank != 0) return;      // nothing reads this block's shared memory
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    for (int i = n + tid; i < ng; i += kSelThreads) {
+      const uint64_t k = keys[i];
+      if (k != ~0ull) {
+        hmin = min(hmin, (uint32_t)(k >> 32));
+        hmax = max(hmax, (uint32_t)(k >> 32));
       }
     }
   }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    kmin = min(kmin, __shfl_xor_sync(0xffffffffu, kmin, o));
-    kmax = max(kmax, __shfl_xor_sync(0xffffffffu, kmax, o));
-  }
+  hmin = __reduce_min_sync(0xffffffffu, hmin);
+  hmax = __reduce_max_sync(0xffffffffu, hmax);
   if (lane == 0) {
-    S.red64[0][warp] = kmin;
-    S.red64[1][warp] = kmax;
+    S.red[2][warp] = hmin;
+    S.red[3][warp] = hmax;
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kSelThreads / 32; ++i) {
-    kmin = min(kmin, S.red64[0][i]);
-    kmax = max(kmax, S.red64[1][i]);
+  for (int i = 0; i < kSelWarps; ++i) {
+    hmin = min(hmin, S.red[2][i]);
+    hmax = max(hmax, S.red[3][i]);
   }
 
   // ---- the m-th largest key, 8 bits at a time from the first bit in which
-  // the scored keys differ; kept groups are above every one of them
+  // the scored keys' upper words differ; kept groups are above every one of them
   const int forced = min(ng, p.keep_first) + min(max(ng - p.keep_first, 0), p.keep_last);
   int need = m - forced;                   // still to choose among the scored groups with `prefix`
-  int bits = kmax > kmin ? 64 - __clzll((long long)(kmin ^ kmax)) : 0;   // undecided low bits
-  uint64_t prefix = bits < 64 ? kmin >> bits : 0;                        // the bits above them
-  bool all = false;                        // every key with the prefix is chosen
-  while (bits > 0 && need > 0 && !all) {
+  int bits = 64 - __clz((int)(hmin ^ hmax));      // undecided low bits, at least 32
+  uint64_t prefix = bits < 64 ? (uint64_t)hmin >> (bits - 32) : 0;       // the bits above them
+  int inbin = INT32_MAX;                   // scored groups with the prefix, once counted
+  auto has_prefix = [&](uint64_t k) { return k != ~0ull && (bits == 64 || (k >> bits) == prefix); };
+  while (bits > 0 && need > 0 && need != inbin && inbin > kSelRank) {
     const int d = min(bits, 8), low = bits - d;
-    if (tid < 256) S.hist[tid] = 0;
-    __syncthreads();
-    for (int g = tid; g < ng; g += kSelThreads) {
-      const uint64_t k = keys[g];
-      if (k != ~0ull && (bits == 64 || (k >> bits) == prefix)) atomicAdd(&S.hist[(uint32_t)(k >> low) & ((1u << d) - 1)], 1u);
+    for (int i = tid; i < ng; i += kSelThreads) {
+      const uint64_t k = keys[i];
+      if (has_prefix(k)) atomicAdd(&S.hist[(uint32_t)(k >> low) & ((1u << d) - 1)], 1u);
     }
     __syncthreads();
     if (warp == 0) {
       // lane l owns digits 255 - 8 l .. 248 - 8 l, the largest first
-      uint32_t c[8], sum = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        c[i] = S.hist[255 - 8 * lane - i];
-        sum += c[i];
-      }
+      const uint4 x = reinterpret_cast<const uint4*>(S.hist)[2 * (31 - lane) + 1];
+      const uint4 y = reinterpret_cast<const uint4*>(S.hist)[2 * (31 - lane)];
+      const uint32_t c[8] = {x.w, x.z, x.y, x.x, y.w, y.z, y.y, y.x};
+      const uint32_t sum = x.x + x.y + x.z + x.w + y.x + y.y + y.z + y.w;
       uint32_t before = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t up2 = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += up2;
+        const uint32_t lower = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += lower;
       }
       before -= sum;                       // keys in larger digits than this lane's
       if (before < (uint32_t)need && (uint32_t)need <= before + sum) {
@@ -291,56 +394,96 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const __grid_consta
     }
     __syncthreads();
     need -= (int)S.above;
-    all = (uint32_t)need == S.inbin;
+    inbin = (int)S.inbin;
     prefix = (prefix << d) | S.digit;
     bits = low;
+    S.hist[tid] = 0;
+    __syncthreads();
   }
-  // chosen: keys whose top bits are above the prefix; of those equal to it all,
-  // or (every bit decided) the `need` lowest groups
-  const uint64_t limit = prefix;
-  if (all) need = INT32_MAX;
-
-  // ---- the chosen groups in ascending order
-  int done_gt = 0, done_eq = 0;
-  for (int g0 = 0; g0 < ng; g0 += kSelThreads) {
-    const int g = g0 + tid;
-    bool gt = false, eq = false;
-    if (g < ng) {
-      const uint64_t k = keys[g];
-      const uint64_t t = bits < 64 ? k >> bits : 0;
-      gt = k == ~0ull || t > limit;
-      eq = !gt && t == limit;
-    }
-    const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    __syncthreads();
-    if (lane == 0) {
-      S.cnt[0][warp] = __popc(bg);
-      S.cnt[1][warp] = __popc(be);
-    }
-    __syncthreads();
-    int ngt = done_gt, neq = done_eq;
-#pragma unroll
-    for (int i = 0; i < kSelThreads / 32; ++i) {
-      const int x = S.cnt[0][i], y = S.cnt[1][i];
-      if (i < warp) {
-        ngt += x;
-        neq += y;
+  // chosen: keys whose top bits are above the prefix; of those equal to it
+  // all, or the `need` first by (key, group): where at most kSelRank share the
+  // prefix they are ranked; where every bit is decided they are equal
+  uint64_t limit_key = 0;       // the last chosen (key, group) of the ranked ones
+  int limit_group = INT32_MAX;
+  bool ranked = false;
+  if (need == inbin) {
+    need = INT32_MAX;
+  } else if (bits > 0 && need > 0) {
+    ranked = true;
+    for (int i = tid; i < ng; i += kSelThreads) {
+      const uint64_t k = keys[i];
+      if (has_prefix(k)) {
+        const uint32_t at = atomicAdd(&S.n_cand, 1u);
+        if (at < (uint32_t)kSelRank) {
+          S.cand[at] = k;
+          S.cand_group[at] = i;
+        }
       }
-      done_gt += x;
-      done_eq += y;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const bool on = lane < inbin;
+      const uint64_t k = on ? S.cand[lane] : 0;
+      const int g = on ? S.cand_group[lane] : INT32_MAX;
+      int before = 0;
+      for (int i = 0; i < inbin; ++i) {
+        const uint64_t ki = S.cand[i];
+        before += ki > k || (ki == k && S.cand_group[i] < g);
+      }
+      if (on && before == need - 1) {
+        S.limit_key = k;
+        S.limit_group = g;
+      }
+    }
+    __syncthreads();
+    limit_key = S.limit_key;
+    limit_group = S.limit_group;
+  }
+
+  // ---- the chosen groups in ascending order: `above` are chosen, of those
+  // `at` the limit (equal keys, or the whole bin) the first `need`
+  int done2 = 0, done1 = 0;
+  for (int i0 = 0, turn = 0; i0 < ng; i0 += kSelThreads, turn ^= 1) {
+    const int i = i0 + tid;
+    bool above = false, at = false;
+    if (i < ng) {
+      const uint64_t k = keys[i];
+      const uint64_t t = bits < 64 ? k >> bits : 0;
+      above = k == ~0ull || t > prefix;
+      if (!above && t == prefix) {
+        if (ranked) above = k > limit_key || (k == limit_key && i <= limit_group);
+        else at = true;
+      }
+    }
+    const uint32_t b2 = __ballot_sync(0xffffffffu, above), b1 = __ballot_sync(0xffffffffu, at);
+    if (lane == 0) {
+      S.cnt[turn][0][warp] = __popc(b2);
+      S.cnt[turn][1][warp] = __popc(b1);
+    }
+    __syncthreads();
+    int n2 = done2, n1 = done1;
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) {
+      const int x = S.cnt[turn][0][w], y = S.cnt[turn][1][w];
+      if (w < warp) {
+        n2 += x;
+        n1 += y;
+      }
+      done2 += x;
+      done1 += y;
     }
     const uint32_t below = (1u << lane) - 1;
-    ngt += __popc(bg & below);
-    neq += __popc(be & below);
-    if (gt || (eq && neq < need)) out[ngt + min(neq, need)] = g;
+    n2 += __popc(b2 & below);
+    n1 += __popc(b1 & below);
+    if (above || (at && n1 < need)) out[n2 + min(n1, need)] = i;
   }
 }
 
 template <int MAXS, bool M16>
 cudaError_t launch_index_t(const IndexParams<MAXS>& p, const uint8_t* arena, int groups, cudaStream_t stream) {
   constexpr int per = kIdxThreads / 32;
-  index_kernel<MAXS, M16><<<dim3((groups + per - 1) / per, p.hkv, p.n_seqs), kIdxThreads, 0, stream>>>(p, arena);
-  return cudaGetLastError();
+  return launch_dependent(index_kernel<MAXS, M16>, dim3((groups + per - 1) / per, p.hkv, p.n_seqs), dim3(kIdxThreads),
+                          0, stream, 1, p, arena);
 }
 
 }  // namespace
@@ -354,25 +497,37 @@ cudaError_t launch_index(const IndexParams<MAXS>& p, const uint8_t* arena, bool 
                 : launch_index_t<MAXS, false>(p, arena, groups, stream);
 }
 
-size_t select_smem_bytes(int q_group, int groups) {
-  return (size_t)q_group * 32 * (sizeof(int4) + sizeof(int2)) + (size_t)groups * sizeof(uint64_t);
-}
-
 template <int MAXS>
-cudaError_t launch_select(const SelectParams<MAXS>& p, cudaStream_t stream) {
+cudaError_t launch_select(const SelectParams<MAXS>& params, int sms, cudaStream_t stream) {
+  SelectParams<MAXS> p = params;
   int groups = 0;
   for (int i = 0; i < p.n_seqs; ++i) groups = std::max(groups, p.seq[i].ng);
-  const size_t smem = groups > p.n_select ? select_smem_bytes(p.q_group, groups) : 0;
+  if (groups <= p.n_select) groups = 0;
+  const int rows = p.n_seqs * p.hkv;
+  // blocks of a row: more while each keeps at least 64 groups and the grid
+  // stays within two blocks per SM
+  int blocks = 1;
+  while (blocks < kSelMaxBlocks && groups >= 128 * blocks && (int64_t)rows * blocks <= sms) blocks *= 2;
+  const int chunks = ((groups + blocks - 1) / blocks + kSelChunk - 1) / kSelChunk;
+  p.blocks = blocks;
+  // every copy in flight at once up to 512 groups a block; longer slices turn two stages over
+  p.stages = chunks <= kSelStages ? std::max(chunks, 1) : 2;
+  const size_t smem = (size_t)p.stages * kSelChunk * 256 + (size_t)p.q_group * 32 * (sizeof(int4) + sizeof(int2)) +
+                      (size_t)groups * sizeof(uint64_t);
+  static_assert(kSelStages * kSelChunk * 256 + kSelectMaxHeads * 32 * 24 + kSelStages * kSelChunk * kSelMaxBlocks * 8 <=
+                        kSelectMaxSmem &&
+                    2 * kSelChunk * 256 + kSelectMaxHeads * 32 * 24 + kSelectMaxGroups * 8 <= kSelectMaxSmem,
+                "the largest selection fits");
   static bool attr_done[64] = {};
   cudaError_t e = ensure_smem_attr(select_kernel<MAXS>, kSelectMaxSmem, attr_done);
   if (e != cudaSuccess) return e;
-  select_kernel<MAXS><<<(unsigned)(p.n_seqs * p.hkv), kSelThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(select_kernel<MAXS>, dim3((unsigned)(rows * blocks)), dim3(kSelThreads), smem, stream,
+                          (unsigned)blocks, p);
 }
 
 #define OSCAR_INSTANTIATE(N)                                                                                  \
   template cudaError_t launch_index<N>(const IndexParams<N>&, const uint8_t*, bool, cudaStream_t);            \
-  template cudaError_t launch_select<N>(const SelectParams<N>&, cudaStream_t);
+  template cudaError_t launch_select<N>(const SelectParams<N>&, int, cudaStream_t);
 OSCAR_INSTANTIATE(kDecodeSeqsSmall)
 OSCAR_INSTANTIATE(kDecodeSeqsLarge)
 #undef OSCAR_INSTANTIATE

@@ -143,12 +143,11 @@ def _write_index(cache, lo, hi, w):
     cache.index[at:at + 8 * ng] = torch.from_numpy(np.ascontiguousarray(w, "<f4").view(np.uint8).reshape(-1).copy()).cuda()
 
 
-@pytest.mark.parametrize("ng,n", [(1100, 1), (1100, 64), (1100, 600), (1100, 1099), (513, 512), (40, 7)])
+@pytest.mark.parametrize("ng,n", [(1100, 1), (1100, 64), (1100, 600), (1100, 1099), (513, 512), (40, 7), (5003, 90)])
 @pytest.mark.parametrize("kind", ["ties", "two levels", "spread", "wide", "negative"])
 def test_selection_of_given_summaries(ng, n, kind):
     """Index contents made for the selection: equal scores everywhere, a few
     distinct ones, magnitudes over the whole float32 range, all below zero."""
-    cache = make([0], 1, index=False)
     cache = U.lib().OscarCache(1, 1, 128 * ng)
     rng = np.random.default_rng(ng + n)
     g = torch.Generator().manual_seed(1)
@@ -195,8 +194,6 @@ def test_queries_at_the_edges():
 
 def test_a_planted_group_is_found():
     """A key far along the query's direction puts its group in front."""
-    cache0 = make([0], 1, index=False)
-    cache0.close()
     gen = torch.Generator().manual_seed(4)
     k, v = W.make_sequence_kv(4096, 1, W.KVRecipe(), gen)
     q = W.make_q(1, 1, seed=6)
