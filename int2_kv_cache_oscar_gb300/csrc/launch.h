@@ -165,7 +165,9 @@ struct RotaryParams {
   const int32_t* positions;   // [n]
   int64_t n;
   int32_t dim;                // rotated channels
-  int32_t block_tokens;       // set by the launch
+  int32_t block_tokens;       // set by the launch: tokens of a block,
+  int32_t step_tokens;        // and a thread's step from one of its rows to
+  int32_t step_rows;          // the next, tokens and heads
   int32_t transpose;
   float factor;
   uint64_t freq[kHeadDim / 2];   // turns per position, 2^64 to the turn

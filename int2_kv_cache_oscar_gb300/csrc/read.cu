@@ -17,7 +17,10 @@
 //   keys:   thread = token.  Its codes are 8 words; channels c and c + 64 sit
 //           at the same bit of two of them and share a packed pair, so six
 //           transform stages are packed adds in registers and the last one is
-//           within the pairs.
+//           within the pairs.  The thread puts its row into shared memory (rows
+//           16 bytes apart in banks) and sends it off with one bulk store:
+//           stored from registers, 32 rows of different lines a warp, the keys
+//           kept the load/store unit busy for a quarter of the time.
 //   values: thread = 8 channels x 16 tokens (8 words), so that 16 lanes write
 //           one token's row.
 // Bound by HBM writes (512 or 1,024 bytes written per 108 or 86 read).
@@ -35,13 +38,20 @@ constexpr int kReadStages = 2;
 constexpr float kTwo23 = 8388608.0f;
 constexpr uint32_t kTwo23Bits = 0x4B000000u;
 
-template <bool M16>
+template <bool M16, bool F32>
 struct ReadSmem {
+  static constexpr int kRow = kHeadDim * (F32 ? 4 : 2);
+  static constexpr int kPitch = kRow + 16;
   alignas(128) uint8_t stage[kReadStages][Blk<M16>::kBytes];
+  alignas(16) uint8_t krow[kGroup][kPitch];   // key rows on their way out
   alignas(16) float4 kp[kHeadDim / 2];   // channels (c, c + 64): scale 2^-b (2), zero (2), b the codes' bit
   alignas(8) uint64_t full[kReadStages];
   int abort_flag;
 };
+
+static_assert(sizeof(ReadSmem<false, true>) <= 113 * 1024 && sizeof(ReadSmem<false, false>) <= 75 * 1024,
+              "two and three blocks per SM");
+static_assert(ReadSmem<false, false>::kPitch % 16 == 0 && ReadSmem<true, true>::kPitch % 16 == 0, "bulk stores");
 
 // Bit of the code of column c within its (half) word once the upper 16 bits
 // have been shifted down for odd columns: 4 kk + 2 hf.
@@ -56,6 +66,14 @@ __device__ __forceinline__ float2 codes2(uint32_t w0, uint32_t w1, int b) {
   return __fadd2_rn(f, make_float2(-kTwo23, -kTwo23));
 }
 
+// One row from shared to global memory (bytes a multiple of 16), in this
+// thread's current bulk group.
+__device__ __forceinline__ void bulk_s2g(void* gmem_dst, const void* smem_src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gmem_dst), "r"(smem_u32(smem_src)),
+               "r"(bytes)
+               : "memory");
+}
+
 __device__ __forceinline__ void st_row32(void* p, uint4 lo, uint4 hi) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(lo.x), "r"(lo.y), "r"(lo.z),
                "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
@@ -64,11 +82,17 @@ __device__ __forceinline__ void st_row32(void* p, uint4 lo, uint4 hi) {
 
 // 8 channels of a row (32-byte store pieces in float32, one 16-byte one in bf16)
 template <bool F32>
-__device__ __forceinline__ void store8(void* row, int c, const float* f) {
+__device__ __forceinline__ void store8(void* row, int c, const float* f, bool wide) {
   if constexpr (F32) {
     float* d = static_cast<float*>(row) + c;
-    reinterpret_cast<float4*>(d)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(d)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    const uint4 lo = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    const uint4 hi = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+    if (wide) {      // 32-byte aligned: whole sectors
+      st_row32(d, lo, hi);
+    } else {
+      reinterpret_cast<uint4*>(d)[0] = lo;
+      reinterpret_cast<uint4*>(d)[1] = hi;
+    }
   } else {   // nearest even: the output type
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(row) + c) =
         make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
@@ -98,7 +122,8 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
   using MR = Meta<M16>;
   using Out = typename std::conditional<F32, float, uint16_t>::type;
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  ReadSmem<M16>& S = *reinterpret_cast<ReadSmem<M16>*>(smem_raw);
+  using Smem = ReadSmem<M16, F32>;
+  Smem& S = *reinterpret_cast<Smem*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int s = 0; s < kReadStages; ++s) mbar_init(&S.full[s], 1);
@@ -158,6 +183,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
             if (mbar_try_wait(&S.full[ii & 1], (ii >> 1) & 1)) break;
         }
       }
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
       return;
     }
     if (!packed) {
@@ -175,7 +201,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
           if constexpr (F32) {
             const float f[8] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y),
                                 bf16_lo(w.z), bf16_hi(w.z), bf16_lo(w.w), bf16_hi(w.w)};
-            store8<true>(out_row(base, t), c, f);
+            store8<true>(out_row(base, t), c, f, p.wide);
           } else {
             *reinterpret_cast<uint4*>(out_row(base, t) + c) = w;
           }
@@ -211,7 +237,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
             f[g] = v.x;
             f[g + 1] = v.y;
           }
-          if (t >= lo && t < hi) store8<F32>(out_row(vout, t), 8 * c8, f);
+          if (t >= lo && t < hi) store8<F32>(out_row(vout, t), 8 * c8, f, p.wide);
         }
       }
     }
@@ -253,49 +279,42 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
       }
       // last stage within the pairs, times n / sqrt(128)
       const float n = MR::one(blk + B::kKNorm, t) * 0.088388347648318440550f;
-      if (t >= lo && t < hi) {
-        Out* row = out_row(kout, t);
+      // (this thread's previous row has been read from shared memory)
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      uint8_t* srow = S.krow[t];
 #pragma unroll
-        for (int up = 0; up < 2; ++up) {
+      for (int up = 0; up < 2; ++up) {
 #pragma unroll
-          for (int c = 0; c < 64; c += 16) {
-            float f[16];
+        for (int c = 0; c < 64; c += 8) {
+          float f[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float a = x[c + i].x * n;
-              f[i] = fmaf(x[c + i].y, up ? -n : n, a);
-            }
-            if constexpr (F32) {
-              store8<true>(row, 64 * up + c, f);
-              store8<true>(row, 64 * up + c + 8, f + 8);
-            } else {
-              const uint4 y0 = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                                          pack_bf16x2(f[6], f[7]));
-              const uint4 y1 = make_uint4(pack_bf16x2(f[8], f[9]), pack_bf16x2(f[10], f[11]),
-                                          pack_bf16x2(f[12], f[13]), pack_bf16x2(f[14], f[15]));
-              if (p.wide) {
-                st_row32(row + 64 * up + c, y0, y1);
-              } else {
-                *reinterpret_cast<uint4*>(row + 64 * up + c) = y0;
-                *reinterpret_cast<uint4*>(row + 64 * up + c + 8) = y1;
-              }
-            }
+          for (int i = 0; i < 8; ++i) {
+            const float a = x[c + i].x * n;
+            f[i] = fmaf(x[c + i].y, up ? -n : n, a);
           }
+          store8<F32>(srow, 64 * up + c, f, false);
         }
       }
+      if (t >= lo && t < hi) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        bulk_s2g(out_row(kout, t), srow, Smem::kRow);
+      }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
     __syncthreads();   // everyone is done with this stage and the parameter table
   }
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the last rows are written
 }
 
 template <int MAXS, bool M16, bool F32>
 cudaError_t launch_read_t(const ReadParams<MAXS>& p, const uint8_t* arena, int sms, cudaStream_t stream) {
   if (p.n_tiles <= 0) return cudaSuccess;
-  const int smem = (int)sizeof(ReadSmem<M16>);
+  const int smem = (int)sizeof(ReadSmem<M16, F32>);
   static bool attr_done[64] = {};
   cudaError_t e = ensure_smem_attr(read_kernel<MAXS, M16, F32>, smem, attr_done);
   if (e != cudaSuccess) return e;
-  const unsigned grid = (unsigned)std::min<int64_t>(p.n_tiles, 3 * (int64_t)sms);
+  // resident blocks per SM: registers allow three, a float32 row buffer two
+  const unsigned grid = (unsigned)std::min<int64_t>(p.n_tiles, (F32 ? 2 : 3) * (int64_t)sms);
   return launch_dependent(read_kernel<MAXS, M16, F32>, dim3(grid), dim3(kReadThreads), (size_t)smem, stream, 1, p, arena);
 }
 

@@ -70,98 +70,94 @@ struct Row<true> {
 
 // A row is cut into items of two 16-byte pieces: in the half layout piece i of
 // the first half and of the second half of the rotated channels, in the
-// interleaved layout (and behind the rotated channels) two neighbours.
+// interleaved layout (and behind the rotated channels) two neighbours.  A
+// thread keeps its item of the row and walks over the rows (token, head) of
+// the block; an item's cosines and sines are V / 2 float4 (two pairs each),
+// stored so that the threads of a row read neighbouring ones.
 template <bool F32, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(const __grid_constant__ RotaryParams p) {
   using R = Row<F32>;
   constexpr int V = R::kVec;
   constexpr int kRowItems = kHeadDim / (2 * V);
-  __shared__ __align__(16) float2 table[kRotMaxTokens][kHeadDim / 2];
+  __shared__ __align__(16) float4 table[kRotMaxTokens][V / 2][kRowItems];   // (cos, cos, sin, sin)
   const int64_t t0 = (int64_t)blockIdx.x * p.block_tokens;
   const int tokens = (int)min((int64_t)p.block_tokens, (int64_t)p.n - t0);
   const int rows = p.q.heads + p.k.heads;
-  const int items = tokens * rows * kRowItems;
   const int rot_items = p.dim / (2 * V);
   const int half = p.dim / 2;
-
-  auto place = [&](int idx, const uint8_t*& src, uint8_t*& dst, int& a, int& b, int& tok) {
-    const int j = idx % kRowItems;
-    const int row = idx / kRowItems;
-    tok = row / rows;
-    const int h = row - tok * rows;
-    const bool isq = h < p.q.heads;
-    const RotaryRows& x = isq ? p.q : p.k;
-    const int head = isq ? h : h - p.q.heads;
-    src = x.in + (t0 + tok) * x.in_token + head * x.in_head;
-    dst = x.out + (t0 + tok) * x.out_token + head * x.out_head;
-    if (INTERLEAVED || j >= rot_items) {
-      a = 2 * V * j;
-      b = a + V;
-    } else {
-      a = V * j;
-      b = half + V * j;
-    }
-  };
+  const int j = threadIdx.x % kRowItems;
+  const bool turned = j < rot_items;
+  // byte offsets of the two pieces
+  const int at_a = (!INTERLEAVED && turned ? V * j : 2 * V * j) * (16 / V);
+  const int at_b = !INTERLEAVED && turned ? at_a + half * (16 / V) : at_a + 16;
+  int tok = (int)(threadIdx.x / kRowItems) / rows;
+  int h = (int)(threadIdx.x / kRowItems) - tok * rows;
 
   grid_dependency_wait();
   allow_dependents();
-  for (int base = 0; base < items; base += kRotThreads * kRotItems) {
+  bool first = true;
+  for (int done = 0; done < tokens * rows; done += kRotThreads / kRowItems * kRotItems) {
     uint4 xa[kRotItems], xb[kRotItems];
+    uint8_t* dst[kRotItems];
+    int tk[kRotItems];
 #pragma unroll
     for (int i = 0; i < kRotItems; ++i) {
-      const int idx = base + i * kRotThreads + threadIdx.x;
-      if (idx < items) {
-        const uint8_t* src;
-        uint8_t* dst;
-        int a, b, tok;
-        place(idx, src, dst, a, b, tok);
-        xa[i] = *reinterpret_cast<const uint4*>(src + a * (16 / V));
-        xb[i] = *reinterpret_cast<const uint4*>(src + b * (16 / V));
+      tk[i] = tok;
+      if (tok < tokens) {
+        const bool isq = h < p.q.heads;
+        const RotaryRows& x = isq ? p.q : p.k;
+        const int64_t head = isq ? h : h - p.q.heads;
+        const uint8_t* src = x.in + (t0 + tok) * x.in_token + head * x.in_head;
+        dst[i] = x.out + (t0 + tok) * x.out_token + head * x.out_head;
+        xa[i] = *reinterpret_cast<const uint4*>(src + at_a);
+        xb[i] = *reinterpret_cast<const uint4*>(src + at_b);
+      }
+      h += p.step_rows;
+      tok += p.step_tokens;
+      if (h >= rows) {
+        h -= rows;
+        ++tok;
       }
     }
-    if (base == 0) {
+    if (first) {
+      first = false;
       for (int i = threadIdx.x; i < tokens * half; i += kRotThreads) {
-        const int tok = i / half, pair = i - tok * half;
-        const uint64_t pos = (uint64_t)(int64_t)p.positions[t0 + tok];
+        const int t = i / half, pair = i - t * half;
+        const uint64_t pos = (uint64_t)(int64_t)p.positions[t0 + t];
         const float2 cs = phase_cos_sin(pos * p.freq[pair]);
-        table[tok][pair] = make_float2(cs.x * p.factor, cs.y * (p.transpose ? -p.factor : p.factor));
+        float* e = reinterpret_cast<float*>(&table[t][(pair % V) / 2][pair / V]) + (pair & 1);
+        e[0] = cs.x * p.factor;
+        e[2] = cs.y * (p.transpose ? -p.factor : p.factor);
       }
       __syncthreads();
     }
 #pragma unroll
     for (int i = 0; i < kRotItems; ++i) {
-      const int idx = base + i * kRotThreads + threadIdx.x;
-      if (idx < items) {
-        const uint8_t* src;
-        uint8_t* dst;
-        int a, b, tok;
-        place(idx, src, dst, a, b, tok);
-        const int j = idx % kRowItems;
-        uint4 ya = xa[i], yb = xb[i];
-        if (j < rot_items) {
-          float u[2 * V];
-          R::widen(ya, u);
-          R::widen(yb, u + V);
-          const float4* cs = reinterpret_cast<const float4*>(&table[tok][V * j]);
+      if (tk[i] >= tokens) continue;
+      uint4 ya = xa[i], yb = xb[i];
+      if (turned) {
+        float u[2 * V];
+        R::widen(ya, u);
+        R::widen(yb, u + V);
 #pragma unroll
-          for (int e = 0; e < V; e += 2) {
-            const float4 w = cs[e / 2];   // (cos, sin) of two pairs
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              const float c = o ? w.z : w.x, s = o ? w.w : w.y;
-              const int ia = INTERLEAVED ? 2 * (e + o) : e + o;
-              const int ib = INTERLEAVED ? ia + 1 : V + e + o;
-              const float x0 = u[ia], x1 = u[ib];
-              u[ia] = fmaf(x0, c, -(x1 * s));
-              u[ib] = fmaf(x0, s, x1 * c);
-            }
-          }
-          ya = R::narrow(u);
-          yb = R::narrow(u + V);
+        for (int e = 0; e < V / 2; ++e) {   // pairs 2 e, 2 e + 1 of the item
+          const float4 w = table[tk[i]][e][j];
+          const float2 c = make_float2(w.x, w.y), s = make_float2(w.z, w.w);
+          const int a0 = INTERLEAVED ? 4 * e : 2 * e, b0 = INTERLEAVED ? 4 * e + 1 : V + 2 * e;
+          const int a1 = INTERLEAVED ? 4 * e + 2 : 2 * e + 1, b1 = INTERLEAVED ? 4 * e + 3 : V + 2 * e + 1;
+          const float2 a = make_float2(u[a0], u[a1]), b = make_float2(u[b0], u[b1]);
+          const float2 bs = __fmul2_rn(b, s), bc = __fmul2_rn(b, c);
+          const float2 y = __ffma2_rn(a, c, make_float2(-bs.x, -bs.y)), z = __ffma2_rn(a, s, bc);
+          u[a0] = y.x;
+          u[a1] = y.y;
+          u[b0] = z.x;
+          u[b1] = z.y;
         }
-        *reinterpret_cast<uint4*>(dst + a * (16 / V)) = ya;
-        *reinterpret_cast<uint4*>(dst + b * (16 / V)) = yb;
+        ya = R::narrow(u);
+        yb = R::narrow(u + V);
       }
+      *reinterpret_cast<uint4*>(dst[i] + at_a) = ya;
+      *reinterpret_cast<uint4*>(dst[i] + at_b) = yb;
     }
   }
 }
@@ -178,6 +174,9 @@ cudaError_t launch_rotary(const RotaryParams& params, bool f32, bool interleaved
   int64_t tokens = std::min<int64_t>(kRotThreads * kRotItems / per_token, (p.n + 2 * sms - 1) / (2 * sms));
   tokens = std::max<int64_t>(1, std::min<int64_t>(tokens, kRotMaxTokens));
   p.block_tokens = (int32_t)tokens;
+  const int step = kRotThreads / (kHeadDim / (2 * (f32 ? Row<true>::kVec : Row<false>::kVec)));   // rows per round
+  p.step_tokens = step / rows;
+  p.step_rows = step % rows;
   const unsigned grid = (unsigned)((p.n + tokens - 1) / tokens);
   const auto kernel = f32 ? (interleaved ? rotary_kernel<true, true> : rotary_kernel<true, false>)
                           : (interleaved ? rotary_kernel<false, true> : rotary_kernel<false, false>);
