@@ -214,10 +214,15 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
       // ---- values: channels 8 c8 .. + 7, tokens of (token half jt, tig)
       const int c8 = lane & 15, x = 2 * warp + (lane >> 4);
       const int tig = x & 3, jt = x >> 2;
-      const uint32_t* words = reinterpret_cast<const uint32_t*>(blk + B::kVCodes);
+      const uint32_t* words = reinterpret_cast<const uint32_t*>(blk + B::kVCodes) +
+                              ((((c8 >> 1) * 2 + jt) * 32 + tig) * 2 + (c8 & 1));
       uint32_t w[8];
 #pragma unroll
-      for (int g = 0; g < 8; ++g) w[g] = words[(((c8 >> 1) * 2 + jt) * 32 + 4 * g + tig) * 2 + (c8 & 1)];
+      for (int g = 0; g < 8; ++g) w[g] = words[8 * g];
+      const int t0 = 64 * jt + 2 * tig;      // this thread's tokens are t0 + 8 q + e
+      const int m0 = t0 * 4 + (c8 >> 2);     // and their scales and zeros (see vmeta_row: e swaps where q is odd)
+      Out* row0p = out_row(vout, t0) + 8 * c8;
+      const int64_t pitch = (int64_t)p.hkv * kHeadDim;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (e) {
@@ -227,8 +232,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
 #pragma unroll
         for (int q = 0; q < 8; ++q) {   // kk = q >> 1, hf = q & 1
           const int bit = 4 * (q >> 1) + 2 * (q & 1);
-          const int t = 64 * jt + 8 * q + 2 * tig + e;
-          const int at = (M16 ? t : vmeta_row(t)) * 4 + (c8 >> 2);
+          const int at = m0 + 4 * (8 * q + (M16 ? e : e ^ (q & 1)));
           const float sc = MR::one(blk + B::kVScale, at) * exp2i(-bit), ze = MR::one(blk + B::kVZero, at);
           float f[8];
 #pragma unroll
@@ -237,7 +241,8 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
             f[g] = v.x;
             f[g + 1] = v.y;
           }
-          if (t >= lo && t < hi) store8<F32>(out_row(vout, t), 8 * c8, f, p.wide);
+          const int t = t0 + 8 * q + e;
+          if (t >= lo && t < hi) store8<F32>(row0p + (8 * q + e) * pitch, 0, f, p.wide);
         }
       }
     }
@@ -274,11 +279,13 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
           const int i = ((n >> hb) << (hb + 1)) | (n & (h - 1));
           const float2 a = x[i], d = x[i + h];
           x[i] = __fadd2_rn(a, d);
-          x[i + h] = __fadd2_rn(a, make_float2(-d.x, -d.y));
+          x[i + h] = __ffma2_rn(d, make_float2(-1.0f, -1.0f), a);   // a - d (no negated packed operand)
         }
       }
       // last stage within the pairs, times n / sqrt(128)
       const float n = MR::one(blk + B::kKNorm, t) * 0.088388347648318440550f;
+#pragma unroll
+      for (int i = 0; i < 64; ++i) x[i] = __fmul2_rn(x[i], make_float2(n, n));
       // (this thread's previous row has been read from shared memory)
       asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
       uint8_t* srow = S.krow[t];
@@ -289,8 +296,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
           float f[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float a = x[c + i].x * n;
-            f[i] = fmaf(x[c + i].y, up ? -n : n, a);
+            f[i] = up ? x[c + i].x - x[c + i].y : x[c + i].x + x[c + i].y;
           }
           store8<F32>(srow, 64 * up + c, f, false);
         }

@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kRotThreads = 256;
 constexpr int kRotItems = 4;        // row pieces in flight per thread
+constexpr int kRotBlocks = 3;       // blocks per SM (four: 64 registers, spills, slower)
 constexpr int kRotMaxTokens = 32;   // tokens of one block
 
 // cos and sin of a phase (turns, 2^64 to the turn)
@@ -75,7 +76,7 @@ struct Row<true> {
 // the block; an item's cosines and sines are V / 2 float4 (two pairs each),
 // stored so that the threads of a row read neighbouring ones.
 template <bool F32, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRotThreads, 3) rotary_kernel(const __grid_constant__ RotaryParams p) {
+__global__ void __launch_bounds__(kRotThreads, kRotBlocks) rotary_kernel(const __grid_constant__ RotaryParams p) {
   using R = Row<F32>;
   constexpr int V = R::kVec;
   constexpr int kRowItems = kHeadDim / (2 * V);
@@ -169,9 +170,11 @@ cudaError_t launch_rotary(const RotaryParams& params, bool f32, bool interleaved
   const int rows = p.q.heads + p.k.heads;
   if (p.n <= 0 || rows <= 0) return cudaSuccess;
   const int per_token = rows * (kHeadDim / (2 * (f32 ? Row<true>::kVec : Row<false>::kVec)));
-  // as many tokens as give every thread its kRotItems pieces, but no fewer
-  // blocks than two per SM
-  int64_t tokens = std::min<int64_t>(kRotThreads * kRotItems / per_token, (p.n + 2 * sms - 1) / (2 * sms));
+  // as many tokens as give every thread its kRotItems pieces; between one and
+  // two waves of blocks, as many as make it one
+  const int64_t slots = (int64_t)kRotBlocks * sms;
+  int64_t tokens = std::max<int64_t>(1, kRotThreads * kRotItems / per_token);
+  if (p.n <= tokens * 2 * slots) tokens = (p.n + slots - 1) / slots;
   tokens = std::max<int64_t>(1, std::min<int64_t>(tokens, kRotMaxTokens));
   p.block_tokens = (int32_t)tokens;
   const int step = kRotThreads / (kHeadDim / (2 * (f32 ? Row<true>::kVec : Row<false>::kVec)));   // rows per round
