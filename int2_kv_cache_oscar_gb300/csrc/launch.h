@@ -253,6 +253,7 @@ struct SelectParams {
   SelectSeq seq[MAXS];
 };
 
+constexpr int kSelectSeqsSmall = 64;     // a small launch's sequences (index and selection)
 constexpr int kSelectMaxSmem = 224 * 1024;
 constexpr int kSelectMaxHeads = 64;       // query heads per KV head
 constexpr int kSelectMaxGroups = 12000;   // groups of a sequence to choose among (their keys in shared memory)

@@ -1345,7 +1345,7 @@ oscar_status oscar_index_update(oscar_cache* c, int32_t n_seqs, const int32_t* s
     DeviceGuard dg(c->cfg.device);
     if (dg.err != cudaSuccess) return cuda_fail(dg.err, "cudaSetDevice");
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    s = seqs.size() <= (size_t)kDecodeSeqsSmall ? run_index<kDecodeSeqsSmall>(c, seqs, st)
+    s = seqs.size() <= (size_t)kSelectSeqsSmall ? run_index<kSelectSeqsSmall>(c, seqs, st)
                                                 : run_index<kDecodeSeqsLarge>(c, seqs, st);
     if (s != OSCAR_OK) return s;
     for (const IndexSeq& x : seqs) c->indexed[x.slot] = x.end;
@@ -1392,8 +1392,8 @@ oscar_status oscar_select_groups(oscar_cache* c, int32_t n_seqs, const int32_t* 
     if ((s = device_view_as(q, "q", c->cfg.device, &q)) != OSCAR_OK) return s;
     if ((s = device_view_as(groups, "groups", c->cfg.device, &groups, false)) != OSCAR_OK) return s;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    s = n_seqs <= kDecodeSeqsSmall
-            ? run_select<kDecodeSeqsSmall>(c, seqs, q, num_q_heads, n_select, keep_first, keep_last, groups, st)
+    s = n_seqs <= kSelectSeqsSmall
+            ? run_select<kSelectSeqsSmall>(c, seqs, q, num_q_heads, n_select, keep_first, keep_last, groups, st)
             : run_select<kDecodeSeqsLarge>(c, seqs, q, num_q_heads, n_select, keep_first, keep_last, groups, st);
     if (s != OSCAR_OK) return s;
     return ok();

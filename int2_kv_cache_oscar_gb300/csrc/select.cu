@@ -55,12 +55,23 @@ __device__ __forceinline__ float finite_or_zero(float x) {
 }
 
 // ----------------------------------------------------------- summaries
-// One warp per group: lane l summarises channels 4 l .. 4 l + 3.
+// One warp per group; lane l summarises channels 4 l .. 4 l + 3.  Bound by HBM:
+// 1,536 (768) bytes read and 264 written per group.  (Two or four groups in
+// flight per warp took as long, within 2 %.)
+template <bool M16>
+__device__ __forceinline__ float4 meta4(const uint8_t* section, int lane) {   // elements 4 lane .. + 3
+  if constexpr (M16) {
+    const uint2 h = *reinterpret_cast<const uint2*>(section + 8 * lane);
+    return make_float4(half_lo_to_float(h.x), half_hi_to_float(h.x), half_lo_to_float(h.y), half_hi_to_float(h.y));
+  } else {
+    return *reinterpret_cast<const float4*>(section + 16 * lane);
+  }
+}
+
 template <int MAXS, bool M16>
 __global__ void __launch_bounds__(kIdxThreads)
     index_kernel(const __grid_constant__ IndexParams<MAXS> p, const uint8_t* __restrict__ arena) {
   using B = Blk<M16>;
-  using MR = Meta<M16>;
   grid_dependency_wait();
   allow_dependents();
   const IndexSeq sq = p.seq[blockIdx.z];
@@ -69,34 +80,32 @@ __global__ void __launch_bounds__(kIdxThreads)
   const int lane = threadIdx.x & 31;
   const int64_t at = ((int64_t)sq.slot * gridDim.y + blockIdx.y) * p.max_groups + g;
   const uint8_t* blk = arena + p.blocks_off + at * (int64_t)B::kBytes;
-  const float2 s0 = MR::two(blk + B::kKScale, 4 * lane), s1 = MR::two(blk + B::kKScale, 4 * lane + 2);
-  const float2 z0 = MR::two(blk + B::kKZero, 4 * lane), z1 = MR::two(blk + B::kKZero, 4 * lane + 2);
-  const float2 n0 = MR::two(blk + B::kKNorm, 4 * lane), n1 = MR::two(blk + B::kKNorm, 4 * lane + 2);
-  const float s[4] = {s0.x, s0.y, s1.x, s1.y};
-  const float z[4] = {z0.x, z0.y, z1.x, z1.y};
+  const float4 s4 = meta4<M16>(blk + B::kKScale, lane), z4 = meta4<M16>(blk + B::kKZero, lane),
+               n4 = meta4<M16>(blk + B::kKNorm, lane);
+  const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+  const float z[4] = {z4.x, z4.y, z4.z, z4.w};
+  const float n[4] = {fabsf(finite_or_zero(n4.x)), fabsf(finite_or_zero(n4.y)), fabsf(finite_or_zero(n4.z)),
+                      fabsf(finite_or_zero(n4.w))};
   float lo[4], hi[4], top = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    lo[i] = finite_or_zero(z[i]);
-    hi[i] = finite_or_zero(__fmaf_rn(3.0f, s[i], z[i]));
-    top = fmaxf(top, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
+  for (int c = 0; c < 4; ++c) {
+    lo[c] = finite_or_zero(z[c]);
+    hi[c] = finite_or_zero(__fmaf_rn(3.0f, s[c], z[c]));
+    top = fmaxf(top, fmaxf(fabsf(lo[c]), fabsf(hi[c])));
   }
-  const float n[4] = {finite_or_zero(n0.x), finite_or_zero(n0.y), finite_or_zero(n1.x), finite_or_zero(n1.y)};
   // non-negative floats order as their bit patterns
   const uint32_t tb = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-  const uint32_t nmax = __reduce_max_sync(
-      0xffffffffu, __float_as_uint(fmaxf(fmaxf(fabsf(n[0]), fabsf(n[1])), fmaxf(fabsf(n[2]), fabsf(n[3])))));
-  const uint32_t nmin = __reduce_min_sync(
-      0xffffffffu, __float_as_uint(fminf(fminf(fabsf(n[0]), fabsf(n[1])), fminf(fabsf(n[2]), fabsf(n[3])))));
+  const uint32_t nmax = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(n[0], n[1]), fmaxf(n[2], n[3]))));
+  const uint32_t nmin = __reduce_min_sync(0xffffffffu, __float_as_uint(fminf(fminf(n[0], n[1]), fminf(n[2], n[3]))));
   // top = m 2^x, m in [1/2, 1): 127 2^(x - 7) >= top where m <= 127/128
   int e = (int)(tb >> 23) - 126 - ((tb & 0x7fffffu) <= 0x7e0000u ? 7 : 6);
   e = tb == 0u ? kIdxMinExp : max(e, kIdxMinExp);
   const float f = exp2i(-e);
   uint32_t wl = 0, wh = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    wl |= ((uint32_t)__float2int_rn(lo[i] * f) & 0xffu) << (8 * i);
-    wh |= ((uint32_t)__float2int_rn(hi[i] * f) & 0xffu) << (8 * i);
+  for (int c = 0; c < 4; ++c) {
+    wl |= ((uint32_t)__float2int_rn(lo[c] * f) & 0xffu) << (8 * c);
+    wh |= ((uint32_t)__float2int_rn(hi[c] * f) & 0xffu) << (8 * c);
   }
   p.codes[at * 32 + lane] = make_uint2(wl, wh);
   if (lane == 0) p.weights[at] = make_float2(__uint_as_float(nmax) * exp2i(e), __uint_as_float(nmin) * exp2i(e));
@@ -528,7 +537,7 @@ cudaError_t launch_select(const SelectParams<MAXS>& params, int sms, cudaStream_
 #define OSCAR_INSTANTIATE(N)                                                                                  \
   template cudaError_t launch_index<N>(const IndexParams<N>&, const uint8_t*, bool, cudaStream_t);            \
   template cudaError_t launch_select<N>(const SelectParams<N>&, int, cudaStream_t);
-OSCAR_INSTANTIATE(kDecodeSeqsSmall)
+OSCAR_INSTANTIATE(kSelectSeqsSmall)
 OSCAR_INSTANTIATE(kDecodeSeqsLarge)
 #undef OSCAR_INSTANTIATE
 

@@ -150,8 +150,10 @@ def _check(status: int):
 
 
 def _i32(seq: Sequence[int]):
-    arr = (ctypes.c_int32 * len(seq))(*[int(x) for x in seq])
-    return arr
+    try:
+        return (ctypes.c_int32 * len(seq))(*seq)
+    except TypeError:      # entries that are not plain ints
+        return (ctypes.c_int32 * len(seq))(*[int(x) for x in seq])
 
 
 def _stream(stream) -> ctypes.c_void_p:
