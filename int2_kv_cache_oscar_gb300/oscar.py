@@ -156,21 +156,31 @@ def _i32(seq: Sequence[int]):
         return (ctypes.c_int32 * len(seq))(*[int(x) for x in seq])
 
 
-def _stream(stream) -> ctypes.c_void_p:
+_cuda_ready = False
+
+
+def _stream(stream) -> int:
+    """Handle of a torch stream, a raw handle, or (None) the current stream of
+    the current device."""
+    global _cuda_ready
     if stream is None:
-        if _raw_stream is not None and torch.cuda.is_initialized():
-            return ctypes.c_void_p(_raw_stream(_raw_device()))
+        if _raw_stream is not None and (_cuda_ready or torch.cuda.is_initialized()):
+            _cuda_ready = True
+            return _raw_stream(_raw_device())
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _dense(t, dtype, shape, name: str) -> Optional[int]:
     """Address of a caller buffer, checked as by _buf; the exact shape is
     accepted at once."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:     # not a tensor: _buf says so
+        pass
     return _buf(t, dtype, shape, name).value
 
 
@@ -467,11 +477,11 @@ def oscar_index_update(handle, seq_ids: Sequence[int], rebuild: bool = False, st
 
 def _groups(groups, n: int):
     """Address and entries per row of a group list [n, kv heads, entries]."""
-    if isinstance(groups, torch.Tensor) and groups.dim() == 3:
+    if isinstance(groups, torch.Tensor):
         shape = groups.shape
-        return _dense(groups, torch.int32, (n, shape[1], shape[2]), "groups"), shape[2]
-    _buf(groups, torch.int32, (n, None, None), "groups")
-    raise AssertionError
+        if groups.dtype is torch.int32 and len(shape) == 3 and shape[0] == n and groups.is_contiguous():
+            return groups.data_ptr(), shape[2]
+    return _buf(groups, torch.int32, (n, None, None), "groups").value, groups.shape[2]
 
 
 def oscar_select_groups(handle, seq_ids: Sequence[int], q: torch.Tensor, num_q_heads: int, groups: torch.Tensor,
