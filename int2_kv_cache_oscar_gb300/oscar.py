@@ -1,4 +1,7 @@
-"""Thin ctypes binding of liboscar.so (include/oscar.h).
+"""Thin binding of liboscar.so (include/oscar.h): ctypes, and for the calls
+made once per layer and step around the cache (rotary, reading back, group
+index and selection, decode over listed groups) the compiled _calls module
+(csrc/binding.cpp), whose argument checks take a tenth of the time.
 
 Argument marshalling only: every step of the path runs in the library's CUDA
 kernels.  Device buffers are torch tensors (PyTorch supplies device memory
@@ -11,7 +14,6 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
-import struct
 from typing import Optional, Sequence
 
 import torch
@@ -67,8 +69,11 @@ class oscar_rotary_table(ctypes.Structure):
                 ("reserved", ctypes.c_int32), ("phase", ctypes.c_uint64 * (128 // 2))]
 
 
-# oscar_rotary_rows: in, out, four strides (elements), heads
-_rotary_rows_pack = struct.Struct("@PPqqqqi4x").pack
+class oscar_rotary_rows(ctypes.Structure):
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p),
+                ("src_token_stride", ctypes.c_int64), ("src_head_stride", ctypes.c_int64),
+                ("dst_token_stride", ctypes.c_int64), ("dst_head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32)]
 
 
 def _load() -> ctypes.CDLL:
@@ -106,7 +111,8 @@ def _load() -> ctypes.CDLL:
         "oscar_rotary_frequencies": [ctypes.POINTER(oscar_rotary_config), ctypes.POINTER(ctypes.c_double),
                                      ctypes.POINTER(ctypes.c_double)],
         "oscar_rotary_prepare": [ctypes.POINTER(oscar_rotary_config), ctypes.POINTER(oscar_rotary_table)],
-        "oscar_rotary": [P, ctypes.c_int64, P, I32, ctypes.c_char_p, ctypes.c_char_p, I32, P],
+        "oscar_rotary": [P, ctypes.c_int64, P, I32, ctypes.POINTER(oscar_rotary_rows),
+                         ctypes.POINTER(oscar_rotary_rows), I32, P],
         "oscar_cache_read": [P, I32, I32P, I32P, I32P, I32, P, P, P],
         "oscar_cache_export": [P, I32, P, P, P, P],
         "oscar_cache_import": [P, I32, I32, P, P, P, P],
@@ -126,6 +132,7 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
+from int2_kv_cache_oscar_gb300 import _calls  # noqa: E402  (linked against the library just loaded)
 
 # The current stream's handle without building a Stream object (3 us a call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -171,17 +178,6 @@ def _stream(stream) -> int:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
-
-
-def _dense(t, dtype, shape, name: str) -> Optional[int]:
-    """Address of a caller buffer, checked as by _buf; the exact shape is
-    accepted at once."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:     # not a tensor: _buf says so
-        pass
-    return _buf(t, dtype, shape, name).value
 
 
 def _ptr(t: Optional[torch.Tensor]) -> ctypes.c_void_p:
@@ -337,14 +333,6 @@ def oscar_prefill_attention(handle, seq: int, q: torch.Tensor, num_q_heads: int,
                                         ctypes.c_size_t(ws_bytes), _stream(stream)))
 
 
-def _float_type(dtype, name: str) -> int:
-    if dtype == torch.bfloat16:
-        return OSCAR_BF16
-    if dtype == torch.float32:
-        return OSCAR_F32
-    raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {dtype}")
-
-
 class RotaryConfig:
     """A rotary configuration and its prepared table (keep it beside the model)."""
 
@@ -378,34 +366,6 @@ def oscar_rotary_frequencies(config: RotaryConfig):
     return [f[i] for i in range(config.rotary_dim // 2)], m.value
 
 
-def _rotary_rows(x, out, n: int, dtype, name: str) -> Optional[bytes]:
-    if x is None:
-        return None
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    shape = x.shape
-    if len(shape) != 3 or shape[0] != n or shape[2] != HEAD_DIM:
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected {(n, 'heads', HEAD_DIM)}")
-    if x.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {x.dtype}")
-    token, head, channel = x.stride()
-    if channel != 1:
-        raise ValueError(f"{name} must have contiguous channels")
-    src = x.data_ptr()
-    if out is None:
-        return _rotary_rows_pack(src, src, token, head, token, head, shape[1])
-    if not isinstance(out, torch.Tensor):
-        raise TypeError(f"{name}_out must be a torch.Tensor")
-    if out.dtype is not dtype:
-        raise ValueError(f"{name}_out must be {dtype}, got {out.dtype}")
-    if out.shape != shape:
-        raise ValueError(f"{name}_out has shape {tuple(out.shape)}, expected {tuple(shape)}")
-    out_token, out_head, channel = out.stride()
-    if channel != 1:
-        raise ValueError(f"{name}_out must have contiguous channels")
-    return _rotary_rows_pack(src, out.data_ptr(), token, head, out_token, out_head, shape[1])
-
-
 def oscar_rotary(config: RotaryConfig, positions: torch.Tensor, q: torch.Tensor,
                  k: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
                  k_out: Optional[torch.Tensor] = None, transpose: bool = False, stream=None) -> None:
@@ -413,37 +373,15 @@ def oscar_rotary(config: RotaryConfig, positions: torch.Tensor, q: torch.Tensor,
     strides with contiguous channels) by their tokens' positions (int32 [n])
     into q_out and k_out, or in place without them.  transpose: the transposed
     rotation (the gradient)."""
-    if not isinstance(q, torch.Tensor):
-        raise TypeError("q must be a torch.Tensor")
-    dtype = q.dtype
-    kind = _float_type(dtype, "q")
-    n = q.shape[0]
-    _check(_lib.oscar_rotary(config.address, n, _dense(positions, torch.int32, (n,), "positions"), kind,
-                             _rotary_rows(q, q_out, n, dtype, "q"), _rotary_rows(k, k_out, n, dtype, "k"),
-                             1 if transpose else 0, _stream(stream)))
+    _check(_calls.rotary(config.address, positions, q, k, q_out, k_out, transpose, stream))
 
 
 def oscar_cache_read(handle, seq_ids: Sequence[int], start: Sequence[int], end: Sequence[int],
-                     k_out: Optional[torch.Tensor], v_out: Optional[torch.Tensor], stream=None) -> None:
+                     k_out: Optional[torch.Tensor], v_out: Optional[torch.Tensor], stream=None, *,
+                     num_kv_heads: int = -1) -> None:
     """Tokens start[i] .. end[i] - 1 of each slot seq_ids[i] as rows of k_out
     and v_out [rows, kv heads, 128] (bf16 or float32; either may be None)."""
-    n = len(seq_ids)
-    if len(start) != n or len(end) != n:
-        raise ValueError("seq_ids, start and end must have the same length")
-    rows = sum(end) - sum(start)     # the library refuses a range that runs backwards
-    first = v_out if k_out is None else k_out
-    kind, kp, vp = OSCAR_BF16, None, None
-    if first is not None:
-        if not isinstance(first, torch.Tensor):
-            raise TypeError("k_out and v_out must be torch.Tensors")
-        dtype = first.dtype
-        kind = _float_type(dtype, "k_out" if first is k_out else "v_out")
-        shape = (rows, first.shape[1] if first.dim() == 3 else -1, HEAD_DIM)
-        if k_out is not None:
-            kp = _dense(k_out, dtype, shape, "k_out")
-        if v_out is not None:
-            vp = _dense(v_out, dtype, shape, "v_out")
-    _check(_lib.oscar_cache_read(handle, n, _i32(seq_ids), _i32(start), _i32(end), kind, kp, vp, _stream(stream)))
+    _check(_calls.read(handle, num_kv_heads, seq_ids, start, end, k_out, v_out, stream))
 
 
 def oscar_cache_export(handle, seq: int, blocks: Optional[torch.Tensor], window: Optional[torch.Tensor],
@@ -472,46 +410,25 @@ def oscar_index_attach(handle, index: Optional[torch.Tensor]) -> None:
 
 
 def oscar_index_update(handle, seq_ids: Sequence[int], rebuild: bool = False, stream=None) -> None:
-    _check(_lib.oscar_index_update(handle, len(seq_ids), _i32(seq_ids), int(bool(rebuild)), _stream(stream)))
-
-
-def _groups(groups, n: int):
-    """Address and entries per row of a group list [n, kv heads, entries]."""
-    if isinstance(groups, torch.Tensor):
-        shape = groups.shape
-        if groups.dtype is torch.int32 and len(shape) == 3 and shape[0] == n and groups.is_contiguous():
-            return groups.data_ptr(), shape[2]
-    return _buf(groups, torch.int32, (n, None, None), "groups").value, groups.shape[2]
+    _check(_calls.index_update(handle, seq_ids, rebuild, stream))
 
 
 def oscar_select_groups(handle, seq_ids: Sequence[int], q: torch.Tensor, num_q_heads: int, groups: torch.Tensor,
-                        keep_first: int = 0, keep_last: int = 0, stream=None) -> None:
+                        keep_first: int = 0, keep_last: int = 0, stream=None, *, num_kv_heads: int = -1) -> None:
     """The groups with the largest scores of each (sequence, KV head), into
     groups int32 [n_seqs, kv heads, n_select]."""
-    n = len(seq_ids)
-    gp, n_select = _groups(groups, n)
-    _check(_lib.oscar_select_groups(handle, n, _i32(seq_ids),
-                                    _dense(q, torch.bfloat16, (n, num_q_heads, HEAD_DIM), "q"), num_q_heads,
-                                    n_select, keep_first, keep_last, gp, _stream(stream)))
+    _check(_calls.select_groups(handle, num_kv_heads, seq_ids, q, num_q_heads, groups, keep_first, keep_last, stream))
 
 
 def oscar_sparse_decode_attention(handle, seq_ids: Sequence[int], q: torch.Tensor, num_q_heads: int,
                                   softmax_scale: float, groups: torch.Tensor, out: torch.Tensor,
-                                  workspace: torch.Tensor, lse: Optional[torch.Tensor] = None, stream=None) -> None:
+                                  workspace: torch.Tensor, lse: Optional[torch.Tensor] = None, stream=None, *,
+                                  num_kv_heads: int = -1) -> None:
     """Decode attention over the listed groups (int32 [n_seqs, kv heads,
     n_select], entries outside a sequence's groups are empty) and the window;
     out bf16 or float32."""
-    n = len(seq_ids)
-    shape = (n, num_q_heads, HEAD_DIM)
-    gp, n_select = _groups(groups, n)
-    if not isinstance(out, torch.Tensor):
-        raise TypeError("out must be a torch.Tensor")
-    dtype = out.dtype
-    _check(_lib.oscar_sparse_decode_attention(
-        handle, n, _i32(seq_ids), _dense(q, torch.bfloat16, shape, "q"), num_q_heads, softmax_scale, gp, n_select,
-        _float_type(dtype, "out"), _dense(out, dtype, shape, "out"),
-        None if lse is None else _dense(lse, torch.float32, (n, num_q_heads), "lse"),
-        _dense(workspace, torch.uint8, None, "workspace"), workspace.numel(), _stream(stream)))
+    _check(_calls.sparse_decode(handle, num_kv_heads, seq_ids, q, num_q_heads, softmax_scale, groups, out, workspace,
+                                lse, stream))
 
 
 def oscar_cache_bytes(handle, seq: int, kind: int) -> int:
@@ -641,9 +558,7 @@ class OscarCache:
             raise ValueError(f"{name} has {t.shape[dim]} KV heads, the cache {self.num_kv_heads}")
 
     def read(self, seq_ids, start, end, k_out=None, v_out=None, stream=None):
-        self._heads(k_out, 1, "k_out")
-        self._heads(v_out, 1, "v_out")
-        oscar_cache_read(self.handle, seq_ids, start, end, k_out, v_out, stream)
+        oscar_cache_read(self.handle, seq_ids, start, end, k_out, v_out, stream, num_kv_heads=self.num_kv_heads)
 
     @property
     def block_bytes(self) -> int:
@@ -684,11 +599,10 @@ class OscarCache:
         oscar_index_update(self.handle, seq_ids, rebuild, stream)
 
     def select_groups(self, seq_ids, q, num_q_heads, groups, keep_first=0, keep_last=0, stream=None):
-        self._heads(groups, 1, "groups")
-        oscar_select_groups(self.handle, seq_ids, q, num_q_heads, groups, keep_first, keep_last, stream)
+        oscar_select_groups(self.handle, seq_ids, q, num_q_heads, groups, keep_first, keep_last, stream,
+                            num_kv_heads=self.num_kv_heads)
 
     def sparse_decode(self, seq_ids, q, num_q_heads, groups, out, workspace, lse=None, softmax_scale=0.0,
                       stream=None):
-        self._heads(groups, 1, "groups")
         oscar_sparse_decode_attention(self.handle, seq_ids, q, num_q_heads, softmax_scale, groups, out, workspace,
-                                      lse, stream)
+                                      lse, stream, num_kv_heads=self.num_kv_heads)

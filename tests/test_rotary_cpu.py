@@ -86,7 +86,7 @@ def test_bad_configurations(O, change, status):
 def test_refusals_before_any_gpu_call(O):
     lib = O.raw_library()
     cfg = O.make_rotary_config()
-    rows = O._rotary_rows_pack(4096, 4096, 128, 128, 128, 128, 1)
+    rows = ctypes.byref(O.oscar_rotary_rows(4096, 4096, 128, 128, 128, 128, 1))
     pos = ctypes.c_void_p(4096)
     call = lambda n=1, p=pos, t=0, tr=0: lib.oscar_rotary(cfg.address, n, p, t, rows, None, tr, None)  # noqa: E731
     assert call(n=-1) == O.OSCAR_ERR_INVALID_ARG
@@ -143,6 +143,14 @@ def test_binding_refusals(O):
         O.oscar_sparse_decode_attention(None, [0], q1, 4, 0.0, groups[0], q1, torch.zeros(64, dtype=torch.uint8))
     with pytest.raises(ValueError, match="out must be"):
         O.oscar_sparse_decode_attention(None, [0], q1, 4, 0.0, groups, q1.half(), torch.zeros(64, dtype=torch.uint8))
+    with pytest.raises(TypeError, match="q must be a torch.Tensor"):
+        O.oscar_rotary(cfg, pos, [1.0])
+    with pytest.raises(TypeError):
+        O.oscar_cache_read(None, [0.5], [0], [1], None, None)
+    with pytest.raises(ValueError, match="out of range"):
+        O.oscar_cache_read(None, [2 ** 40], [0], [1], None, None)
+    with pytest.raises(ValueError, match="KV heads"):
+        O.oscar_select_groups(None, [0], q1, 4, groups, num_kv_heads=2)
     with pytest.raises(ValueError, match="same length"):
         O.oscar_cache_read(None, [0], [0, 1], [2], None, None)
     with pytest.raises(ValueError, match="shape"):
