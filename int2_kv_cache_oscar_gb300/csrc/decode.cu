@@ -755,7 +755,7 @@ __global__ void __launch_bounds__(kCombineThreads)
   const DecodeSeq sq = p.seq[b];
   const int hkv = p.h.hkv, gqa = p.h.gqa;
   const bool active = h < gqa;
-  const int ng = p.h.groups != nullptr ? row_units<true>(p, b) : units_of_len(sq.len, p.h.bf16_mode);
+  const int ng = units_of_len(sq.len, p.h.bf16_mode);
   const int wlen = p.h.bf16_mode ? 0 : (sq.len % kGroup);
   // fused append: the newest window row comes from the input (the host only
   // fuses when no group closes, so wlen >= 1); the others from the arena
@@ -920,18 +920,193 @@ __global__ void __launch_bounds__(kCombineThreads)
     }
   }
   if (active) {
-    // listed groups can leave a row without a token: zeros, log-sum-exp -inf
-    const bool none = p.h.groups != nullptr && Mh == -INFINITY;
-    const float ov = none ? 0.0f : Oh / Lh;
-    if (p.h.lse != nullptr && c == 0)
-      p.h.lse[(int64_t)b * p.h.hq + j * p.h.q_group + p.h.q_head0 + h] =
-          none ? -INFINITY : fmaf(Mh, 0.693147180559945309f, logf(Lh));
+    const float ov = Oh / Lh;
     const int64_t oi = ((int64_t)b * p.h.hq + j * p.h.q_group + p.h.q_head0 + h) * kHeadDim + c;
     if (p.h.out_f32)
       reinterpret_cast<float*>(p.h.out)[oi] = ov;
     else
       p.h.out[oi] = (uint16_t)f32_to_bf16_bits(ov);
   }
+}
+
+// ------------------------------------------------- combine, listed groups
+// One CTA of 4 warps per (sequence, query head), little shared memory: where
+// the main grid leaves room (the host sees to it while the rows are few) these
+// CTAs attend to the window beside it.  Window rows and partial records are
+// read in place, many loads in flight:
+//   window: a warp takes 32 tokens, 16 lanes a row (16 bytes each), its own
+//           softmax state;
+//   merge:  128 records at a time, thread = record for their weights; warp w
+//           then sums records w, w + 4, ... (and its window state), lane = 4
+//           channels; the first ones are requested before the weights are known.
+constexpr int kListWarps = 4;
+constexpr int kListAhead = 6;      // records of a warp requested ahead
+
+struct ListSmem {
+  alignas(16) float o[kListWarps][kHeadDim];
+  float wts[kListWarps * 32];
+  float red[2][kListWarps];
+};
+
+template <int MAXS>
+__global__ void __launch_bounds__(kListWarps * 32, 8)
+    combine_listed_kernel(const __grid_constant__ DecodeParams<MAXS> p, const uint8_t* __restrict__ arena) {
+  __shared__ ListSmem S;
+  constexpr int kThreads = kListWarps * 32;
+  const int gqa = p.h.gqa, hkv = p.h.hkv;
+  const int h = blockIdx.x % gqa;                      // query head within the group
+  const int row = blockIdx.x / gqa, b = row / hkv, j = row - b * hkv;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const DecodeSeq sq = p.seq[b];
+  const int64_t head = (int64_t)b * p.h.hq + j * p.h.q_group + p.h.q_head0 + h;
+  const int wlen = sq.len % kGroup;
+  int turn = 0;                        // of `red`
+  auto block_reduce = [&](float v, bool is_max) {
+    float* r = S.red[turn & 1];
+    ++turn;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+      const float other = __shfl_xor_sync(0xffffffffu, v, o);
+      v = is_max ? fmaxf(v, other) : v + other;
+    }
+    if (lane == 0) r[warp] = v;
+    __syncthreads();
+    return is_max ? fmaxf(fmaxf(r[0], r[1]), fmaxf(r[2], r[3])) : (r[0] + r[1]) + (r[2] + r[3]);
+  };
+
+  // ---- window (the kernels before the main one are complete: it triggers
+  // this grid only after its own wait): state of this warp's tokens
+  float mw = -INFINITY, lw = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);    // channels 4 lane .. + 3
+  if (32 * warp < wlen) {
+    const int part = lane & 15;                        // channels 8 part .. + 7 of token 32 warp + 2 i + (lane >> 4)
+    const int t0 = 32 * warp + (lane >> 4);
+    const uint4* kr = reinterpret_cast<const uint4*>(arena + p.h.windows_off +
+                                                     ((int64_t)sq.slot * hkv + j) * kWindowBytes) +
+                      t0 * (kHeadDim / 8) + part;
+    const uint4* vr = kr + kGroup * (kHeadDim / 8);
+    float q[8];
+    {
+      const uint4 u = *reinterpret_cast<const uint4*>(p.h.q + head * kHeadDim + 8 * part);
+      q[0] = bf16_lo(u.x); q[1] = bf16_hi(u.x); q[2] = bf16_lo(u.y); q[3] = bf16_hi(u.y);
+      q[4] = bf16_lo(u.z); q[5] = bf16_hi(u.z); q[6] = bf16_lo(u.w); q[7] = bf16_hi(u.w);
+    }
+    float s[16];
+#pragma unroll
+    for (int i0 = 0; i0 < 16; i0 += 8) {
+      uint4 k[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        k[i] = t0 + 2 * (i0 + i) < wlen ? kr[(i0 + i) * (2 * kHeadDim / 8)] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float a0 = q[0] * bf16_lo(k[i].x), a1 = q[1] * bf16_hi(k[i].x);
+        a0 = fmaf(q[2], bf16_lo(k[i].y), a0); a1 = fmaf(q[3], bf16_hi(k[i].y), a1);
+        a0 = fmaf(q[4], bf16_lo(k[i].z), a0); a1 = fmaf(q[5], bf16_hi(k[i].z), a1);
+        a0 = fmaf(q[6], bf16_lo(k[i].w), a0); a1 = fmaf(q[7], bf16_hi(k[i].w), a1);
+        float d = a0 + a1;
+#pragma unroll
+        for (int o = 8; o >= 1; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+        s[i0 + i] = t0 + 2 * (i0 + i) < wlen ? d * p.h.scale_log2 : -INFINITY;
+        mw = fmaxf(mw, s[i0 + i]);
+      }
+    }
+    mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, 16));
+    float o[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = 0.0f;
+#pragma unroll
+    for (int i0 = 0; i0 < 16; i0 += 8) {
+      uint4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = t0 + 2 * (i0 + i) < wlen ? vr[(i0 + i) * (2 * kHeadDim / 8)] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float pt = exp2f(s[i0 + i] - mw);        // 0 behind the window
+        lw += pt;
+        o[0] = fmaf(pt, bf16_lo(v[i].x), o[0]); o[1] = fmaf(pt, bf16_hi(v[i].x), o[1]);
+        o[2] = fmaf(pt, bf16_lo(v[i].y), o[2]); o[3] = fmaf(pt, bf16_hi(v[i].y), o[3]);
+        o[4] = fmaf(pt, bf16_lo(v[i].z), o[4]); o[5] = fmaf(pt, bf16_hi(v[i].z), o[5]);
+        o[6] = fmaf(pt, bf16_lo(v[i].w), o[6]); o[7] = fmaf(pt, bf16_hi(v[i].w), o[7]);
+      }
+    }
+    lw += __shfl_xor_sync(0xffffffffu, lw, 16);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] += __shfl_xor_sync(0xffffffffu, o[e], 16);
+    float4* dst = reinterpret_cast<float4*>(&S.o[warp][8 * part]);
+    if (lane < 16) {
+      dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+    }
+    __syncwarp();
+    acc = *reinterpret_cast<const float4*>(&S.o[warp][4 * lane]);
+  }
+  float M = block_reduce(mw, true);
+  float L = block_reduce(lane == 0 && mw != -INFINITY ? lw * exp2f(mw - M) : 0.0f, false);
+  {
+    const float f = mw == -INFINITY ? 0.0f : exp2f(mw - M);
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+  }
+
+  // ---- merge with the row's partial records
+  const int units = row_units<true>(p, b);
+  int64_t first = 0;
+  int count = 0;
+  if (units > 0) {
+    const int64_t T = p.h.n_units, N = p.h.n_ctas;
+    const int64_t U = sq.ubase + (int64_t)j * units;
+    first = cta_of_unit(U, T, N);
+    count = (int)(cta_of_unit(U + units - 1, T, N) - first) + 1;
+    first += (int64_t)hkv * sq.rank + j;
+  }
+  const float* rec = p.h.partials + (first * gqa + h) * kPartialFloats;
+  const int64_t pitch = (int64_t)gqa * kPartialFloats;
+  grid_dependency_wait();            // the main kernel's partials are complete and visible
+  allow_dependents();
+  for (int r0 = 0; r0 < count; r0 += kThreads) {
+    const int n = min(kThreads, count - r0);
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (tid < n) ml = *reinterpret_cast<const float2*>(rec + (r0 + tid) * pitch + kHeadDim);
+    const float* mine = rec + (r0 + warp) * pitch + 4 * lane;      // this warp's records: warp, warp + 4, ...
+    float4 ahead[kListAhead];
+#pragma unroll
+    for (int i = 0; i < kListAhead; ++i)
+      ahead[i] = warp + kListWarps * i < n ? *reinterpret_cast<const float4*>(mine + kListWarps * i * pitch)
+                                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float Mn = fmaxf(M, block_reduce(ml.x, true));
+    const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - Mn);
+    const float f = M == -INFINITY ? 0.0f : exp2f(M - Mn);
+    S.wts[tid] = w;                  // (the last chunk's readers have passed the barrier above)
+    L = fmaf(L, f, block_reduce(w * ml.y, false));      // (its barrier publishes the weights)
+    M = Mn;
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+    auto add = [&](int i, const float4& x) {
+      const float wi = S.wts[warp + kListWarps * i];
+      acc.x = fmaf(wi, x.x, acc.x);
+      acc.y = fmaf(wi, x.y, acc.y);
+      acc.z = fmaf(wi, x.z, acc.z);
+      acc.w = fmaf(wi, x.w, acc.w);
+    };
+#pragma unroll
+    for (int i = 0; i < kListAhead; ++i)
+      if (warp + kListWarps * i < n) add(i, ahead[i]);
+#pragma unroll 6
+    for (int i = kListAhead; warp + kListWarps * i < n; ++i)
+      add(i, *reinterpret_cast<const float4*>(mine + kListWarps * i * pitch));
+  }
+  __syncwarp();
+  *reinterpret_cast<float4*>(&S.o[warp][4 * lane]) = acc;
+  __syncthreads();
+  // a row without a token: zeros, log-sum-exp -inf
+  const bool none = M == -INFINITY;
+  const float O = (S.o[0][tid] + S.o[1][tid]) + (S.o[2][tid] + S.o[3][tid]);
+  const float ov = none ? 0.0f : O / L;
+  if (p.h.out_f32)
+    reinterpret_cast<float*>(p.h.out)[head * kHeadDim + tid] = ov;
+  else
+    p.h.out[head * kHeadDim + tid] = (uint16_t)f32_to_bf16_bits(ov);
+  if (p.h.lse != nullptr && tid == 0) p.h.lse[head] = none ? -INFINITY : fmaf(M, 0.693147180559945309f, logf(L));
 }
 
 }  // namespace
@@ -991,6 +1166,9 @@ cudaError_t launch_decode_int2(const DecodeParams<MAXS>& p, const uint8_t* arena
 
 template <int MAXS>
 cudaError_t launch_combine(const DecodeParams<MAXS>& p, const uint8_t* arena, cudaStream_t stream) {
+  if (p.h.groups != nullptr)
+    return launch_dependent(combine_listed_kernel<MAXS>, dim3((unsigned)(p.h.n_seqs * p.h.hkv * p.h.gqa)),
+                            dim3(kListWarps * 32), 0, stream, 1, p, arena);
   static bool attr_done[64] = {};
   cudaError_t e = ensure_smem_attr(combine_kernel<MAXS>, kCombineSmem, attr_done);
   if (e != cudaSuccess) return e;

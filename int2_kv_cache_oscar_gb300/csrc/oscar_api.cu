@@ -235,17 +235,16 @@ oscar_status run_decode(int device, int sms, int ctas_per_sm, int32_t n, const i
   // no more than one unit per consumer warp (4 per CTA): fewer partial records
   // and CTA launches (8K-token batch-1 step 15.3 -> 14.0 us)
   int64_t N = std::min(std::min(T, maxN), (T + 3) / 4);
-  bool windows = false;
-  for (int32_t i = 0; i < n; ++i) windows = windows || (!bf16_mode && lens[i] % kGroup != 0);
   if (n_sel > 0) {
-    // Listed groups: as many CTAs per row as give each consumer warp one entry
-    // (4 a CTA; with two head sets 2), so that no CTA works on two rows (1 of
-    // 1,024 groups, 8 rows: 19.7 -> 7.6 us; 64 of them for 8 query heads a KV
-    // head: 13.1 -> 10.2 us).  Where those are more than fit, one slot per row
-    // is left free for the combine, whose window part then overlaps (152
-    // groups and a window: 14.2 -> 11.4 us).
-    const int64_t per_row = (n_sel + (q_group > kMaxGqa ? 1 : 3)) / (q_group > kMaxGqa ? 2 : 4);
-    const int64_t most = windows && rows <= maxN / 8 ? maxN - rows : maxN;
+    // Listed groups: as many CTAs per row as give each consumer warp one entry,
+    // so that no CTA works on two rows (1 of 1,024 groups, 8 rows: 19.7 -> 6.8 us)
+    const int64_t per_row = (n_sel + 3) / 4;
+    // Few rows with windows: slots are left free for the combine's CTAs (one
+    // per query head, four to a slot), which attend to the windows meanwhile.
+    bool windows = false;
+    for (int32_t i = 0; i < n; ++i) windows = windows || lens[i] % kGroup != 0;
+    const int64_t room = windows ? ((int64_t)n * hkv * std::min(q_group, kMaxGqaInt2) + 3) / 4 : 0;
+    const int64_t most = room <= maxN / 8 ? maxN - room : maxN;
     N = rows * per_row <= most ? rows * per_row : std::min(T, most);
   }
   const int max_gqa = bf16_mode ? kMaxGqa : kMaxGqaInt2;   // query heads per KV head in one launch
@@ -302,8 +301,7 @@ oscar_status run_decode(int device, int sms, int ctas_per_sm, int32_t n, const i
   // GPU has SMs: several then share an SM once the main grid is gone.  With
   // fewer, the full size keeps combine CTAs off SMs where a main CTA still runs
   // (measured: sharing one slows short contexts, 8K 15.3 -> 16.4 us).
-  // Listed groups: sized too, so that a combine CTA fits beside a main CTA.
-  const bool pack = (int64_t)n * hkv > sms || n_sel > 0;
+  const bool pack = (int64_t)n * hkv > sms;
   P.h.comb_wrows = pack ? (wrows + 7) & ~7 : kGroup;   // multiples of 8 rows keep 16-byte alignment
   for (int head0 = 0; head0 < q_group; head0 += max_gqa) {
     P.h.gqa = q_group - head0 < max_gqa ? q_group - head0 : max_gqa;
