@@ -930,123 +930,276 @@ __global__ void __launch_bounds__(kCombineThreads)
 }
 
 // ------------------------------------------------- combine, listed groups
-// One CTA of 4 warps per (sequence, query head), little shared memory: where
-// the main grid leaves room (the host sees to it while the rows are few) these
-// CTAs attend to the window beside it.  Window rows and partial records are
-// read in place, many loads in flight:
-//   window: a warp takes 32 tokens, 16 lanes a row (16 bytes each), its own
-//           softmax state;
-//   merge:  128 records at a time, thread = record for their weights; warp w
-//           then sums records w, w + 4, ... (and its window state), lane = 4
-//           channels; the first ones are requested before the weights are known.
-constexpr int kListWarps = 4;
+// Attends to the bf16 window and merges a row's partial records, 4 warps per
+// query head: records are read in place, 128 at a time, thread = record for
+// their weights; warp `sub` of a head then sums records sub, sub + 4, ..., lane
+// = 4 channels; the first ones are requested before the weights are known.
+//
+// Two forms, for where the window is attended to:
+//   a CTA per query head (ROW false): 64 registers and 128 threads, four fit
+//     where a main CTA would, and the host leaves such places free while the
+//     CTAs are few: the window costs nothing then.  Window rows are read in
+//     place; a warp takes 32 tokens, 16 lanes a row (16 bytes each).
+//   a CTA per KV head (ROW true), where they are many and run after the main
+//     grid: the window is staged once for all heads (one copy's latency) and
+//     attended to on the tensor cores.
+//     scores: warp w < 8 takes tokens 16 w .. + 15, S = K Q^T, m16n8k16, columns
+//             = the heads; K fragments straight from the staged rows (16 bytes a
+//             lane: the channels in any order, the same for K and Q);
+//     values: warps w < 8 share the channels, O^T = V^T P^T over the token tiles
+//             (ldmatrix.trans), p in three bf16 terms (24 bits).
+// Step with a 77-token window, 4 query heads a KV head, the first form against
+// the second: 8 rows of 152 entries 10.5 / 13.1 us, 32 rows of 20 9.2 / 11.2 us,
+// 64 rows of 32 19.2 / 15.9 us, 128 rows of 17 21.9 / 18.4 us; without windows
+// the first is never slower (128 rows of 16: 13.5 / 13.9 us).
 constexpr int kListAhead = 6;      // records of a warp requested ahead
+constexpr int kListHeads = 4;      // warps of a head
 
+// Per-head shared state of `HEADS` heads.
+template <int HEADS>
 struct ListSmem {
-  alignas(16) float o[kListWarps][kHeadDim];
-  float wts[kListWarps * 32];
-  float red[2][kListWarps];
+  alignas(16) float o[HEADS * kListHeads][kHeadDim];       // a warp's sum of records (window outputs before)
+  float wts[HEADS][kListHeads * 32];
+  float red[2][HEADS][kListHeads];
+};
+struct WindowSmem {
+  alignas(16) float o[kMaxGqaInt2][kHeadDim];
+  float p[kGroup][kMaxGqaInt2];                             // window weights
+  float mx[8][kMaxGqaInt2], sum[8][kMaxGqaInt2];            // per token tile
+  alignas(8) uint64_t bar;
+  int abort_flag;
 };
 
-template <int MAXS>
-__global__ void __launch_bounds__(kListWarps * 32, 8)
+template <int MAXS, bool ROW>
+__global__ void __launch_bounds__(ROW ? 128 * kMaxGqaInt2 : 128, ROW ? 1 : 8)
     combine_listed_kernel(const __grid_constant__ DecodeParams<MAXS> p, const uint8_t* __restrict__ arena) {
-  __shared__ ListSmem S;
-  constexpr int kThreads = kListWarps * 32;
+  extern __shared__ __align__(128) uint8_t smem_raw[];      // ROW: window keys [16 tiles][128], values (bf16)
+  __shared__ ListSmem<ROW ? kMaxGqaInt2 : 1> S;
   const int gqa = p.h.gqa, hkv = p.h.hkv;
-  const int h = blockIdx.x % gqa;                      // query head within the group
-  const int row = blockIdx.x / gqa, b = row / hkv, j = row - b * hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int hl = ROW ? warp / kListHeads : 0;              // this warp's head within the CTA
+  const int sub = warp % kListHeads;
+  const int row = ROW ? (int)blockIdx.x : (int)blockIdx.x / gqa;
+  const int h = ROW ? hl : (int)blockIdx.x - row * gqa;    // and within the group
+  const int b = row / hkv, j = row - b * hkv;
   const DecodeSeq sq = p.seq[b];
-  const int64_t head = (int64_t)b * p.h.hq + j * p.h.q_group + p.h.q_head0 + h;
+  const int64_t head0 = (int64_t)b * p.h.hq + j * p.h.q_group + p.h.q_head0;
+  const int64_t head = head0 + h;
   const int wlen = sq.len % kGroup;
   int turn = 0;                        // of `red`
-  auto block_reduce = [&](float v, bool is_max) {
-    float* r = S.red[turn & 1];
+  auto head_reduce = [&](float v, bool is_max) {           // over the 4 warps of a head (the whole CTA calls it)
+    float* r = S.red[turn & 1][hl];
     ++turn;
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) {
       const float other = __shfl_xor_sync(0xffffffffu, v, o);
       v = is_max ? fmaxf(v, other) : v + other;
     }
-    if (lane == 0) r[warp] = v;
+    if (lane == 0) r[sub] = v;
     __syncthreads();
     return is_max ? fmaxf(fmaxf(r[0], r[1]), fmaxf(r[2], r[3])) : (r[0] + r[1]) + (r[2] + r[3]);
   };
 
   // ---- window (the kernels before the main one are complete: it triggers
-  // this grid only after its own wait): state of this warp's tokens
-  float mw = -INFINITY, lw = 0.0f;
+  // this grid only after its own wait): this warp's share of the outputs, the
+  // head's largest score M and weight L
+  float M = -INFINITY, L = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);    // channels 4 lane .. + 3
-  if (32 * warp < wlen) {
-    const int part = lane & 15;                        // channels 8 part .. + 7 of token 32 warp + 2 i + (lane >> 4)
-    const int t0 = 32 * warp + (lane >> 4);
-    const uint4* kr = reinterpret_cast<const uint4*>(arena + p.h.windows_off +
-                                                     ((int64_t)sq.slot * hkv + j) * kWindowBytes) +
-                      t0 * (kHeadDim / 8) + part;
-    const uint4* vr = kr + kGroup * (kHeadDim / 8);
-    float q[8];
+  if constexpr (!ROW) {
+    float mw = -INFINITY, lw = 0.0f;
+    if (32 * warp < wlen) {
+      const int part = lane & 15;                        // channels 8 part .. + 7 of token 32 warp + 2 i + (lane >> 4)
+      const int t0 = 32 * warp + (lane >> 4);
+      const uint4* kr = reinterpret_cast<const uint4*>(arena + p.h.windows_off +
+                                                       ((int64_t)sq.slot * hkv + j) * kWindowBytes) +
+                        t0 * (kHeadDim / 8) + part;
+      const uint4* vr = kr + kGroup * (kHeadDim / 8);
+      float q[8];
+      {
+        const uint4 u = *reinterpret_cast<const uint4*>(p.h.q + head * kHeadDim + 8 * part);
+        q[0] = bf16_lo(u.x); q[1] = bf16_hi(u.x); q[2] = bf16_lo(u.y); q[3] = bf16_hi(u.y);
+        q[4] = bf16_lo(u.z); q[5] = bf16_hi(u.z); q[6] = bf16_lo(u.w); q[7] = bf16_hi(u.w);
+      }
+      float s[16];
+#pragma unroll
+      for (int i0 = 0; i0 < 16; i0 += 8) {
+        uint4 k[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          k[i] = t0 + 2 * (i0 + i) < wlen ? kr[(i0 + i) * (2 * kHeadDim / 8)] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float a0 = q[0] * bf16_lo(k[i].x), a1 = q[1] * bf16_hi(k[i].x);
+          a0 = fmaf(q[2], bf16_lo(k[i].y), a0); a1 = fmaf(q[3], bf16_hi(k[i].y), a1);
+          a0 = fmaf(q[4], bf16_lo(k[i].z), a0); a1 = fmaf(q[5], bf16_hi(k[i].z), a1);
+          a0 = fmaf(q[6], bf16_lo(k[i].w), a0); a1 = fmaf(q[7], bf16_hi(k[i].w), a1);
+          float d = a0 + a1;
+#pragma unroll
+          for (int o = 8; o >= 1; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+          s[i0 + i] = t0 + 2 * (i0 + i) < wlen ? d * p.h.scale_log2 : -INFINITY;
+          mw = fmaxf(mw, s[i0 + i]);
+        }
+      }
+      mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, 16));
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = 0.0f;
+#pragma unroll
+      for (int i0 = 0; i0 < 16; i0 += 8) {
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          v[i] = t0 + 2 * (i0 + i) < wlen ? vr[(i0 + i) * (2 * kHeadDim / 8)] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float pt = exp2f(s[i0 + i] - mw);        // 0 behind the window
+          lw += pt;
+          o[0] = fmaf(pt, bf16_lo(v[i].x), o[0]); o[1] = fmaf(pt, bf16_hi(v[i].x), o[1]);
+          o[2] = fmaf(pt, bf16_lo(v[i].y), o[2]); o[3] = fmaf(pt, bf16_hi(v[i].y), o[3]);
+          o[4] = fmaf(pt, bf16_lo(v[i].z), o[4]); o[5] = fmaf(pt, bf16_hi(v[i].z), o[5]);
+          o[6] = fmaf(pt, bf16_lo(v[i].w), o[6]); o[7] = fmaf(pt, bf16_hi(v[i].w), o[7]);
+        }
+      }
+      lw += __shfl_xor_sync(0xffffffffu, lw, 16);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] += __shfl_xor_sync(0xffffffffu, o[e], 16);
+      float4* dst = reinterpret_cast<float4*>(&S.o[warp][8 * part]);
+      if (lane < 16) {
+        dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+      }
+      __syncwarp();
+      acc = *reinterpret_cast<const float4*>(&S.o[warp][4 * lane]);
+    }
+    M = head_reduce(mw, true);
+    L = head_reduce(lane == 0 && mw != -INFINITY ? lw * exp2f(mw - M) : 0.0f, false);
     {
-      const uint4 u = *reinterpret_cast<const uint4*>(p.h.q + head * kHeadDim + 8 * part);
-      q[0] = bf16_lo(u.x); q[1] = bf16_hi(u.x); q[2] = bf16_lo(u.y); q[3] = bf16_hi(u.y);
-      q[4] = bf16_lo(u.z); q[5] = bf16_hi(u.z); q[6] = bf16_lo(u.w); q[7] = bf16_hi(u.w);
+      const float f = mw == -INFINITY ? 0.0f : exp2f(mw - M);
+      acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
     }
-    float s[16];
-#pragma unroll
-    for (int i0 = 0; i0 < 16; i0 += 8) {
-      uint4 k[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        k[i] = t0 + 2 * (i0 + i) < wlen ? kr[(i0 + i) * (2 * kHeadDim / 8)] : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float a0 = q[0] * bf16_lo(k[i].x), a1 = q[1] * bf16_hi(k[i].x);
-        a0 = fmaf(q[2], bf16_lo(k[i].y), a0); a1 = fmaf(q[3], bf16_hi(k[i].y), a1);
-        a0 = fmaf(q[4], bf16_lo(k[i].z), a0); a1 = fmaf(q[5], bf16_hi(k[i].z), a1);
-        a0 = fmaf(q[6], bf16_lo(k[i].w), a0); a1 = fmaf(q[7], bf16_hi(k[i].w), a1);
-        float d = a0 + a1;
-#pragma unroll
-        for (int o = 8; o >= 1; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-        s[i0 + i] = t0 + 2 * (i0 + i) < wlen ? d * p.h.scale_log2 : -INFINITY;
-        mw = fmaxf(mw, s[i0 + i]);
+  } else {
+    __shared__ WindowSmem W;
+    const int tiles = (wlen + 15) / 16, g = lane >> 2, tig = lane & 3;
+    const uint8_t* wk = smem_raw;
+    const uint8_t* wv = smem_raw + tiles * 16 * kHeadDim * 2;
+    if (wlen > 0) {
+      if (tid == 0) {
+        mbar_init(&W.bar, 1);
+        W.abort_flag = 0;
+        fence_mbar_init();
+        const uint32_t bytes = (uint32_t)wlen * kHeadDim * 2;
+        const uint8_t* src = arena + p.h.windows_off + ((int64_t)sq.slot * hkv + j) * kWindowBytes;
+        mbar_arrive_expect_tx(&W.bar, 2 * bytes);
+        bulk_g2s(smem_raw, src, bytes, &W.bar);
+        bulk_g2s(smem_raw + tiles * 16 * kHeadDim * 2, src + kGroup * kHeadDim * 2, bytes, &W.bar);
       }
-    }
-    mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, 16));
-    float o[8];
+      __syncthreads();
+      mbar_wait_bounded(&W.bar, 0, &W.abort_flag, p.h.err_word);
+      const int warps = min(8, kListHeads * gqa);
+      // scores of tokens 16 t + g (s[0], s[1]: heads 2 tig, + 1) and + 8 (s[2], s[3])
+      uint4 qv[4];                             // head g, channels 32 i + 8 tig .. + 7
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = 0.0f;
+      for (int i = 0; i < 4; ++i)
+        qv[i] = g < gqa && warp < warps ? *reinterpret_cast<const uint4*>(p.h.q + (head0 + g) * kHeadDim + 32 * i + 8 * tig)
+                                        : make_uint4(0u, 0u, 0u, 0u);
+      if (warp < warps) {
+        for (int t = warp; t < tiles; t += warps) {
+          float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i0 = 0; i0 < 16; i0 += 8) {
-      uint4 v[8];
+          for (int i = 0; i < 4; ++i) {
+            const uint4 ka = *reinterpret_cast<const uint4*>(wk + (16 * t + g) * 256 + 64 * i + 16 * tig);
+            const uint4 kb = *reinterpret_cast<const uint4*>(wk + (16 * t + g + 8) * 256 + 64 * i + 16 * tig);
+            mma_bf16_16816(s, ka.x, kb.x, ka.y, kb.y, qv[i].x, qv[i].y);
+            mma_bf16_16816(s, ka.z, kb.z, ka.w, kb.w, qv[i].z, qv[i].w);
+          }
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] = t0 + 2 * (i0 + i) < wlen ? vr[(i0 + i) * (2 * kHeadDim / 8)] : make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < 4; ++i)          // (rows behind the window: whatever the stage holds)
+            s[i] = 16 * t + g + 8 * (i >> 1) < wlen ? s[i] * p.h.scale_log2 : -INFINITY;
+          *reinterpret_cast<float2*>(&W.p[16 * t + g][2 * tig]) = make_float2(s[0], s[1]);
+          *reinterpret_cast<float2*>(&W.p[16 * t + g + 8][2 * tig]) = make_float2(s[2], s[3]);
+          float m0 = fmaxf(s[0], s[2]), m1 = fmaxf(s[1], s[3]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float pt = exp2f(s[i0 + i] - mw);        // 0 behind the window
-        lw += pt;
-        o[0] = fmaf(pt, bf16_lo(v[i].x), o[0]); o[1] = fmaf(pt, bf16_hi(v[i].x), o[1]);
-        o[2] = fmaf(pt, bf16_lo(v[i].y), o[2]); o[3] = fmaf(pt, bf16_hi(v[i].y), o[3]);
-        o[4] = fmaf(pt, bf16_lo(v[i].z), o[4]); o[5] = fmaf(pt, bf16_hi(v[i].z), o[5]);
-        o[6] = fmaf(pt, bf16_lo(v[i].w), o[6]); o[7] = fmaf(pt, bf16_hi(v[i].w), o[7]);
+          for (int o = 4; o <= 16; o <<= 1) {
+            m0 = fmaxf(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+          }
+          if (g == 0) {
+            W.mx[t][2 * tig] = m0;
+            W.mx[t][2 * tig + 1] = m1;
+          }
+        }
       }
-    }
-    lw += __shfl_xor_sync(0xffffffffu, lw, 16);
+      __syncthreads();
+      if (warp < warps) {
+        float M0 = -INFINITY, M1 = -INFINITY;
+        for (int t = 0; t < tiles; ++t) {
+          M0 = fmaxf(M0, W.mx[t][2 * tig]);
+          M1 = fmaxf(M1, W.mx[t][2 * tig + 1]);
+        }
+        for (int t = warp; t < tiles; t += warps) {
+          float l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] += __shfl_xor_sync(0xffffffffu, o[e], 16);
-    float4* dst = reinterpret_cast<float4*>(&S.o[warp][8 * part]);
-    if (lane < 16) {
-      dst[0] = make_float4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_float4(o[4], o[5], o[6], o[7]);
+          for (int i = 0; i < 2; ++i) {
+            float2* x = reinterpret_cast<float2*>(&W.p[16 * t + g + 8 * i][2 * tig]);
+            const float2 w = make_float2(exp2f(x->x - M0), exp2f(x->y - M1));
+            *x = w;
+            l0 += w.x;
+            l1 += w.y;
+          }
+#pragma unroll
+          for (int o = 4; o <= 16; o <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+          }
+          if (g == 0) {
+            W.sum[t][2 * tig] = l0;
+            W.sum[t][2 * tig + 1] = l1;
+          }
+        }
+      }
+      __syncthreads();
+      for (int t = 0; t < tiles; ++t) {        // this warp's head
+        M = fmaxf(M, W.mx[t][hl]);
+        L += W.sum[t][hl];
+      }
+      if (warp < warps) {
+        for (int ct = warp; ct < 8; ct += warps) {   // channels 16 ct + g (c[0], c[1]: heads 2 tig, + 1), + 8
+          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          const uint32_t vaddr =
+              smem_u32(wv) + ((lane & 7) + 8 * (lane >> 4)) * 256 + ((lane >> 3) & 1) * 16 + 32 * ct;
+          for (int t = 0; t < tiles; ++t) {
+            uint32_t v0, v1, v2, v3;
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(v0), "=r"(v1), "=r"(v2), "=r"(v3)
+                         : "r"(vaddr + t * 16 * 256));
+            const int n = wlen - 16 * t;       // rows behind the window hold whatever the stage held: cleared
+            const uint32_t mlo = (2 * tig < n ? 0xffffu : 0u) | (2 * tig + 1 < n ? 0xffff0000u : 0u);
+            const uint32_t mhi = (2 * tig + 8 < n ? 0xffffu : 0u) | (2 * tig + 9 < n ? 0xffff0000u : 0u);
+            v0 &= mlo;
+            v1 &= mlo;
+            v2 &= mhi;
+            v3 &= mhi;
+            const float* pt = &W.p[16 * t + 2 * tig][g];      // tokens 2 tig, + 1, + 8, + 9 of head g
+            float x[4] = {pt[0], pt[kMaxGqaInt2], pt[8 * kMaxGqaInt2], pt[9 * kMaxGqaInt2]};
+#pragma unroll
+            for (int term = 0; term < 3; ++term) {
+              const uint32_t b0 = pack_bf16x2(x[0], x[1]), b1 = pack_bf16x2(x[2], x[3]);
+              mma_bf16_16816(c, v0, v1, v2, v3, b0, b1);
+              x[0] -= bf16_lo(b0);
+              x[1] -= bf16_hi(b0);
+              x[2] -= bf16_lo(b1);
+              x[3] -= bf16_hi(b1);
+            }
+          }
+          W.o[2 * tig][16 * ct + g] = c[0];
+          W.o[2 * tig + 1][16 * ct + g] = c[1];
+          W.o[2 * tig][16 * ct + g + 8] = c[2];
+          W.o[2 * tig + 1][16 * ct + g + 8] = c[3];
+        }
+      }
+      __syncthreads();
+      if (sub == 0) acc = *reinterpret_cast<const float4*>(&W.o[hl][4 * lane]);
     }
-    __syncwarp();
-    acc = *reinterpret_cast<const float4*>(&S.o[warp][4 * lane]);
-  }
-  float M = block_reduce(mw, true);
-  float L = block_reduce(lane == 0 && mw != -INFINITY ? lw * exp2f(mw - M) : 0.0f, false);
-  {
-    const float f = mw == -INFINITY ? 0.0f : exp2f(mw - M);
-    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
   }
 
   // ---- merge with the row's partial records
@@ -1060,29 +1213,31 @@ __global__ void __launch_bounds__(kListWarps * 32, 8)
     count = (int)(cta_of_unit(U + units - 1, T, N) - first) + 1;
     first += (int64_t)hkv * sq.rank + j;
   }
+  constexpr int kChunk = kListHeads * 32;
   const float* rec = p.h.partials + (first * gqa + h) * kPartialFloats;
   const int64_t pitch = (int64_t)gqa * kPartialFloats;
+  const int at = 32 * sub + lane;    // this thread's record of a chunk
   grid_dependency_wait();            // the main kernel's partials are complete and visible
   allow_dependents();
-  for (int r0 = 0; r0 < count; r0 += kThreads) {
-    const int n = min(kThreads, count - r0);
+  for (int r0 = 0; r0 < count; r0 += kChunk) {
+    const int n = min(kChunk, count - r0);
     float2 ml = make_float2(-INFINITY, 0.0f);
-    if (tid < n) ml = *reinterpret_cast<const float2*>(rec + (r0 + tid) * pitch + kHeadDim);
-    const float* mine = rec + (r0 + warp) * pitch + 4 * lane;      // this warp's records: warp, warp + 4, ...
+    if (at < n) ml = *reinterpret_cast<const float2*>(rec + (r0 + at) * pitch + kHeadDim);
+    const float* mine = rec + (r0 + sub) * pitch + 4 * lane;       // this warp's records: sub, sub + 4, ...
     float4 ahead[kListAhead];
 #pragma unroll
     for (int i = 0; i < kListAhead; ++i)
-      ahead[i] = warp + kListWarps * i < n ? *reinterpret_cast<const float4*>(mine + kListWarps * i * pitch)
-                                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const float Mn = fmaxf(M, block_reduce(ml.x, true));
+      ahead[i] = sub + kListHeads * i < n ? *reinterpret_cast<const float4*>(mine + kListHeads * i * pitch)
+                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float Mn = fmaxf(M, head_reduce(ml.x, true));
     const float w = ml.x == -INFINITY ? 0.0f : exp2f(ml.x - Mn);
     const float f = M == -INFINITY ? 0.0f : exp2f(M - Mn);
-    S.wts[tid] = w;                  // (the last chunk's readers have passed the barrier above)
-    L = fmaf(L, f, block_reduce(w * ml.y, false));      // (its barrier publishes the weights)
+    S.wts[hl][at] = w;               // (the last chunk's readers have passed the barrier above)
+    L = fmaf(L, f, head_reduce(w * ml.y, false));      // (its barrier publishes the weights)
     M = Mn;
     acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
     auto add = [&](int i, const float4& x) {
-      const float wi = S.wts[warp + kListWarps * i];
+      const float wi = S.wts[hl][sub + kListHeads * i];
       acc.x = fmaf(wi, x.x, acc.x);
       acc.y = fmaf(wi, x.y, acc.y);
       acc.z = fmaf(wi, x.z, acc.z);
@@ -1090,23 +1245,24 @@ __global__ void __launch_bounds__(kListWarps * 32, 8)
     };
 #pragma unroll
     for (int i = 0; i < kListAhead; ++i)
-      if (warp + kListWarps * i < n) add(i, ahead[i]);
+      if (sub + kListHeads * i < n) add(i, ahead[i]);
 #pragma unroll 6
-    for (int i = kListAhead; warp + kListWarps * i < n; ++i)
-      add(i, *reinterpret_cast<const float4*>(mine + kListWarps * i * pitch));
+    for (int i = kListAhead; sub + kListHeads * i < n; ++i)
+      add(i, *reinterpret_cast<const float4*>(mine + kListHeads * i * pitch));
   }
   __syncwarp();
   *reinterpret_cast<float4*>(&S.o[warp][4 * lane]) = acc;
   __syncthreads();
   // a row without a token: zeros, log-sum-exp -inf
   const bool none = M == -INFINITY;
-  const float O = (S.o[0][tid] + S.o[1][tid]) + (S.o[2][tid] + S.o[3][tid]);
+  const float(*o)[kHeadDim] = &S.o[kListHeads * hl];
+  const float O = (o[0][at] + o[1][at]) + (o[2][at] + o[3][at]);
   const float ov = none ? 0.0f : O / L;
   if (p.h.out_f32)
-    reinterpret_cast<float*>(p.h.out)[head * kHeadDim + tid] = ov;
+    reinterpret_cast<float*>(p.h.out)[head * kHeadDim + at] = ov;
   else
-    p.h.out[head * kHeadDim + tid] = (uint16_t)f32_to_bf16_bits(ov);
-  if (p.h.lse != nullptr && tid == 0) p.h.lse[head] = none ? -INFINITY : fmaf(M, 0.693147180559945309f, logf(L));
+    p.h.out[head * kHeadDim + at] = (uint16_t)f32_to_bf16_bits(ov);
+  if (p.h.lse != nullptr && at == 0) p.h.lse[head] = none ? -INFINITY : fmaf(M, 0.693147180559945309f, logf(L));
 }
 
 }  // namespace
@@ -1166,9 +1322,17 @@ cudaError_t launch_decode_int2(const DecodeParams<MAXS>& p, const uint8_t* arena
 
 template <int MAXS>
 cudaError_t launch_combine(const DecodeParams<MAXS>& p, const uint8_t* arena, cudaStream_t stream) {
-  if (p.h.groups != nullptr)
-    return launch_dependent(combine_listed_kernel<MAXS>, dim3((unsigned)(p.h.n_seqs * p.h.hkv * p.h.gqa)),
-                            dim3(kListWarps * 32), 0, stream, 1, p, arena);
+  if (p.h.groups != nullptr) {
+    const unsigned rows = (unsigned)(p.h.n_seqs * p.h.hkv);
+    if (!p.h.comb_row)
+      return launch_dependent(combine_listed_kernel<MAXS, false>, dim3(rows * p.h.gqa), dim3(128), 0, stream, 1, p, arena);
+    static bool listed_done[64] = {};
+    const cudaError_t el = ensure_smem_attr(combine_listed_kernel<MAXS, true>, kWindowBytes, listed_done);
+    if (el != cudaSuccess) return el;
+    // comb_wrows: the longest window of the batch, in whole tiles of 16 tokens
+    return launch_dependent(combine_listed_kernel<MAXS, true>, dim3(rows), dim3(128 * p.h.gqa),
+                            (size_t)2 * p.h.comb_wrows * kHeadDim * 2, stream, 1, p, arena);
+  }
   static bool attr_done[64] = {};
   cudaError_t e = ensure_smem_attr(combine_kernel<MAXS>, kCombineSmem, attr_done);
   if (e != cudaSuccess) return e;

@@ -134,6 +134,7 @@ struct DecodeHeader {
   // the sequence) is skipped (NULL: a row's units are its groups)
   const int32_t* groups;
   int32_t n_sel;
+  int32_t comb_row;      // listed groups: the combine's CTAs take a KV head (else a query head)
   float* lse;            // [n_seqs, hq] natural-log log-sum-exp of the rows, or NULL
 };
 

@@ -236,16 +236,27 @@ oscar_status run_decode(int device, int sms, int ctas_per_sm, int32_t n, const i
   // and CTA launches (8K-token batch-1 step 15.3 -> 14.0 us)
   int64_t N = std::min(std::min(T, maxN), (T + 3) / 4);
   if (n_sel > 0) {
-    // Listed groups: as many CTAs per row as give each consumer warp one entry,
-    // so that no CTA works on two rows (1 of 1,024 groups, 8 rows: 19.7 -> 6.8 us)
-    const int64_t per_row = (n_sel + 3) / 4;
-    // Few rows with windows: slots are left free for the combine's CTAs (one
-    // per query head, four to a slot), which attend to the windows meanwhile.
+    // Listed groups: the same number of CTAs for every row, so that none works
+    // on two rows, as few as give each consumer warp (a pair of them with two
+    // head sets) r entries, for the smallest r that fits.  128 rows of 16
+    // entries: 13.5 us, 17.4 split evenly over all places; 1 entry, 8 rows: 7.0
+    // against 19.7 with a CTA per 4 entries whatever their rows.
     bool windows = false;
     for (int32_t i = 0; i < n; ++i) windows = windows || lens[i] % kGroup != 0;
-    const int64_t room = windows ? ((int64_t)n * hkv * std::min(q_group, kMaxGqaInt2) + 3) / 4 : 0;
-    const int64_t most = room <= maxN / 8 ? maxN - room : maxN;
-    N = rows * per_row <= most ? rows * per_row : std::min(T, most);
+    // many query heads with windows: see combine_listed_kernel; few: places are
+    // left for the combine's CTAs, four to a main CTA's
+    const int64_t heads = (int64_t)n * hkv * std::min(q_group, kMaxGqaInt2);
+    P.h.comb_row = windows && heads > sms + sms / 2;
+    const int64_t room = (heads + 3) / 4;
+    const int64_t most = windows && room <= maxN / 8 ? maxN - room : maxN;
+    const int64_t per = q_group > kMaxGqa ? 2 : 4;
+    const auto per_row = [&](int64_t r) { return (n_sel + r * per - 1) / (r * per); };
+    int64_t r = 1;
+    while (r * per < n_sel && rows * per_row(r) > most) ++r;
+    N = rows * per_row(r);
+    // an even split where whole CTAs per row would leave too many places empty
+    // (256 rows of 64 entries: 64.5 us, 68.5 with 256 CTAs of 304)
+    if (N > maxN || r > T / (per * maxN) + 2) N = std::min(T, maxN);
   }
   const int max_gqa = bf16_mode ? kMaxGqa : kMaxGqaInt2;   // query heads per KV head in one launch
   const size_t need = partial_bytes(N + rows, q_group < max_gqa ? q_group : max_gqa);
@@ -302,7 +313,7 @@ oscar_status run_decode(int device, int sms, int ctas_per_sm, int32_t n, const i
   // fewer, the full size keeps combine CTAs off SMs where a main CTA still runs
   // (measured: sharing one slows short contexts, 8K 15.3 -> 16.4 us).
   const bool pack = (int64_t)n * hkv > sms;
-  P.h.comb_wrows = pack ? (wrows + 7) & ~7 : kGroup;   // multiples of 8 rows keep 16-byte alignment
+  P.h.comb_wrows = n_sel > 0 ? (wrows + 15) & ~15 : pack ? (wrows + 7) & ~7 : kGroup;   // whole 16-byte (tile) rows
   for (int head0 = 0; head0 < q_group; head0 += max_gqa) {
     P.h.gqa = q_group - head0 < max_gqa ? q_group - head0 : max_gqa;
     P.h.q_head0 = head0;
