@@ -948,10 +948,10 @@ __global__ void __launch_bounds__(kCombineThreads)
 //             lane: the channels in any order, the same for K and Q);
 //     values: warps w < 8 share the channels, O^T = V^T P^T over the token tiles
 //             (ldmatrix.trans), p in three bf16 terms (24 bits).
-// Step with a 77-token window, 4 query heads a KV head, the first form against
-// the second: 8 rows of 152 entries 10.5 / 13.1 us, 32 rows of 20 9.2 / 11.2 us,
-// 64 rows of 32 19.2 / 15.9 us, 128 rows of 17 21.9 / 18.4 us; without windows
-// the first is never slower (128 rows of 16: 13.5 / 13.9 us).
+// The first form against the second, 4 query heads a KV head: with a 77-token
+// window 8 rows of 152 entries 10.5 / 13.1 us, 32 rows of 20 9.2 / 11.2 us, 64
+// rows of 32 19.2 / 15.9 us, 128 rows of 17 21.9 / 18.0 us; without windows 256
+// rows of 64 63.2 / 58.3 us.
 constexpr int kListAhead = 6;      // records of a warp requested ahead
 constexpr int kListHeads = 4;      // warps of a head
 

@@ -243,10 +243,10 @@ oscar_status run_decode(int device, int sms, int ctas_per_sm, int32_t n, const i
     // against 19.7 with a CTA per 4 entries whatever their rows.
     bool windows = false;
     for (int32_t i = 0; i < n; ++i) windows = windows || lens[i] % kGroup != 0;
-    // many query heads with windows: see combine_listed_kernel; few: places are
-    // left for the combine's CTAs, four to a main CTA's
+    // many query heads: see combine_listed_kernel; few, with windows: places
+    // are left for the combine's CTAs, four to a main CTA's
     const int64_t heads = (int64_t)n * hkv * std::min(q_group, kMaxGqaInt2);
-    P.h.comb_row = windows && heads > sms + sms / 2;
+    P.h.comb_row = heads > sms + sms / 2;
     const int64_t room = (heads + 3) / 4;
     const int64_t most = windows && room <= maxN / 8 ? maxN - room : maxN;
     const int64_t per = q_group > kMaxGqa ? 2 : 4;
