@@ -452,7 +452,10 @@ oscar_status oscar_cache_import(oscar_cache* cache, int32_t seq, int32_t length,
  * the smallest exponent >= -100 with |lo|, |hi| <= 127 2^e over the channels
  * (e = -100 for an all-zero group); values that are not finite count as 0.
  * The caller owns the index buffer (256-byte aligned device memory), attaches
- * it once, and brings it up to date after groups have closed.
+ * it once, and brings it up to date after groups have closed.  Which groups
+ * are in it is recorded on the host when oscar_index_update returns (as the
+ * lengths are): a graph that captured the call must be replayed before the
+ * record holds.
  */
 oscar_status oscar_index_required_bytes(const oscar_cache* cache, size_t* out_bytes);
 
@@ -483,7 +486,7 @@ oscar_status oscar_index_update(oscar_cache* cache, int32_t n_seqs, const int32_
  *   q           bf16 [n_seqs, num_q_heads, 128], 16-byte aligned, device or
  *               page-locked host memory; num_q_heads a multiple of Hkv, at most
  *               64 per KV head
- *   n_select    >= 1
+ *   n_select    1 .. 2^24
  *   keep_first, keep_last  that many first and last groups of each sequence are
  *               always chosen (attention sinks, recent tokens); >= 0, together
  *               <= n_select
@@ -502,7 +505,7 @@ oscar_status oscar_select_groups(oscar_cache* cache, int32_t n_seqs, const int32
  *   groups    int32 [n_seqs, Hkv, n_select] in device memory, read on
  *             `stream` (oscar_select_groups may produce it); an entry outside
  *             [0, length / 128) is empty, a group listed twice counts twice
- *   n_select  >= 1
+ *   n_select  1 .. 2^24
  *   type      OSCAR_BF16 or OSCAR_F32: type of out
  *   lse       float32 [n_seqs, num_q_heads] or NULL: ln sum exp(score) over the
  *             attended tokens (natural log, scores times softmax_scale)

@@ -250,13 +250,13 @@ oscar_status run_decode(int device, int sms, int ctas_per_sm, int32_t n, const i
     const int64_t room = (heads + 3) / 4;
     const int64_t most = windows && room <= maxN / 8 ? maxN - room : maxN;
     const int64_t per = q_group > kMaxGqa ? 2 : 4;
-    const auto per_row = [&](int64_t r) { return (n_sel + r * per - 1) / (r * per); };
-    int64_t r = 1;
-    while (r * per < n_sel && rows * per_row(r) > most) ++r;
-    N = rows * per_row(r);
-    // an even split where whole CTAs per row would leave too many places empty
-    // (256 rows of 64 entries: 64.5 us, 68.5 with 256 CTAs of 304)
-    if (N > maxN || r > T / (per * maxN) + 2) N = std::min(T, maxN);
+    // r: the smallest with rows * ceil(n_sel / (r per)) <= most
+    const int64_t fit = rows > 0 ? most / rows : 1;
+    const int64_t r = fit > 0 ? (n_sel + per * fit - 1) / (per * fit) : INT64_MAX;
+    // an even split where whole CTAs per row do not fit or would leave too many
+    // places empty (256 rows of 64 entries: 64.5 us, 68.5 with 256 CTAs of 304)
+    if (r > T / (per * maxN) + 2) N = std::min(T, maxN);
+    else N = rows * ((n_sel + r * per - 1) / (r * per));
   }
   const int max_gqa = bf16_mode ? kMaxGqa : kMaxGqaInt2;   // query heads per KV head in one launch
   const size_t need = partial_bytes(N + rows, q_group < max_gqa ? q_group : max_gqa);
@@ -973,6 +973,13 @@ oscar_status check_type(int32_t type) {
   return OSCAR_OK;
 }
 
+// Entries of a row's group list: at most the groups that the longest sequence has.
+oscar_status check_entries(int32_t n_select) {
+  if (n_select < 1 || n_select > (1 << 24))
+    return fail(OSCAR_ERR_INVALID_ARG, "n_select must be in [1, 2^24] (got %d)", n_select);
+  return OSCAR_OK;
+}
+
 // Frequencies and factor of a rotary configuration.
 oscar_status rotary_frequencies(const oscar_rotary_config* c, double* f, double* m) {
   if (!c) return fail(OSCAR_ERR_INVALID_ARG, "config is NULL");
@@ -1130,6 +1137,20 @@ oscar_status run_select(const oscar_cache* c, const std::vector<SelectSeq>& seqs
   return e == cudaSuccess ? OSCAR_OK : cuda_fail(e, "select launch");
 }
 
+// Copy `rows` rows of `width` bytes; pitches past what a 2-D copy takes go row
+// by row.
+cudaError_t copy_rows(void* dst, size_t dst_pitch, const void* src, size_t src_pitch, size_t width, size_t rows,
+                      cudaStream_t st) {
+  if (width == 0) return cudaSuccess;
+  if (std::max(dst_pitch, src_pitch) <= (size_t)INT32_MAX)
+    return cudaMemcpy2DAsync(dst, dst_pitch, src, src_pitch, width, rows, cudaMemcpyDefault, st);
+  cudaError_t e = cudaSuccess;
+  for (size_t i = 0; i < rows && e == cudaSuccess; ++i)
+    e = cudaMemcpyAsync(static_cast<uint8_t*>(dst) + i * dst_pitch, static_cast<const uint8_t*>(src) + i * src_pitch,
+                        width, cudaMemcpyDefault, st);
+  return e;
+}
+
 // Addresses and byte counts of one slot's state for the copies of export and import.
 struct SlotCopies {
   uint8_t *blocks, *window, *smax, *zmax;
@@ -1282,12 +1303,9 @@ oscar_status oscar_cache_export(oscar_cache* c, int32_t seq, void* blocks, void*
   const SlotCopies r = slot_copies(c, seq, length);
   const size_t hkv = (size_t)c->cfg.num_kv_heads;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaSuccess;
-  if (r.block_row > 0)
-    e = cudaMemcpy2DAsync(blocks, r.block_row, r.blocks, r.block_pitch, r.block_row, hkv, cudaMemcpyDefault, st);
-  if (e == cudaSuccess && r.window_row > 0)
-    e = cudaMemcpy2DAsync(window, kWindowBytes / 2, r.window, kWindowBytes / 2, r.window_row, 2 * hkv,
-                          cudaMemcpyDefault, st);
+  cudaError_t e = copy_rows(blocks, r.block_row, r.blocks, r.block_pitch, r.block_row, hkv, st);
+  if (e == cudaSuccess)
+    e = copy_rows(window, kWindowBytes / 2, r.window, kWindowBytes / 2, r.window_row, 2 * hkv, st);
   if (e == cudaSuccess) e = cudaMemcpyAsync(maxima, r.smax, hkv * 4, cudaMemcpyDefault, st);
   if (e == cudaSuccess) e = cudaMemcpyAsync(maxima + hkv, r.zmax, hkv * 4, cudaMemcpyDefault, st);
   if (e != cudaSuccess) return cuda_fail(e, "export copy");
@@ -1313,11 +1331,9 @@ oscar_status oscar_cache_import(oscar_cache* c, int32_t seq, int32_t length, con
   c->len[seq] = 0;
   c->fresh_from[seq] = 0;
   c->indexed[seq] = 0;
-  if (r.block_row > 0)
-    e = cudaMemcpy2DAsync(r.blocks, r.block_pitch, blocks, r.block_row, r.block_row, hkv, cudaMemcpyDefault, st);
-  if (e == cudaSuccess && r.window_row > 0)
-    e = cudaMemcpy2DAsync(r.window, kWindowBytes / 2, window, kWindowBytes / 2, r.window_row, 2 * hkv,
-                          cudaMemcpyDefault, st);
+  e = copy_rows(r.blocks, r.block_pitch, blocks, r.block_row, r.block_row, hkv, st);
+  if (e == cudaSuccess)
+    e = copy_rows(r.window, kWindowBytes / 2, window, kWindowBytes / 2, r.window_row, 2 * hkv, st);
   if (e == cudaSuccess) e = cudaMemcpyAsync(r.smax, maxima, hkv * 4, cudaMemcpyDefault, st);
   if (e == cudaSuccess) e = cudaMemcpyAsync(r.zmax, maxima + hkv, hkv * 4, cudaMemcpyDefault, st);
   if (e != cudaSuccess) return cuda_fail(e, "import copy");
@@ -1390,7 +1406,7 @@ oscar_status oscar_select_groups(oscar_cache* c, int32_t n_seqs, const int32_t* 
       return fail(OSCAR_ERR_INVALID_ARG, "num_q_heads must be a positive multiple of Hkv");
     if (num_q_heads / hkv > kSelectMaxHeads)
       return fail(OSCAR_ERR_UNSUPPORTED, "at most %d query heads per KV head", kSelectMaxHeads);
-    if (n_select < 1) return fail(OSCAR_ERR_INVALID_ARG, "n_select must be >= 1");
+    if ((s = check_entries(n_select)) != OSCAR_OK) return s;
     if (keep_first < 0 || keep_last < 0 || (int64_t)keep_first + keep_last > n_select)
       return fail(OSCAR_ERR_INVALID_ARG, "keep_first and keep_last must be >= 0, together <= n_select");
     if (n_seqs == 0) return ok();
@@ -1430,10 +1446,11 @@ oscar_status oscar_sparse_decode_attention(oscar_cache* c, int32_t n_seqs, const
                                            int32_t n_select, int32_t type, void* out, float* lse, void* workspace,
                                            size_t workspace_bytes, void* stream) {
   if (!groups) return fail(OSCAR_ERR_INVALID_ARG, "groups is NULL");
-  if (n_select < 1) return fail(OSCAR_ERR_INVALID_ARG, "n_select must be >= 1");
+  oscar_status s = check_entries(n_select);
+  if (s != OSCAR_OK) return s;
   if (!aligned(groups, 4) || !aligned(lse, 4))
     return fail(OSCAR_ERR_INVALID_ARG, "groups and lse must be 4-byte aligned");
-  const oscar_status s = check_type(type);
+  s = check_type(type);
   if (s != OSCAR_OK) return s;
   return decode_call(c, n_seqs, seq_ids, q, num_q_heads, softmax_scale, out, type == OSCAR_F32, workspace,
                      workspace_bytes, stream, groups, n_select, lse);

@@ -6,7 +6,8 @@
 // lowest and highest value, lo = z and hi = fl32(z + 3 s), in whole steps of
 // 2^e (nearest even), e the smallest exponent >= -100 that keeps them within
 // +-127, and the largest and smallest norm times 2^e:
-//   lo8, hi8 = rne(lo 2^-e), rne(hi 2^-e);  w_max, w_min = fl32(n 2^e).
+//   lo8, hi8 = rne(lo 2^-e), rne(hi 2^-e);  w_max, w_min = fl32(n 2^e), at most
+//   the largest float32.  What is not finite counts as 0.
 //
 // Score of a group for the query heads of a KV head:
 //   a = rne(q 2^(22 - E)), E the smallest exponent >= -100 with |q| < 2^E over
@@ -31,6 +32,7 @@
 // bit in which the row's keys differ, and, once at most 32 keys share a digit,
 // by ranking those.  Everything is latency and, for many rows, instructions.
 #include <algorithm>
+#include <cfloat>
 #include <cstddef>
 
 #include "common.cuh"
@@ -108,7 +110,9 @@ __global__ void __launch_bounds__(kIdxThreads)
     wh |= ((uint32_t)__float2int_rn(hi[c] * f) & 0xffu) << (8 * c);
   }
   p.codes[at * 32 + lane] = make_uint2(wl, wh);
-  if (lane == 0) p.weights[at] = make_float2(__uint_as_float(nmax) * exp2i(e), __uint_as_float(nmin) * exp2i(e));
+  if (lane == 0)
+    p.weights[at] = make_float2(fminf(__uint_as_float(nmax) * exp2i(e), FLT_MAX),
+                                fminf(__uint_as_float(nmin) * exp2i(e), FLT_MAX));
 }
 
 // ------------------------------------------------------------ selection

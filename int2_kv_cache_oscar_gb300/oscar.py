@@ -132,7 +132,12 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
-from int2_kv_cache_oscar_gb300 import _calls  # noqa: E402  (linked against the library just loaded)
+
+try:                      # linked against the library just loaded
+    from int2_kv_cache_oscar_gb300 import _calls  # noqa: E402
+except ImportError as e:
+    raise ImportError(f"_calls.so cannot be loaded beside {_LIB_PATH} ({e}): "
+                      "build it with int2_kv_cache_oscar_gb300.build.build()") from e
 
 # The current stream's handle without building a Stream object (3 us a call).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)

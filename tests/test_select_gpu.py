@@ -261,6 +261,42 @@ def test_stream_graph_and_many_sequences():
     assert np.array_equal(out.cpu().numpy(), want)
 
 
+def test_queries_in_page_locked_memory_and_a_single_group():
+    cache = make([300, 128], 2, seed=21)
+    q = W.make_q(2, 4, seed=3)
+    want = run(cache, [0, 1], q.cuda(), 1, 0, 0)
+    assert np.array_equal(run(cache, [0, 1], q.pin_memory(), 1, 0, 0), want)
+    check(cache, [0, 1], q.cuda(), 1)
+
+
+def test_an_imported_sequence_is_indexed_anew():
+    O = U.lib()
+    cache = make([1400, 1500], 2, seed=22)
+    q = W.make_q(1, 4, seed=4).cuda()
+    state = cache.export_sequence(1)
+    cache.import_sequence(0, *state)
+    with pytest.raises(O.OscarError, match="index"):
+        run(cache, [0], q, 3, 0, 0)
+    cache.update_index([0])
+    check(cache, [0], q, 3)
+    assert np.array_equal(run(cache, [0], q, 3, 0, 0), run(cache, [1], q, 3, 0, 0))
+
+
+def test_two_streams_at_once():
+    cache = make([128 * 150, 128 * 40], 2, seed=23)
+    q = [W.make_q(2, 8, seed=30 + i).cuda() for i in range(2)]
+    want = [run(cache, [0, 1], q[i], 7, 1, 1) for i in range(2)]
+    outs = [torch.zeros((20, 2, 2, 7), dtype=torch.int32, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for k in range(20):
+        for i in range(2):
+            cache.select_groups([0, 1], q[i], 8, outs[i][k], 1, 1, stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(np.array_equal(outs[i][k].cpu().numpy(), want[i]) for k in range(20))
+
+
 def test_refusals():
     O = U.lib()
     cache = make([600, 0], 2, index=False)

@@ -101,6 +101,59 @@ def test_against_the_oracle(lens, hkv, hq, n, empty, meta):
     check(cache, ids, q, lists(cache, ids, n, 8, empty), torch.bfloat16, scale=0.03)
 
 
+@pytest.mark.parametrize("lens,hkv,hq,n,meta", [
+    ([128 * (1 + i % 5) + 3 * i for i in range(40)], 2, 8, 3, 32),      # windows of every length, more rows than SMs
+    ([128 * (1 + i % 4) for i in range(40)], 2, 8, 2, 16),              # no windows
+    ([30 + 17 * i for i in range(33)], 1, 8, 2, 32),                    # some without a group, 8 heads
+    ([140 + 9 * i for i in range(41)], 2, 6, 5, 16),                    # 3 heads
+    ([16, 32, 48, 127, 128, 255, 256, 257] * 32, 1, 1, 1, 32),          # whole tiles of 16 window tokens
+    ([1000] * 20, 1, 13, 6, 32),                                        # two passes: 8 and 5 heads
+    ([260 + i for i in range(36)], 1, 7, 2, 32)])
+def test_many_rows(lens, hkv, hq, n, meta):
+    """More query heads than 1.5 per SM: the combine with a CTA per KV head."""
+    cache = make(lens, hkv, meta, seed=hq + n)
+    ids = list(range(len(lens)))
+    q = W.make_q(len(lens), hq, seed=4).cuda()
+    check(cache, ids, q, lists(cache, ids, n, 11, 0.2))
+
+
+def test_wait_that_runs_out():
+    """A copy left unissued (the library's own hook): the bounded waits give
+    up, the call reports it, later calls are unaffected."""
+    O = U.lib()
+    cache = make([2000], 1, seed=15)
+    q = W.make_q(1, 4, seed=16).cuda()
+    groups = torch.arange(8, dtype=torch.int32).view(1, 1, 8).cuda()
+    want = check(cache, [0], q, groups)
+    out, ws = torch.empty((1, 4, 128), device="cuda"), cache.workspace(1, 4)
+    O.oscar_test_arm_wait_timeout()
+    cache.sparse_decode([0], q, 4, groups, out, ws)
+    with pytest.raises(O.OscarError) as e:
+        O.oscar_cache_check(cache.handle)
+    assert e.value.status == O.OSCAR_ERR_DEVICE_TIMEOUT
+    again = check(cache, [0], q, groups)
+    assert torch.equal(want[0], again[0]) and torch.equal(want[1], again[1])
+
+
+def test_two_streams_at_once():
+    """Calls on two streams with their own workspaces, lists and outputs."""
+    cache = make([3000, 2900], 2, seed=17)
+    q = [W.make_q(2, 8, seed=18 + i).cuda() for i in range(2)]
+    g = [lists(cache, [0, 1], 9, 20 + i, 0.1) for i in range(2)]
+    want = [check(cache, [0, 1], q[i], g[i]) for i in range(2)]
+    ws = [cache.workspace(2, 8) for _ in range(2)]
+    outs = [torch.empty((20, 2, 8, 128), device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for k in range(20):
+        for i in range(2):
+            cache.sparse_decode([0, 1], q[i], 8, g[i], outs[i][k], ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    U.lib().oscar_cache_check(cache.handle)
+    for i in range(2):
+        assert all(torch.equal(outs[i][k], want[i][0]) for k in range(20))
+
+
 def test_many_entries_per_block():
     """More entries than a block's ring and than one look-up of 32."""
     cache = make([128 * 500 + 3], 1, seed=31)
@@ -269,6 +322,9 @@ def test_refusals():
             fn()
         assert e.value.status == status
     refused(lambda: cache.sparse_decode([0], q, 4, groups.cpu(), out, ws))
+    refused(lambda: O.oscar_sparse_decode_attention(cache.handle, [0, 0], q.expand(2, 4, 128).contiguous(), 4, 0.0,
+                                                    groups.expand(2, 2, 3).contiguous(),
+                                                    out.expand(2, 4, 128).contiguous(), ws))
     refused(lambda: cache.sparse_decode([0], q, 4, groups[..., :0].contiguous(), out, ws))
     refused(lambda: cache.sparse_decode([1], q, 4, groups, out, ws))
     refused(lambda: cache.sparse_decode([0], q, 4, groups, out, ws[:64]), O.OSCAR_ERR_CAPACITY)
