@@ -13,7 +13,8 @@
 // One block of 128 threads per (128-token tile, KV head), taken from a list of
 // tiles in a persistent grid; the next tile's packed block (13,824 or 11,008
 // bytes) is on its way into a second shared-memory stage (one bulk copy)
-// meanwhile.
+// meanwhile.  The values come first: one barrier between the two parts of a
+// tile is enough, and warps drift apart by up to a part.
 //   keys:   thread = token.  Its codes are 8 words; channels c and c + 64 sit
 //           at the same bit of two of them and share a packed pair, so six
 //           transform stages are packed adds in registers and the last one is
@@ -44,7 +45,7 @@ struct ReadSmem {
   static constexpr int kPitch = kRow + 16;
   alignas(128) uint8_t stage[kReadStages][Blk<M16>::kBytes];
   alignas(16) uint8_t krow[kGroup][kPitch];   // key rows on their way out
-  alignas(16) float4 kp[kHeadDim / 2];   // channels (c, c + 64): scale 2^-b (2), zero (2), b the codes' bit
+  alignas(16) float4 kp[kReadStages][kHeadDim / 2];   // channels (c, c + 64): scale 2^-b (2), zero (2), b the codes' bit
   alignas(8) uint64_t full[kReadStages];
   int abort_flag;
 };
@@ -153,7 +154,6 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
   if (tid == 0 && u < p.n_tiles) request(u, 0);
   for (uint32_t it = 0; u < p.n_tiles; ++it, u += gridDim.x) {
     const int s = it & 1;
-    if (tid == 0 && u + gridDim.x < p.n_tiles) request(u + gridDim.x, s ^ 1);
     int b, j, tile;
     locate_tile(p, u, b, j, tile);
     const ReadSeq sq = p.seq[b];
@@ -170,21 +170,8 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
     const uint8_t* blk = S.stage[s];
     if (packed && tid < kHeadDim / 2) {
       const float f = exp2i(-col_bit(tid));
-      S.kp[tid] = make_float4(MR::one(blk + B::kKScale, tid) * f, MR::one(blk + B::kKScale, tid + 64) * f,
-                              MR::one(blk + B::kKZero, tid), MR::one(blk + B::kKZero, tid + 64));
-    }
-    if (__syncthreads_or(late)) {
-      // a wait gave up: wait (bounded) for the copies in flight and leave
-      if (tid == 0) {
-        for (uint32_t i = 0; i < 2; ++i) {
-          if (i == 1 && u + gridDim.x >= p.n_tiles) break;
-          const uint32_t ii = it + i;
-          for (uint32_t n = 0; n < kSpinLimit; ++n)
-            if (mbar_try_wait(&S.full[ii & 1], (ii >> 1) & 1)) break;
-        }
-      }
-      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-      return;
+      S.kp[s][tid] = make_float4(MR::one(blk + B::kKScale, tid) * f, MR::one(blk + B::kKScale, tid + 64) * f,
+                                 MR::one(blk + B::kKZero, tid), MR::one(blk + B::kKZero, tid + 64));
     }
     if (!packed) {
       // ---- window rows: 16 lanes a row
@@ -207,10 +194,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
           }
         }
       }
-      __syncthreads();   // the stage's next request comes after every thread is past it
-      continue;
-    }
-    if (vout != nullptr) {
+    } else if (vout != nullptr) {
       // ---- values: channels 8 c8 .. + 7, tokens of (token half jt, tig)
       const int c8 = lane & 15, x = 2 * warp + (lane >> 4);
       const int tig = x & 3, jt = x >> 2;
@@ -247,7 +231,19 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
       }
     }
 
-    if (kout != nullptr) {
+    // One barrier a tile: the parameter table is complete, and everyone is done
+    // with the previous tile, whose stage takes the next one.
+    if (__syncthreads_or(late)) {
+      // a wait gave up: leave (no copy of a later tile has been requested; this
+      // tile's gets its time, bounded)
+      if (tid == 0)
+        for (uint32_t n = 0; n < kSpinLimit; ++n)
+          if (mbar_try_wait(&S.full[s], (it >> 1) & 1)) break;
+      break;
+    }
+    if (tid == 0 && u + gridDim.x < p.n_tiles) request(u + gridDim.x, s ^ 1);
+
+    if (packed && kout != nullptr) {
       // ---- keys: token tid
       const int t = tid, mt = t >> 4, r = (t >> 3) & 1, g = t & 7;
       const uint32_t* words = reinterpret_cast<const uint32_t*>(blk + kOffKCodes);
@@ -265,7 +261,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             const int c = 8 * q + 2 * tig + e;
-            const float4 kp = S.kp[c];
+            const float4 kp = S.kp[s][c];
             x[c] = __ffma2_rn(codes2(w0, w1, 4 * (q >> 1) + 2 * (q & 1)), make_float2(kp.x, kp.y),
                               make_float2(kp.z, kp.w));
           }
@@ -307,7 +303,6 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
       }
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
-    __syncthreads();   // everyone is done with this stage and the parameter table
   }
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the last rows are written
 }
