@@ -431,7 +431,7 @@ oscar_status oscar_cache_read(oscar_cache* cache, int32_t n_seqs, const int32_t*
  *   window  bf16 [Hkv, 2, 128, 128]: key rows, then value rows; the first w
  *           rows of each are read or written, the others left as they are
  *   maxima  float32 [2, Hkv]: the largest value scale, the largest |value zero|
- * Device or page-locked host memory, 16-byte aligned; blocks may be NULL when
+ * Device or page-locked host memory of any alignment; blocks may be NULL when
  * g = 0 and window when w = 0.  Plain copies on `stream`.
  * oscar_cache_import replaces what the slot holds by `length` tokens.
  */

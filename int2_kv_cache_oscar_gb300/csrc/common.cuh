@@ -289,26 +289,28 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float x) {
 // right shift, i.e. at bits 2(i - 5).  An extracted fp16 is then the
 // subnormal code * 2^(p - 24).
 //
-// HIGH: every slot is read at bits 4 to 9 instead (i <= 1 after a 4-bit left
-// shift, i >= 5 after a 6-bit right shift; one shift more per word).  The
-// tensor core aligns products by their operands' nominal exponents and drops
-// what falls below, and a subnormal operand sits 10 - p bits under its
-// nominal exponent: at p = 0 the products of factors well below the largest
-// lose their last bits.  Measured on score sums over outlier keys: 1e-6 to
-// 4e-6 of the score with p = 0..8, about a sixteenth of that with p = 4..8.
-template <bool HIGH = false>
+// MODE 1 and 2 read the slots higher up: at bits 4 to 9 (i <= 1 after a 4-bit
+// left shift, i >= 5 after a 6-bit right shift; two shifts a word instead of
+// one) and at bits 6 to 9 (left by 6, 6, 4, in place, right by 4, 4, 6; four
+// shifts).  The tensor core aligns products by their operands' nominal
+// exponents and drops what falls below, and a subnormal operand sits 10 - p
+// bits under its nominal exponent: at p = 0 the products of factors well below
+// the largest lose their last bits.
+template <int MODE = 0>
 __host__ __device__ constexpr int frag_p(int i) {
-  return HIGH ? (i <= 1 ? 2 * i + 4 : i <= 4 ? 2 * i : 2 * i - 6) : (i <= 4 ? 2 * i : 2 * (i - 5));
+  return 2 * i + (MODE == 2   ? (i <= 1 ? 6 : i == 2 ? 4 : i <= 4 ? 0 : i <= 6 ? -4 : -6)
+                  : MODE == 1 ? (i <= 1 ? 4 : i <= 4 ? 0 : -6)
+                              : (i <= 4 ? 0 : -10));
 }
 
 // Extract the half2 (two subnormal fp16 codes) of fragment slot i from word w.
-template <int I, bool HIGH = false>
+template <int I, int MODE = 0>
 __device__ __forceinline__ uint32_t frag_extract(uint32_t w) {
-  constexpr uint32_t mask = 0x00030003u << frag_p<HIGH>(I);
-  if constexpr (I >= 2 && I <= 4) return w & mask;
-  else if constexpr (HIGH) return (I <= 1 ? w << 4 : w >> 6) & mask;
-  else if constexpr (I <= 1) return w & mask;
-  else return (w >> 10) & mask;
+  constexpr int left = frag_p<MODE>(I) - 2 * I;
+  constexpr uint32_t mask = 0x00030003u << frag_p<MODE>(I);
+  if constexpr (left > 0) return (w << left) & mask;
+  else if constexpr (left < 0) return (w >> -left) & mask;
+  else return w & mask;
 }
 
 // Metadata of a staged block as float: float32 sections, or float16 ones

@@ -117,23 +117,23 @@ __device__ __forceinline__ int range_exponent(float bound) {
 }
 
 // A fragment of k-step kk (= ks & 3) from the words of rows g and g+8.
-template <int KK, bool HIGH>
+template <int KK, int MODE>
 __device__ __forceinline__ void frag_a(uint32_t w0, uint32_t w1, uint32_t& a0, uint32_t& a1, uint32_t& a2,
                                        uint32_t& a3) {
-  a0 = frag_extract<2 * KK, HIGH>(w0);
-  a1 = frag_extract<2 * KK, HIGH>(w1);
-  a2 = frag_extract<2 * KK + 1, HIGH>(w0);
-  a3 = frag_extract<2 * KK + 1, HIGH>(w1);
+  a0 = frag_extract<2 * KK, MODE>(w0);
+  a1 = frag_extract<2 * KK, MODE>(w1);
+  a2 = frag_extract<2 * KK + 1, MODE>(w0);
+  a3 = frag_extract<2 * KK + 1, MODE>(w1);
 }
 
-template <bool HIGH>
+template <int MODE>
 __device__ __forceinline__ void frag_a_dyn(int kk, uint32_t w0, uint32_t w1, uint32_t& a0, uint32_t& a1,
                                            uint32_t& a2, uint32_t& a3) {
   switch (kk) {
-    case 0: frag_a<0, HIGH>(w0, w1, a0, a1, a2, a3); break;
-    case 1: frag_a<1, HIGH>(w0, w1, a0, a1, a2, a3); break;
-    case 2: frag_a<2, HIGH>(w0, w1, a0, a1, a2, a3); break;
-    default: frag_a<3, HIGH>(w0, w1, a0, a1, a2, a3); break;
+    case 0: frag_a<0, MODE>(w0, w1, a0, a1, a2, a3); break;
+    case 1: frag_a<1, MODE>(w0, w1, a0, a1, a2, a3); break;
+    case 2: frag_a<2, MODE>(w0, w1, a0, a1, a2, a3); break;
+    default: frag_a<3, MODE>(w0, w1, a0, a1, a2, a3); break;
   }
 }
 
@@ -166,12 +166,21 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-template <int MAXS, bool M16, bool PAIRS, bool SPARSE>
+// LISTED: 0 every group; listed groups with 1 bf16, 2 float32 outputs
+template <int MAXS, bool M16, bool PAIRS, int LISTED>
 __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
     decode_int2_kernel(const __grid_constant__ DecodeParams<MAXS> p, const uint8_t* __restrict__ arena) {
   using DecSmem = DecSmemT<M16>;
   using B = Blk<M16>;
   using MR = Meta<M16>;
+  constexpr bool SPARSE = LISTED != 0;
+  // Bit positions at which codes are read (see frag_p).  Score sums over outlier
+  // keys are off by 1e-6 to 4e-6 of the score in mode 0 (1.6e-5 of the outputs)
+  // and at float32 rounding in mode 1 (mode 2 changes nothing more); with that
+  // the value sums are off by 1.1e-5 of the outputs in mode 0, 2.1e-6 in mode 1,
+  // 1.2e-6 in mode 2 (32-bit products and sums: 1.4e-6).  bf16 outputs round by
+  // 1.4e-3, so mode 2 is for float32 ones: it takes 5 % longer.
+  constexpr int kKeyMode = SPARSE ? 1 : 0, kValueMode = LISTED == 2 ? 2 : 0;
   constexpr int kStages = DecSmem::kStages;
   constexpr int kStageBytes = B::kBytes;
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -429,7 +438,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
         const int c = 16 * ks + 2 * tig + 8 * half;
-        const int pp = half ? frag_p<SPARSE>(2 * (ks & 3) + 1) : frag_p<SPARSE>(2 * (ks & 3));
+        const int pp = half ? frag_p<kKeyMode>(2 * (ks & 3) + 1) : frag_p<kKeyMode>(2 * (ks & 3));
         const float f = pow2f(Fk_b - pp);
         q2[2 * ks] = S.qrot[h0 + hb][c] * f;
         q2[2 * ks + 1] = S.qrot[h0 + hb][c + 1] * f;
@@ -454,9 +463,8 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
     const int vzl0 = 16 * g, vzl1 = 16 * ((g + 8) ^ 1);               //        tokens g, g + 8
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
-      const int pp = half ? frag_p<SPARSE>(2 * kk + 1) : frag_p<SPARSE>(2 * kk);
-      zwk[kk] = pow2f(pp);
-      fsc[kk] = fv * pow2f(-pp);
+      zwk[kk] = pow2f(half ? frag_p<kKeyMode>(2 * kk + 1) : frag_p<kKeyMode>(2 * kk));
+      fsc[kk] = fv * pow2f(half ? -frag_p<kValueMode>(2 * kk + 1) : -frag_p<kValueMode>(2 * kk));
     }
 
     float m_run = -INFINITY;   // running max (log2 units) of head tig
@@ -545,7 +553,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
               const uint32_t w0 = (ks < 4) ? w[m].x : w[m].z;
               const uint32_t w1 = (ks < 4) ? w[m].y : w[m].w;
               uint32_t a0, a1, a2, a3;
-              frag_a_dyn<SPARSE>(ks & 3, w0, w1, a0, a1, a2, a3);
+              frag_a_dyn<kKeyMode>(ks & 3, w0, w1, a0, a1, a2, a3);
               mma_f16_16816(acc[m], a0, a1, a2, a3, bk[ks][0], bk[ks][1]);
             }
           }
@@ -635,7 +643,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
               for (int h2 = 0; h2 < 2; ++h2) {
                 const int mt = 2 * gr + h2;
                 uint32_t a0, a1, a2, a3;
-                frag_a_dyn<SPARSE>(kk2, vw[mt].x, vw[mt].y, a0, a1, a2, a3);
+                frag_a_dyn<kValueMode>(kk2, vw[mt].x, vw[mt].y, a0, a1, a2, a3);
                 mma_f16_16816(pacc[mt], a0, a1, a2, a3, b0, b1);
               }
             }
@@ -1275,13 +1283,13 @@ int num_sms(int device) {
   return n;
 }
 
-template <int MAXS, bool M16, bool PAIRS, bool SPARSE>
+template <int MAXS, bool M16, bool PAIRS, int LISTED>
 cudaError_t launch_decode_int2_t(const DecodeParams<MAXS>& p, const uint8_t* arena, cudaStream_t stream,
                                  cudaEvent_t ev_start, cudaEvent_t ev_stop) {
   if (p.h.n_units <= 0) return cudaSuccess;
   const int smem = (int)sizeof(DecSmemT<M16>);
   static bool attr_done[64] = {};
-  cudaError_t e = ensure_smem_attr(decode_int2_kernel<MAXS, M16, PAIRS, SPARSE>, smem, attr_done);
+  cudaError_t e = ensure_smem_attr(decode_int2_kernel<MAXS, M16, PAIRS, LISTED>, smem, attr_done);
   if (e != cudaSuccess) return e;
   if (ev_start) cudaEventRecord(ev_start, stream);
   // programmatic dependent launch: the grid may start while the previous
@@ -1296,7 +1304,7 @@ cudaError_t launch_decode_int2_t(const DecodeParams<MAXS>& p, const uint8_t* are
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, decode_int2_kernel<MAXS, M16, PAIRS, SPARSE>, p, arena);
+  e = cudaLaunchKernelEx(&cfg, decode_int2_kernel<MAXS, M16, PAIRS, LISTED>, p, arena);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (ev_stop) cudaEventRecord(ev_stop, stream);
   return e;
@@ -1306,18 +1314,18 @@ template <int MAXS>
 cudaError_t launch_decode_int2(const DecodeParams<MAXS>& p, const uint8_t* arena, bool meta16, cudaStream_t stream,
                                cudaEvent_t ev_start, cudaEvent_t ev_stop) {
   // more than kMaxGqa query heads per KV head: two head sets on the same blocks
-  auto launch = [&](auto m16, auto pairs, auto sparse) {
-    return launch_decode_int2_t<MAXS, decltype(m16)::value, decltype(pairs)::value, decltype(sparse)::value>(
+  auto launch = [&](auto m16, auto pairs, auto listed) {
+    return launch_decode_int2_t<MAXS, decltype(m16)::value, decltype(pairs)::value, decltype(listed)::value>(
         p, arena, stream, ev_start, ev_stop);
   };
   using T = std::true_type;
   using F = std::false_type;
-  if (p.h.groups != nullptr) {
-    if (p.h.gqa > kMaxGqa) return meta16 ? launch(T{}, T{}, T{}) : launch(F{}, T{}, T{});
-    return meta16 ? launch(T{}, F{}, T{}) : launch(F{}, F{}, T{});
-  }
-  if (p.h.gqa > kMaxGqa) return meta16 ? launch(T{}, T{}, F{}) : launch(F{}, T{}, F{});
-  return meta16 ? launch(T{}, F{}, F{}) : launch(F{}, F{}, F{});
+  auto by_layout = [&](auto listed) {
+    if (p.h.gqa > kMaxGqa) return meta16 ? launch(T{}, T{}, listed) : launch(F{}, T{}, listed);
+    return meta16 ? launch(T{}, F{}, listed) : launch(F{}, F{}, listed);
+  };
+  if (p.h.groups == nullptr) return by_layout(std::integral_constant<int, 0>{});
+  return p.h.out_f32 ? by_layout(std::integral_constant<int, 2>{}) : by_layout(std::integral_constant<int, 1>{});
 }
 
 template <int MAXS>

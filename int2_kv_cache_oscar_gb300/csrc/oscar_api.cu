@@ -1174,8 +1174,6 @@ oscar_status check_slot_buffers(const oscar_cache* c, int32_t length, const void
                                 const float* maxima) {
   if ((length >= kGroup && !blocks) || (length % kGroup != 0 && !window) || !maxima)
     return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
-  if (!aligned(blocks, 16) || !aligned(window, 16) || !aligned(maxima, 16))
-    return fail(OSCAR_ERR_INVALID_ARG, "blocks, window and maxima must be 16-byte aligned");
   const void* v = nullptr;
   oscar_status s = OSCAR_OK;
   if (length >= kGroup) s = device_view(blocks, "blocks", c->cfg.device, &v);

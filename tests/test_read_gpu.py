@@ -179,6 +179,19 @@ def test_export_import(meta, pinned):
     assert torch.equal(x, y)
 
 
+def test_export_import_of_slices():
+    """Buffers that start anywhere: rows of a batch's tensors, one KV head."""
+    cache, _ = make([700, 390], 1, seed=14, capacity=900)
+    n, blocks, window, maxima = cache.export_sequence(0)
+    batch = torch.zeros((3, 2, 1), device="cuda")
+    flat = torch.zeros(blocks.numel() + 1, dtype=torch.uint8, device="cuda")
+    win = torch.zeros(window.numel() + 1, dtype=torch.bfloat16, device="cuda")
+    batch[1], flat[1:], win[1:] = maxima, blocks.view(-1), window.view(-1)
+    cache.import_sequence(1, n, flat[1:].view(blocks.shape), win[1:].view(window.shape), batch[1])
+    a = U.read_arena(cache)
+    assert np.array_equal(U.live_bytes(cache, a, 0), U.live_bytes(cache, a, 1))
+
+
 def test_import_after_a_decode_is_attended():
     """A decode that follows an import on the stream of earlier decodes sees
     the new blocks (none of the slot's old ones copied early)."""
