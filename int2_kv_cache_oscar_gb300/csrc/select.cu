@@ -17,9 +17,9 @@
 //   score = S w_max if S >= 0, else S w_min.
 // Up to the 8-bit steps this is the largest score that a key inside the
 // group's box could reach.  Everything up to S is whole numbers and the score
-// is a 22-bit times a 24-bit number in float64, so scores are exact, the order
-// does not depend on how the sums are split, and ties are true ties (the
-// lowest group wins).
+// is a 21-bit times a 24-bit number, so scores are exact, the order does not
+// depend on how the sums are split, and ties are true ties (the lowest group
+// wins).
 //
 // Selection: a cluster of 1 to 8 blocks per (sequence, KV head) row, each
 // scoring a contiguous slice of its groups and storing the scores' keys into
@@ -117,10 +117,19 @@ __global__ void __launch_bounds__(kIdxThreads)
 
 // ------------------------------------------------------------ selection
 
-// Order-preserving bits of a float64 (no NaN; -0 already made +0).
-__device__ __forceinline__ uint64_t order_key(double x) {
-  const uint64_t u = (uint64_t)__double_as_longlong(x);
-  return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
+// Order-preserving key of the exact product s w (|s| <= 2^22, w >= 0 finite):
+// sign, exponent and the product's 46 bits, in whole-number operations (a
+// float64 instruction costs a warp 64 to 76 cycles on this chip: five of them
+// per eight groups were three quarters of the scoring time).
+__device__ __forceinline__ uint64_t score_key(int s, float w) {
+  const uint32_t wb = __float_as_uint(w);
+  const uint32_t ex = wb >> 23;
+  const uint32_t mant = ex ? (wb & 0x7fffffu) | 0x800000u : wb;      // w = mant 2^(max(ex, 1) - 150)
+  const uint64_t p = (uint64_t)(uint32_t)abs(s) * mant;
+  if (p == 0) return 1ull << 63;
+  const int lz = __clzll((long long)p);
+  const uint64_t mag = ((uint64_t)(max(ex, 1u) + 63 - lz) << 46) | (((p << lz) >> 17) & ((1ull << 46) - 1));
+  return s >= 0 ? (1ull << 63) | mag : ~((1ull << 63) | mag);
 }
 
 struct SelSmem {
@@ -319,9 +328,8 @@ __global__ void __launch_bounds__(kSelThreads)
       if (part == 0 && gl < here) {
         const int g = first + i;
         const float2 wt = *reinterpret_cast<const float2*>(&keys[i]);
-        const double score = (double)best * (double)(best >= 0 ? wt.x : wt.y) + 0.0;   // -0 + 0 = +0
         const bool kept = g < p.keep_first || g >= ng - p.keep_last;
-        const uint64_t key = kept ? ~0ull : order_key(score);
+        const uint64_t key = kept ? ~0ull : score_key(best, best >= 0 ? wt.x : wt.y);
         dst[g] = key;
         if (!kept) {
           hmin = min(hmin, (uint32_t)(key >> 32));
