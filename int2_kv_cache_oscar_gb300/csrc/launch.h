@@ -245,7 +245,8 @@ struct SelectParams {
   int32_t keep_first;
   int32_t keep_last;
   int32_t blocks;      // of a row (a cluster), set by the launch
-  int32_t stages;      // copies in flight, set by the launch
+  int32_t stages;      // copies in flight and the bytes of each, set by the launch
+  int32_t stage_bytes;
   uint32_t* err_word;
   const uint2* codes;
   const float2* weights;

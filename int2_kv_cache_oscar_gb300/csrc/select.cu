@@ -24,7 +24,7 @@
 // Selection: a cluster of 1 to 8 blocks per (sequence, KV head) row, each
 // scoring a contiguous slice of its groups and storing the scores' keys into
 // the first block's shared memory; that block then chooses.  A slice's codes
-// come by bulk copies of 128 groups (32 KB), up to four in flight, requested
+// come by bulk copies of up to 256 groups (64 KB), two in flight, requested
 // before the queries are turned.  Four lanes score a group: each holds a
 // quarter of the query bytes of four heads in registers, so a group costs a
 // warp 12 instructions (a warp per group, with a warp sum per head, took 51).
@@ -44,10 +44,11 @@ namespace {
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelHeads = 4;      // query heads scored at once
-constexpr int kSelChunk = 128;    // groups of one bulk copy
-constexpr int kSelStages = 4;     // copies in flight
+constexpr int kSelChunk = 256;    // groups of one bulk copy at most: 4 batches of 8 a warp
+constexpr int kSelStages = 2;     // copies in flight
 constexpr int kSelRank = 32;      // keys ranked directly
 static_assert(kSelThreads == 256, "one thread per digit of the histogram");
+static_assert(kSelChunk == 4 * 8 * kSelWarps, "a lane per group of a chunk");
 constexpr int kIdxThreads = 256;
 constexpr int kIdxMinExp = -100;
 
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kSelThreads)
   // a lane), [gqa][32] their bytes (parts below and above zero), [ng] score
   // keys (the first block's; the others use it for their weights)
   uint8_t* stages = smem_raw;
-  int4* turned = reinterpret_cast<int4*>(stages + (size_t)p.stages * kSelChunk * 256);
+  int4* turned = reinterpret_cast<int4*>(stages + (size_t)p.stages * p.stage_bytes);
   int2* q8 = reinterpret_cast<int2*>(turned + (size_t)gqa * 32);
   uint64_t* keys = reinterpret_cast<uint64_t*>(q8 + (size_t)gqa * 32);
   if (tid == 0) {
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(kSelThreads)
     const int s = c % p.stages;
     const uint32_t bytes = (uint32_t)min(kSelChunk, n - c * kSelChunk) * 256;
     mbar_arrive_expect_tx(&S.full[s], bytes);
-    bulk_g2s(stages + (size_t)s * kSelChunk * 256, p.codes + (row + c * kSelChunk) * 32, bytes, &S.full[s]);
+    bulk_g2s(stages + (size_t)s * p.stage_bytes, p.codes + (row + c * kSelChunk) * 32, bytes, &S.full[s]);
   };
   if (tid == 0)
     for (int c = 0; c < min(chunks, p.stages); ++c) request(c);
@@ -298,14 +299,20 @@ __global__ void __launch_bounds__(kSelThreads)
   for (int c = 0; c < chunks; ++c) {
     const int s = c % p.stages;
     mbar_wait_bounded(&S.full[s], (uint32_t)((c / p.stages) & 1), &S.abort_flag, p.err_word);
-    const int4* codes = reinterpret_cast<const int4*>(stages + (size_t)s * kSelChunk * 256);
+    const int4* codes = reinterpret_cast<const int4*>(stages + (size_t)s * p.stage_bytes);
     const int here = min(kSelChunk, n - c * kSelChunk);
-    for (int g0 = warp * 8; g0 < here; g0 += kSelWarps * 8) {
+    // batches of 8 groups, warp by warp: t 8 + warp; lane `part` then makes the
+    // key of its group of batch `part`
+    int best = INT32_MIN;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int g0 = (t * kSelWarps + warp) * 8;
+      if (g0 >= here) break;
       const int gl = g0 + (lane >> 2);    // behind the last group: whatever the stage holds, not used
       int4 w[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) w[k] = codes[gl * 16 + part + 4 * k];
-      int best = INT32_MIN;
+      int top_s = INT32_MIN;
       for (int h0 = 0; h0 < gqa; h0 += kSelHeads) {
         if (gqa > kSelHeads) load_heads(h0);
 #pragma unroll
@@ -321,20 +328,21 @@ __global__ void __launch_bounds__(kSelThreads)
           a += d;
           a += __shfl_xor_sync(0xffffffffu, a, 1);
           a += __shfl_xor_sync(0xffffffffu, a, 2);
-          best = max(best, a);
+          top_s = max(top_s, a);
         }
       }
-      const int i = c * kSelChunk + gl;
-      if (part == 0 && gl < here) {
-        const int g = first + i;
-        const float2 wt = *reinterpret_cast<const float2*>(&keys[i]);
-        const bool kept = g < p.keep_first || g >= ng - p.keep_last;
-        const uint64_t key = kept ? ~0ull : score_key(best, best >= 0 ? wt.x : wt.y);
-        dst[g] = key;
-        if (!kept) {
-          hmin = min(hmin, (uint32_t)(key >> 32));
-          hmax = max(hmax, (uint32_t)(key >> 32));
-        }
+      if (part == t) best = top_s;
+    }
+    const int gl = (part * kSelWarps + warp) * 8 + (lane >> 2);
+    if (gl < here) {
+      const int i = c * kSelChunk + gl, g = first + i;
+      const float2 wt = *reinterpret_cast<const float2*>(&keys[i]);
+      const bool kept = g < p.keep_first || g >= ng - p.keep_last;
+      const uint64_t key = kept ? ~0ull : score_key(best, best >= 0 ? wt.x : wt.y);
+      dst[g] = key;
+      if (!kept) {
+        hmin = min(hmin, (uint32_t)(key >> 32));
+        hmax = max(hmax, (uint32_t)(key >> 32));
       }
     }
     if (c + p.stages < chunks) {
@@ -529,21 +537,22 @@ cudaError_t launch_select(const SelectParams<MAXS>& params, int sms, cudaStream_
   // stays within two blocks per SM
   int blocks = 1;
   while (blocks < kSelMaxBlocks && groups >= 128 * blocks && (int64_t)rows * blocks <= sms) blocks *= 2;
-  const int chunks = ((groups + blocks - 1) / blocks + kSelChunk - 1) / kSelChunk;
+  const int slice = (groups + blocks - 1) / blocks, chunks = (slice + kSelChunk - 1) / kSelChunk;
   p.blocks = blocks;
-  // every copy in flight at once up to 512 groups a block; longer slices turn two stages over
-  p.stages = chunks <= kSelStages ? std::max(chunks, 1) : 2;
-  const size_t smem = (size_t)p.stages * kSelChunk * 256 + (size_t)p.q_group * 32 * (sizeof(int4) + sizeof(int2)) +
-                      (size_t)groups * sizeof(uint64_t);
-  static_assert(kSelStages * kSelChunk * 256 + kSelectMaxHeads * 32 * 24 + kSelStages * kSelChunk * kSelMaxBlocks * 8 <=
-                        kSelectMaxSmem &&
-                    2 * kSelChunk * 256 + kSelectMaxHeads * 32 * 24 + kSelectMaxGroups * 8 <= kSelectMaxSmem,
-                "the largest selection fits");
+  // (whole batches: lanes behind the last group read the stage too)
+  p.stage_bytes = std::max(8, std::min((slice + 7) & ~7, kSelChunk)) * 256;
+  const auto smem = [&](int stages) {
+    return (size_t)stages * p.stage_bytes + (size_t)p.q_group * 32 * (sizeof(int4) + sizeof(int2)) +
+           (size_t)groups * sizeof(uint64_t);
+  };
+  static_assert(kSelChunk * 256 + kSelectMaxHeads * 32 * 24 + kSelectMaxGroups * 8 <= kSelectMaxSmem,
+                "the largest selection fits with one stage");
+  p.stages = chunks < 2 || smem(kSelStages) > (size_t)kSelectMaxSmem ? 1 : kSelStages;
   static bool attr_done[64] = {};
   cudaError_t e = ensure_smem_attr(select_kernel<MAXS>, kSelectMaxSmem, attr_done);
   if (e != cudaSuccess) return e;
-  return launch_dependent(select_kernel<MAXS>, dim3((unsigned)(rows * blocks)), dim3(kSelThreads), smem, stream,
-                          (unsigned)blocks, p);
+  return launch_dependent(select_kernel<MAXS>, dim3((unsigned)(rows * blocks)), dim3(kSelThreads), smem(p.stages),
+                          stream, (unsigned)blocks, p);
 }
 
 #define OSCAR_INSTANTIATE(N)                                                                                  \

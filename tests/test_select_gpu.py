@@ -180,6 +180,47 @@ def test_selection_of_given_summaries(ng, n, kind):
         assert run(cache, [0], q, n, first, last)[0, 0].tolist() == choose(q8, groups, n, first, last)
 
 
+@pytest.mark.parametrize("ng,hq", [(9001, 3), (2600, 64), (12000, 64)])
+def test_long_sequences(ng, hq):
+    """Slices that turn their stages over, with one stage and with two."""
+    cache = U.lib().OscarCache(1, 1, 128 * ng)
+    k = torch.randn((128 * ng, 1, 128), device="cuda").bfloat16()
+    cache.append([0], [0, 128 * ng], k, k)
+    del k
+    cache.enable_index()
+    cache.update_index([0])
+    rng = np.random.default_rng(ng)
+    lo = rng.integers(-127, 128, (ng, 128))
+    hi = np.minimum(lo + rng.integers(0, 100, lo.shape), 127)
+    w = np.abs(rng.standard_normal((ng, 2))).astype(np.float32)
+    _write_index(cache, lo, hi, w)
+    q = W.make_q(1, hq, seed=5).cuda()
+    q8 = query8(U.f64(q)[0])
+    pos, neg = np.maximum(q8, 0), np.minimum(q8, 0)
+    s = (pos @ hi.T + neg @ lo.T).max(0).astype(np.float64)      # whole numbers below 2^22
+    score = s * np.where(s >= 0, w[:, 0], w[:, 1]).astype(np.float64)     # 22 x 24 bits: exact
+    order = sorted(range(ng), key=lambda g: (-score[g], g))
+    for n in (1, 100, ng - 1):
+        assert run(cache, [0], q, n, 0, 0)[0, 0].tolist() == sorted(order[:n])
+
+
+def test_a_sequence_too_long_is_refused():
+    O = U.lib()
+    cache = O.OscarCache(1, 1, 128 * 12001)
+    k = torch.zeros((128 * 12001, 1, 128), dtype=torch.bfloat16, device="cuda")
+    cache.append([0], [0, 128 * 12001], k, k)
+    cache.enable_index()
+    cache.update_index([0])
+    out = torch.zeros((1, 1, 5), dtype=torch.int32, device="cuda")
+    q = W.make_q(1, 1, seed=5).cuda()
+    with pytest.raises(O.OscarError) as e:
+        cache.select_groups([0], q, 1, out)
+    assert e.value.status == O.OSCAR_ERR_UNSUPPORTED
+    out = torch.zeros((1, 1, 12001), dtype=torch.int32, device="cuda")
+    cache.select_groups([0], q, 1, out)                          # all of them: nothing to choose
+    assert out[0, 0].tolist() == list(range(12001))
+
+
 def test_queries_at_the_edges():
     """Zero, tiny, huge and non-finite queries choose what the definition says."""
     cache = make([1920], 2, seed=8)
