@@ -1272,7 +1272,10 @@ oscar_status oscar_cache_read(oscar_cache* c, int32_t n_seqs, const int32_t* seq
     if (!aligned(k_out, 16) || !aligned(v_out, 16))
       return fail(OSCAR_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
     if (rows == 0 || (!k_out && !v_out)) return ok();
-    if (k_out == v_out) return fail(OSCAR_ERR_INVALID_ARG, "k_out and v_out are the same buffer");
+    const int64_t bytes = rows * c->cfg.num_kv_heads * kHeadDim * (type == OSCAR_F32 ? 4 : 2);
+    const intptr_t ka = reinterpret_cast<intptr_t>(k_out), va = reinterpret_cast<intptr_t>(v_out);
+    if (k_out && v_out && ka < va + bytes && va < ka + bytes)
+      return fail(OSCAR_ERR_INVALID_ARG, "k_out and v_out overlap");
     DeviceGuard dg(c->cfg.device);
     if (dg.err != cudaSuccess) return cuda_fail(dg.err, "cudaSetDevice");
     if (k_out && (s = device_view_as(k_out, "k_out", c->cfg.device, &k_out, false)) != OSCAR_OK) return s;

@@ -347,7 +347,10 @@ class RotaryConfig:
         self.interleaved = bool(cfg.interleaved)
         self._table = oscar_rotary_table()
         _check(_lib.oscar_rotary_prepare(ctypes.byref(cfg), ctypes.byref(self._table)))
-        self.address = ctypes.addressof(self._table)
+
+    @property
+    def address(self) -> int:      # of this object's own table: copies have theirs
+        return ctypes.addressof(self._table)
 
 
 def make_rotary_config(rotary_dim: int = HEAD_DIM, base: float = 10000.0, interleaved: bool = False,

@@ -230,6 +230,8 @@ def test_refusals():
     refused(bad, [-1], [0], [0])
     refused(bad, [1], [0], [1])
     refused(bad, [0], [0], [300], k, k)
+    both = torch.zeros((301, 2, 128), dtype=torch.bfloat16, device="cuda")
+    refused(bad, [0], [0], [300], both[:300], both[1:])      # the buffers overlap
     refused(bad, [0], [0], [300], k.cpu(), v)
     flat = torch.zeros(300 * 256 + 8, device="cuda")
     refused(bad, [0], [0], [300], flat[2:2 + 300 * 256].view(300, 2, 128), v)

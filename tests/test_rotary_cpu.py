@@ -1,7 +1,9 @@
 """Rotary configuration on the host: frequencies against the formulas in
 Python floats, and the refusals that need no GPU."""
+import copy
 import ctypes
 import math
+import pickle
 
 import pytest
 import torch
@@ -158,3 +160,15 @@ def test_binding_refusals(O):
     with pytest.raises(ValueError, match="float32"):
         O.oscar_cache_read(None, [0], [0], [4], torch.zeros((4, 1, 128)),
                            torch.zeros((4, 1, 128), dtype=torch.bfloat16))
+
+
+def test_copies_have_their_own_table(O):
+    """A copied or unpickled configuration does not point into the original."""
+    cfg = O.make_rotary_config(rotary_dim=64, base=500.0)
+    table = bytes(cfg._table)
+    deep, back, shallow = copy.deepcopy(cfg), pickle.loads(pickle.dumps(cfg)), copy.copy(cfg)
+    assert deep.address != cfg.address and back.address != cfg.address
+    del cfg
+    for c in (deep, back, shallow):
+        assert c.address == ctypes.addressof(c._table)
+        assert bytes((ctypes.c_char * ctypes.sizeof(c._table)).from_address(c.address)) == table
