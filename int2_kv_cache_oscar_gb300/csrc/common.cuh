@@ -291,14 +291,16 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float x) {
 //
 // MODE 1 and 2 read the slots higher up: at bits 4 to 9 (i <= 1 after a 4-bit
 // left shift, i >= 5 after a 6-bit right shift; two shifts a word instead of
-// one) and at bits 6 to 9 (left by 6, 6, 4, in place, right by 4, 4, 6; four
-// shifts).  The tensor core aligns products by their operands' nominal
-// exponents and drops what falls below, and a subnormal operand sits 10 - p
-// bits under its nominal exponent: at p = 0 the products of factors well below
-// the largest lose their last bits.
+// one) and at bits 7 to 10 (left by 7 and 3, right by 1 and 5; four shifts).
+// The tensor core aligns products by their operands' nominal exponents and
+// drops what falls below, and a subnormal operand sits 10 - p bits under its
+// nominal exponent: at p = 0 the products of factors well below the largest
+// lose their last bits.  (At p = 9 the codes 2 and 3 reach bit 10, the lowest
+// exponent bit, and are the normal numbers 2^-14 and 1.5 2^-14: still
+// code * 2^(p - 24).)
 template <int MODE = 0>
 __host__ __device__ constexpr int frag_p(int i) {
-  return 2 * i + (MODE == 2   ? (i <= 1 ? 6 : i == 2 ? 4 : i <= 4 ? 0 : i <= 6 ? -4 : -6)
+  return 2 * i + (MODE == 2   ? (i <= 1 ? 7 : i <= 3 ? 3 : i <= 5 ? -1 : -5)
                   : MODE == 1 ? (i <= 1 ? 4 : i <= 4 ? 0 : -6)
                               : (i <= 4 ? 0 : -10));
 }

@@ -177,10 +177,17 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
   // Bit positions at which codes are read (see frag_p).  Score sums over outlier
   // keys are off by 1e-6 to 4e-6 of the score in mode 0 (1.6e-5 of the outputs)
   // and at float32 rounding in mode 1 (mode 2 changes nothing more); with that
-  // the value sums are off by 1.1e-5 of the outputs in mode 0, 2.1e-6 in mode 1,
-  // 1.2e-6 in mode 2 (32-bit products and sums: 1.4e-6).  bf16 outputs round by
-  // 1.4e-3, so mode 2 is for float32 ones: it takes 5 % longer.
+  // the value sums are off by 1.1e-5 of the outputs in mode 0.  bf16 outputs
+  // round by 1.4e-3; for float32 ones the values are read in mode 2 and every
+  // k-step's products are added in float32 registers (kSteps): the tensor core
+  // cuts its sums off instead of rounding them, and sums of non-negative codes
+  // and factors all lose in one direction, while the outputs are small
+  // differences of them and the zero terms.  26 shapes of 84 to 130K tokens, 1 to
+  // 159 entries: off by 0.1 to 2.9e-6 with the tensor core's sums over a group at
+  // bits 6 to 9, 0.1 to 1.9e-6 with those over a k-step, 0.1 to 1.2e-6 with both
+  // (32-bit products and sums: 0.1 to 1.7e-6), in the same time.
   constexpr int kKeyMode = SPARSE ? 1 : 0, kValueMode = LISTED == 2 ? 2 : 0;
+  constexpr bool kSteps = LISTED == 2;
   constexpr int kStages = DecSmem::kStages;
   constexpr int kStageBytes = B::kBytes;
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -615,6 +622,11 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
         float pacc[8][4];
 #pragma unroll
         for (int mt = 0; mt < 8; ++mt) pacc[mt][0] = pacc[mt][1] = pacc[mt][2] = pacc[mt][3] = 0.0f;
+        const float2 al2 = make_float2(alpha, alpha);
+        if constexpr (kSteps) {
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt) o_acc[mt] = __fmul2_rn(o_acc[mt], al2);
+        }
 #pragma unroll
         for (int jh = 0; jh < 2; ++jh) {
           uint2 vw[8];
@@ -645,14 +657,19 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
                 uint32_t a0, a1, a2, a3;
                 frag_a_dyn<kValueMode>(kk2, vw[mt].x, vw[mt].y, a0, a1, a2, a3);
                 mma_f16_16816(pacc[mt], a0, a1, a2, a3, b0, b1);
+                if constexpr (kSteps) {
+                  o_acc[mt] = __fadd2_rn(o_acc[mt], make_float2(pacc[mt][0] - pacc[mt][1], pacc[mt][2] - pacc[mt][3]));
+                  pacc[mt][0] = pacc[mt][1] = pacc[mt][2] = pacc[mt][3] = 0.0f;
+                }
               }
             }
           }
         }
-        const float2 al2 = make_float2(alpha, alpha);
+        if constexpr (!kSteps) {
 #pragma unroll
-        for (int mt = 0; mt < 8; ++mt)
-          o_acc[mt] = __ffma2_rn(o_acc[mt], al2, make_float2(pacc[mt][0] - pacc[mt][1], pacc[mt][2] - pacc[mt][3]));
+          for (int mt = 0; mt < 8; ++mt)
+            o_acc[mt] = __ffma2_rn(o_acc[mt], al2, make_float2(pacc[mt][0] - pacc[mt][1], pacc[mt][2] - pacc[mt][3]));
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.empty[s]);
