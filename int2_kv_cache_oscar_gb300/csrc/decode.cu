@@ -184,10 +184,16 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
   // and factors all lose in one direction, while the outputs are small
   // differences of them and the zero terms.  26 shapes of 84 to 130K tokens, 1 to
   // 159 entries: off by 0.1 to 2.9e-6 with the tensor core's sums over a group at
-  // bits 6 to 9, 0.1 to 1.9e-6 with those over a k-step, 0.1 to 1.2e-6 with both
-  // (32-bit products and sums: 0.1 to 1.7e-6), in the same time.
+  // bits 6 to 9, 0.1 to 1.9e-6 with sums over a k-step, 0.1 to 1.2e-6 with those
+  // at bits 7 to 10 (32-bit products and sums: 0.1 to 1.7e-6), in the same time.
   constexpr int kKeyMode = SPARSE ? 1 : 0, kValueMode = LISTED == 2 ? 2 : 0;
   constexpr bool kSteps = LISTED == 2;
+  // bf16 outputs from listed groups take the value factors p s^V in fp16 alone,
+  // off by 2^-11 at most where the output is rounded by 2^-8: errors of 1.47e-3
+  // to 1.67e-3 stay as they are, or grow by 6 % at most.  Without a remainder
+  // column the two columns of a head take half of the tokens each, so that no
+  // lane needs its partner's factors (256 rows of 64 entries 63.4 -> 57.2 us).
+  constexpr bool kHalfFactors = LISTED == 1;
   constexpr int kStages = DecSmem::kStages;
   constexpr int kStageBytes = B::kBytes;
   extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -615,7 +621,8 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
       }
       __syncwarp();
 
-      // ---- P.V: O^T[channel][head x {hi, lo}] = codes^V^T x (p * s^V); each
+      // ---- P.V: O^T[channel][head x {hi, lo}] = codes^V^T x (p * s^V) (or head x
+      // {tokens, other tokens}, see kHalfFactors); each
       // k-step's factors are built once and feed all 8 channel m-tiles
       {
         const float* pbh = S.pbuf[warp][hb];
@@ -650,7 +657,13 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
               const float sa = gr == 0 ? s0.x : gr == 1 ? s0.y : gr == 2 ? s0.z : s0.w;
               const float sb = gr == 0 ? s1.x : gr == 1 ? s1.y : gr == 2 ? s1.z : s1.w;
               uint32_t b0, b1;
-              split_exchange(pr.x * sa, pr.y * sb, lo_lane, b0, b1);
+              if constexpr (kHalfFactors) {
+                const uint32_t x = pack_half2(pr.x * sa, pr.y * sb);
+                b0 = lo_lane ? 0u : x;
+                b1 = lo_lane ? x : 0u;
+              } else {
+                split_exchange(pr.x * sa, pr.y * sb, lo_lane, b0, b1);
+              }
 #pragma unroll
               for (int h2 = 0; h2 < 2; ++h2) {
                 const int mt = 2 * gr + h2;
@@ -668,7 +681,9 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
         if constexpr (!kSteps) {
 #pragma unroll
           for (int mt = 0; mt < 8; ++mt)
-            o_acc[mt] = __ffma2_rn(o_acc[mt], al2, make_float2(pacc[mt][0] - pacc[mt][1], pacc[mt][2] - pacc[mt][3]));
+            o_acc[mt] = __ffma2_rn(o_acc[mt], al2,
+                                   kHalfFactors ? make_float2(pacc[mt][0] + pacc[mt][1], pacc[mt][2] + pacc[mt][3])
+                                                : make_float2(pacc[mt][0] - pacc[mt][1], pacc[mt][2] - pacc[mt][3]));
         }
       }
       __syncwarp();
