@@ -26,8 +26,10 @@
 // the first block's shared memory; that block then chooses.  A slice's codes
 // come by bulk copies of up to 256 groups (64 KB), two in flight, requested
 // before the queries are turned.  Four lanes score a group: each holds a
-// quarter of the query bytes of four heads in registers, so a group costs a
-// warp 12 instructions (a warp per group, with a warp sum per head, took 51).
+// quarter of the query bytes of four heads in registers (a warp per group,
+// with a warp sum per head, took four times the instructions), then each makes
+// the key of one of its warp's four batches (8.9 -> 8.3 us for 256 rows of 256
+// groups; every lane making every key costs four times the key's operations).
 // The m-th largest key is found by a radix histogram, starting at the first
 // bit in which the row's keys differ, and, once at most 32 keys share a digit,
 // by ranking those.  Everything is latency and, for many rows, instructions.
@@ -119,9 +121,9 @@ __global__ void __launch_bounds__(kIdxThreads)
 // ------------------------------------------------------------ selection
 
 // Order-preserving key of the exact product s w (|s| <= 2^22, w >= 0 finite):
-// sign, exponent and the product's 46 bits, in whole-number operations (a
-// float64 instruction costs a warp 64 to 76 cycles on this chip: five of them
-// per eight groups were three quarters of the scoring time).
+// sign, exponent and the product's 46 bits, in whole-number operations (as
+// float64 products, whose instructions cost a warp 64 to 76 cycles on this
+// chip, 256 rows of 256 groups took 10.0 us instead of 8.9).
 __device__ __forceinline__ uint64_t score_key(int s, float w) {
   const uint32_t wb = __float_as_uint(w);
   const uint32_t ex = wb >> 23;
