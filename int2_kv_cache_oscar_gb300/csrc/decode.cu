@@ -818,6 +818,10 @@ __global__ void __launch_bounds__(kCombineThreads)
     abort_flag = 0;
     fence_mbar_init();
   }
+  // Without a unit no main kernel ran: the kernel before this grid is the
+  // caller's or another of the library's, which may still be writing the
+  // queries, the new token or the window.
+  if (T == 0) grid_dependency_wait();
   qs[h][c] = active ? __uint_as_float((uint32_t)p.h.q[((int64_t)b * p.h.hq + j * p.h.q_group + p.h.q_head0 + h) * kHeadDim + c] << 16)
                     : 0.0f;
   if (fused && tid < 32) {
@@ -1039,6 +1043,10 @@ __global__ void __launch_bounds__(ROW ? 128 * kMaxGqaInt2 : 128, ROW ? 1 : 8)
     __syncthreads();
     return is_max ? fmaxf(fmaxf(r[0], r[1]), fmaxf(r[2], r[3])) : (r[0] + r[1]) + (r[2] + r[3]);
   };
+
+  // Without a unit no main kernel ran: the kernel before this grid may still be
+  // writing the queries or the window.
+  if (p.h.n_units == 0) grid_dependency_wait();
 
   // ---- window (the kernels before the main one are complete: it triggers
   // this grid only after its own wait): this warp's share of the outputs, the

@@ -64,3 +64,45 @@ def test_serving_loop(meta):
         s = U.f64(qr)[0, 4 * j:4 * j + 4] @ U.f64(k)[:, j].T / np.sqrt(128)
         ref = OR.softmax_attend(s.T, U.f64(v)[:, j])
         assert np.abs(ref - U.f64(full)[0, 4 * j:4 * j + 4]).max() <= 2e-3     # the decode's own bound
+
+
+@pytest.mark.parametrize("how", ["all", "listed", "fused"])
+def test_short_sequences_right_after_rotation(how):
+    """Sequences without a group: the window is attended by the only kernel of
+    the decode, which must not read queries (or a new token) before the rotation
+    has written them."""
+    O = U.lib()
+    n, hkv, hq, steps = 16, 8, 32, 24
+    gen = torch.Generator().manual_seed(82)
+    cfg = O.make_rotary_config(128)
+    k, v = (torch.randn((n * 90, hkv, 128), generator=gen).bfloat16().cuda() for _ in range(2))
+    cu, ids = [90 * i for i in range(n + 1)], list(range(n))
+    caches = [O.OscarCache(n, hkv, 128) for _ in range(2)]
+    for c in caches:
+        c.append(ids, cu, k, v)
+    ws = caches[0].workspace(n, hq)
+    groups = torch.zeros((n, hkv, 1), dtype=torch.int32, device="cuda")
+    v_new = torch.randn((n, hkv, 128), generator=gen).bfloat16().cuda()
+
+    def step(cache, q, k_new, wait):
+        qr, kr = torch.zeros_like(q), torch.zeros_like(k_new)
+        out = torch.zeros_like(q)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(1 << 20)         # both launches are enqueued before the first one runs
+        O.oscar_rotary(cfg, pos, q, k_new, qr, kr)
+        if wait:
+            torch.cuda.synchronize()
+        if how == "all":
+            cache.decode(ids, qr, hq, out, ws)
+        elif how == "listed":
+            cache.sparse_decode(ids, qr, hq, groups, out, ws)
+        else:
+            cache.append_decode(ids, kr, v_new, qr, hq, out, ws)
+        torch.cuda.synchronize()
+        return out
+
+    for i in range(steps):
+        pos = torch.full((n,), 7 * i, dtype=torch.int32, device="cuda")
+        q = torch.randn((n, hq, 128), generator=gen).bfloat16().cuda()
+        k_new = torch.randn((n, hkv, 128), generator=gen).bfloat16().cuda()
+        assert torch.equal(step(caches[0], q, k_new, False), step(caches[1], q, k_new, True)), i
