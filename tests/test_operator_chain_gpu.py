@@ -106,3 +106,59 @@ def test_short_sequences_right_after_rotation(how):
         q = torch.randn((n, hq, 128), generator=gen).bfloat16().cuda()
         k_new = torch.randn((n, hkv, 128), generator=gen).bfloat16().cuda()
         assert torch.equal(step(caches[0], q, k_new, False), step(caches[1], q, k_new, True)), i
+
+
+@pytest.mark.parametrize("meta", [32, 16])
+def test_queued_calls_match_waited_ones(meta):
+    """Every call of the loop enqueued behind a busy stream, so that each kernel
+    may start while the one before it finishes, against the same calls with a
+    wait after each: the same bits."""
+    O = U.lib()
+    hkv, hq, keep = 2, 8, 3
+    lens = [700, 383, 90, 127, 255]
+    n, ids = len(lens), list(range(len(lens)))
+    gen = torch.Generator().manual_seed(83)
+    cfg = O.make_rotary_config(96, interleaved=True, scaling="yarn", factor=4.0, original_length=4096)
+    kv = [W.make_sequence_kv(m, hkv, W.LLAMA_RECIPE, gen) for m in lens]
+    steps = [torch.randn((n, hq + 2 * hkv, 128), generator=gen).bfloat16().cuda() for _ in range(6)]
+
+    def run(queued):
+        cache = O.OscarCache(n, hkv, 1200, meta_bits=meta)
+        cache.enable_index()
+        for i, (k, v) in enumerate(kv):
+            cache.append([i], [0, lens[i]], k.cuda(), v.cuda())
+        cache.update_index(ids)
+        ws, made = cache.workspace(n, hq), []
+        for step, x in enumerate(steps):
+            pos = torch.tensor([cache.length(i) for i in ids], dtype=torch.int32).cuda()
+            q, k, v = x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:].contiguous()
+            new = lambda *shape, dtype=torch.bfloat16: torch.zeros(shape, dtype=dtype, device="cuda")
+            qr, kr, out, dense, fused = new(n, hq, 128), new(n, hkv, 128), new(n, hq, 128), new(n, hq, 128), new(n, hq, 128)
+            groups, lse = new(n, hkv, keep, dtype=torch.int32), new(n, hq, dtype=torch.float32)
+            tail = [cache.length(i) - 50 for i in ids]
+            rows = [new(50 * n + n, hkv, 128, dtype=torch.float32) for _ in range(2)]
+            calls = [lambda: O.oscar_rotary(cfg, pos, q, k, qr, kr),
+                     lambda: cache.append(ids, list(range(n + 1)), kr, v),
+                     lambda: cache.update_index(ids),
+                     lambda: cache.select_groups(ids, qr, hq, groups, keep_last=1),
+                     lambda: cache.sparse_decode(ids, qr, hq, groups, out, ws, lse=lse),
+                     lambda: O.oscar_rotary(cfg, pos, qr, transpose=True),
+                     lambda: cache.decode(ids, qr, hq, dense, ws),
+                     lambda: O.oscar_rotary(cfg, pos, kr),
+                     lambda: cache.append_decode(ids, kr, v, qr, hq, fused, ws),
+                     lambda: cache.read(ids, tail, [t + 51 for t in tail], *rows),
+                     lambda: cache.update_index(ids)]
+            torch.cuda.synchronize()
+            if queued:
+                torch.cuda._sleep(1 << 22)
+            for call in calls:
+                call()
+                if not queued:
+                    torch.cuda.synchronize()
+            torch.cuda.synchronize()
+            O.oscar_cache_check(cache.handle)
+            made += [qr, kr, groups, out, lse, dense, fused, *rows]
+        return made
+
+    for a, b in zip(run(True), run(False)):
+        assert torch.equal(a, b)
