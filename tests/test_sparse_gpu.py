@@ -15,7 +15,10 @@ x_t = p_t s_t 2^(F - p) with 2^14 <= 2^F S < 2^15 for the head's largest value
 scale S, and p <= 8.  Normal x_t are off by 2^-11 x_t at most, subnormal ones by
 2^-25, which is at most 2^-25 2^8 2^-14 S = 2^-31 S of p_t s_t.  The weights
 p_t / l sum to 1 and l >= 1, so n tokens' value sums are off by
-3 (2^-11 + n 2^-31) S at most."""
+3 (2^-11 + n 2^-31) S at most, S in the first term the largest scale attended.
+float32 outputs take them as fp16 hi + lo, p <= 9: where the remainder is
+subnormal it is off by 2^-25, 2^-30 S of p_t s_t (this counts where S, the largest
+of the whole sequence, is far above the scales attended): 3 n 2^-30 S."""
 import numpy as np
 import pytest
 import torch
@@ -59,8 +62,11 @@ def check_head(q, h, got, lse, scale, half, largest):
         a.append((np.abs(h.window_k) @ np.abs(q).T).max() * sc)
     d = 2.0 ** -16 * max(a) + 2.0 ** -20
     room = (np.expm1(2 * d) + 2.0 ** -16) * np.abs(OR.decode_values(h)).max()
-    if half == 2.0 ** -8 and h.num_groups:
-        room += 3 * (2.0 ** -11 + h.length * 2.0 ** -31) * largest
+    if h.num_groups:
+        if half == 2.0 ** -8:
+            room += 3 * (2.0 ** -11 * h.values.scale.max() + h.length * 2.0 ** -31 * largest)
+        else:
+            room += 3 * h.length * 2.0 ** -30 * largest
     err = np.abs(got - ref)
     assert np.all(err <= room + half * (np.abs(ref) + room)), f"{err.max():.3e} > {room:.3e}"
     assert np.all(np.abs(lse - rl) <= d + 2.0 ** -20 * (1 + np.abs(rl)))
@@ -205,6 +211,21 @@ def test_rows_with_nothing():
     # every row of the call empty
     out, lse = check(cache, [0, 3], q[:2], torch.full((2, 2, 3), -1, dtype=torch.int32, device="cuda"), torch.bfloat16)
     assert torch.all(out == 0)
+
+
+@pytest.mark.parametrize("factor", [300.0, 1e4])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_token_of_large_values(factor, dtype):
+    """One token's values far above the others': the value factors are scaled
+    by the sequence's largest, also where its group is not listed."""
+    gen = torch.Generator().manual_seed(51)
+    k, v = W.make_sequence_kv(1100, 2, W.LLAMA_RECIPE, gen)
+    v[300] *= factor
+    cache = U.lib().OscarCache(1, 2, 1300)
+    U.append_all(cache, [0], [k], [v], chunk=4096)
+    q = W.make_q(1, 8, seed=52).cuda()
+    for idx in ([0, 2, 5], [0, 1, 4, 7], [1, 3, 6], [7]):
+        check(cache, [0], q, torch.tensor(idx, dtype=torch.int32).repeat(1, 2, 1).cuda(), dtype)
 
 
 def test_all_groups_listed_is_the_full_decode():
