@@ -510,9 +510,10 @@ oscar_status oscar_select_groups(oscar_cache* cache, int32_t n_seqs, const int32
  *   lse       float32 [n_seqs, num_q_heads] or NULL: ln sum exp(score) over the
  *             attended tokens (natural log, scores times softmax_scale)
  * A row with nothing to attend (no valid entry, empty window) gets zeros and
- * an lse of -infinity.  q, out and lse may be device or page-locked host
- * memory; every other argument, the workspace and the stream order are those
- * of oscar_decode_attention.
+ * an lse of -infinity; a query head that is not finite and has a token to
+ * attend gets NaN outputs and lse, the other heads are unaffected.  q, out and
+ * lse may be device or page-locked host memory; every other argument, the
+ * workspace and the stream order are those of oscar_decode_attention.
  */
 oscar_status oscar_sparse_decode_attention(oscar_cache* cache, int32_t n_seqs, const int32_t* seq_ids,
                                            const void* q, int32_t num_q_heads, float softmax_scale,

@@ -1120,7 +1120,8 @@ __global__ void __launch_bounds__(ROW ? 128 * kMaxGqaInt2 : 128, ROW ? 1 : 8)
       acc = *reinterpret_cast<const float4*>(&S.o[warp][4 * lane]);
     }
     M = head_reduce(mw, true);
-    L = head_reduce(lane == 0 && mw != -INFINITY ? lw * exp2f(mw - M) : 0.0f, false);
+    // (no maximum: a warp without a token, lw = 0, or without a finite score, lw = NaN)
+    L = head_reduce(lane != 0 ? 0.0f : mw == -INFINITY ? lw : lw * exp2f(mw - M), false);
     {
       const float f = mw == -INFINITY ? 0.0f : exp2f(mw - M);
       acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
@@ -1301,8 +1302,9 @@ __global__ void __launch_bounds__(ROW ? 128 * kMaxGqaInt2 : 128, ROW ? 1 : 8)
   __syncwarp();
   *reinterpret_cast<float4*>(&S.o[warp][4 * lane]) = acc;
   __syncthreads();
-  // a row without a token: zeros, log-sum-exp -inf
-  const bool none = M == -INFINITY;
+  // a row without a token: zeros, log-sum-exp -inf.  The maxima pass over NaN
+  // scores, so a row whose scores are all NaN has none either, but the weight NaN.
+  const bool none = M == -INFINITY && L == 0.0f;
   const float(*o)[kHeadDim] = &S.o[kListHeads * hl];
   const float O = (o[0][at] + o[1][at]) + (o[2][at] + o[3][at]);
   const float ov = none ? 0.0f : O / L;

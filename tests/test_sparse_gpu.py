@@ -364,3 +364,46 @@ def test_refusals():
     refused(lambda: cache.sparse_decode([0], q, 4, groups, out, ws))
     with pytest.raises(ValueError):
         cache.sparse_decode([0], q, 4, groups[:, :1].contiguous(), out, ws)
+
+
+NAN_SHAPES = [([1000], 1, 4, 3), ([1030, 900], 2, 6, 4), ([2048, 400], 1, 8, 5),      # the combine per query head
+              ([300 + i for i in range(40)], 2, 8, 2), ([256 + i % 2 for i in range(35)], 1, 7, 2)]   # per KV head
+
+
+@pytest.mark.parametrize("lens,hkv,hq,n", NAN_SHAPES)
+@pytest.mark.parametrize("attend", ["groups", "window", "both"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_query_that_is_not_finite(lens, hkv, hq, n, attend, value, dtype):
+    """NaN outputs and log-sum-exp for that query head wherever it has a token
+    to attend (its scores are NaN, as are the full decode's outputs), zeros and
+    -inf where it has none; the other heads' bits do not change."""
+    cache = make([x // 128 * 128 for x in lens] if attend == "groups" else lens, hkv, seed=hq + n)
+    ids, gqa = list(range(len(lens))), hq // hkv
+    groups = lists(cache, ids, n, 21, 0.2)
+    if attend == "window":
+        groups.fill_(-1)
+    q = W.make_q(len(lens), hq, seed=8).cuda()
+    ws = cache.workspace(len(lens), hq)
+
+    def call(x):
+        out, lse = torch.empty((len(lens), hq, 128), dtype=dtype, device="cuda"), torch.empty((len(lens), hq), device="cuda")
+        cache.sparse_decode(ids, x, hq, groups, out, ws, lse)
+        U.lib().oscar_cache_check(cache.handle)
+        return out, lse
+    out, lse = call(q)
+    bad = torch.zeros((len(lens), hq), dtype=torch.bool, device="cuda")
+    bad[0, 1] = bad[-1, -1] = bad[len(lens) // 2, 0] = True
+    qb = q.clone()
+    qb[..., 37] = torch.where(bad, torch.full_like(q[..., 37], value), q[..., 37])
+    got, got_lse = call(qb)
+    used = torch.tensor([[any(0 <= g < cache.length(s) // 128 for g in groups[i, h // gqa].tolist()) or
+                          cache.length(s) % 128 > 0 for h in range(hq)] for i, s in enumerate(ids)], device="cuda")
+    nan = bad & used
+    assert nan.any()
+    assert torch.all(got[nan].isnan()) and torch.all(got_lse[nan].isnan())
+    assert torch.equal(got[~nan], out[~nan]) and torch.equal(got_lse[~nan], lse[~nan])
+    assert torch.all(got[bad & ~used] == 0) and torch.all(got_lse[bad & ~used] == -float("inf"))
+    full = torch.empty((len(lens), hq, 128), device="cuda")
+    cache.decode_f32(ids, qb, hq, full, ws)
+    assert torch.all(full[bad].isnan())
