@@ -153,6 +153,9 @@ oscar_status oscar_cache_reset(oscar_cache* cache, int32_t seq, void* stream);
 /* Current length (tokens) of slot `seq`. */
 oscar_status oscar_cache_length(const oscar_cache* cache, int32_t seq, int32_t* out_len);
 
+/* The configuration the cache was created with (meta_bits 32 or 16, never 0). */
+oscar_status oscar_cache_get_config(const oscar_cache* cache, oscar_cache_config* out);
+
 /*
  * Append new tokens to `n_seqs` sequences (prefill chunks or single decode
  * tokens; the method's compression step, OScaR abstract / ai-papers.net

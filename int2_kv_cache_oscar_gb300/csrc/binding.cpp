@@ -6,7 +6,8 @@
 //
 // Every function returns the oscar_status of the C call (0: done) and raises
 // TypeError or ValueError for what the C ABI cannot see behind a pointer:
-// dtype, shape, contiguity, the cache's KV heads (hkv; -1: unchecked).
+// dtype, shape, contiguity, the cache's KV heads (those of the handle, always;
+// an argument hkv >= 0 is the caller's own expectation and checked beside them).
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -83,9 +84,18 @@ int32_t float_type(const at::Tensor& t, const char* name) {
   refuse(PyExc_ValueError, "%s must be torch.bfloat16 or torch.float32, got %s", name, type_name(t.scalar_type()));
 }
 
-void heads(const at::Tensor& t, int64_t dim, int64_t hkv, const char* name) {
-  if (hkv >= 0 && t.dim() > dim && t.size(dim) != hkv)
-    refuse(PyExc_ValueError, "%s has %lld KV heads, the cache %lld", name, (long long)t.size(dim), (long long)hkv);
+// KV heads of the cache; -1 for a NULL handle, which the C call refuses.
+int64_t cache_heads(const oscar_cache* cache) {
+  oscar_cache_config cfg;
+  return cache != nullptr && oscar_cache_get_config(cache, &cfg) == OSCAR_OK ? cfg.num_kv_heads : -1;
+}
+
+// The KV-head dimension of a buffer: the kernels index it with the cache's
+// number, so a smaller one would be read or written past its end.
+void heads(const at::Tensor& t, int64_t dim, int64_t hkv, const oscar_cache* cache, const char* name) {
+  for (const int64_t want : {hkv, cache_heads(cache)})
+    if (want >= 0 && t.dim() > dim && t.size(dim) != want)
+      refuse(PyExc_ValueError, "%s has %lld KV heads, the cache %lld", name, (long long)t.size(dim), (long long)want);
 }
 
 int64_t integer(PyObject* o) {
@@ -219,6 +229,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // handle, hkv, seq_ids, start, end, k_out, v_out, stream
 PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return call(n, 8, [&] {
+    auto* cache = address<oscar_cache>(a[0]);
     const int64_t hkv = integer(a[1]);
     const std::vector<int32_t> ids = integers(a[2], "seq_ids"), start = integers(a[3], "start"),
                                end = integers(a[4], "end");
@@ -237,10 +248,9 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
         first = &t;
         type = float_type(t, name);
       }
-      heads(t, 1, hkv, name);
+      heads(t, 1, hkv, cache, name);
       out[i] = dense(t, first->scalar_type(), {rows, first->dim() == 3 ? first->size(1) : (int64_t)1, kDim}, name);
     }
-    auto* cache = address<oscar_cache>(a[0]);
     void* stream = stream_of(a[7]);
     return unlocked([&] {
       return oscar_cache_read(cache, (int32_t)ids.size(), ids.data(), start.data(), end.data(), type, out[0], out[1],
@@ -262,9 +272,9 @@ PyObject* index_update(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // A group list [n, kv heads, entries]
-int32_t* group_list(PyObject* o, int64_t n, int64_t hkv, int32_t* entries) {
+int32_t* group_list(PyObject* o, int64_t n, int64_t hkv, const oscar_cache* cache, int32_t* entries) {
   const at::Tensor& t = tensor(o, "groups");
-  heads(t, 1, hkv, "groups");
+  heads(t, 1, hkv, cache, "groups");
   void* p = dense(t, at::kInt, {n, -1, -1}, "groups");
   if (t.size(2) > INT32_MAX) refuse(PyExc_ValueError, "groups has too many entries");
   *entries = (int32_t)t.size(2);
@@ -278,9 +288,9 @@ PyObject* select_groups(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t hq = integer32(a[4], "num_q_heads");
     const void* q = dense(tensor(a[3], "q"), at::kBFloat16, {(int64_t)ids.size(), hq, kDim}, "q");
     int32_t entries = 0;
-    int32_t* groups = group_list(a[5], (int64_t)ids.size(), integer(a[1]), &entries);
-    const int32_t first = integer32(a[6], "keep_first"), last = integer32(a[7], "keep_last");
     auto* cache = address<oscar_cache>(a[0]);
+    int32_t* groups = group_list(a[5], (int64_t)ids.size(), integer(a[1]), cache, &entries);
+    const int32_t first = integer32(a[6], "keep_first"), last = integer32(a[7], "keep_last");
     void* stream = stream_of(a[8]);
     return unlocked([&] {
       return oscar_select_groups(cache, (int32_t)ids.size(), ids.data(), q, hq, entries, first, last, groups, stream);
@@ -298,7 +308,8 @@ PyObject* sparse_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (scale == -1.0 && PyErr_Occurred()) throw Raised();
     const void* q = dense(tensor(a[3], "q"), at::kBFloat16, {b, hq, kDim}, "q");
     int32_t entries = 0;
-    const int32_t* groups = group_list(a[6], b, integer(a[1]), &entries);
+    auto* cache = address<oscar_cache>(a[0]);
+    const int32_t* groups = group_list(a[6], b, integer(a[1]), cache, &entries);
     const at::Tensor& o = tensor(a[7], "out");
     const int32_t type = float_type(o, "out");
     void* out = dense(o, o.scalar_type(), {b, hq, kDim}, "out");
@@ -306,7 +317,6 @@ PyObject* sparse_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* w = dense(ws, at::kByte, ws.sizes(), "workspace");
     float* lse = a[9] == Py_None ? nullptr : static_cast<float*>(dense(tensor(a[9], "lse"), at::kFloat, {b, hq}, "lse"));
     const size_t w_bytes = (size_t)ws.numel();
-    auto* cache = address<oscar_cache>(a[0]);
     void* stream = stream_of(a[10]);
     return unlocked([&] {
       return oscar_sparse_decode_attention(cache, (int32_t)b, ids.data(), q, hq, (float)scale, groups, entries, type, out,

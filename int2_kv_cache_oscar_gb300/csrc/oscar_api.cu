@@ -430,6 +430,13 @@ oscar_status oscar_cache_length(const oscar_cache* c, int32_t seq, int32_t* out_
   return ok();
 }
 
+oscar_status oscar_cache_get_config(const oscar_cache* c, oscar_cache_config* out) {
+  if (!c || !out) return fail(OSCAR_ERR_INVALID_ARG, "NULL argument");
+  *out = c->cfg;
+  out->meta_bits = c->meta16 ? 16 : 32;
+  return ok();
+}
+
 oscar_status oscar_quantize_append(oscar_cache* c, int32_t n_seqs, const int32_t* seq_ids, const int32_t* cu_new,
                                    const void* k, const void* v, void* stream) {
   try {

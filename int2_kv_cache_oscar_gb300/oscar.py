@@ -113,6 +113,7 @@ def _load() -> ctypes.CDLL:
         "oscar_rotary_prepare": [ctypes.POINTER(oscar_rotary_config), ctypes.POINTER(oscar_rotary_table)],
         "oscar_rotary": [P, ctypes.c_int64, P, I32, ctypes.POINTER(oscar_rotary_rows),
                          ctypes.POINTER(oscar_rotary_rows), I32, P],
+        "oscar_cache_get_config": [P, ctypes.POINTER(oscar_cache_config)],
         "oscar_cache_read": [P, I32, I32P, I32P, I32P, I32, P, P, P],
         "oscar_cache_export": [P, I32, P, P, P, P],
         "oscar_cache_import": [P, I32, I32, P, P, P, P],
@@ -245,6 +246,12 @@ def oscar_cache_length(handle, seq: int) -> int:
     out = ctypes.c_int32(0)
     _check(_lib.oscar_cache_length(handle, seq, ctypes.byref(out)))
     return out.value
+
+
+def oscar_cache_get_config(handle) -> oscar_cache_config:
+    out = oscar_cache_config()
+    _check(_lib.oscar_cache_get_config(handle, ctypes.byref(out)))
+    return out
 
 
 def oscar_quantize_append(handle, seq_ids: Sequence[int], cu_new: Sequence[int],
@@ -388,7 +395,9 @@ def oscar_cache_read(handle, seq_ids: Sequence[int], start: Sequence[int], end: 
                      k_out: Optional[torch.Tensor], v_out: Optional[torch.Tensor], stream=None, *,
                      num_kv_heads: int = -1) -> None:
     """Tokens start[i] .. end[i] - 1 of each slot seq_ids[i] as rows of k_out
-    and v_out [rows, kv heads, 128] (bf16 or float32; either may be None)."""
+    and v_out [rows, kv heads, 128] (bf16 or float32; either may be None).
+    Here and below the KV heads must be the cache's; num_kv_heads (-1: not
+    given) is checked beside them."""
     _check(_calls.read(handle, num_kv_heads, seq_ids, start, end, k_out, v_out, stream))
 
 
@@ -566,7 +575,7 @@ class OscarCache:
             raise ValueError(f"{name} has {t.shape[dim]} KV heads, the cache {self.num_kv_heads}")
 
     def read(self, seq_ids, start, end, k_out=None, v_out=None, stream=None):
-        oscar_cache_read(self.handle, seq_ids, start, end, k_out, v_out, stream, num_kv_heads=self.num_kv_heads)
+        oscar_cache_read(self.handle, seq_ids, start, end, k_out, v_out, stream)
 
     @property
     def block_bytes(self) -> int:
@@ -607,10 +616,9 @@ class OscarCache:
         oscar_index_update(self.handle, seq_ids, rebuild, stream)
 
     def select_groups(self, seq_ids, q, num_q_heads, groups, keep_first=0, keep_last=0, stream=None):
-        oscar_select_groups(self.handle, seq_ids, q, num_q_heads, groups, keep_first, keep_last, stream,
-                            num_kv_heads=self.num_kv_heads)
+        oscar_select_groups(self.handle, seq_ids, q, num_q_heads, groups, keep_first, keep_last, stream)
 
     def sparse_decode(self, seq_ids, q, num_q_heads, groups, out, workspace, lse=None, softmax_scale=0.0,
                       stream=None):
         oscar_sparse_decode_attention(self.handle, seq_ids, q, num_q_heads, softmax_scale, groups, out, workspace,
-                                      lse, stream, num_kv_heads=self.num_kv_heads)
+                                      lse, stream)

@@ -162,3 +162,41 @@ def test_queued_calls_match_waited_ones(meta):
 
     for a, b in zip(run(True), run(False)):
         assert torch.equal(a, b)
+
+
+def test_the_cache_s_kv_heads_are_checked_by_every_form_of_a_call():
+    """Buffers for another number of KV heads are refused by the functions and
+    by the methods (the kernels would run past them): nothing is enqueued."""
+    O = U.lib()
+    gen = torch.Generator().manual_seed(71)
+    k, v = W.make_sequence_kv(700, 4, W.LLAMA_RECIPE, gen)
+    cache = O.OscarCache(1, 4, 1000)
+    U.append_all(cache, [0], [k], [v])
+    cache.enable_index()
+    cache.update_index([0])
+    assert O.oscar_cache_get_config(cache.handle).num_kv_heads == 4
+    q, out = W.make_q(1, 8, seed=72).cuda(), torch.full((1, 8, 128), 7.0, device="cuda")
+    ws = cache.workspace(1, 8)
+    for heads in (1, 2, 3, 5, 8):
+        rows = torch.full((700, heads, 128), 7.0, device="cuda")
+        groups = torch.full((1, heads, 3), 7, dtype=torch.int32, device="cuda")
+        right = torch.empty((700, 4, 128), device="cuda")
+        for call in [lambda: O.oscar_cache_read(cache.handle, [0], [0], [700], rows, None),
+                     lambda: O.oscar_cache_read(cache.handle, [0], [0], [700], right, rows),
+                     lambda: O.oscar_cache_read(cache.handle, [0], [0], [700], rows, None, num_kv_heads=heads),
+                     lambda: cache.read([0], [0], [700], None, rows),
+                     lambda: O.oscar_select_groups(cache.handle, [0], q, 8, groups),
+                     lambda: O.oscar_select_groups(cache.handle, [0], q, 8, groups, num_kv_heads=heads),
+                     lambda: cache.select_groups([0], q, 8, groups),
+                     lambda: O.oscar_sparse_decode_attention(cache.handle, [0], q, 8, 0.0, groups, out, ws),
+                     lambda: O.oscar_sparse_decode_attention(cache.handle, [0], q, 8, 0.0, groups, out, ws,
+                                                             num_kv_heads=heads),
+                     lambda: cache.sparse_decode([0], q, 8, groups, out, ws)]:
+            with pytest.raises(ValueError, match="KV heads"):
+                call()
+        torch.cuda.synchronize()
+        assert torch.all(rows == 7.0) and torch.all(groups == 7) and torch.all(out == 7.0)
+    O.oscar_cache_read(cache.handle, [0], [0], [700], right, None)
+    groups = torch.zeros((1, 4, 3), dtype=torch.int32, device="cuda")
+    O.oscar_select_groups(cache.handle, [0], q, 8, groups, num_kv_heads=4)
+    O.oscar_cache_check(cache.handle)
