@@ -401,18 +401,31 @@ def oscar_cache_read(handle, seq_ids: Sequence[int], start: Sequence[int], end: 
     _check(_calls.read(handle, num_kv_heads, seq_ids, start, end, k_out, v_out, stream))
 
 
+def _state_buffers(handle, length: int, blocks, window, maxima):
+    """Pointers of a moved sequence's buffers, large enough for `length` tokens
+    of the cache (the copies take sizes from the cache; a length that the
+    library refuses anyway is left to it)."""
+    cfg = oscar_cache_get_config(handle)
+    if 0 <= length <= cfg.max_seq_len and isinstance(blocks, torch.Tensor):
+        need = cfg.num_kv_heads * (length // GROUP) * (BLOCK_BYTES_META16 if cfg.meta_bits == 16 else BLOCK_BYTES)
+        if blocks.numel() < need:
+            raise ValueError(f"blocks has {blocks.numel()} bytes, {length} tokens of the cache need {need}")
+    rows = cfg.num_kv_heads if length % GROUP else None
+    return (_buf(blocks, torch.uint8, None, "blocks", optional=True),
+            _buf(window, torch.bfloat16, (rows, 2, GROUP, HEAD_DIM), "window", optional=True),
+            _buf(maxima, torch.float32, (2, cfg.num_kv_heads), "maxima"))
+
+
 def oscar_cache_export(handle, seq: int, blocks: Optional[torch.Tensor], window: Optional[torch.Tensor],
                        maxima: torch.Tensor, stream=None) -> None:
-    _check(_lib.oscar_cache_export(handle, seq, _buf(blocks, torch.uint8, None, "blocks", optional=True),
-                                   _buf(window, torch.bfloat16, (None, 2, GROUP, HEAD_DIM), "window", optional=True),
-                                   _buf(maxima, torch.float32, (2, None), "maxima"), _stream(stream)))
+    bufs = _state_buffers(handle, oscar_cache_length(handle, seq), blocks, window, maxima)
+    _check(_lib.oscar_cache_export(handle, seq, *bufs, _stream(stream)))
 
 
 def oscar_cache_import(handle, seq: int, length: int, blocks: Optional[torch.Tensor],
                        window: Optional[torch.Tensor], maxima: torch.Tensor, stream=None) -> None:
-    _check(_lib.oscar_cache_import(handle, seq, length, _buf(blocks, torch.uint8, None, "blocks", optional=True),
-                                   _buf(window, torch.bfloat16, (None, 2, GROUP, HEAD_DIM), "window", optional=True),
-                                   _buf(maxima, torch.float32, (2, None), "maxima"), _stream(stream)))
+    bufs = _state_buffers(handle, length, blocks, window, maxima)
+    _check(_lib.oscar_cache_import(handle, seq, length, *bufs, _stream(stream)))
 
 
 def oscar_index_required_bytes(handle) -> int:

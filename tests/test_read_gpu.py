@@ -254,3 +254,34 @@ def test_refusals():
     with pytest.raises(O.OscarError):
         O.oscar_cache_import(cache.handle, 0, 100000, blocks, window, maxima)
     assert cache.length(0) == 301
+
+
+@pytest.mark.parametrize("meta", [32, 16])
+def test_state_buffers_too_small_are_refused(meta):
+    """Buffers for fewer heads or tokens than the copies would take, in the
+    functions as in the methods; the slot keeps what it holds."""
+    O = U.lib()
+    cache, _ = make([700, 640], 4, meta, seed=33, capacity=1000)
+    n, blocks, window, maxima = cache.export_sequence(0)
+    before = U.read_arena(cache)
+    for state in [(blocks[:3], window, maxima), (blocks[:, :4].contiguous(), window, maxima),
+                  (blocks.view(-1)[:-1], window, maxima), (blocks, window[:2], maxima),
+                  (blocks, window, maxima[:, :1].contiguous()), (blocks, window, maxima[:1])]:
+        with pytest.raises(ValueError):
+            O.oscar_cache_export(cache.handle, 0, *state)
+        with pytest.raises(ValueError):
+            O.oscar_cache_import(cache.handle, 1, n, *state)
+    with pytest.raises(ValueError):
+        O.oscar_cache_import(cache.handle, 1, n + 128 - n % 128, blocks, None, maxima)     # one group more
+    assert cache.length(1) == 640
+    after = U.read_arena(cache)
+    assert np.array_equal(U.live_bytes(cache, before, 1), U.live_bytes(cache, after, 1))
+    # larger ones, and none where nothing is copied
+    more = torch.zeros(blocks.numel() + 5, dtype=torch.uint8, device="cuda")
+    O.oscar_cache_export(cache.handle, 0, more, window, maxima)
+    assert torch.equal(more[:-5], blocks.view(-1)) and torch.all(more[-5:] == 0)
+    O.oscar_cache_export(cache.handle, 1, more, None, maxima)
+    O.oscar_cache_import(cache.handle, 0, 640, more, None, maxima)
+    torch.cuda.synchronize()
+    after = U.read_arena(cache)
+    assert np.array_equal(U.live_bytes(cache, before, 1), U.live_bytes(cache, after, 0))
