@@ -231,7 +231,15 @@ def oscar_cache_create(cfg: oscar_cache_config, arena: torch.Tensor) -> ctypes.c
     h = ctypes.c_void_p(0)
     _check(_lib.oscar_cache_create(ctypes.byref(cfg), _buf(arena, torch.uint8, None, "arena"),
                                    arena.numel() * arena.element_size(), ctypes.byref(h)))
+    h.num_kv_heads = cfg.num_kv_heads      # (per-call checks read it here, not through the library)
     return h
+
+
+def _kv_heads(handle) -> Optional[int]:
+    """KV heads of the cache, also of a bare handle (None for no handle, which
+    the library refuses)."""
+    n = getattr(handle, "num_kv_heads", None)
+    return n if n is not None or handle is None else oscar_cache_get_config(handle).num_kv_heads
 
 
 def oscar_cache_destroy(handle) -> None:
@@ -260,7 +268,7 @@ def oscar_quantize_append(handle, seq_ids: Sequence[int], cu_new: Sequence[int],
     if rows == 0:
         kp = vp = ctypes.c_void_p(0)
     else:
-        kp = _buf(k, torch.bfloat16, (rows, None, HEAD_DIM), "k")
+        kp = _buf(k, torch.bfloat16, (rows, _kv_heads(handle), HEAD_DIM), "k")
         vp = _buf(v, torch.bfloat16, (rows,) + tuple(k.shape[1:]), "v")
     _check(_lib.oscar_quantize_append(handle, len(seq_ids), _i32(seq_ids), _i32(cu_new), kp, vp,
                                       _stream(stream)))
@@ -313,7 +321,7 @@ def oscar_append_decode(handle, seq_ids: Sequence[int], k_new: torch.Tensor, v_n
     """Append one token per sequence and decode, in one call (one launch when
     no group closes)."""
     shape = (len(seq_ids), num_q_heads, HEAD_DIM)
-    kp = _buf(k_new, torch.bfloat16, (len(seq_ids), None, HEAD_DIM), "k_new")
+    kp = _buf(k_new, torch.bfloat16, (len(seq_ids), _kv_heads(handle), HEAD_DIM), "k_new")
     vp = _buf(v_new, torch.bfloat16, (len(seq_ids),) + tuple(k_new.shape[1:]), "v_new")
     _check(_lib.oscar_append_decode(handle, len(seq_ids), _i32(seq_ids), kp, vp,
                                     _buf(q, torch.bfloat16, shape, "q"), num_q_heads,

@@ -116,3 +116,26 @@ def test_append_decode_gqa8_matches_separate_calls():
     ra, rb = U.read_arena(a), U.read_arena(b)
     for s in ids:
         assert np.array_equal(U.live_bytes(a, ra, s), U.live_bytes(b, rb, s))
+
+
+def test_the_module_functions_check_the_kv_heads():
+    """Appends through the module functions refuse keys and values of another
+    number of KV heads than the cache's (the kernels would read past them)."""
+    O = U.lib()
+    cache = O.OscarCache(1, 4, 512)
+    q, out = W.make_q(1, 8, seed=3).cuda(), torch.empty((1, 8, 128), dtype=torch.bfloat16, device="cuda")
+    ws = cache.workspace(1, 8)
+    right = torch.zeros((1, 4, 128), dtype=torch.bfloat16, device="cuda")
+    for handle in (cache.handle, cache.handle.value):
+        for heads in (1, 3, 5):
+            kv = torch.zeros((1, heads, 128), dtype=torch.bfloat16, device="cuda")
+            for k, v in ((kv, kv), (right, kv)):
+                with pytest.raises(ValueError, match="shape"):
+                    O.oscar_quantize_append(handle, [0], [0, 1], k, v)
+                with pytest.raises(ValueError, match="shape"):
+                    O.oscar_append_decode(handle, [0], k, v, q, 8, 0.0, out, ws)
+        assert cache.length(0) == 0
+    O.oscar_quantize_append(cache.handle.value, [0], [0, 1], right, right)
+    O.oscar_append_decode(cache.handle, [0], right, right, q, 8, 0.0, out, ws)
+    O.oscar_cache_check(cache.handle)
+    assert cache.length(0) == 2
