@@ -435,7 +435,8 @@ oscar_status oscar_cache_read(oscar_cache* cache, int32_t n_seqs, const int32_t*
  *           rows of each are read or written, the others left as they are
  *   maxima  float32 [2, Hkv]: the largest value scale, the largest |value zero|
  * Device or page-locked host memory of any alignment; blocks may be NULL when
- * g = 0 and window when w = 0.  Plain copies on `stream`.
+ * g = 0 and window when w = 0.  Plain copies on `stream`: until they have run
+ * the buffers must stay allocated, those of an import unchanged.
  * oscar_cache_import replaces what the slot holds by `length` tokens.
  */
 oscar_status oscar_cache_export(oscar_cache* cache, int32_t seq, void* blocks, void* window,

@@ -19,6 +19,7 @@
 #include <string>
 #include <vector>
 
+#include <ATen/core/CachingHostAllocator.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -325,9 +326,23 @@ PyObject* sparse_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// tensor, stream id, device index, device type (as torch streams name
+// themselves): the stream uses a page-locked tensor until what is enqueued on
+// it now has run.  Its memory, if it came from torch, is not handed out again
+// before (record_stream, which torch offers for device tensors only).
+PyObject* host_in_use(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 4, [&] {
+    const at::Tensor& t = tensor(a[0], "tensor");
+    const c10::Stream stream = c10::Stream::unpack3(integer(a[1]), (c10::DeviceIndex)integer(a[2]),
+                                                    (c10::DeviceType)integer(a[3]));
+    at::getHostAllocator(at::kCUDA)->record_event(t.data_ptr(), t.storage().data_ptr().get_context(), stream);
+    return OSCAR_OK;
+  });
+}
+
 #define OSCAR_FAST(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {OSCAR_FAST(rotary),        OSCAR_FAST(read),         OSCAR_FAST(index_update),
-                         OSCAR_FAST(select_groups), OSCAR_FAST(sparse_decode),
+                         OSCAR_FAST(select_groups), OSCAR_FAST(sparse_decode), OSCAR_FAST(host_in_use),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "Calls of liboscar.so on torch tensors.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -11,7 +11,6 @@ CPU fallback: importing this module fails loudly if the library is missing.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -184,6 +183,34 @@ def _stream(stream) -> int:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _torch_stream(stream, device) -> torch.cuda.Stream:
+    """The torch stream of a call's stream argument (raw handles included)."""
+    if stream is None:
+        return torch.cuda.current_stream()
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = int(stream)       # 0 and 1: the legacy default stream
+    return torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device)
+
+
+def _in_use(stream, device, *tensors) -> None:
+    """Marks tensors as used by the copies just enqueued on `stream`: torch does
+    not hand out their memory again before these have run, also when the caller
+    drops them now.  (Not within a graph capture: the captured copies read or
+    write these addresses at every replay, so the caller keeps the tensors.)"""
+    s = _torch_stream(stream, device)
+    with torch.cuda.stream(s):
+        if torch.cuda.is_current_stream_capturing():
+            return
+    for t in tensors:
+        if t is None or t.numel() == 0:
+            continue
+        if t.is_cuda:
+            t.record_stream(s)
+        else:
+            _calls.host_in_use(t, s.stream_id, s.device_index, s.device_type)
 
 
 def _ptr(t: Optional[torch.Tensor]) -> ctypes.c_void_p:
@@ -410,7 +437,7 @@ def oscar_cache_read(handle, seq_ids: Sequence[int], start: Sequence[int], end: 
 
 
 def _state_buffers(handle, length: int, blocks, window, maxima):
-    """Pointers of a moved sequence's buffers, large enough for `length` tokens
+    """The cache's device and the pointers of a moved sequence's buffers, large enough for `length` tokens
     of the cache (the copies take sizes from the cache; a length that the
     library refuses anyway is left to it)."""
     cfg = oscar_cache_get_config(handle)
@@ -419,21 +446,26 @@ def _state_buffers(handle, length: int, blocks, window, maxima):
         if blocks.numel() < need:
             raise ValueError(f"blocks has {blocks.numel()} bytes, {length} tokens of the cache need {need}")
     rows = cfg.num_kv_heads if length % GROUP else None
-    return (_buf(blocks, torch.uint8, None, "blocks", optional=True),
+    return (cfg.device, _buf(blocks, torch.uint8, None, "blocks", optional=True),
             _buf(window, torch.bfloat16, (rows, 2, GROUP, HEAD_DIM), "window", optional=True),
             _buf(maxima, torch.float32, (2, cfg.num_kv_heads), "maxima"))
 
 
 def oscar_cache_export(handle, seq: int, blocks: Optional[torch.Tensor], window: Optional[torch.Tensor],
                        maxima: torch.Tensor, stream=None) -> None:
-    bufs = _state_buffers(handle, oscar_cache_length(handle, seq), blocks, window, maxima)
+    """The caller may drop the buffers at once: memory of torch's allocators is
+    not reused before the copies have run (import too); other page-locked
+    memory, and every buffer of a captured call, stays the caller's to keep."""
+    device, *bufs = _state_buffers(handle, oscar_cache_length(handle, seq), blocks, window, maxima)
     _check(_lib.oscar_cache_export(handle, seq, *bufs, _stream(stream)))
+    _in_use(stream, device, blocks, window, maxima)
 
 
 def oscar_cache_import(handle, seq: int, length: int, blocks: Optional[torch.Tensor],
                        window: Optional[torch.Tensor], maxima: torch.Tensor, stream=None) -> None:
-    bufs = _state_buffers(handle, length, blocks, window, maxima)
+    device, *bufs = _state_buffers(handle, length, blocks, window, maxima)
     _check(_lib.oscar_cache_import(handle, seq, length, *bufs, _stream(stream)))
+    _in_use(stream, device, blocks, window, maxima)
 
 
 def oscar_index_required_bytes(handle) -> int:
@@ -612,11 +644,12 @@ class OscarCache:
 
     def export_sequence(self, seq: int, pinned: bool = False, stream=None):
         """The packed state of a slot, (length, blocks, window, maxima), in new
-        tensors on the cache's device or in page-locked host memory."""
+        tensors on the cache's device or in page-locked host memory: complete
+        once the stream has been waited for."""
         n = self.length(seq)
         where = dict(pin_memory=True) if pinned else dict(device=self.arena.device)
         # device tensors belong to the stream that fills them
-        with torch.cuda.stream(stream) if isinstance(stream, torch.cuda.Stream) else contextlib.nullcontext():
+        with torch.cuda.stream(_torch_stream(stream, self.arena.device)):
             blocks = torch.empty((self.num_kv_heads, n // GROUP, self.block_bytes), dtype=torch.uint8, **where)
             window = torch.empty((self.num_kv_heads, 2, GROUP, HEAD_DIM), dtype=torch.bfloat16, **where)
             maxima = torch.empty((2, self.num_kv_heads), dtype=torch.float32, **where)

@@ -285,3 +285,49 @@ def test_state_buffers_too_small_are_refused(meta):
     torch.cuda.synchronize()
     after = U.read_arena(cache)
     assert np.array_equal(U.live_bytes(cache, before, 1), U.live_bytes(cache, after, 0))
+
+
+@pytest.mark.parametrize("pinned", [False, True])
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_state_dropped_before_its_copies_ran(pinned, raw):
+    """Export and import queued behind a busy stream that is not the current
+    one, and the state dropped at once: its memory is not handed out again
+    before the copies have run, and they carry the right bytes."""
+    cache, _ = make([1061, 1061], 2, seed=31)
+    torch.cuda.synchronize()
+    before = U.read_arena(cache)
+    s = torch.cuda.Stream()
+    stream = s.cuda_stream if raw else s
+    where = dict(pin_memory=True) if pinned else dict(device="cuda")
+
+    def others(like):      # what an allocation of the same sizes gets
+        return [torch.empty(t.shape, dtype=t.dtype, **where) for t in like]
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)
+    state = cache.export_sequence(0, pinned=pinned, stream=stream)
+    at = [t.data_ptr() for t in state[1:]]
+    like = [torch.empty_like(t, device="meta") for t in state[1:]]
+    del state
+    held = others(like)
+    assert not s.query()                                       # the copies are still queued
+    assert not set(at) & {t.data_ptr() for t in held}
+    torch.cuda.synchronize()
+    del held
+    state = cache.export_sequence(0, pinned=pinned)            # complete, on the current stream
+    torch.cuda.synchronize()
+    U.lib().oscar_cache_reset(cache.handle, 1)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)
+    cache.import_sequence(1, *state, stream=stream)
+    at = [t.data_ptr() for t in state[1:]]
+    del state
+    held = others(like)
+    assert not s.query()
+    assert not set(at) & {t.data_ptr() for t in held}
+    for t in held:
+        t.fill_(0)
+    torch.cuda.synchronize()
+    after = U.read_arena(cache)
+    assert np.array_equal(U.live_bytes(cache, before, 0), U.live_bytes(cache, after, 1))
+    assert cache.length(1) == 1061
