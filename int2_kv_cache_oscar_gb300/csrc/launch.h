@@ -203,6 +203,8 @@ struct ReadParams {
   int64_t n_tiles;
   void* k_out;         // [rows, hkv, 128], or NULL
   void* v_out;
+  uint32_t spin_limit; // polls of a bounded wait; the test hook's `fault` (1) leaves
+  int32_t fault;       // the copy of tile 0 unissued, with a small limit
   ReadSeq seq[MAXS];
 };
 

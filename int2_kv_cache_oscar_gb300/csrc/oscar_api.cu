@@ -49,9 +49,17 @@ namespace {
 thread_local std::string g_err;
 thread_local cudaEvent_t g_ev_start = nullptr;
 thread_local cudaEvent_t g_ev_stop = nullptr;
-// armed by oscar_test_arm_wait_timeout: the next INT2 decode launch on this
-// thread leaves one copy unissued and gives up its waits early
+// armed by oscar_test_arm_wait_timeout: the next INT2 decode or read-back
+// launch on this thread leaves one copy unissued and gives up its waits early
 thread_local bool g_arm_timeout = false;
+constexpr uint32_t kArmedSpinLimit = 1u << 14;
+
+// Whether this launch is the armed one (which disarms).
+bool take_armed_timeout() {
+  const bool armed = g_arm_timeout;
+  g_arm_timeout = false;
+  return armed;
+}
 
 oscar_status fail(oscar_status s, const char* fmt, ...) {
   char buf[512];
@@ -281,9 +289,8 @@ oscar_status run_decode(int device, int sms, int ctas_per_sm, int32_t n, const i
   P.h.out_f32 = out_f32 ? 1 : 0;
   P.h.spin_limit = kSpinLimit;
   P.h.fault_unit = -1;
-  if (g_arm_timeout && !bf16_mode) {
-    g_arm_timeout = false;
-    P.h.spin_limit = 1u << 14;
+  if (!bf16_mode && take_armed_timeout()) {
+    P.h.spin_limit = kArmedSpinLimit;
     P.h.fault_unit = 0;
   }
   // The kernels serve at most max_gqa query heads of a KV head per launch (mma
@@ -1095,6 +1102,8 @@ oscar_status run_read(oscar_cache* c, const std::vector<ReadSeq>& seqs, size_t f
   P.windows_off = c->layout.windows_off;
   P.k_out = k;
   P.v_out = v;
+  P.fault = take_armed_timeout() ? 1 : 0;
+  P.spin_limit = P.fault ? kArmedSpinLimit : kSpinLimit;
   int64_t ubase = 0;
   for (size_t i = 0; i < n; ++i) {
     P.seq[i] = seqs[first + i];

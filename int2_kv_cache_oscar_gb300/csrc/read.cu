@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
     }
     const uint8_t* src =
         arena + p.blocks_off + (((int64_t)p.seq[b].slot * p.hkv + j) * p.max_groups + tile) * (int64_t)B::kBytes;
+    if (p.fault && u == 0) return;
     mbar_arrive_expect_tx(&S.full[s], B::kBytes);
     bulk_g2s(S.stage[s], src, B::kBytes, &S.full[s]);
   };
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
     Out* vout = static_cast<Out*>(p.v_out);
     auto out_row = [&](Out* base, int t) { return base + ((row0 + t) * p.hkv + j) * kHeadDim; };
 
-    const bool late = !mbar_wait_bounded(&S.full[s], (it >> 1) & 1, &S.abort_flag, err);
+    const bool late = !mbar_wait_bounded(&S.full[s], (it >> 1) & 1, &S.abort_flag, err, p.spin_limit);
     const bool packed = (tile + 1) * (int64_t)kGroup <= sq.len;
     const uint8_t* blk = S.stage[s];
     if (packed && tid < kHeadDim / 2) {
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
       // a wait gave up: leave (no copy of a later tile has been requested; this
       // tile's gets its time, bounded)
       if (tid == 0)
-        for (uint32_t n = 0; n < kSpinLimit; ++n)
+        for (uint32_t n = 0; n < p.spin_limit; ++n)
           if (mbar_try_wait(&S.full[s], (it >> 1) & 1)) break;
       break;
     }

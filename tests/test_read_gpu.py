@@ -331,3 +331,27 @@ def test_a_state_dropped_before_its_copies_ran(pinned, raw):
     after = U.read_arena(cache)
     assert np.array_equal(U.live_bytes(cache, before, 0), U.live_bytes(cache, after, 1))
     assert cache.length(1) == 1061
+
+
+@pytest.mark.parametrize("meta", [32, 16])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_wait_that_runs_out(dtype, meta):
+    """A copy left unissued (the library's own hook): the bounded wait gives
+    up, the call reports it, later calls are unaffected.  With more tiles than
+    blocks, so that the block that gives up has a further tile."""
+    O = U.lib()
+    cache, _ = make([128 * 60 + 5], 8, meta, seed=41, chunk=4096)
+    assert 61 * 8 > 3 * torch.cuda.get_device_properties(0).multi_processor_count
+    n = cache.length(0)
+    want, got = (torch.empty((2, n, 8, 128), dtype=dtype, device="cuda") for _ in range(2))
+    cache.read([0], [0], [n], want[0], want[1])
+    O.oscar_cache_check(cache.handle)
+    O.oscar_test_arm_wait_timeout()
+    cache.read([0], [0], [n], got[0], got[1])
+    with pytest.raises(O.OscarError) as e:
+        O.oscar_cache_check(cache.handle)
+    assert e.value.status == O.OSCAR_ERR_DEVICE_TIMEOUT
+    O.oscar_cache_check(cache.handle)
+    cache.read([0], [0], [n], got[0], got[1])
+    O.oscar_cache_check(cache.handle)
+    assert torch.equal(got, want)
