@@ -540,10 +540,10 @@ oscar_status oscar_cache_window_offset(const oscar_cache* cache, int32_t seq, in
                                        size_t* out_offset);
 
 /*
- * Test hook of the failure path: the next INT2 decode or read-back launch made
- * on the calling thread (oscar_decode_attention, _f32, oscar_append_decode,
- * oscar_sparse_decode_attention, oscar_cache_read) has one bulk copy of its
- * first CTA left unissued, and its bounded waits give up after 2^14 polls
+ * Test hook of the failure path: the next INT2 decode, read-back or selection
+ * launch made on the calling thread (oscar_decode_attention, _f32,
+ * oscar_append_decode, oscar_sparse_decode_attention, oscar_cache_read,
+ * oscar_select_groups) has one bulk copy of its first CTA left unissued, and its bounded waits give up after 2^14 polls
  * instead of 2^24.  The consumer waiting for that copy then
  * gives up, the kernel sets the arena's error flag, skips its remaining work
  * and returns (no fault, no hang; the results of that call are undefined),

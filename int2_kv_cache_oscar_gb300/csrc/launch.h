@@ -249,6 +249,8 @@ struct SelectParams {
   int32_t blocks;      // of a row (a cluster), set by the launch
   int32_t stages;      // copies in flight and the bytes of each, set by the launch
   int32_t stage_bytes;
+  uint32_t spin_limit; // as in ReadParams; `fault`: chunk 0 of block 0
+  int32_t fault;
   uint32_t* err_word;
   const uint2* codes;
   const float2* weights;

@@ -49,8 +49,8 @@ namespace {
 thread_local std::string g_err;
 thread_local cudaEvent_t g_ev_start = nullptr;
 thread_local cudaEvent_t g_ev_stop = nullptr;
-// armed by oscar_test_arm_wait_timeout: the next INT2 decode or read-back
-// launch on this thread leaves one copy unissued and gives up its waits early
+// armed by oscar_test_arm_wait_timeout: the next INT2 decode, read-back or
+// selection launch on this thread leaves one copy unissued and gives up its waits early
 thread_local bool g_arm_timeout = false;
 constexpr uint32_t kArmedSpinLimit = 1u << 14;
 
@@ -1143,6 +1143,8 @@ oscar_status run_select(const oscar_cache* c, const std::vector<SelectSeq>& seqs
   P.n_select = n_select;
   P.keep_first = keep_first;
   P.keep_last = keep_last;
+  P.fault = take_armed_timeout() ? 1 : 0;
+  P.spin_limit = P.fault ? kArmedSpinLimit : kSpinLimit;
   P.err_word = reinterpret_cast<uint32_t*>(c->arena);
   P.codes = c->index_codes;
   P.weights = c->index_weights;

@@ -203,8 +203,11 @@ __global__ void __launch_bounds__(kSelThreads)
 
   const int64_t row = ((int64_t)p.seq[b].slot * p.hkv + j) * p.max_groups + first;
   const int chunks = (n + kSelChunk - 1) / kSelChunk;
+  int issued = 0;                  // chunks requested (thread 0)
   auto request = [&](int c) {      // chunk c into its stage
     const int s = c % p.stages;
+    issued = c + 1;
+    if (p.fault && blockIdx.x == 0 && c == 0) return;
     const uint32_t bytes = (uint32_t)min(kSelChunk, n - c * kSelChunk) * 256;
     mbar_arrive_expect_tx(&S.full[s], bytes);
     bulk_g2s(stages + (size_t)s * p.stage_bytes, p.codes + (row + c * kSelChunk) * 32, bytes, &S.full[s]);
@@ -300,7 +303,7 @@ __global__ void __launch_bounds__(kSelThreads)
   load_heads(0);
   for (int c = 0; c < chunks; ++c) {
     const int s = c % p.stages;
-    mbar_wait_bounded(&S.full[s], (uint32_t)((c / p.stages) & 1), &S.abort_flag, p.err_word);
+    mbar_wait_bounded(&S.full[s], (uint32_t)((c / p.stages) & 1), &S.abort_flag, p.err_word, p.spin_limit);
     const int4* codes = reinterpret_cast<const int4*>(stages + (size_t)s * p.stage_bytes);
     const int here = min(kSelChunk, n - c * kSelChunk);
     // batches of 8 groups, warp by warp: t 8 + warp; lane `part` then makes the
@@ -353,9 +356,10 @@ __global__ void __launch_bounds__(kSelThreads)
     }
   }
   if (S.abort_flag && tid == 0) {
-    // a wait gave up: wait (bounded) for the copies still in flight
-    for (int c = max(0, chunks - p.stages); c < chunks; ++c)
-      for (uint32_t i = 0; i < kSpinLimit; ++i)
+    // a wait gave up and nothing was requested since: wait (bounded) for the
+    // copies that may still be in flight, the last of each stage
+    for (int c = max(0, issued - p.stages); c < issued; ++c)
+      for (uint32_t i = 0; i < p.spin_limit; ++i)
         if (mbar_try_wait(&S.full[c % p.stages], (uint32_t)((c / p.stages) & 1))) break;
   }
   if (blocks > 1) {

@@ -374,3 +374,33 @@ def test_refusals():
     assert torch.all(out == -1)
     O.oscar_index_attach(cache.handle, None)
     refused(lambda: cache.select_groups([0], q, 4, out))
+
+
+@pytest.mark.parametrize("ng,hkv,n", [(64, 1, 16), (5000, 1, 90), (5003, 2, 64), (11900, 1, 30)])
+def test_wait_that_runs_out(ng, hkv, n):
+    """A copy left unissued (the library's own hook): the bounded wait gives
+    up, the call reports it, later calls are unaffected.  Slices of one chunk,
+    of three with two stages (the copy of the second is in flight when the wait
+    for the first gives up), and of more."""
+    O = U.lib()
+    cache = O.OscarCache(1, hkv, 128 * ng + 128)
+    blocks = torch.randint(0, 60, (hkv, ng, cache.block_bytes), dtype=torch.uint8, device="cuda")   # finite parameters
+    cache.import_sequence(0, 128 * ng, blocks, None, torch.ones((2, hkv), device="cuda"))
+    del blocks
+    cache.enable_index()
+    cache.update_index([0])
+    q = W.make_q(1, 4 * hkv, seed=42).cuda()
+    want, got = (torch.full((1, hkv, n), -5, dtype=torch.int32, device="cuda") for _ in range(2))
+    cache.select_groups([0], q, 4 * hkv, want, 1, 1)
+    O.oscar_cache_check(cache.handle)
+    assert torch.all(want >= 0) and torch.all(want[..., 1:] > want[..., :-1])
+    O.oscar_test_arm_wait_timeout()
+    cache.select_groups([0], q, 4 * hkv, got, 1, 1)
+    with pytest.raises(O.OscarError) as e:
+        O.oscar_cache_check(cache.handle)
+    assert e.value.status == O.OSCAR_ERR_DEVICE_TIMEOUT
+    O.oscar_cache_check(cache.handle)
+    for _ in range(2):
+        cache.select_groups([0], q, 4 * hkv, got, 1, 1)
+    O.oscar_cache_check(cache.handle)
+    assert torch.equal(got, want)
