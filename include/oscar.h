@@ -544,7 +544,8 @@ oscar_status oscar_cache_window_offset(const oscar_cache* cache, int32_t seq, in
  * launch made on the calling thread (oscar_decode_attention, _f32,
  * oscar_append_decode, oscar_sparse_decode_attention, oscar_cache_read,
  * oscar_select_groups) has one bulk copy of its first CTA left unissued, and its bounded waits give up after 2^14 polls
- * instead of 2^24.  The consumer waiting for that copy then
+ * instead of 2^24.  (A listed decode of sequences without a group: the window
+ * copies of its combine, where it has any.)  The consumer waiting for that copy then
  * gives up, the kernel sets the arena's error flag, skips its remaining work
  * and returns (no fault, no hang; the results of that call are undefined),
  * and oscar_cache_check reports OSCAR_ERR_DEVICE_TIMEOUT.  Later calls are

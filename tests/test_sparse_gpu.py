@@ -407,3 +407,30 @@ def test_a_query_that_is_not_finite(lens, hkv, hq, n, attend, value, dtype):
     full = torch.empty((len(lens), hq, 128), device="cuda")
     cache.decode_f32(ids, qb, hq, full, ws)
     assert torch.all(full[bad].isnan())
+
+
+@pytest.mark.parametrize("lens,hkv,hq", [([5 + i % 120 for i in range(200)], 2, 4), ([127] * 40, 1, 8)])
+def test_window_wait_that_runs_out(lens, hkv, hq):
+    """Sequences without a group, so many that a block per KV head stages the
+    window: its copies left unissued (the library's own hook)."""
+    O = U.lib()
+    cache = make(lens, hkv, seed=81)
+    ids = list(range(len(lens)))
+    assert len(lens) * hq > 1.5 * torch.cuda.get_device_properties(0).multi_processor_count
+    q = W.make_q(len(lens), hq, seed=82).cuda()
+    groups = torch.zeros((len(lens), hkv, 2), dtype=torch.int32, device="cuda")
+    want = check(cache, ids, q, groups)
+    out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+    ws = cache.workspace(len(lens), hq)
+    O.oscar_test_arm_wait_timeout()
+    cache.sparse_decode(ids, q, hq, groups, out, ws, lse)
+    with pytest.raises(O.OscarError) as e:
+        O.oscar_cache_check(cache.handle)
+    assert e.value.status == O.OSCAR_ERR_DEVICE_TIMEOUT
+    # only the first block's row was given up
+    gqa = hq // hkv
+    assert torch.equal(out[1:], want[0][1:]) and torch.equal(out[0, gqa:], want[0][0, gqa:])
+    assert torch.equal(lse[1:], want[1][1:])
+    cache.sparse_decode(ids, q, hq, groups, out, ws, lse)
+    O.oscar_cache_check(cache.handle)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
