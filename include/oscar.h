@@ -396,7 +396,8 @@ typedef struct oscar_rotary_rows {
  *              negative
  *   type       OSCAR_BF16 or OSCAR_F32 (q and k, in and out)
  *   q, k       rows on the current device; k may be NULL; 16-byte aligned
- *              pointers, strides of 16-byte multiples; inputs may have any
+ *              pointers, strides of 16-byte multiples (those of a single
+ *              token or head are not looked at); inputs may have any
  *              strides (0 broadcasts), output rows must be distinct: either
  *              the heads of a token or the tokens of a head side by side.
  *              Zero heads or zero tokens: nothing is done.

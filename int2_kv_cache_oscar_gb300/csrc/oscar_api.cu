@@ -1052,10 +1052,15 @@ oscar_status rotary_frequencies(const oscar_rotary_config* c, double* f, double*
 }
 
 // One tensor's rows of a rotary call.
-oscar_status rotary_rows(const oscar_rotary_rows* x, const char* name, int64_t n, int elem, int device,
+oscar_status rotary_rows(const oscar_rotary_rows* rows, const char* name, int64_t n, int elem, int device,
                          RotaryRows* out) {
   std::memset(out, 0, sizeof(*out));
-  if (x == nullptr || x->heads == 0) return OSCAR_OK;
+  if (rows == nullptr || rows->heads == 0) return OSCAR_OK;
+  // the stride of a single token or head takes part in no address
+  oscar_rotary_rows one = *rows;
+  if (n == 1) one.in_token_stride = one.out_token_stride = 0;
+  if (one.heads == 1) one.in_head_stride = one.out_head_stride = 0;
+  const oscar_rotary_rows* x = &one;
   if (x->heads < 0 || x->heads > (1 << 16))
     return fail(OSCAR_ERR_INVALID_ARG, "%s: heads must be in [0, 65536]", name);
   if (!x->in || !x->out) return fail(OSCAR_ERR_INVALID_ARG, "%s: NULL rows", name);

@@ -208,3 +208,21 @@ def test_refusals():
     refused(cfg, pos, x, None, x[:1].expand(4, 2, 128))                      # one output row for all tokens
     refused(cfg, pos, x, None, flat.as_strided((4, 2, 128), (128, 64, 1)))   # overlapping output rows
     refused(cfg, pos, x, None, x.as_strided((4, 2, 128), (128, 512, 1)))     # "in place" with other strides
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_the_stride_of_a_single_token_or_head_does_not_matter(dtype):
+    """One token, or one head, taken out of a tensor whose pitch along that
+    dimension is no multiple of 16 bytes."""
+    cfg = U.lib().make_rotary_config(128, base=500000.0)
+    x = torch.randn((6, 128), device="cuda").to(dtype)
+    for shape, strides in [((1, 6, 128), (771, 128, 1)), ((6, 1, 128), (128, 5, 1)), ((1, 6, 128), (1, 128, 1))]:
+        odd = x.as_strided(shape, strides)
+        pos = torch.arange(9, 9 + shape[0], dtype=torch.int32, device="cuda")
+        want, got = torch.empty(shape, dtype=dtype, device="cuda"), torch.empty(shape, dtype=dtype, device="cuda")
+        U.lib().oscar_rotary(cfg, pos, odd.clone(memory_format=torch.contiguous_format), None, want)
+        U.lib().oscar_rotary(cfg, pos, odd, None, got)
+        assert torch.equal(got, want)
+        y = x.clone().as_strided(shape, strides)
+        U.lib().oscar_rotary(cfg, pos, y)                      # in place
+        assert torch.equal(y, want)
