@@ -416,8 +416,8 @@ oscar_status oscar_rotary(const oscar_rotary_table* table, int64_t n_tokens, con
  *                        slot may appear more than once
  *   type                 OSCAR_BF16 or OSCAR_F32
  *   k_out, v_out         [sum(end - start), Hkv, 128], 16-byte aligned device
- *                        memory (bf16 keys are written faster when both are
- *                        32-byte aligned); either may be NULL
+ *                        memory (float32 values are written in 32-byte pieces
+ *                        when both are 32-byte aligned); either may be NULL
  * A quantised key is H_d (n (code s + z)) (back in the basis in which it was
  * appended), a quantised value code s + z, both in float32 and rounded once to
  * the output type; window tokens are their stored bf16 rows.

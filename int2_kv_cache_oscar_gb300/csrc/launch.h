@@ -197,7 +197,8 @@ struct ReadParams {
   int32_t n_seqs;      // sequences with a non-empty range
   int32_t hkv;
   int32_t max_groups;
-  int32_t wide;        // 1: both outputs are 32-byte aligned
+  int32_t wide;        // 1: both outputs are 32-byte aligned (float32: 32-byte stores of
+                       // values and window rows)
   int64_t blocks_off;
   int64_t windows_off;
   int64_t n_tiles;
