@@ -388,8 +388,9 @@ typedef struct oscar_rotary_rows {
 
 /*
  * Rotary positions of queries and keys, before the keys are appended and the
- * queries attend: with t = positions[token] * frequency (evaluated to 2^-31
- * of a turn at any int32 position) and m the attention factor,
+ * queries attend: with t = positions[token] * frequency (a phase within 2^-31
+ * of a turn at any int32 position, whose distance from the nearest quarter turn
+ * is then rounded to float32: 2^-28 of a turn at most) and m the attention factor,
  *   (y_a, y_b) = m (x_a cos t - x_b sin t, x_a sin t + x_b cos t)
  * for every pair (a, b); channels from rotary_dim on are copied.
  *   positions  int32 [n_tokens], device or page-locked host memory, may be

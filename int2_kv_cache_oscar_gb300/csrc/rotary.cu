@@ -10,7 +10,8 @@
 // turns modulo one, in 64-bit fixed point: phase = position * F mod 2^64 with
 // F = frequency / (2 pi) * 2^64, exact integer arithmetic (off by 2^-33 of a
 // turn at position 2^31).  Its top 32 bits give the quadrant and the remainder
-// (at most an eighth of a turn) for sincospif.
+// (at most an eighth of a turn) for sincospif; as a float32 that is off by
+// 2^-28 of a turn at most.
 //
 // What bounds it: every element is read and written once, so HBM for long
 // runs and the launch for one token.  A block computes the cosines and sines
