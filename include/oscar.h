@@ -439,7 +439,10 @@ oscar_status oscar_cache_read(oscar_cache* cache, int32_t n_seqs, const int32_t*
  * Device or page-locked host memory of any alignment; blocks may be NULL when
  * g = 0 and window when w = 0.  Plain copies on `stream`: until they have run
  * the buffers must stay allocated, those of an import unchanged.
- * oscar_cache_import replaces what the slot holds by `length` tokens.
+ * oscar_cache_import replaces what the slot holds by `length` tokens.  It takes
+ * the maxima as they are: they set the range of the float16 factors of every
+ * decode and prefill over the slot.  Below the blocks' own scales or |zeros|
+ * these overflow (infinite or NaN outputs), far above them they lose bits.
  */
 oscar_status oscar_cache_export(oscar_cache* cache, int32_t seq, void* blocks, void* window,
                                 float* maxima, void* stream);
