@@ -221,3 +221,13 @@ def test_binding_checks_buffers_before_any_call():
         kc = torch.zeros((1, 8, 256, 128), dtype=torch.bfloat16)
         O.oscar_bf16_decode_attention([0, 1], [10, 10], kc, kc, 8, 256, q, 32, 0.0, out, ws)
 
+
+
+def test_a_half_built_tree_is_told_from_a_fresh_and_a_whole_one(tmp_path):
+    from tests.conftest import half_built
+    lib, calls = tmp_path / "lib.so", tmp_path / "calls.so"
+    assert not half_built(lib, calls)
+    lib.touch()
+    assert half_built(lib, calls)
+    calls.touch()
+    assert not half_built(lib, calls)
