@@ -231,3 +231,11 @@ def test_a_half_built_tree_is_told_from_a_fresh_and_a_whole_one(tmp_path):
     assert half_built(lib, calls)
     calls.touch()
     assert not half_built(lib, calls)
+
+
+def test_get_config_refuses_null(O):
+    lib, cfg = O.raw_library(), O.oscar_cache_config()
+    assert lib.oscar_cache_get_config(None, ctypes.byref(cfg)) == O.OSCAR_ERR_INVALID_ARG
+    with pytest.raises(O.OscarError) as e:
+        O.oscar_cache_get_config(None)
+    assert e.value.status == O.OSCAR_ERR_INVALID_ARG
