@@ -90,11 +90,12 @@ enum {
  *
  *   [0, 256)                       status words; word 0 = device error flags
  *   [256, 256 + 4 S H)             per (slot, kv head): float32 bit pattern of
- *                                  the largest value scale s_v quantised so
- *                                  far (4 bytes each; S = max_batch, H = Hkv)
+ *                                  the largest finite value scale s_v
+ *                                  quantised so far (4 bytes each;
+ *                                  S = max_batch, H = Hkv)
  *   [256 + 4 S H, M)               per (slot, kv head): float32 bit pattern of
- *                                  the largest |value zero| z_v quantised so
- *                                  far, M = 256-aligned end
+ *                                  the largest finite |value zero| z_v
+ *                                  quantised so far, M = 256-aligned end
  *   blocks  (base = M)             one block of B bytes per
  *                                  (slot, kv head, group g):
  *                                  base + ((slot*Hkv + head)*max_groups + g)*B,
@@ -435,7 +436,7 @@ oscar_status oscar_cache_read(oscar_cache* cache, int32_t n_seqs, const int32_t*
  *           or 11,008)
  *   window  bf16 [Hkv, 2, 128, 128]: key rows, then value rows; the first w
  *           rows of each are read or written, the others left as they are
- *   maxima  float32 [2, Hkv]: the largest value scale, the largest |value zero|
+ *   maxima  float32 [2, Hkv]: the largest finite value scale and |value zero|
  * Device or page-locked host memory of any alignment; blocks may be NULL when
  * g = 0 and window when w = 0.  Plain copies on `stream`: until they have run
  * the buffers must stay allocated, those of an import unchanged.

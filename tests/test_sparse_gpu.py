@@ -434,3 +434,39 @@ def test_window_wait_that_runs_out(lens, hkv, hq):
     cache.sparse_decode(ids, q, hq, groups, out, ws, lse)
     O.oscar_cache_check(cache.handle)
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("meta", [32, 16])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+def test_a_value_that_is_not_finite(value, dtype, meta):
+    """One channel of one token is not finite.  Lists without its group are not
+    touched by it (the value factors are scaled by the largest finite value
+    scale); with it an infinity costs its 32 channels only.  (A NaN leaves the
+    quantiser's minimum and maximum alone and is stored as some code.)"""
+    gen = torch.Generator().manual_seed(53)
+    k, v = W.make_sequence_kv(1100, 2, W.LLAMA_RECIPE, gen)
+    v = (8 * v.float()).bfloat16()
+    v[300, 0, 37] = value
+    cache = U.lib().OscarCache(1, 2, 1300, meta_bits=meta)
+    U.append_all(cache, [0], [k], [v], chunk=4096)
+    q = W.make_q(1, 8, seed=54).cuda()
+    ws, arena = cache.workspace(1, 8), U.read_arena(cache)
+    for idx in ([0, 1, 4, 7], [0, 2, 5], [2])[:1 if np.isnan(value) else 3]:
+        groups = torch.tensor(idx, dtype=torch.int32).repeat(1, 2, 1).cuda()
+        out, lse = torch.empty((1, 8, 128), dtype=dtype, device="cuda"), torch.empty((1, 8), device="cuda")
+        cache.sparse_decode([0], q, 8, groups, out, ws, lse)
+        U.lib().oscar_cache_check(cache.handle)
+        got, gl = U.f64(out)[0], U.f64(lse)[0]
+        for j in range(2):
+            heads = slice(4 * j, 4 * j + 4)
+            full = U.gpu_head(cache, arena, 0, j)
+            if j == 0 and np.isinf(value):      # the token's second value group as zeros: 32 channels of no account
+                assert not np.isfinite(full.values.scale * full.values.zero).all()
+                full.values.scale[2, 44, 1] = full.values.zero[2, 44, 1] = 0
+                assert np.isfinite(full.values.scale).all() and np.isfinite(full.values.zero).all()
+            h, g = listed(full, idx), got[heads].copy()
+            if j == 0 and 2 in idx:
+                assert not np.isfinite(g[:, 32:64]).any()
+                g[:, 32:64] = OR.history_attention(U.f64(q)[0, heads], h, None)[0][:, 32:64]
+            check_head(U.f64(q)[0, heads], h, g, gl[heads], None, torch.finfo(dtype).eps / 2, full.values.scale.max())
