@@ -523,7 +523,9 @@ oscar_status oscar_select_groups(oscar_cache* cache, int32_t n_seqs, const int32
  *             A and in the whole sequence S, bf16 outputs are off by 3 (2^-11 A
  *             + n 2^-31 S) at most through that, beside their own rounding: RMS
  *             errors up to 1.8e-3 of the output, at most 8 % above those of
- *             32-bit factors rounded once, in what was measured
+ *             32-bit factors rounded once, in what was measured.  float32
+ *             outputs lose 3 n 2^-30 S at most, which counts only where S is far
+ *             above A
  *   lse       float32 [n_seqs, num_q_heads] or NULL: ln sum exp(score) over the
  *             attended tokens (natural log, scores times softmax_scale)
  * A row with nothing to attend (no valid entry, empty window) gets zeros and
