@@ -581,6 +581,7 @@ class OscarCache:
         self.arena = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.handle = oscar_cache_create(self.cfg, self.arena)
         self.num_kv_heads = num_kv_heads
+        self.index = None
         self.max_batch = max_batch
         self.max_seq_len = max_seq_len
 
@@ -661,9 +662,11 @@ class OscarCache:
         oscar_cache_import(self.handle, seq, length, blocks, window, maxima, stream)
 
     def enable_index(self):
-        """Allocates and attaches the group index (kept with the cache)."""
-        n = oscar_index_required_bytes(self.handle)
-        self.index = torch.empty(n, dtype=torch.uint8, device=self.arena.device)
+        """Allocates and attaches the group index (kept with the cache; called
+        again, it is emptied: queued calls may still use its memory)."""
+        if self.index is None:
+            n = oscar_index_required_bytes(self.handle)
+            self.index = torch.empty(n, dtype=torch.uint8, device=self.arena.device)
         oscar_index_attach(self.handle, self.index)
 
     def update_index(self, seq_ids, rebuild: bool = False, stream=None):

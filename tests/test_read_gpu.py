@@ -355,3 +355,23 @@ def test_wait_that_runs_out(dtype, meta):
     cache.read([0], [0], [n], got[0], got[1])
     O.oscar_cache_check(cache.handle)
     assert torch.equal(got, want)
+
+
+def test_export_import_of_registered_host_memory():
+    """Page-locked memory that is not torch's (the caller keeps it)."""
+    cache, _ = make([700, 0], 2, seed=35, capacity=900)
+    n, blocks, window, maxima = cache.export_sequence(0)
+    host = [torch.zeros(t.shape, dtype=t.dtype) for t in (blocks, window, maxima)]
+    rt = torch.cuda.cudart()
+    for t in host:
+        assert int(rt.cudaHostRegister(t.data_ptr(), t.numel() * t.element_size(), 0)) == 0
+    try:
+        U.lib().oscar_cache_export(cache.handle, 0, *host)
+        cache.import_sequence(1, n, *host)
+        torch.cuda.synchronize()
+    finally:
+        for t in host:
+            rt.cudaHostUnregister(t.data_ptr())
+    assert torch.equal(host[0], blocks.cpu()) and torch.equal(host[2], maxima.cpu())
+    a = U.read_arena(cache)
+    assert np.array_equal(U.live_bytes(cache, a, 0), U.live_bytes(cache, a, 1))

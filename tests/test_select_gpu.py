@@ -404,3 +404,20 @@ def test_wait_that_runs_out(ng, hkv, n):
         cache.select_groups([0], q, 4 * hkv, got, 1, 1)
     O.oscar_cache_check(cache.handle)
     assert torch.equal(got, want)
+
+
+def test_enabling_the_index_again_keeps_its_memory():
+    """Queued updates and selections may still use it: nothing is valid in it
+    any more, but it is not handed out to others."""
+    cache = make([1300], 2)
+    q = W.make_q(1, 8, seed=45).cuda()
+    want, got = (torch.empty((1, 2, 4), dtype=torch.int32, device="cuda") for _ in range(2))
+    cache.select_groups([0], q, 8, want)
+    at = cache.index.data_ptr()
+    cache.enable_index()
+    assert cache.index.data_ptr() == at
+    with pytest.raises(U.lib().OscarError):
+        cache.select_groups([0], q, 8, got)
+    cache.update_index([0])
+    cache.select_groups([0], q, 8, got)
+    assert torch.equal(got, want)
