@@ -263,7 +263,7 @@ oscar_status oscar_append_decode(oscar_cache* cache, int32_t n_seqs, const int32
  * (quantised groups and window; no mask, the cache precedes the chunk), with
  * the decode path's scores and values (OScaR abstract; ai-papers.net
  * "OScaRの提案手法").  Call it before appending the chunk; the chunk's own
- * causal attention is merged in by the caller with lse.
+ * causal attention (oscar_chunk_attention) is merged in with lse.
  *   q            bf16 [n_q, num_q_heads, 128], 16-byte aligned
  *   out          bf16 [n_q, num_q_heads, 128], 16-byte aligned
  *   lse          fp32 [n_q, num_q_heads] or NULL: ln sum_t exp(s_t) per row
@@ -539,6 +539,68 @@ oscar_status oscar_sparse_decode_attention(oscar_cache* cache, int32_t n_seqs, c
                                            const int32_t* groups, int32_t n_select, int32_t type,
                                            void* out, float* lse, void* workspace,
                                            size_t workspace_bytes, void* stream);
+
+/*
+ * How scores are changed before the softmax, beyond their scale: with s = q . k
+ * softmax_scale,
+ *   s = cap tanh(s / cap)               where cap is not 0,
+ *   s = s - slopes[query head] distance where slopes is not NULL, distance the
+ *                                       tokens between query and key (>= 0)
+ */
+typedef struct oscar_score_rule {
+  float cap;               /* 0: none; else in [2^-10, 2^10]: scores are then off
+                              by cap 2^-21 at most                            */
+  int32_t reserved;        /* 0                                               */
+  const float* slopes;     /* NULL, or float32 [num_q_heads], device or
+                              page-locked host memory                         */
+} oscar_score_rule;
+
+/* Rows of a tensor [tokens, heads, 128] that is read: strides in elements,
+ * channels contiguous. */
+typedef struct oscar_rows {
+  const void* data;
+  int64_t token_stride, head_stride;
+} oscar_rows;
+
+/*
+ * Attention within a new chunk of packed documents, before its keys and values
+ * are appended: token i of a document (0 its first) attends to the document's
+ * tokens t < max(i + 1, prefix), under the score rule, and the result is merged
+ * with what the same queries got over the tokens that precede the chunk
+ * (oscar_prefill_attention and its lse).
+ *   n_seqs        documents, at most 1,024
+ *   cu_seqlens    host int32 [n_seqs + 1], cu_seqlens[0] = 0, non-decreasing:
+ *                 document d is rows cu_seqlens[d] .. cu_seqlens[d + 1] - 1 (may
+ *                 be none); rows behind the last document are neither read nor
+ *                 written
+ *   prefix        host int32 [n_seqs] or NULL (all 0): leading tokens that every
+ *                 token of the document sees, 0 .. its tokens
+ *   q, k, v       bf16, num_q_heads and num_kv_heads heads, on the current
+ *                 device, 16-byte aligned; strides positive multiples of 8 (those
+ *                 of a single token or head are not looked at), below 2^36
+ *   num_q_heads   a multiple of num_kv_heads, together at most 2^16 heads
+ *   rule          NULL: scores as they are
+ *   prior_out, prior_lse  bf16 [rows, num_q_heads, 128] and float32 [rows,
+ *                 num_q_heads], or both NULL: normalised rows and their
+ *                 log-sum-exp; out and lse of the call may be the same memory. A
+ *                 row whose prior_lse is -infinity has nothing before it (its
+ *                 prior_out is not read)
+ *   out           bf16 [rows, num_q_heads, 128], 16-byte aligned; must not overlap
+ *                 q, k or v
+ *   lse           float32 [rows, num_q_heads] or NULL: natural log-sum-exp of the
+ *                 merged row
+ *   prior_out, prior_lse, out and lse: device or page-locked host memory
+ *   softmax_scale 0 means 1 / sqrt(128)
+ * Keys and values that a token does not see have no part in its row, whatever
+ * they hold.  Softmax weights are rounded to bf16 for the product with the
+ * values (row sums are not); the rest is float32.  Should a bounded wait within
+ * the kernel give up, the rows that it keeps from being computed are NaN.
+ */
+oscar_status oscar_chunk_attention(int32_t n_seqs, const int32_t* cu_seqlens, const int32_t* prefix,
+                                   const oscar_rows* q, const oscar_rows* k, const oscar_rows* v,
+                                   int32_t num_q_heads, int32_t num_kv_heads, float softmax_scale,
+                                   const oscar_score_rule* rule, const void* prior_out, const float* prior_lse,
+                                   void* out, float* lse, void* stream);
 
 /* Footprint: kind = OSCAR_BYTES_USED / _BF16_EQUIVALENT for slot `seq`
  * (or all slots if seq == -1), or OSCAR_BYTES_ARENA.  Host arithmetic:

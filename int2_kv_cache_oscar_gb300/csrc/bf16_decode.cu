@@ -16,6 +16,7 @@
 #include <cudaTypedefs.h>
 
 #include "decode_common.cuh"
+#include "tensor_map.h"
 
 namespace oscar {
 namespace {
@@ -369,16 +370,8 @@ __global__ void __launch_bounds__(kThreadsB, 2)
 // 2-D tensor map over rows of 128 bf16 channels: box = 64 channels x 64 rows,
 // 128-byte swizzle.
 bool encode_rows_map(CUtensorMap* map, const void* base, uint64_t rows) {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-  if (encode == nullptr) {
-    cudaDriverEntryPointQueryResult q;
-    void* fn = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || fn == nullptr)
-      return false;
-    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (encode == nullptr) return false;
   const cuuint64_t dims[2] = {kHeadDim, rows};
   const cuuint64_t strides[1] = {kHeadDim * 2};
   const cuuint32_t box[2] = {64, kTile};

@@ -326,6 +326,72 @@ PyObject* sparse_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// x [>= n, heads (-1: any), 128] in bf16 with contiguous channels
+oscar_rows rows(const at::Tensor& x, int64_t n, int64_t heads, const char* name) {
+  if (x.scalar_type() != at::kBFloat16)
+    refuse(PyExc_ValueError, "%s must be torch.bfloat16, got %s", name, type_name(x.scalar_type()));
+  if (x.dim() != 3 || x.size(0) < n || (heads >= 0 && x.size(1) != heads) || x.size(2) != kDim)
+    refuse(PyExc_ValueError, "%s has shape %s, expected %s (leading dimension at least)", name, text(x.sizes()).c_str(),
+           text({n, heads, kDim}).c_str());
+  if (x.stride(2) != 1) refuse(PyExc_ValueError, "%s must have contiguous channels", name);
+  if (x.size(1) > INT32_MAX) refuse(PyExc_ValueError, "%s has too many heads", name);
+  return oscar_rows{x.data_ptr(), x.stride(0), x.stride(1)};
+}
+
+double real(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Raised();
+  return v;
+}
+
+// A score rule from cap and slopes (None or float32 [hq])
+oscar_score_rule score_rule(PyObject* cap, PyObject* slopes, int64_t hq) {
+  oscar_score_rule r{(float)real(cap), 0, nullptr};
+  if (slopes != Py_None) {
+    const at::Tensor& t = tensor(slopes, "slopes");
+    if (t.dim() != 1 || t.size(0) != hq)
+      refuse(PyExc_ValueError, "slopes has shape %s, expected (%lld)", text(t.sizes()).c_str(), (long long)hq);
+    r.slopes = static_cast<const float*>(dense(t, at::kFloat, {hq}, "slopes"));
+  }
+  return r;
+}
+
+// cu_seqlens, prefix, q, k, v, softmax_scale, cap, slopes, prior_out, prior_lse, out, lse, stream
+PyObject* chunk(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 13, [&] {
+    const std::vector<int32_t> cu = integers(a[0], "cu_seqlens");
+    if (cu.empty()) refuse(PyExc_ValueError, "cu_seqlens must have an entry more than there are documents");
+    const size_t docs = cu.size() - 1;
+    std::vector<int32_t> prefix;
+    if (a[1] != Py_None) {
+      prefix = integers(a[1], "prefix");
+      if (prefix.size() != docs) refuse(PyExc_ValueError, "prefix must have an entry for each document");
+    }
+    const int64_t tokens = *std::max_element(cu.begin(), cu.end());
+    const at::Tensor &q = tensor(a[2], "q"), &k = tensor(a[3], "k"), &v = tensor(a[4], "v");
+    const oscar_rows rq = rows(q, tokens, -1, "q"), rk = rows(k, tokens, -1, "k"), rv = rows(v, tokens, k.size(1), "v");
+    const int64_t hq = q.size(1), hkv = k.size(1);
+    const double scale = real(a[5]);
+    const oscar_score_rule rule = score_rule(a[6], a[7], hq);
+    auto row_buffer = [&](PyObject* o, const char* name) -> void* {
+      return o == Py_None ? nullptr : dense(tensor(o, name), at::kBFloat16, {tokens, hq, kDim}, name);
+    };
+    auto lse_buffer = [&](PyObject* o, const char* name) -> float* {
+      return o == Py_None ? nullptr : static_cast<float*>(dense(tensor(o, name), at::kFloat, {tokens, hq}, name));
+    };
+    const void* prior_out = row_buffer(a[8], "prior_out");
+    const float* prior_lse = lse_buffer(a[9], "prior_lse");
+    if (a[10] == Py_None) refuse(PyExc_TypeError, "out must be a torch.Tensor");
+    void* out = row_buffer(a[10], "out");
+    float* lse = lse_buffer(a[11], "lse");
+    void* stream = stream_of(a[12]);
+    return unlocked([&] {
+      return oscar_chunk_attention((int32_t)docs, cu.data(), prefix.empty() ? nullptr : prefix.data(), &rq, &rk, &rv,
+                                   (int32_t)hq, (int32_t)hkv, (float)scale, &rule, prior_out, prior_lse, out, lse, stream);
+    });
+  });
+}
+
 // tensor, stream id, device index, device type (as torch streams name
 // themselves): the stream uses a page-locked tensor until what is enqueued on
 // it now has run.  Its memory, if it came from torch, is not handed out again
@@ -342,7 +408,8 @@ PyObject* host_in_use(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 #define OSCAR_FAST(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {OSCAR_FAST(rotary),        OSCAR_FAST(read),         OSCAR_FAST(index_update),
-                         OSCAR_FAST(select_groups), OSCAR_FAST(sparse_decode), OSCAR_FAST(host_in_use),
+                         OSCAR_FAST(select_groups), OSCAR_FAST(sparse_decode), OSCAR_FAST(chunk),
+                         OSCAR_FAST(host_in_use),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "Calls of liboscar.so on torch tensors.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -306,6 +306,43 @@ cudaError_t launch_prefill(const PrefillParams& p, const uint8_t* arena, bool me
 // the tcgen05 history kernel (prefill_tc.cu); launch_prefill adds the merge of split parts
 cudaError_t launch_prefill_tc(const PrefillParams& p, const uint8_t* arena, bool meta16, cudaStream_t stream);
 
+// ------------------------------------------------------------------- chunk
+
+// One document of a packed chunk: its first token, tokens, the prefix that
+// every token sees, and the first of its row tiles in the launch.
+struct ChunkSeq {
+  int32_t row0;
+  int32_t len;
+  int32_t prefix;
+  int32_t tbase;       // set by the launch
+};
+
+template <int MAXS>
+struct ChunkParams {
+  int32_t n_seqs;      // documents with tokens, the longest first
+  int32_t hkv;
+  int32_t gqa;
+  int32_t hq;
+  int32_t cta_rows;    // (token, head) rows of a CTA, 128 or 256; set by the launch
+  float scale_log2;    // softmax_scale * log2(e)
+  float cap_in;        // 2 softmax_scale log2(e) / cap
+  float cap_out;       // -2 cap log2(e)
+  float cap_log2;      // cap log2(e); 0: no cap
+  const float* slopes; // [hq], or NULL
+  const uint16_t* q;
+  const uint16_t* v;
+  int64_t q_token, q_head, v_token, v_head;   // strides in elements
+  const uint16_t* prior_out;   // [tokens, hq, 128], with prior_lse or both NULL
+  const float* prior_lse;      // [tokens, hq]
+  uint16_t* out;               // [tokens, hq, 128]
+  float* lse;                  // [tokens, hq], or NULL
+  ChunkSeq seq[MAXS];
+};
+
+template <int MAXS>
+cudaError_t launch_chunk(ChunkParams<MAXS>& p, const uint16_t* k, int64_t k_token, int64_t k_head, int64_t tokens,
+                         int sms, cudaStream_t stream);
+
 int num_sms(int device);
 int decode_int2_ctas_per_sm();
 int decode_bf16_ctas_per_sm();

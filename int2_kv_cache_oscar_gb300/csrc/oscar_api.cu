@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdarg>
+#include <cstddef>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -1478,6 +1479,155 @@ oscar_status oscar_sparse_decode_attention(oscar_cache* c, int32_t n_seqs, const
   if (s != OSCAR_OK) return s;
   return decode_call(c, n_seqs, seq_ids, q, num_q_heads, softmax_scale, out, type == OSCAR_F32, workspace,
                      workspace_bytes, stream, groups, n_select, lse);
+}
+
+// ------------------------------------------------------------------------
+// Attention within a chunk.
+
+}  // extern "C"
+
+namespace {
+
+// softmax_scale as given to a call (0: 1 / sqrt(128)).
+float scale_of(float softmax_scale) { return softmax_scale == 0.0f ? 1.0f / std::sqrt((float)kHeadDim) : softmax_scale; }
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// A score rule as the kernels use it; the slopes' address with the call's device current.
+oscar_status check_rule(const oscar_score_rule* r) {
+  if (r == nullptr) return OSCAR_OK;
+  if (r->reserved != 0) return fail(OSCAR_ERR_INVALID_ARG, "rule: reserved must be 0");
+  if (r->cap != 0.0f && !(r->cap >= 0x1p-10f && r->cap <= 0x1p10f))
+    return fail(OSCAR_ERR_INVALID_ARG, "rule: cap must be 0 or in [2^-10, 2^10]");
+  if (!aligned(r->slopes, 4)) return fail(OSCAR_ERR_INVALID_ARG, "rule: slopes must be 4-byte aligned");
+  return OSCAR_OK;
+}
+
+// One input of a chunk call; extents in bytes from its address.
+oscar_status chunk_rows(const oscar_rows* x, const char* name, int64_t tokens, int64_t heads, int device, oscar_rows* out,
+                        int64_t* extent) {
+  if (!x || !x->data) return fail(OSCAR_ERR_INVALID_ARG, "%s is NULL", name);
+  if (!aligned(x->data, 16)) return fail(OSCAR_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
+  *out = *x;
+  // the stride of a single token or head takes part in no address
+  if (tokens == 1) out->token_stride = kHeadDim;
+  if (heads == 1) out->head_stride = kHeadDim;
+  for (const int64_t s : {out->token_stride, out->head_stride})
+    if (s <= 0 || s % 8 != 0 || s >= (int64_t)1 << 36)
+      return fail(OSCAR_ERR_INVALID_ARG, "%s: strides must be positive multiples of 8 elements below 2^36", name);
+  *extent = 2 * ((tokens - 1) * out->token_stride + (heads - 1) * out->head_stride + kHeadDim);
+  return device_view(x->data, name, device, &out->data, false);
+}
+
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const intptr_t x = reinterpret_cast<intptr_t>(a), y = reinterpret_cast<intptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+template <int CAP>
+cudaError_t run_chunk(const ChunkParams<1>& head, const std::vector<ChunkSeq>& seqs, const oscar_rows& k, int64_t tokens,
+                      int sms, cudaStream_t st) {
+  ChunkParams<CAP> P;
+  std::memcpy(&P, &head, offsetof(ChunkParams<1>, seq));
+  static_assert(offsetof(ChunkParams<1>, seq) == offsetof(ChunkParams<CAP>, seq), "the same header");
+  P.n_seqs = (int32_t)seqs.size();
+  std::copy(seqs.begin(), seqs.end(), P.seq);
+  return launch_chunk(P, static_cast<const uint16_t*>(k.data), k.token_stride, k.head_stride, tokens, sms, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+oscar_status oscar_chunk_attention(int32_t n_seqs, const int32_t* cu, const int32_t* prefix, const oscar_rows* q,
+                                   const oscar_rows* k, const oscar_rows* v, int32_t hq, int32_t hkv,
+                                   float softmax_scale, const oscar_score_rule* rule, const void* prior_out,
+                                   const float* prior_lse, void* out, float* lse, void* stream) {
+  try {
+    if (n_seqs < 0) return fail(OSCAR_ERR_INVALID_ARG, "n_seqs < 0");
+    if (n_seqs > kDecodeSeqsLarge) return fail(OSCAR_ERR_CAPACITY, "at most %d documents per call", kDecodeSeqsLarge);
+    if (hkv < 1 || hq < hkv || hq % hkv != 0)
+      return fail(OSCAR_ERR_INVALID_ARG, "num_q_heads must be a positive multiple of num_kv_heads");
+    if ((int64_t)hq + hkv > (1 << 16)) return fail(OSCAR_ERR_INVALID_ARG, "too many heads");
+    if (!(softmax_scale >= 0.0f) || std::isinf(softmax_scale))
+      return fail(OSCAR_ERR_INVALID_ARG, "softmax_scale must be finite and >= 0");
+    oscar_status s = check_rule(rule);
+    if (s != OSCAR_OK) return s;
+    if ((prior_out == nullptr) != (prior_lse == nullptr))
+      return fail(OSCAR_ERR_INVALID_ARG, "pass both prior_out and prior_lse or neither");
+    if (n_seqs == 0) return ok();
+    if (!cu) return fail(OSCAR_ERR_INVALID_ARG, "cu_seqlens is NULL");
+    if (cu[0] != 0) return fail(OSCAR_ERR_INVALID_ARG, "cu_seqlens[0] must be 0");
+    const int32_t gqa = hq / hkv;
+    std::vector<ChunkSeq> seqs;
+    for (int32_t i = 0; i < n_seqs; ++i) {
+      if (cu[i + 1] < cu[i]) return fail(OSCAR_ERR_INVALID_ARG, "cu_seqlens must be non-decreasing");
+      const int32_t len = cu[i + 1] - cu[i], pre = prefix ? prefix[i] : 0;
+      if (pre < 0 || pre > len)
+        return fail(OSCAR_ERR_INVALID_ARG, "prefix[%d] = %d outside the document's %d tokens", i, pre, len);
+      if (len > 0) seqs.push_back(ChunkSeq{cu[i], len, pre, 0});
+    }
+    const int64_t tokens = cu[n_seqs];
+    if (tokens == 0) return ok();
+    if (tokens * hq > (int64_t)INT32_MAX / 2) return fail(OSCAR_ERR_CAPACITY, "too many query rows");
+    if (!out) return fail(OSCAR_ERR_INVALID_ARG, "out is NULL");
+    if (!aligned(out, 16) || !aligned(prior_out, 16) || !aligned(lse, 4) || !aligned(prior_lse, 4))
+      return fail(OSCAR_ERR_INVALID_ARG, "out and prior_out must be 16-byte aligned, lse and prior_lse 4-byte aligned");
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    oscar_rows rq, rk, rv;
+    int64_t eq = 0, ek = 0, ev = 0;
+    if ((s = chunk_rows(q, "q", tokens, hq, dev, &rq, &eq)) != OSCAR_OK) return s;
+    if ((s = chunk_rows(k, "k", tokens, hkv, dev, &rk, &ek)) != OSCAR_OK) return s;
+    if ((s = chunk_rows(v, "v", tokens, hkv, dev, &rv, &ev)) != OSCAR_OK) return s;
+    const int64_t bytes = tokens * hq * kHeadDim * 2;
+    if (overlap(out, bytes, q->data, eq) || overlap(out, bytes, k->data, ek) || overlap(out, bytes, v->data, ev))
+      return fail(OSCAR_ERR_INVALID_ARG, "out overlaps q, k or v");
+    if (prior_out && prior_out != out && overlap(out, bytes, prior_out, bytes))
+      return fail(OSCAR_ERR_INVALID_ARG, "out and prior_out overlap without being the same");
+    if (prior_lse && lse && prior_lse != lse && overlap(lse, tokens * hq * 4, prior_lse, tokens * hq * 4))
+      return fail(OSCAR_ERR_INVALID_ARG, "lse and prior_lse overlap without being the same");
+    const float* slopes = rule ? rule->slopes : nullptr;
+    if ((s = device_view_as(out, "out", dev, &out)) != OSCAR_OK) return s;
+    if (lse && (s = device_view_as(lse, "lse", dev, &lse)) != OSCAR_OK) return s;
+    if (prior_out && (s = device_view_as(prior_out, "prior_out", dev, &prior_out)) != OSCAR_OK) return s;
+    if (prior_lse && (s = device_view_as(prior_lse, "prior_lse", dev, &prior_lse)) != OSCAR_OK) return s;
+    if (slopes && (s = device_view_as(slopes, "slopes", dev, &slopes)) != OSCAR_OK) return s;
+    // the longest documents first: their last tiles take the longest
+    std::stable_sort(seqs.begin(), seqs.end(), [](const ChunkSeq& a, const ChunkSeq& b) { return a.len > b.len; });
+    ChunkParams<1> P;
+    std::memset(&P, 0, sizeof(P));
+    P.hkv = hkv;
+    P.gqa = gqa;
+    P.hq = hq;
+    const float scale = scale_of(softmax_scale), cap = rule ? rule->cap : 0.0f;
+    P.scale_log2 = scale * kLog2e;
+    if (cap != 0.0f) {
+      P.cap_in = 2.0f * scale * kLog2e / cap;
+      P.cap_log2 = cap * kLog2e;
+      P.cap_out = -2.0f * P.cap_log2;
+    }
+    P.slopes = slopes;
+    P.q = static_cast<const uint16_t*>(rq.data);
+    P.v = static_cast<const uint16_t*>(rv.data);
+    P.q_token = rq.token_stride;
+    P.q_head = rq.head_stride;
+    P.v_token = rv.token_stride;
+    P.v_head = rv.head_stride;
+    P.prior_out = static_cast<const uint16_t*>(prior_out);
+    P.prior_lse = prior_lse;
+    P.out = static_cast<uint16_t*>(out);
+    P.lse = lse;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const int sms = num_sms(dev);
+    e = seqs.size() <= (size_t)kDecodeSeqsSmall ? run_chunk<kDecodeSeqsSmall>(P, seqs, rk, tokens, sms, st)
+                                                : run_chunk<kDecodeSeqsLarge>(P, seqs, rk, tokens, sms, st);
+    if (e != cudaSuccess) return cuda_fail(e, "chunk launch");
+    return ok();
+  } catch (const std::exception& ex) {
+    return fail(OSCAR_ERR_INVALID_ARG, "host allocation failed: %s", ex.what());
+  }
 }
 
 // ------------------------------------------------------------------------

@@ -68,6 +68,14 @@ class oscar_rotary_table(ctypes.Structure):
                 ("reserved", ctypes.c_int32), ("phase", ctypes.c_uint64 * (128 // 2))]
 
 
+class oscar_score_rule(ctypes.Structure):
+    _fields_ = [("cap", ctypes.c_float), ("reserved", ctypes.c_int32), ("slopes", ctypes.c_void_p)]
+
+
+class oscar_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
 class oscar_rotary_rows(ctypes.Structure):
     _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p),
                 ("src_token_stride", ctypes.c_int64), ("src_head_stride", ctypes.c_int64),
@@ -120,6 +128,9 @@ def _load() -> ctypes.CDLL:
         "oscar_index_attach": [P, P, SZ],
         "oscar_index_update": [P, I32, I32P, I32, P],
         "oscar_select_groups": [P, I32, I32P, P, I32, I32, I32, I32, P, P],
+        "oscar_chunk_attention": [I32, I32P, I32P, ctypes.POINTER(oscar_rows), ctypes.POINTER(oscar_rows),
+                                  ctypes.POINTER(oscar_rows), I32, I32, ctypes.c_float,
+                                  ctypes.POINTER(oscar_score_rule), P, P, P, P, P],
         "oscar_sparse_decode_attention": [P, I32, I32P, P, I32, ctypes.c_float, P, I32, I32, P, P, P, SZ, P],
     }
     for name, args in sigs.items():
@@ -499,6 +510,21 @@ def oscar_sparse_decode_attention(handle, seq_ids: Sequence[int], q: torch.Tenso
     out bf16 or float32."""
     _check(_calls.sparse_decode(handle, num_kv_heads, seq_ids, q, num_q_heads, softmax_scale, groups, out, workspace,
                                 lse, stream))
+
+
+def oscar_chunk_attention(cu_seqlens: Sequence[int], q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                          out: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                          prefix: Optional[Sequence[int]] = None, cap: float = 0.0,
+                          slopes: Optional[torch.Tensor] = None, prior_out: Optional[torch.Tensor] = None,
+                          prior_lse: Optional[torch.Tensor] = None, softmax_scale: float = 0.0,
+                          stream=None) -> None:
+    """Attention within a chunk of packed documents (rows cu_seqlens[d] ..
+    cu_seqlens[d + 1] - 1 of q [n, heads, 128], k and v [n, kv heads, 128],
+    bf16, any strides with contiguous channels): causal, the first prefix[d]
+    tokens of a document seen by all of its tokens, scores capped to cap
+    tanh(s / cap) and lowered by slopes[head] per token of distance, merged with
+    prior_out and prior_lse (which may be out and lse themselves)."""
+    _check(_calls.chunk(cu_seqlens, prefix, q, k, v, softmax_scale, cap, slopes, prior_out, prior_lse, out, lse, stream))
 
 
 def oscar_cache_bytes(handle, seq: int, kind: int) -> int:
