@@ -451,6 +451,41 @@ oscar_status oscar_cache_import(oscar_cache* cache, int32_t seq, int32_t length,
                                 const void* window, const float* maxima, void* stream);
 
 /*
+ * Copy the first length[i] tokens of slot src[i] to slot dst[i], which then
+ * holds nothing else: forks of a sequence, prefixes taken over by another one;
+ * with dst[i] = src[i] the slot is cut to that length in place.
+ *   src, dst, length  host int32 [n], n <= 1,024; dst distinct; 0 <= length <=
+ *                     the source's tokens; a source may appear in many pairs,
+ *                     but a slot that one pair writes is read by no other
+ * Group blocks, window rows and the maxima are the source's own (the maxima also
+ * where the groups that they come from stay behind: they set the range of the
+ * float16 factors, see oscar_cache_import).  Where length ends inside a
+ * quantised group, that group's tokens continue as window rows, with the values
+ * that oscar_cache_read gives in bf16.  Other slots' copies leave the index
+ * behind (oscar_index_update); a cut keeps the entries of the groups left.
+ * Lengths are updated on the host when the call returns, so a captured call is
+ * replayed only on slots that hold the lengths that it was captured with.
+ */
+oscar_status oscar_cache_fork(oscar_cache* cache, int32_t n, const int32_t* src, const int32_t* dst,
+                              const int32_t* length, void* stream);
+
+/*
+ * Compact: slot dst[i] holds the listed groups of slot src[i], side by side in
+ * their order, then its window; with dst[i] = src[i] in place.
+ *   src, dst   as for oscar_cache_fork
+ *   cu_groups  host int32 [n + 1], cu_groups[0] = 0, non-decreasing
+ *   groups     host int32 [cu_groups[n]]: groups cu_groups[i] .. cu_groups[i + 1]
+ *              - 1 are those that pair i keeps (of every KV head), ascending,
+ *              within the source's groups; none leaves the window alone
+ * The new length is 128 tokens a group and the window.  Keys stay as they were
+ * appended (a rotation is of their position then); distances of a score rule
+ * count the tokens left.  Maxima, index and lengths as for oscar_cache_fork (in
+ * place, index entries of the groups that did not move are kept).
+ */
+oscar_status oscar_cache_keep_groups(oscar_cache* cache, int32_t n, const int32_t* src, const int32_t* dst,
+                                     const int32_t* cu_groups, const int32_t* groups, void* stream);
+
+/*
  * Choosing the groups worth attending.  An index holds an 8-bit summary of
  * every quantised group, 264 bytes per (slot, KV head, group):
  *   +0            int8 [slot][Hkv][max_groups][32][2][4]: for channels 4 l .. 4 l + 3
@@ -602,6 +637,32 @@ oscar_status oscar_chunk_attention(int32_t n_seqs, const int32_t* cu_seqlens, co
                                    const oscar_score_rule* rule, const void* prior_out, const float* prior_lse,
                                    void* out, float* lse, void* stream);
 
+/*
+ * oscar_decode_attention under a score rule (the query of a sequence is its
+ * newest token: a cached token t is at distance length - 1 - t).
+ *   rule  NULL, or with neither cap nor slopes: oscar_decode_attention, or its
+ *         float32 form
+ *   type  OSCAR_BF16 or OSCAR_F32: type of out.  Value factors are held as in
+ *         oscar_sparse_decode_attention (float16 for bf16 outputs)
+ * Every other argument, the workspace and the stream order are those of
+ * oscar_decode_attention.
+ */
+oscar_status oscar_scored_decode_attention(oscar_cache* cache, int32_t n_seqs, const int32_t* seq_ids,
+                                           const void* q, int32_t num_q_heads, float softmax_scale,
+                                           const oscar_score_rule* rule, int32_t type, void* out,
+                                           void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * oscar_prefill_attention under a score rule: query i of the chunk is at
+ * position length + i (a cached token t is at distance length + i - t).  rule
+ * NULL, or with neither cap nor slopes: oscar_prefill_attention.  Every other
+ * argument and the workspace are those of oscar_prefill_attention.
+ */
+oscar_status oscar_scored_prefill_attention(oscar_cache* cache, int32_t seq, int32_t n_q, const void* q,
+                                            int32_t num_q_heads, float softmax_scale,
+                                            const oscar_score_rule* rule, void* out, float* lse, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+
 /* Footprint: kind = OSCAR_BYTES_USED / _BF16_EQUIVALENT for slot `seq`
  * (or all slots if seq == -1), or OSCAR_BYTES_ARENA.  Host arithmetic:
  * a full group costs 13,824 B per KV head (108 B per token) versus 65,536 B
@@ -619,7 +680,7 @@ oscar_status oscar_cache_window_offset(const oscar_cache* cache, int32_t seq, in
 /*
  * Test hook of the failure path: the next INT2 decode, read-back or selection
  * launch made on the calling thread (oscar_decode_attention, _f32,
- * oscar_append_decode, oscar_sparse_decode_attention, oscar_cache_read,
+ * oscar_scored_decode_attention, oscar_append_decode, oscar_sparse_decode_attention, oscar_cache_read,
  * oscar_select_groups) has one bulk copy of its first CTA left unissued, and its bounded waits give up after 2^14 polls
  * instead of 2^24.  (A listed decode of sequences without a group: the window
  * copies of its combine, where it has any.)  The consumer waiting for that copy then

@@ -392,6 +392,105 @@ PyObject* chunk(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// handle, seq_ids, q, num_q_heads, softmax_scale, cap, slopes, out, workspace, stream
+PyObject* scored_decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 10, [&] {
+    const std::vector<int32_t> ids = integers(a[1], "seq_ids");
+    const int64_t b = (int64_t)ids.size();
+    const int32_t hq = integer32(a[3], "num_q_heads");
+    const void* q = dense(tensor(a[2], "q"), at::kBFloat16, {b, hq, kDim}, "q");
+    const double scale = real(a[4]);
+    const oscar_score_rule rule = score_rule(a[5], a[6], hq);
+    const at::Tensor& o = tensor(a[7], "out");
+    const int32_t type = float_type(o, "out");
+    void* out = dense(o, o.scalar_type(), {b, hq, kDim}, "out");
+    const at::Tensor& ws = tensor(a[8], "workspace");
+    void* w = dense(ws, at::kByte, ws.sizes(), "workspace");
+    const size_t w_bytes = (size_t)ws.numel();
+    auto* cache = address<oscar_cache>(a[0]);
+    void* stream = stream_of(a[9]);
+    return unlocked([&] {
+      return oscar_scored_decode_attention(cache, (int32_t)b, ids.data(), q, hq, (float)scale, &rule, type, out, w,
+                                           w_bytes, stream);
+    });
+  });
+}
+
+// handle, seq, q, num_q_heads, softmax_scale, cap, slopes, out, lse, workspace, stream
+PyObject* scored_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 11, [&] {
+    const int32_t seq = integer32(a[1], "seq"), hq = integer32(a[3], "num_q_heads");
+    const at::Tensor& qt = tensor(a[2], "q");
+    const void* q = dense(qt, at::kBFloat16, {-1, hq, kDim}, "q");
+    const int32_t rows = (int32_t)std::min<int64_t>(qt.size(0), INT32_MAX);
+    const double scale = real(a[4]);
+    const oscar_score_rule rule = score_rule(a[5], a[6], hq);
+    void* out = dense(tensor(a[7], "out"), at::kBFloat16, {rows, hq, kDim}, "out");
+    float* lse = a[8] == Py_None ? nullptr : static_cast<float*>(dense(tensor(a[8], "lse"), at::kFloat, {rows, hq}, "lse"));
+    void* w = nullptr;
+    size_t w_bytes = 0;
+    if (a[9] != Py_None) {
+      const at::Tensor& ws = tensor(a[9], "workspace");
+      w = dense(ws, at::kByte, ws.sizes(), "workspace");
+      w_bytes = (size_t)ws.numel();
+    }
+    auto* cache = address<oscar_cache>(a[0]);
+    void* stream = stream_of(a[10]);
+    return unlocked([&] {
+      return oscar_scored_prefill_attention(cache, seq, rows, q, hq, (float)scale, &rule, out, lse, w, w_bytes, stream);
+    });
+  });
+}
+
+// Slots to read from and to write to, one of each a pair
+void pairs(PyObject* so, PyObject* dst_o, std::vector<int32_t>* src, std::vector<int32_t>* dst) {
+  *src = integers(so, "src");
+  *dst = integers(dst_o, "dst");
+  if (src->size() != dst->size()) refuse(PyExc_ValueError, "src and dst must have the same length");
+}
+
+// handle, src, dst, length, stream
+PyObject* fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 5, [&] {
+    std::vector<int32_t> src, dst;
+    pairs(a[1], a[2], &src, &dst);
+    const std::vector<int32_t> length = integers(a[3], "length");
+    if (length.size() != src.size()) refuse(PyExc_ValueError, "length must have an entry for each pair");
+    auto* cache = address<oscar_cache>(a[0]);
+    void* stream = stream_of(a[4]);
+    return unlocked([&] { return oscar_cache_fork(cache, (int32_t)src.size(), src.data(), dst.data(), length.data(), stream); });
+  });
+}
+
+// handle, src, dst, groups (a sequence for each pair), stream
+PyObject* keep_groups(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return call(n, 5, [&] {
+    std::vector<int32_t> src, dst;
+    pairs(a[1], a[2], &src, &dst);
+    PyObject* lists = PySequence_Fast(a[3], "groups must be a sequence of sequences of integers");
+    if (!lists) throw Raised();
+    std::vector<int32_t> groups, cu{0};
+    try {
+      for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(lists); ++i) {
+        const std::vector<int32_t> g = integers(PySequence_Fast_GET_ITEM(lists, i), "groups");
+        groups.insert(groups.end(), g.begin(), g.end());
+        if (groups.size() > (size_t)INT32_MAX) refuse(PyExc_ValueError, "groups has too many entries");
+        cu.push_back((int32_t)groups.size());
+      }
+    } catch (...) {
+      Py_DECREF(lists);
+      throw;
+    }
+    Py_DECREF(lists);
+    if (cu.size() != src.size() + 1) refuse(PyExc_ValueError, "groups must have a list for each pair");
+    auto* cache = address<oscar_cache>(a[0]);
+    void* stream = stream_of(a[4]);
+    return unlocked([&] {
+      return oscar_cache_keep_groups(cache, (int32_t)src.size(), src.data(), dst.data(), cu.data(), groups.data(), stream);
+    });
+  });
+}
+
 // tensor, stream id, device index, device type (as torch streams name
 // themselves): the stream uses a page-locked tensor until what is enqueued on
 // it now has run.  Its memory, if it came from torch, is not handed out again
@@ -409,6 +508,8 @@ PyObject* host_in_use(PyObject*, PyObject* const* a, Py_ssize_t n) {
 #define OSCAR_FAST(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {OSCAR_FAST(rotary),        OSCAR_FAST(read),         OSCAR_FAST(index_update),
                          OSCAR_FAST(select_groups), OSCAR_FAST(sparse_decode), OSCAR_FAST(chunk),
+                         OSCAR_FAST(scored_decode), OSCAR_FAST(scored_prefill), OSCAR_FAST(fork),
+                         OSCAR_FAST(keep_groups),
                          OSCAR_FAST(host_in_use),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", "Calls of liboscar.so on torch tensors.", -1, methods,

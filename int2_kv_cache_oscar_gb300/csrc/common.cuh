@@ -284,6 +284,43 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float x) {
   return u >> 16;
 }
 
+// cap tanh(s / cap), all in log2 units: s, cap, and inv = 1 / cap.  Within 0.4
+// of zero the odd series of tanh (to x^13: the next term is 2^-25 of the sum
+// there), elsewhere 1 - 2 / (1 + e^2x) with the hardware's exponential and
+// reciprocal: tanh is off by 2^-23 at most there, by 2^-23 of itself within.
+// `all_small`: every |s| of the warp is within 0.4 cap (uniform); the series
+// alone is then worked out, in packed pairs.
+__device__ __forceinline__ float2 tanh_series(float2 x) {
+  const float2 y = __fmul2_rn(x, x);
+  auto c = [](float v) { return make_float2(v, v); };
+  float2 t = c(21844.0f / 6081075.0f);
+  t = __ffma2_rn(t, y, c(-1382.0f / 155925.0f));
+  t = __ffma2_rn(t, y, c(62.0f / 2835.0f));
+  t = __ffma2_rn(t, y, c(-17.0f / 315.0f));
+  t = __ffma2_rn(t, y, c(2.0f / 15.0f));
+  t = __ffma2_rn(t, y, c(-1.0f / 3.0f));
+  return __ffma2_rn(__fmul2_rn(t, y), x, x);
+}
+
+__device__ __forceinline__ float tanh_far(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(2.8853900817779268f * x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return fmaf(-2.0f, r, 1.0f);
+}
+
+constexpr float kTanhNear = 0.4f;
+
+__device__ __forceinline__ float2 capped(float2 s, float cap, float inv, bool all_small) {
+  const float2 x = __fmul2_rn(s, make_float2(inv, inv));
+  float2 t = tanh_series(x);
+  if (!all_small) {
+    if (!(fabsf(x.x) <= kTanhNear)) t.x = tanh_far(x.x);   // (NaN too)
+    if (!(fabsf(x.y) <= kTanhNear)) t.y = tanh_far(x.y);
+  }
+  return __fmul2_rn(t, make_float2(cap, cap));
+}
+
 // Bit position exponent p of fragment slot i = 2*kk + hf: codes at bits
 // 2i (i <= 4) are read in place; codes at i = 5..7 are read after a 10-bit
 // right shift, i.e. at bits 2(i - 5).  An extracted fp16 is then the

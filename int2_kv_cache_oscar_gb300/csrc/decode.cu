@@ -166,14 +166,16 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
-// LISTED: 0 every group; listed groups with 1 bf16, 2 float32 outputs
-template <int MAXS, bool M16, bool PAIRS, int LISTED>
+// LISTED: 0 every group; listed groups with 1 bf16, 2 float32 outputs.
+// RULE: every group under a score rule, with LISTED's arithmetic for its output
+// type (1 or 2) but without a list
+template <int MAXS, bool M16, bool PAIRS, int LISTED, bool RULE>
 __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
     decode_int2_kernel(const __grid_constant__ DecodeParams<MAXS> p, const uint8_t* __restrict__ arena) {
   using DecSmem = DecSmemT<M16>;
   using B = Blk<M16>;
   using MR = Meta<M16>;
-  constexpr bool SPARSE = LISTED != 0;
+  constexpr bool SPARSE = LISTED != 0 && !RULE;
   // Bit positions at which codes are read (see frag_p).  Score sums over outlier
   // keys are off by 1e-6 to 4e-6 of the score in mode 0 (1.6e-5 of the outputs)
   // and at float32 rounding in mode 1 (mode 2 changes nothing more); with that
@@ -186,7 +188,7 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
   // 159 entries: off by 0.1 to 2.9e-6 with the tensor core's sums over a group at
   // bits 6 to 9, 0.1 to 1.9e-6 with sums over a k-step, 0.1 to 1.2e-6 with those
   // at bits 7 to 10 (32-bit products and sums: 0.1 to 1.7e-6), in the same time.
-  constexpr int kKeyMode = SPARSE ? 1 : 0, kValueMode = LISTED == 2 ? 2 : 0;
+  constexpr int kKeyMode = LISTED != 0 ? 1 : 0, kValueMode = LISTED == 2 ? 2 : 0;
   constexpr bool kSteps = LISTED == 2;
   // bf16 outputs from listed groups take the value factors p s^V in fp16 alone,
   // where the output is rounded by 2^-8: off by 2^-11 of a factor while it is a
@@ -485,6 +487,13 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
       fsc[kk] = fv * pow2f(half ? -frag_p<kValueMode>(2 * kk + 1) : -frag_p<kValueMode>(2 * kk));
     }
 
+    // the rule's slope of head tig, and where its query is (the newest token)
+    float slope2 = 0.0f;
+    if constexpr (RULE) {
+      if (p.h.rule.slopes != nullptr && h0 + tig < gqa)
+        slope2 = p.h.rule.slopes[j * p.h.q_group + p.h.q_head0 + h0 + tig] * 1.4426950408889634f;
+    }
+
     float m_run = -INFINITY;   // running max (log2 units) of head tig
     float l_run = 0.0f;        // partial sum of p over this lane's tokens
     float2 o_acc[8];           // head tig, channels 16 mt + g (.x) and + 8 (.y), times 2^(Fv - 24)
@@ -583,6 +592,23 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
             sc[mt] = __fmul2_rn(__ffma2_rn(a, kq2, qz2), make_float2(MR::one(knm, t0), MR::one(knm, t0 + 8)));
           }
         }
+      }
+
+      if constexpr (RULE) {
+        if (p.h.rule.cap != 0.0f) {
+          float top = 0.0f;
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt) top = fmaxf(top, fmaxf(fabsf(sc[mt].x), fabsf(sc[mt].y)));
+          const bool small = __all_sync(0xffffffffu, top * p.h.rule.inv_cap <= kTanhNear);
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt) sc[mt] = capped(sc[mt], p.h.rule.cap, p.h.rule.inv_cap, small);
+        }
+        // distance: tokens from 128 group + 16 mt + g (.x), + 8 (.y) to the newest
+        const float far = (float)(p.seq[b].len - 1 - kGroup * (g0 + (int)(kk - k_begin)) - g);
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt)
+          sc[mt] = __ffma2_rn(make_float2(-slope2, -slope2),
+                              make_float2(far - (float)(16 * mt), far - (float)(16 * mt + 8)), sc[mt]);
       }
 
       // ---- online softmax (head tig)
@@ -877,6 +903,9 @@ __global__ void __launch_bounds__(kCombineThreads)
         a0 = fmaf(qb.z, bf16_lo(kv4.w), a0); a1 = fmaf(qb.w, bf16_hi(kv4.w), a1);
       }
       scw = (a0 + a1) * p.h.scale_log2;
+      if (p.h.rule.cap != 0.0f) scw = capped(make_float2(scw, 0.0f), p.h.rule.cap, p.h.rule.inv_cap, false).x;
+      if (p.h.rule.slopes != nullptr)
+        scw = fmaf(-1.4426950408889634f * p.h.rule.slopes[j * p.h.q_group + p.h.q_head0 + h], (float)(wlen - 1 - t), scw);
     }
     mxw = scw;
 #pragma unroll
@@ -1338,13 +1367,13 @@ int num_sms(int device) {
   return n;
 }
 
-template <int MAXS, bool M16, bool PAIRS, int LISTED>
+template <int MAXS, bool M16, bool PAIRS, int LISTED, bool RULE>
 cudaError_t launch_decode_int2_t(const DecodeParams<MAXS>& p, const uint8_t* arena, cudaStream_t stream,
                                  cudaEvent_t ev_start, cudaEvent_t ev_stop) {
   if (p.h.n_units <= 0) return cudaSuccess;
   const int smem = (int)sizeof(DecSmemT<M16>);
   static bool attr_done[64] = {};
-  cudaError_t e = ensure_smem_attr(decode_int2_kernel<MAXS, M16, PAIRS, LISTED>, smem, attr_done);
+  cudaError_t e = ensure_smem_attr(decode_int2_kernel<MAXS, M16, PAIRS, LISTED, RULE>, smem, attr_done);
   if (e != cudaSuccess) return e;
   if (ev_start) cudaEventRecord(ev_start, stream);
   // programmatic dependent launch: the grid may start while the previous
@@ -1359,7 +1388,7 @@ cudaError_t launch_decode_int2_t(const DecodeParams<MAXS>& p, const uint8_t* are
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, decode_int2_kernel<MAXS, M16, PAIRS, LISTED>, p, arena);
+  e = cudaLaunchKernelEx(&cfg, decode_int2_kernel<MAXS, M16, PAIRS, LISTED, RULE>, p, arena);
   if (e == cudaSuccess) e = cudaGetLastError();
   if (ev_stop) cudaEventRecord(ev_stop, stream);
   return e;
@@ -1369,18 +1398,21 @@ template <int MAXS>
 cudaError_t launch_decode_int2(const DecodeParams<MAXS>& p, const uint8_t* arena, bool meta16, cudaStream_t stream,
                                cudaEvent_t ev_start, cudaEvent_t ev_stop) {
   // more than kMaxGqa query heads per KV head: two head sets on the same blocks
-  auto launch = [&](auto m16, auto pairs, auto listed) {
-    return launch_decode_int2_t<MAXS, decltype(m16)::value, decltype(pairs)::value, decltype(listed)::value>(
-        p, arena, stream, ev_start, ev_stop);
+  auto launch = [&](auto m16, auto pairs, auto listed, auto rule) {
+    return launch_decode_int2_t<MAXS, decltype(m16)::value, decltype(pairs)::value, decltype(listed)::value,
+                                decltype(rule)::value>(p, arena, stream, ev_start, ev_stop);
   };
   using T = std::true_type;
   using F = std::false_type;
-  auto by_layout = [&](auto listed) {
-    if (p.h.gqa > kMaxGqa) return meta16 ? launch(T{}, T{}, listed) : launch(F{}, T{}, listed);
-    return meta16 ? launch(T{}, F{}, listed) : launch(F{}, F{}, listed);
+  auto by_layout = [&](auto listed, auto rule) {
+    if (p.h.gqa > kMaxGqa) return meta16 ? launch(T{}, T{}, listed, rule) : launch(F{}, T{}, listed, rule);
+    return meta16 ? launch(T{}, F{}, listed, rule) : launch(F{}, F{}, listed, rule);
   };
-  if (p.h.groups == nullptr) return by_layout(std::integral_constant<int, 0>{});
-  return p.h.out_f32 ? by_layout(std::integral_constant<int, 2>{}) : by_layout(std::integral_constant<int, 1>{});
+  using Bf16 = std::integral_constant<int, 1>;
+  using F32 = std::integral_constant<int, 2>;
+  if (p.h.rule.any()) return p.h.out_f32 ? by_layout(F32{}, T{}) : by_layout(Bf16{}, T{});
+  if (p.h.groups == nullptr) return by_layout(std::integral_constant<int, 0>{}, F{});
+  return p.h.out_f32 ? by_layout(F32{}, F{}) : by_layout(Bf16{}, F{});
 }
 
 template <int MAXS>

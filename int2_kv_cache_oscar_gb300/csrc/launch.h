@@ -79,6 +79,14 @@ cudaError_t launch_quantize_small(const QuantPlan<kQuantPlanSmall>& plan, uint8_
 cudaError_t launch_quantize_large(const QuantPlan<kQuantPlanLarge>& plan, uint8_t* arena, const uint16_t* k,
                                   const uint16_t* v, bool meta16, cudaStream_t stream);
 
+// The score rule (include/oscar.h) as the cache's kernels use it, in log2 units.
+struct ScoreRule {
+  float cap;             // cap log2(e); 0: none
+  float inv_cap;
+  const float* slopes;   // [query heads], natural units, or NULL
+  __host__ __device__ bool any() const { return cap != 0.0f || slopes != nullptr; }
+};
+
 // ------------------------------------------------------------------ decode
 
 // Per-sequence data of one decode launch.  Work units are (sequence, KV head,
@@ -136,6 +144,7 @@ struct DecodeHeader {
   int32_t n_sel;
   int32_t comb_row;      // listed groups: the combine's CTAs take a KV head (else a query head)
   float* lse;            // [n_seqs, hq] natural-log log-sum-exp of the rows, or NULL
+  ScoreRule rule;        // every group only (not with `groups`)
 };
 
 template <int MAXS>
@@ -202,8 +211,10 @@ struct ReadParams {
   int64_t blocks_off;
   int64_t windows_off;
   int64_t n_tiles;
-  void* k_out;         // [rows, hkv, 128], or NULL
+  void* k_out;         // rows of 128 channels, or NULL
   void* v_out;
+  int64_t row_pitch;   // elements from one row of an output to the next, and from
+  int64_t head_pitch;  // one KV head to the next
   uint32_t spin_limit; // polls of a bounded wait; the test hook's `fault` (1) leaves
   int32_t fault;       // the copy of tile 0 unissued, with a small limit
   ReadSeq seq[MAXS];
@@ -288,6 +299,7 @@ struct PrefillParams {
   int64_t windows_off;
   int64_t zmax_off;      // per (slot, head) largest |value zero| quantised so far (float bits)
   float scale_log2;      // softmax_scale * log2(e)
+  ScoreRule rule;
   int32_t n_parts;       // the groups are split into this many parts (grid.z); 1: no split
   const uint16_t* q;     // [n_q, hq, d] bf16
   uint16_t* out;         // [n_q, hq, d] bf16
@@ -305,6 +317,55 @@ constexpr int kPrefillRecFloats = 132;
 cudaError_t launch_prefill(const PrefillParams& p, const uint8_t* arena, bool meta16, cudaStream_t stream);
 // the tcgen05 history kernel (prefill_tc.cu); launch_prefill adds the merge of split parts
 cudaError_t launch_prefill_tc(const PrefillParams& p, const uint8_t* arena, bool meta16, cudaStream_t stream);
+
+// -------------------------------------------------------------------- move
+
+// Groups g0 .. g0 + groups - 1 of the destinations dst0 .. dst0 + n_dst - 1 of
+// one source slot: the same groups of the source, or (n_runs > 0) those of its
+// runs.  A copy's units are (KV head, group), numbered from ubase.
+struct MoveTask {
+  int32_t src;
+  int32_t dst0, n_dst;
+  int32_t g0, groups;
+  int32_t run0, n_runs;
+  int64_t ubase;
+};
+
+struct MoveDst {
+  int32_t src, slot;     // equal: compacted in place (window and maxima stay)
+  int32_t groups;        // of the destination; a task's destinations in descending order
+  int32_t wlen;          // window rows copied
+};
+
+struct MoveRun {         // destination groups dst, dst + 1, ... are source groups src, src + 1, ...
+  int32_t dst, src;
+};
+
+template <int TASKS, int RUNS>
+struct MoveParams {
+  int32_t n_tasks;
+  int32_t n_dst;
+  int32_t hkv;
+  int32_t max_groups;
+  int32_t block_bytes;
+  int32_t reserved;
+  int64_t n_units;
+  int64_t blocks_off;
+  int64_t windows_off;
+  int64_t zmax_off;
+  MoveTask task[TASKS];
+  MoveDst dst[TASKS];
+  MoveRun run[RUNS];
+};
+
+constexpr int kMoveTasksSmall = 32, kMoveRunsSmall = 64;
+constexpr int kMoveTasksLarge = 400, kMoveRunsLarge = 1200;
+static_assert(sizeof(MoveParams<kMoveTasksLarge, kMoveRunsLarge>) + 16 <= 32764, "kernel parameter limit");
+
+template <int TASKS, int RUNS>
+cudaError_t launch_move(const MoveParams<TASKS, RUNS>& p, uint8_t* arena, int sms, cudaStream_t stream);
+template <int TASKS, int RUNS>
+cudaError_t launch_compact(const MoveParams<TASKS, RUNS>& p, uint8_t* arena, int sms, cudaStream_t stream);
 
 // ------------------------------------------------------------------- chunk
 

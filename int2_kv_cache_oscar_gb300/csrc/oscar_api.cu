@@ -157,6 +157,39 @@ oscar_status device_view_as(T* ptr, const char* name, int device, T** out, bool 
   return s;
 }
 
+oscar_status check_type(int32_t type) {
+  if (type != OSCAR_BF16 && type != OSCAR_F32)
+    return fail(OSCAR_ERR_UNSUPPORTED, "type must be OSCAR_BF16 or OSCAR_F32 (got %d)", type);
+  return OSCAR_OK;
+}
+
+// softmax_scale as given to a call (0: 1 / sqrt(128)).
+float scale_of(float softmax_scale) { return softmax_scale == 0.0f ? 1.0f / std::sqrt((float)kHeadDim) : softmax_scale; }
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// A score rule as the kernels use it; the slopes' address with the call's device current.
+oscar_status check_rule(const oscar_score_rule* r) {
+  if (r == nullptr) return OSCAR_OK;
+  if (r->reserved != 0) return fail(OSCAR_ERR_INVALID_ARG, "rule: reserved must be 0");
+  if (r->cap != 0.0f && !(r->cap >= 0x1p-10f && r->cap <= 0x1p10f))
+    return fail(OSCAR_ERR_INVALID_ARG, "rule: cap must be 0 or in [2^-10, 2^10]");
+  if (!aligned(r->slopes, 4)) return fail(OSCAR_ERR_INVALID_ARG, "rule: slopes must be 4-byte aligned");
+  return OSCAR_OK;
+}
+
+// The rule for the cache's kernels; with the cache's device current.
+oscar_status cache_rule(const oscar_score_rule* r, int device, ScoreRule* out) {
+  *out = ScoreRule{0.0f, 0.0f, nullptr};
+  if (r == nullptr) return OSCAR_OK;
+  if (r->cap != 0.0f) {
+    out->cap = r->cap * kLog2e;
+    out->inv_cap = 1.0f / out->cap;
+  }
+  out->slopes = r->slopes;
+  return out->slopes ? device_view_as(out->slopes, "slopes", device, &out->slopes) : OSCAR_OK;
+}
+
 oscar_status check_slots(const oscar_cache* c, int32_t n, const int32_t* ids, std::vector<char>& seen) {
   seen.assign(c->cfg.max_batch, 0);
   for (int32_t i = 0; i < n; ++i) {
@@ -227,9 +260,11 @@ oscar_status run_decode(int device, int sms, int ctas_per_sm, int32_t n, const i
                         const uint16_t* vc, const void* q, void* out, void* ws, size_t ws_bytes,
                         cudaStream_t stream, const void* k_new = nullptr, const void* v_new = nullptr,
                         bool meta16 = false, bool out_f32 = false, const int32_t* settled = nullptr,
-                        const int32_t* groups = nullptr, int32_t n_sel = 0, float* lse = nullptr) {
+                        const int32_t* groups = nullptr, int32_t n_sel = 0, float* lse = nullptr,
+                        const ScoreRule* rule = nullptr) {
   DecodeParams<MAXS> P;
   std::memset(&P, 0, sizeof(P));
+  if (rule) P.h.rule = *rule;
   int64_t rows = 0;
   fill_decode(P, n, slots, lens, hkv, bf16_mode, n_sel, rows);
   P.h.groups = groups;
@@ -574,10 +609,12 @@ void note_decode(oscar_cache* c, int32_t n, const int32_t* ids, cudaStream_t st)
 }
 
 // oscar_decode_attention and oscar_decode_attention_f32 (out_f32: float32 outputs);
-// with `groups`, oscar_sparse_decode_attention.
+// with `groups`, oscar_sparse_decode_attention; with `rule` (checked),
+// oscar_scored_decode_attention.
 oscar_status decode_call(oscar_cache* c, int32_t n_seqs, const int32_t* seq_ids, const void* q, int32_t num_q_heads,
                          float softmax_scale, void* out, bool out_f32, void* workspace, size_t workspace_bytes,
-                         void* stream, const int32_t* groups = nullptr, int32_t n_sel = 0, float* lse = nullptr) {
+                         void* stream, const int32_t* groups = nullptr, int32_t n_sel = 0, float* lse = nullptr,
+                         const oscar_score_rule* rule = nullptr) {
   try {
     if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
     if (n_seqs < 1) return fail(OSCAR_ERR_INVALID_ARG, "n_seqs must be >= 1");
@@ -606,6 +643,8 @@ oscar_status decode_call(oscar_cache* c, int32_t n_seqs, const int32_t* seq_ids,
     if ((s = device_view_as(workspace, "workspace", c->cfg.device, &workspace, false)) != OSCAR_OK) return s;
     if (groups && (s = device_view_as(groups, "groups", c->cfg.device, &groups, false)) != OSCAR_OK) return s;
     if (lse && (s = device_view_as(lse, "lse", c->cfg.device, &lse)) != OSCAR_OK) return s;
+    ScoreRule how;
+    if ((s = cache_rule(rule, c->cfg.device, &how)) != OSCAR_OK) return s;
     uint32_t* err_word = reinterpret_cast<uint32_t*>(c->arena);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // (listed groups are device data: none of their blocks is copied early)
@@ -615,13 +654,13 @@ oscar_status decode_call(oscar_cache* c, int32_t n_seqs, const int32_t* seq_ids,
                                        lens.data(), hkv, num_q_heads, scale, 0, c->layout.max_groups,
                                        c->layout.blocks_off, c->layout.windows_off, c->arena, err_word, nullptr,
                                        nullptr, q, out, workspace, workspace_bytes, st, nullptr, nullptr,
-                                       c->meta16, out_f32, settled.data(), groups, n_sel, lse);
+                                       c->meta16, out_f32, settled.data(), groups, n_sel, lse, &how);
     else
       s = run_decode<kDecodeSeqsLarge>(c->cfg.device, c->sms, decode_int2_ctas_per_sm(), n_seqs, seq_ids,
                                        lens.data(), hkv, num_q_heads, scale, 0, c->layout.max_groups,
                                        c->layout.blocks_off, c->layout.windows_off, c->arena, err_word, nullptr,
                                        nullptr, q, out, workspace, workspace_bytes, st, nullptr, nullptr,
-                                       c->meta16, out_f32, settled.data(), groups, n_sel, lse);
+                                       c->meta16, out_f32, settled.data(), groups, n_sel, lse, &how);
     if (s != OSCAR_OK) return s;
     note_decode(c, n_seqs, seq_ids, st);
     return ok();
@@ -646,6 +685,17 @@ oscar_status oscar_decode_attention_f32(oscar_cache* c, int32_t n_seqs, const in
                                         size_t workspace_bytes, void* stream) {
   return decode_call(c, n_seqs, seq_ids, q, num_q_heads, softmax_scale, out, true, workspace, workspace_bytes,
                      stream);
+}
+
+oscar_status oscar_scored_decode_attention(oscar_cache* c, int32_t n_seqs, const int32_t* seq_ids, const void* q,
+                                           int32_t num_q_heads, float softmax_scale, const oscar_score_rule* rule,
+                                           int32_t type, void* out, void* workspace, size_t workspace_bytes,
+                                           void* stream) {
+  oscar_status s = check_type(type);
+  if (s == OSCAR_OK) s = check_rule(rule);
+  if (s != OSCAR_OK) return s;
+  return decode_call(c, n_seqs, seq_ids, q, num_q_heads, softmax_scale, out, type == OSCAR_F32, workspace,
+                     workspace_bytes, stream, nullptr, 0, nullptr, rule);
 }
 
 oscar_status oscar_test_settled_groups(const oscar_cache* c, int32_t n_seqs, const int32_t* seq_ids, void* stream,
@@ -777,9 +827,9 @@ oscar_status oscar_prefill_workspace_bytes(const oscar_cache* c, int32_t seq, in
   return ok();
 }
 
-oscar_status oscar_prefill_attention(oscar_cache* c, int32_t seq, int32_t n_q, const void* q, int32_t num_q_heads,
-                                     float softmax_scale, void* out, float* lse, void* workspace,
-                                     size_t workspace_bytes, void* stream) {
+static oscar_status prefill_call(oscar_cache* c, int32_t seq, int32_t n_q, const void* q, int32_t num_q_heads,
+                                 float softmax_scale, const oscar_score_rule* rule, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
   if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
   if (seq < 0 || seq >= c->cfg.max_batch) return fail(OSCAR_ERR_INVALID_ARG, "seq %d out of range", seq);
   if (n_q < 1) return fail(OSCAR_ERR_INVALID_ARG, "n_q must be >= 1");
@@ -834,10 +884,26 @@ oscar_status oscar_prefill_attention(oscar_cache* c, int32_t seq, int32_t n_q, c
     if ((sv = device_view_as(P.q, "q", c->cfg.device, &P.q)) != OSCAR_OK) return sv;
     if ((sv = device_view_as(P.out, "out", c->cfg.device, &P.out)) != OSCAR_OK) return sv;
     if (P.lse != nullptr && (sv = device_view_as(P.lse, "lse", c->cfg.device, &P.lse)) != OSCAR_OK) return sv;
+    if ((sv = cache_rule(rule, c->cfg.device, &P.rule)) != OSCAR_OK) return sv;
   }
   cudaError_t e = launch_prefill(P, c->arena, c->meta16, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
   return ok();
+}
+
+oscar_status oscar_prefill_attention(oscar_cache* c, int32_t seq, int32_t n_q, const void* q, int32_t num_q_heads,
+                                     float softmax_scale, void* out, float* lse, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  return prefill_call(c, seq, n_q, q, num_q_heads, softmax_scale, nullptr, out, lse, workspace, workspace_bytes, stream);
+}
+
+oscar_status oscar_scored_prefill_attention(oscar_cache* c, int32_t seq, int32_t n_q, const void* q,
+                                            int32_t num_q_heads, float softmax_scale, const oscar_score_rule* rule,
+                                            void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                            void* stream) {
+  const oscar_status s = check_rule(rule);
+  if (s != OSCAR_OK) return s;
+  return prefill_call(c, seq, n_q, q, num_q_heads, softmax_scale, rule, out, lse, workspace, workspace_bytes, stream);
 }
 
 oscar_status oscar_cache_bytes(const oscar_cache* c, int32_t seq, int32_t kind, size_t* out_bytes) {
@@ -982,12 +1048,6 @@ oscar_status check_batch(const oscar_cache* c, int32_t n_seqs, const int32_t* se
   return OSCAR_OK;
 }
 
-oscar_status check_type(int32_t type) {
-  if (type != OSCAR_BF16 && type != OSCAR_F32)
-    return fail(OSCAR_ERR_UNSUPPORTED, "type must be OSCAR_BF16 or OSCAR_F32 (got %d)", type);
-  return OSCAR_OK;
-}
-
 // Entries of a row's group list: at most the groups that the longest sequence has.
 oscar_status check_entries(int32_t n_select) {
   if (n_select < 1 || n_select > (1 << 24))
@@ -1097,7 +1157,7 @@ oscar_status rotary_rows(const oscar_rotary_rows* rows, const char* name, int64_
 
 template <int CAP>
 oscar_status run_read(oscar_cache* c, const std::vector<ReadSeq>& seqs, size_t first, size_t n, bool f32, void* k,
-                      void* v, cudaStream_t st) {
+                      void* v, cudaStream_t st, bool to_windows = false) {
   ReadParams<CAP> P;
   std::memset(&P, 0, sizeof(P));
   P.n_seqs = (int32_t)n;
@@ -1108,7 +1168,9 @@ oscar_status run_read(oscar_cache* c, const std::vector<ReadSeq>& seqs, size_t f
   P.windows_off = c->layout.windows_off;
   P.k_out = k;
   P.v_out = v;
-  P.fault = take_armed_timeout() ? 1 : 0;
+  P.row_pitch = to_windows ? kHeadDim : (int64_t)P.hkv * kHeadDim;
+  P.head_pitch = to_windows ? kWindowBytes / 2 : kHeadDim;
+  P.fault = !to_windows && take_armed_timeout() ? 1 : 0;
   P.spin_limit = P.fault ? kArmedSpinLimit : kSpinLimit;
   int64_t ubase = 0;
   for (size_t i = 0; i < n; ++i) {
@@ -1488,21 +1550,6 @@ oscar_status oscar_sparse_decode_attention(oscar_cache* c, int32_t n_seqs, const
 
 namespace {
 
-// softmax_scale as given to a call (0: 1 / sqrt(128)).
-float scale_of(float softmax_scale) { return softmax_scale == 0.0f ? 1.0f / std::sqrt((float)kHeadDim) : softmax_scale; }
-
-constexpr float kLog2e = 1.4426950408889634f;
-
-// A score rule as the kernels use it; the slopes' address with the call's device current.
-oscar_status check_rule(const oscar_score_rule* r) {
-  if (r == nullptr) return OSCAR_OK;
-  if (r->reserved != 0) return fail(OSCAR_ERR_INVALID_ARG, "rule: reserved must be 0");
-  if (r->cap != 0.0f && !(r->cap >= 0x1p-10f && r->cap <= 0x1p10f))
-    return fail(OSCAR_ERR_INVALID_ARG, "rule: cap must be 0 or in [2^-10, 2^10]");
-  if (!aligned(r->slopes, 4)) return fail(OSCAR_ERR_INVALID_ARG, "rule: slopes must be 4-byte aligned");
-  return OSCAR_OK;
-}
-
 // One input of a chunk call; extents in bytes from its address.
 oscar_status chunk_rows(const oscar_rows* x, const char* name, int64_t tokens, int64_t heads, int device, oscar_rows* out,
                         int64_t* extent) {
@@ -1624,6 +1671,220 @@ oscar_status oscar_chunk_attention(int32_t n_seqs, const int32_t* cu, const int3
     e = seqs.size() <= (size_t)kDecodeSeqsSmall ? run_chunk<kDecodeSeqsSmall>(P, seqs, rk, tokens, sms, st)
                                                 : run_chunk<kDecodeSeqsLarge>(P, seqs, rk, tokens, sms, st);
     if (e != cudaSuccess) return cuda_fail(e, "chunk launch");
+    return ok();
+  } catch (const std::exception& ex) {
+    return fail(OSCAR_ERR_INVALID_ARG, "host allocation failed: %s", ex.what());
+  }
+}
+
+// ------------------------------------------------------------------------
+// Sequences copied to other slots and compacted.
+
+}  // extern "C"
+
+namespace {
+
+// Checks shared by both calls: the slots, and that no slot is read by one pair
+// and written by another.
+oscar_status check_pairs(const oscar_cache* c, int32_t n, const int32_t* src, const int32_t* dst) {
+  if (!c) return fail(OSCAR_ERR_INVALID_ARG, "cache is NULL");
+  if (n < 0) return fail(OSCAR_ERR_INVALID_ARG, "n < 0");
+  if (n > kDecodeSeqsLarge) return fail(OSCAR_ERR_CAPACITY, "at most %d sequences per call", kDecodeSeqsLarge);
+  if (n > 0 && (!src || !dst)) return fail(OSCAR_ERR_INVALID_ARG, "src / dst is NULL");
+  std::vector<char> written(c->cfg.max_batch, 0);
+  for (int32_t i = 0; i < n; ++i) {
+    for (const int32_t s : {src[i], dst[i]})
+      if (s < 0 || s >= c->cfg.max_batch) return fail(OSCAR_ERR_INVALID_ARG, "pair %d: slot %d out of range", i, s);
+    if (written[dst[i]]) return fail(OSCAR_ERR_INVALID_ARG, "dst[%d] = %d repeated", i, dst[i]);
+    written[dst[i]] = 1;
+  }
+  for (int32_t i = 0; i < n; ++i)
+    if (src[i] != dst[i] && written[src[i]])
+      return fail(OSCAR_ERR_INVALID_ARG, "src[%d] = %d is written by another pair", i, src[i]);
+  return OSCAR_OK;
+}
+
+// What is enqueued of a fork or a compaction, in as many launches as their
+// parameters need.
+struct MovePlan {
+  std::vector<MoveTask> task;
+  std::vector<MoveDst> dst;
+  std::vector<MoveRun> run;
+};
+
+template <int TASKS, int RUNS>
+oscar_status run_move(const oscar_cache* c, const MovePlan& plan, bool in_place, cudaStream_t st) {
+  MoveParams<TASKS, RUNS> P;
+  std::memset(&P, 0, sizeof(P));
+  P.n_tasks = (int32_t)plan.task.size();
+  P.n_dst = (int32_t)plan.dst.size();
+  P.hkv = c->cfg.num_kv_heads;
+  P.max_groups = c->layout.max_groups;
+  P.block_bytes = c->block_bytes;
+  P.blocks_off = c->layout.blocks_off;
+  P.windows_off = c->layout.windows_off;
+  P.zmax_off = c->layout.zmax_off;
+  std::copy(plan.task.begin(), plan.task.end(), P.task);
+  std::copy(plan.dst.begin(), plan.dst.end(), P.dst);
+  std::copy(plan.run.begin(), plan.run.end(), P.run);
+  for (int32_t i = 0; i < P.n_tasks; ++i) {
+    P.task[i].ubase = P.n_units;
+    P.n_units += (int64_t)P.task[i].groups * P.hkv;
+  }
+  const cudaError_t e = in_place ? launch_compact(P, c->arena, c->sms, st) : launch_move(P, c->arena, c->sms, st);
+  return e == cudaSuccess ? OSCAR_OK : cuda_fail(e, in_place ? "compact launch" : "copy launch");
+}
+
+oscar_status run_plan(const oscar_cache* c, MovePlan* plan, bool in_place, cudaStream_t st) {
+  if (plan->task.empty() && plan->dst.empty()) return OSCAR_OK;
+  const bool small = plan->task.size() <= (size_t)kMoveTasksSmall && plan->dst.size() <= (size_t)kMoveTasksSmall &&
+                     plan->run.size() <= (size_t)kMoveRunsSmall;
+  const oscar_status s = small ? run_move<kMoveTasksSmall, kMoveRunsSmall>(c, *plan, in_place, st)
+                               : run_move<kMoveTasksLarge, kMoveRunsLarge>(c, *plan, in_place, st);
+  *plan = MovePlan{};
+  return s;
+}
+
+}  // namespace
+
+extern "C" {
+
+oscar_status oscar_cache_fork(oscar_cache* c, int32_t n, const int32_t* src, const int32_t* dst, const int32_t* length,
+                              void* stream) {
+  try {
+    oscar_status s = check_pairs(c, n, src, dst);
+    if (s != OSCAR_OK) return s;
+    if (n > 0 && !length) return fail(OSCAR_ERR_INVALID_ARG, "length is NULL");
+    std::vector<ReadSeq> cut;       // ends inside a group: its tokens go to the destination's window
+    std::vector<int32_t> order;
+    for (int32_t i = 0; i < n; ++i) {
+      const int32_t have = c->len[src[i]];
+      if (length[i] < 0 || length[i] > have)
+        return fail(OSCAR_ERR_INVALID_ARG, "length[%d] = %d outside the %d tokens of slot %d", i, length[i], have, src[i]);
+      if (length[i] % kGroup != 0 && length[i] / kGroup < have / kGroup)
+        cut.push_back(ReadSeq{src[i], have, length[i] / kGroup * kGroup, length[i],
+                              (int64_t)dst[i] * c->cfg.num_kv_heads * 2 * kGroup, 0});
+      if (src[i] != dst[i]) order.push_back(i);
+    }
+    if (order.empty() && cut.empty()) {
+      for (int32_t i = 0; i < n; ++i) {
+        c->len[dst[i]] = length[i];
+        c->indexed[dst[i]] = std::min(c->indexed[dst[i]], length[i] / kGroup);
+      }
+      return ok();
+    }
+    DeviceGuard dg(c->cfg.device);
+    if (dg.err != cudaSuccess) return cuda_fail(dg.err, "cudaSetDevice");
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    // forks of one sequence together, the longest first: its blocks are read once
+    std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) {
+      return src[a] != src[b] ? src[a] < src[b] : length[a] > length[b];
+    });
+    // until the copies are known to be enqueued the destinations are empty
+    for (const int32_t i : order) {
+      c->len[dst[i]] = 0;
+      c->fresh_from[dst[i]] = 0;
+      c->indexed[dst[i]] = 0;
+    }
+    MovePlan plan;
+    for (size_t k = 0; k < order.size(); ++k) {
+      const int32_t i = order[k];
+      if (plan.dst.size() == (size_t)kMoveTasksLarge && (s = run_plan(c, &plan, false, st)) != OSCAR_OK) return s;
+      const int32_t groups = length[i] / kGroup, have = c->len[src[i]];
+      const bool whole = groups == have / kGroup;     // the window is the source's own
+      if (plan.task.empty() || plan.task.back().src != src[i]) {
+        if (groups > 0) plan.task.push_back(MoveTask{src[i], (int32_t)plan.dst.size(), 0, 0, groups, 0, 0, 0});
+      }
+      if (groups > 0) ++plan.task.back().n_dst;
+      plan.dst.push_back(MoveDst{src[i], dst[i], groups, whole ? length[i] % kGroup : 0});
+    }
+    if ((s = run_plan(c, &plan, false, st)) != OSCAR_OK) return s;
+    uint8_t* windows = c->arena + c->layout.windows_off;
+    for (size_t b = 0; b < cut.size(); b += kReadSeqsLarge) {
+      const size_t m = std::min(cut.size() - b, (size_t)kReadSeqsLarge);
+      s = m <= (size_t)kDecodeSeqsSmall
+              ? run_read<kDecodeSeqsSmall>(c, cut, b, m, false, windows, windows + kWindowBytes / 2, st, true)
+              : run_read<kReadSeqsLarge>(c, cut, b, m, false, windows, windows + kWindowBytes / 2, st, true);
+      if (s != OSCAR_OK) return s;
+    }
+    for (int32_t i = 0; i < n; ++i) {
+      c->len[dst[i]] = length[i];
+      c->indexed[dst[i]] = std::min(c->indexed[dst[i]], length[i] / kGroup);
+    }
+    return ok();
+  } catch (const std::exception& ex) {
+    return fail(OSCAR_ERR_INVALID_ARG, "host allocation failed: %s", ex.what());
+  }
+}
+
+oscar_status oscar_cache_keep_groups(oscar_cache* c, int32_t n, const int32_t* src, const int32_t* dst,
+                                     const int32_t* cu_groups, const int32_t* groups, void* stream) {
+  try {
+    oscar_status s = check_pairs(c, n, src, dst);
+    if (s != OSCAR_OK) return s;
+    if (n == 0) return ok();
+    if (!cu_groups) return fail(OSCAR_ERR_INVALID_ARG, "cu_groups is NULL");
+    if (cu_groups[0] != 0) return fail(OSCAR_ERR_INVALID_ARG, "cu_groups[0] must be 0");
+    for (int32_t i = 0; i < n; ++i)
+      if (cu_groups[i + 1] < cu_groups[i]) return fail(OSCAR_ERR_INVALID_ARG, "cu_groups must be non-decreasing");
+    if (cu_groups[n] > 0 && !groups) return fail(OSCAR_ERR_INVALID_ARG, "groups is NULL");
+    for (int32_t i = 0; i < n; ++i) {
+      const int32_t have = c->len[src[i]] / kGroup;
+      for (int32_t k = cu_groups[i]; k < cu_groups[i + 1]; ++k)
+        if (groups[k] < 0 || groups[k] >= have || (k > cu_groups[i] && groups[k] <= groups[k - 1]))
+          return fail(OSCAR_ERR_INVALID_ARG, "groups[%d] = %d: groups of a sequence must ascend within its %d", k,
+                      groups[k], have);
+    }
+    DeviceGuard dg(c->cfg.device);
+    if (dg.err != cudaSuccess) return cuda_fail(dg.err, "cudaSetDevice");
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    std::vector<int32_t> length(n);
+    for (int32_t i = 0; i < n; ++i)
+      length[i] = (cu_groups[i + 1] - cu_groups[i]) * kGroup + c->len[src[i]] % kGroup;
+    // pass 0: to other slots; pass 1: in place
+    for (int pass = 0; pass < 2; ++pass) {
+      MovePlan plan;
+      for (int32_t i = 0; i < n; ++i) {
+        const bool in_place = src[i] == dst[i];
+        if (in_place != (pass == 1)) continue;
+        const int32_t* g = groups + cu_groups[i];
+        const int32_t kept = cu_groups[i + 1] - cu_groups[i];
+        int32_t first = 0;              // groups before it stay where they are
+        if (in_place)
+          while (first < kept && g[first] == first) ++first;
+        // until the copies are known to be enqueued: what is certain
+        if (in_place) {
+          c->len[dst[i]] = first * kGroup;
+          c->fresh_from[dst[i]] = std::min(c->fresh_from[dst[i]], first);
+          c->indexed[dst[i]] = std::min(c->indexed[dst[i]], first);
+        } else {
+          c->len[dst[i]] = 0;
+          c->fresh_from[dst[i]] = 0;
+          c->indexed[dst[i]] = 0;
+        }
+        if (plan.dst.size() == (size_t)kMoveTasksLarge && (s = run_plan(c, &plan, pass == 1, st)) != OSCAR_OK) return s;
+        const MoveDst to{src[i], dst[i], kept, in_place ? 0 : length[i] % kGroup};
+        plan.dst.push_back(to);
+        // runs of neighbouring groups, split over tasks (and launches) where
+        // they do not fit; in place the launches keep the groups' order
+        for (int32_t k = first; k < kept;) {
+          if (plan.run.size() == (size_t)kMoveRunsLarge || plan.task.size() == (size_t)kMoveTasksLarge) {
+            if ((s = run_plan(c, &plan, pass == 1, st)) != OSCAR_OK) return s;
+            plan.dst.push_back(to);
+          }
+          if (plan.task.empty() || plan.task.back().dst0 != (int32_t)plan.dst.size() - 1)
+            plan.task.push_back(MoveTask{src[i], (int32_t)plan.dst.size() - 1, 1, k, 0, (int32_t)plan.run.size(), 0, 0});
+          int32_t e = k + 1;
+          while (e < kept && g[e] == g[e - 1] + 1) ++e;
+          plan.run.push_back(MoveRun{k, g[k]});
+          ++plan.task.back().n_runs;
+          plan.task.back().groups += e - k;
+          k = e;
+        }
+      }
+      if ((s = run_plan(c, &plan, pass == 1, st)) != OSCAR_OK) return s;
+    }
+    for (int32_t i = 0; i < n; ++i) c->len[dst[i]] = length[i];
     return ok();
   } catch (const std::exception& ex) {
     return fail(OSCAR_ERR_INVALID_ARG, "host allocation failed: %s", ex.what());

@@ -233,7 +233,9 @@ __device__ __forceinline__ void fwht128_warp(float (&v)[4], int lane) {
   for (int i = 0; i < 4; ++i) v[i] *= 0.088388347648318440550f;   // 1/sqrt(128)
 }
 
-template <bool M16>
+// RULE: scores under the rule of `p` (each row's query is the chunk's token row
+// / gqa behind the history)
+template <bool M16, bool RULE>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefill_tc_kernel(const __grid_constant__ PrefillParams p, const uint8_t* __restrict__ arena) {
   using B = Blk<M16>;
@@ -690,6 +692,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t lane_base = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const float fr = S.fexp[r];
     float m_used = -INFINITY, l = 0.0f;   // l: this warp group's sum of p
+    float slope2 = 0.0f;                  // the rule's slope of the row's head, and its query's position
+    int q_pos = 0;
+    if constexpr (RULE) {
+      q_pos = p.ng * kGroup + p.wlen + row / p.gqa;
+      if (p.rule.slopes != nullptr && row < p.rows) slope2 = p.rule.slopes[j * p.gqa + row % p.gqa] * 1.4426950408889634f;
+    }
     bool ok = true;
     // wait for the P.V of half-step jp (bounded)
     auto pv_done = [&](int jp) {
@@ -748,6 +756,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             w[i + 1] = w01.y;
             w[i + 2] = w23.x;
             w[i + 3] = w23.y;
+          }
+        }
+      }
+      if constexpr (RULE) {
+        if (ok) {
+          if (p.rule.cap != 0.0f) {
+            // (tokens past the window are -inf: they take no part in the choice)
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) top = fmaxf(top, w[i] == -INFINITY ? 0.0f : fabsf(w[i]));
+            const bool small = __all_sync(0xffffffffu, top * p.rule.inv_cap <= kTanhNear);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 y = capped(make_float2(w[i], w[i + 1]), p.rule.cap, p.rule.inv_cap, small);
+              w[i] = y.x;
+              w[i + 1] = y.y;
+            }
+          }
+          const float far = (float)(q_pos - (win ? p.ng : g_begin + k) * kGroup - c0);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) w[i] = fmaf(-slope2, far - (float)i, w[i]);
+          if (win) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = c0 + i < wlen ? w[i] : -INFINITY;
           }
         }
       }
@@ -914,19 +946,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 }  // namespace
 
-template <bool M16>
+template <bool M16, bool RULE>
 cudaError_t launch_prefill_tc_t(const PrefillParams& p, const uint8_t* arena, cudaStream_t stream) {
   static bool attr_done[64] = {};
   const int smem = (int)sizeof(TcSmem) + 1024;
-  cudaError_t e = ensure_smem_attr(prefill_tc_kernel<M16>, smem, attr_done);
+  cudaError_t e = ensure_smem_attr(prefill_tc_kernel<M16, RULE>, smem, attr_done);
   if (e != cudaSuccess) return e;
   const dim3 grid((p.rows + kTcRows - 1) / kTcRows, p.hkv, p.n_parts);
-  prefill_tc_kernel<M16><<<grid, kTcThreads, smem, stream>>>(p, arena);
+  prefill_tc_kernel<M16, RULE><<<grid, kTcThreads, smem, stream>>>(p, arena);
   return cudaGetLastError();
 }
 
 cudaError_t launch_prefill_tc(const PrefillParams& p, const uint8_t* arena, bool meta16, cudaStream_t stream) {
-  return meta16 ? launch_prefill_tc_t<true>(p, arena, stream) : launch_prefill_tc_t<false>(p, arena, stream);
+  if (p.rule.any())
+    return meta16 ? launch_prefill_tc_t<true, true>(p, arena, stream) : launch_prefill_tc_t<false, true>(p, arena, stream);
+  return meta16 ? launch_prefill_tc_t<true, false>(p, arena, stream) : launch_prefill_tc_t<false, false>(p, arena, stream);
 }
 
 }  // namespace oscar

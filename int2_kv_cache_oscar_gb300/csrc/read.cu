@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
     const int hi = (int)min((int64_t)kGroup, (int64_t)sq.end - (int64_t)tile * kGroup);
     Out* kout = static_cast<Out*>(p.k_out);
     Out* vout = static_cast<Out*>(p.v_out);
-    auto out_row = [&](Out* base, int t) { return base + ((row0 + t) * p.hkv + j) * kHeadDim; };
+    auto out_row = [&](Out* base, int t) { return base + (row0 + t) * p.row_pitch + j * p.head_pitch; };
 
     const bool late = !mbar_wait_bounded(&S.full[s], (it >> 1) & 1, &S.abort_flag, err, p.spin_limit);
     const bool packed = (tile + 1) * (int64_t)kGroup <= sq.len;
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
       const int t0 = 64 * jt + 2 * tig;      // this thread's tokens are t0 + 8 q + e
       const int m0 = t0 * 4 + (c8 >> 2);     // and their scales and zeros (see vmeta_row: e swaps where q is odd)
       Out* row0p = out_row(vout, t0) + 8 * c8;
-      const int64_t pitch = (int64_t)p.hkv * kHeadDim;
+      const int64_t pitch = p.row_pitch;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         if (e) {

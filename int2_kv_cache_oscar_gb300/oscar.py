@@ -128,6 +128,12 @@ def _load() -> ctypes.CDLL:
         "oscar_index_attach": [P, P, SZ],
         "oscar_index_update": [P, I32, I32P, I32, P],
         "oscar_select_groups": [P, I32, I32P, P, I32, I32, I32, I32, P, P],
+        "oscar_cache_fork": [P, I32, I32P, I32P, I32P, P],
+        "oscar_cache_keep_groups": [P, I32, I32P, I32P, I32P, I32P, P],
+        "oscar_scored_decode_attention": [P, I32, I32P, P, I32, ctypes.c_float, ctypes.POINTER(oscar_score_rule), I32,
+                                          P, P, SZ, P],
+        "oscar_scored_prefill_attention": [P, I32, I32, P, I32, ctypes.c_float, ctypes.POINTER(oscar_score_rule), P, P,
+                                           P, SZ, P],
         "oscar_chunk_attention": [I32, I32P, I32P, ctypes.POINTER(oscar_rows), ctypes.POINTER(oscar_rows),
                                   ctypes.POINTER(oscar_rows), I32, I32, ctypes.c_float,
                                   ctypes.POINTER(oscar_score_rule), P, P, P, P, P],
@@ -479,6 +485,19 @@ def oscar_cache_import(handle, seq: int, length: int, blocks: Optional[torch.Ten
     _in_use(stream, device, blocks, window, maxima)
 
 
+def oscar_cache_fork(handle, src: Sequence[int], dst: Sequence[int], length: Sequence[int], stream=None) -> None:
+    """The first length[i] tokens of slot src[i] into slot dst[i]; with dst[i] =
+    src[i] the slot is cut to them in place."""
+    _check(_calls.fork(handle, src, dst, length, stream))
+
+
+def oscar_cache_keep_groups(handle, src: Sequence[int], dst: Sequence[int], groups: Sequence[Sequence[int]],
+                            stream=None) -> None:
+    """Slot dst[i] := groups[i] (ascending) of slot src[i], and its window; with
+    dst[i] = src[i] in place."""
+    _check(_calls.keep_groups(handle, src, dst, groups, stream))
+
+
 def oscar_index_required_bytes(handle) -> int:
     out = ctypes.c_size_t(0)
     _check(_lib.oscar_index_required_bytes(handle, ctypes.byref(out)))
@@ -510,6 +529,24 @@ def oscar_sparse_decode_attention(handle, seq_ids: Sequence[int], q: torch.Tenso
     out bf16 or float32."""
     _check(_calls.sparse_decode(handle, num_kv_heads, seq_ids, q, num_q_heads, softmax_scale, groups, out, workspace,
                                 lse, stream))
+
+
+def oscar_scored_decode_attention(handle, seq_ids: Sequence[int], q: torch.Tensor, num_q_heads: int,
+                                  softmax_scale: float, out: torch.Tensor, workspace: torch.Tensor, cap: float = 0.0,
+                                  slopes: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Decode attention with scores capped to cap tanh(s / cap) and lowered by
+    slopes[head] (float32 [num_q_heads]) per token between a cached token and the
+    newest one; out bf16 or float32."""
+    _check(_calls.scored_decode(handle, seq_ids, q, num_q_heads, softmax_scale, cap, slopes, out, workspace, stream))
+
+
+def oscar_scored_prefill_attention(handle, seq: int, q: torch.Tensor, num_q_heads: int, softmax_scale: float,
+                                   out: torch.Tensor, lse: Optional[torch.Tensor] = None,
+                                   workspace: Optional[torch.Tensor] = None, cap: float = 0.0,
+                                   slopes: Optional[torch.Tensor] = None, stream=None) -> None:
+    """oscar_prefill_attention under the same rule; query i stands i tokens
+    behind the cached ones."""
+    _check(_calls.scored_prefill(handle, seq, q, num_q_heads, softmax_scale, cap, slopes, out, lse, workspace, stream))
 
 
 def oscar_chunk_attention(cu_seqlens: Sequence[int], q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -705,3 +742,27 @@ class OscarCache:
                       stream=None):
         oscar_sparse_decode_attention(self.handle, seq_ids, q, num_q_heads, softmax_scale, groups, out, workspace,
                                       lse, stream)
+
+    def scored_decode(self, seq_ids, q, num_q_heads, out, workspace, cap=0.0, slopes=None, softmax_scale=0.0,
+                      stream=None):
+        oscar_scored_decode_attention(self.handle, seq_ids, q, num_q_heads, softmax_scale, out, workspace, cap, slopes,
+                                      stream)
+
+    def scored_prefill(self, seq, q, num_q_heads, out, lse=None, workspace=None, cap=0.0, slopes=None,
+                       softmax_scale=0.0, stream=None):
+        oscar_scored_prefill_attention(self.handle, seq, q, num_q_heads, softmax_scale, out, lse, workspace, cap, slopes,
+                                       stream)
+
+    def fork(self, src, dst, lengths=None, stream=None):
+        """Copies the first lengths[i] tokens (None: all) of each slot src[i] to slot dst[i]."""
+        if lengths is None:
+            lengths = [self.length(s) for s in src]
+        oscar_cache_fork(self.handle, src, dst, lengths, stream)
+
+    def truncate(self, seq_ids, lengths, stream=None):
+        """Cuts each slot to its first lengths[i] tokens."""
+        oscar_cache_fork(self.handle, seq_ids, seq_ids, lengths, stream)
+
+    def keep_groups(self, src, groups, dst=None, stream=None):
+        """Leaves groups[i] of each slot src[i] and its window, in slot dst[i] or (None) in place."""
+        oscar_cache_keep_groups(self.handle, src, src if dst is None else dst, groups, stream)

@@ -73,8 +73,8 @@ def test_binding_refusals(O):  # noqa: F811
     refused("shape", slopes=torch.zeros(3))
     refused("float32", slopes=torch.zeros(4, dtype=torch.float64))
     refused("out of range", cu_seqlens=[0, 2 ** 40])
-    refused("", kind=TypeError, cu_seqlens=[0, 4.5])
-    refused("", kind=TypeError, cap="wide")
+    refused("integer", kind=TypeError, cu_seqlens=[0, 4.5])
+    refused("number", kind=TypeError, cap="wide")
     with pytest.raises(O.OscarError):                      # num_q_heads not a multiple
         O.oscar_chunk_attention(**{**ok, "q": rows(heads=3), "out": rows(heads=3), "stream": 0})
 
