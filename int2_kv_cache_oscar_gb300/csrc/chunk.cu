@@ -187,12 +187,25 @@ __global__ void __launch_bounds__(kChThreads, 1)
                  const __grid_constant__ CUtensorMap tmv) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   ChunkSmem& S = *reinterpret_cast<ChunkSmem*>(smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const ChunkTile T = locate(p);
   const int steps = max(T.steps[0], T.steps[1]);
   const int plain = min(T.plain[0], T.plain[1]);      // steps before this one hide no key from any row
 
-  if (tid == 0) {
+  // the n-th load of the ring: K0, K1, V0, K2, V1, ...
+  auto load = [&](int n) {
+    const int s = n % kChSlots;
+    const bool val = n == 2 * steps - 1 || (n > 0 && (n & 1) == 0);
+    const int j = n == 2 * steps - 1 ? steps - 1 : val ? (n - 2) / 2 : (n + 1) / 2;
+    const CUtensorMap* m = val ? &tmv : &tmk;
+    mbar_arrive_expect_tx(&S.full[s], kTileBytes);
+    tma_load_3d(S.ring[s], m, 0, T.head, T.row0 + j * kChKeys, &S.full[s]);
+    tma_load_3d(S.ring[s] + kBox, m, 64, T.head, T.row0 + j * kChKeys, &S.full[s]);
+    reinterpret_cast<volatile uint32_t*>(S.issued)[s] = (uint32_t)(n / kChSlots) + 1;
+  };
+  const int early = min(kChSlots, 2 * steps);     // loads that no slot has to be waited for
+
+  if (warp == 9 && lane == 0) {
     for (int i = 0; i < kChSlots; ++i) {
       mbar_init(&S.full[i], 1);
       mbar_init(&S.empty[i], 1);
@@ -208,6 +221,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
     mbar_init(&S.drained, 1);
     S.abort_flag = 0;
     fence_mbar_init();
+    grid_dependency_wait();
+    for (int n = 0; n < early; ++n) load(n);
   }
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem_base)),
@@ -218,16 +233,24 @@ __global__ void __launch_bounds__(kChThreads, 1)
   grid_dependency_wait();
   allow_dependents();
   if (warp < 8) {
-    // the queries of the rows, 16 lanes a row (rows behind the last one repeat it)
+    // the queries of the rows, 16 lanes a row (rows behind the last one repeat
+    // it), all of a thread's loads in flight at once
     const int i = warp >> 2;
     if (T.steps[i] > 0) {
-      for (int x = tid & 127; x < kChRows * 16; x += 128) {
-        const int r = x >> 4, c = x & 15;
-        const int row = min(T.first_row + i * kChRows + r, T.rows - 1);
-        const int tok = row / p.gqa, h = T.head * p.gqa + row - tok * p.gqa;
-        *reinterpret_cast<uint4*>(S.q[i] + tile_off(r, c)) =
-            *reinterpret_cast<const uint4*>(p.q + (int64_t)(T.row0 + tok) * p.q_token + (int64_t)h * p.q_head + 8 * c);
+      const int first = T.first_row + i * kChRows, t0 = first / p.gqa, rest = first - t0 * p.gqa;
+      const int c = tid & 15, r0 = (tid & 127) >> 4;
+      const float inv = 1.0f / (float)p.gqa;
+      const uint16_t* base = p.q + (int64_t)(T.row0 + t0) * p.q_token + (int64_t)(T.head * p.gqa) * p.q_head + 8 * c;
+      uint4 u[16];
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const int at = rest + min(r0 + 8 * x, T.rows - 1 - first);
+        // at / gqa: below 2^17, where the half keeps the product off whole numbers
+        const int tok = (int)(((float)at + 0.5f) * inv), h = at - tok * p.gqa;
+        u[x] = *reinterpret_cast<const uint4*>(base + (int64_t)tok * p.q_token + (int64_t)h * p.q_head);
       }
+#pragma unroll
+      for (int x = 0; x < 16; ++x) *reinterpret_cast<uint4*>(S.q[i] + tile_off(r0 + 8 * x, c)) = u[x];
       async_fence();
     }
   }
@@ -238,28 +261,32 @@ __global__ void __launch_bounds__(kChThreads, 1)
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    if (warp == 8 && lane == 0) {
+    if (warp == 8) {
       // ---------------------------------------------------------- MMA issuer
       const uint64_t dq[2] = {desc128(smem_u32(S.q[0]), 16, 1024), desc128(smem_u32(S.q[1]), 16, 1024)};
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const bool ok = mbar_wait_bounded(bar, parity, &S.abort_flag, nullptr);
+        const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, &S.abort_flag, nullptr));
         tfence_after();
         return ok;
       };
-      auto scores = [&](int i, int slot) {
+      // scores of tile i from the keys in a slot; `freed`: the slot's last use
+      auto scores = [&](int i, int slot, bool freed) {
         const uint64_t dk = desc128(smem_u32(S.ring[slot]), 16, 1024);
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          const uint64_t off = (uint64_t)(((ks >> 2) * kBox + (ks & 3) * 32) >> 4);
-          mma_ss(tmem + col_s(i), dq[i] + off, dk + off, kIdescQK, ks > 0);
+          for (int ks = 0; ks < 8; ++ks) {
+            const uint64_t off = (uint64_t)(((ks >> 2) * kBox + (ks & 3) * 32) >> 4);
+            mma_ss(tmem + col_s(i), dq[i] + off, dk + off, kIdescQK, ks > 0);
+          }
+          mma_commit(&S.s_full[i]);
+          if (freed) mma_commit(&S.empty[slot]);
         }
-        mma_commit(&S.s_full[i]);
+        __syncwarp();
       };
       bool ok = wait(&S.full[0], 0);
       if (ok) {
-        for (int i = 0; i < 2; ++i)
-          if (T.steps[i] > 0) scores(i, 0);
-        mma_commit(&S.empty[0]);
+        if (T.steps[0] > 0) scores(0, 0, T.steps[1] == 0);
+        if (T.steps[1] > 0) scores(1, 0, true);
       }
       for (int j = 0; ok && j < steps; ++j) {
         const int kn = key_pos(j + 1), vn = value_pos(j, steps);
@@ -278,43 +305,38 @@ __global__ void __launch_bounds__(kChThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (!ok || j >= T.steps[i]) continue;
+          const bool last = i == 1 || j >= T.steps[1];       // the step's last tile
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            if (!ok) break;
-            ok = wait(&S.p_ready[i][half], j & 1);
-            if (!ok) break;
+            ok = ok && wait(&S.p_ready[i][half], j & 1);
+            if (!ok) continue;
+            if (elect_one()) {
 #pragma unroll
-            for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-              mma_ts(tmem + col_o(i), tmem + col_s(i) + 8 * ks, dv + (uint64_t)((ks * 2048) >> 4), kIdescPV, keep || ks > 0);
+              for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
+                mma_ts(tmem + col_o(i), tmem + col_s(i) + 8 * ks, dv + (uint64_t)((ks * 2048) >> 4), kIdescPV, keep || ks > 0);
+              if (half == 1) {
+                if (last) mma_commit(&S.empty[vs]);
+                if (j + 1 >= T.steps[i]) mma_commit(&S.o_done[i]);
+              }
+            }
+            __syncwarp();
           }
-          if (!ok) continue;
-          const bool last = i == 1 || j >= T.steps[1];       // the step's last tile
-          if (last) mma_commit(&S.empty[vs]);
-          if (j + 1 < T.steps[i]) scores(i, ksl);
-          else mma_commit(&S.o_done[i]);
-          if (last && more) mma_commit(&S.empty[ksl]);
+          if (ok && j + 1 < T.steps[i]) scores(i, ksl, last);
         }
+        // (a tile that ends before the other: the other one's scores free the keys)
       }
       if (!ok) {
         // gave up: what has been issued completes before TMEM is freed (bounded)
-        mma_commit(&S.drained);
+        if (elect_one()) mma_commit(&S.drained);
         for (uint32_t n = 0; n < kSpinLimit; ++n)
           if (mbar_try_wait(&S.drained, 0)) break;
       }
     } else if (warp == 9 && lane == 0) {
       // -------------------------------------------------------------- loads
-      int n = 0;
+      int n = early;
       for (; n < 2 * steps; ++n) {
-        const int s = n % kChSlots;
-        if (n >= kChSlots && !mbar_wait_bounded(&S.empty[s], ((n / kChSlots) - 1) & 1, &S.abort_flag, nullptr)) break;
-        // n = 0: K0; odd n (but the last): K(n + 1) / 2; even n: V(n - 2) / 2
-        const bool val = n == 2 * steps - 1 || (n > 0 && (n & 1) == 0);
-        const int j = n == 2 * steps - 1 ? steps - 1 : val ? (n - 2) / 2 : (n + 1) / 2;
-        const CUtensorMap* m = val ? &tmv : &tmk;
-        mbar_arrive_expect_tx(&S.full[s], kTileBytes);
-        tma_load_3d(S.ring[s], m, 0, T.head, T.row0 + j * kChKeys, &S.full[s]);
-        tma_load_3d(S.ring[s] + kBox, m, 64, T.head, T.row0 + j * kChKeys, &S.full[s]);
-        reinterpret_cast<volatile uint32_t*>(S.issued)[s] = (uint32_t)(n / kChSlots) + 1;
+        if (!mbar_wait_bounded(&S.empty[n % kChSlots], ((n / kChSlots) - 1) & 1, &S.abort_flag, nullptr)) break;
+        load(n);
       }
       if (S.abort_flag) {
         // gave up: the copies in flight get their time (bounded)
@@ -477,58 +499,85 @@ __global__ void __launch_bounds__(kChThreads, 1)
       l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
     }
     if (my_steps > 0) {
+      // o / l, merged with the row over what precedes the chunk.  Rows pass
+      // through the tile's query memory (free by now), a warp's 32 rows by itself:
+      // 16 lanes a row in global memory, a thread a row in between.
+      uint8_t* rows = S.q[i];
+      const int w0 = T.first_row + i * kChRows + 32 * (warp & 3);     // the warp's first row
+      const int t0 = w0 / p.gqa, rest = w0 - t0 * p.gqa, c = lane & 15, r0 = lane >> 4;
+      const float inv = 1.0f / (float)p.gqa;
+      const int64_t base = ((int64_t)(T.row0 + t0) * p.hq + T.head * p.gqa) * kHeadDim + 8 * c;
+      // element of row w0 + r, chunk c
+      auto place = [&](int r) {
+        const int at = rest + r, tk = (int)(((float)at + 0.5f) * inv);
+        return base + ((int64_t)tk * p.hq + (at - tk * p.gqa)) * kHeadDim;
+      };
+      const int64_t at = (int64_t)(T.row0 + tok) * p.hq + h;
+      float before = -INFINITY;
+      uint4 u[16];
+      if (p.prior_lse != nullptr) {
+        before = p.prior_lse[at];
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          u[x] = w0 + r0 + 2 * x < T.rows ? *reinterpret_cast<const uint4*>(p.prior_out + place(r0 + 2 * x))
+                                          : make_uint4(0, 0, 0, 0);
+      }
       if (ok) {
         ok = mbar_wait_bounded(&S.o_done[i], 0, &S.abort_flag, nullptr);
         ok = __all_sync(0xffffffffu, ok);
         tfence_after();
       }
-      // o / l, merged with the row over what precedes the chunk
-      const int64_t at = (int64_t)(T.row0 + tok) * p.hq + h;
+      if (p.prior_lse != nullptr) {
+#pragma unroll
+        for (int x = 0; x < 16; ++x) *reinterpret_cast<uint4*>(rows + tile_off(32 * (warp & 3) + r0 + 2 * x, c)) = u[x];
+        __syncwarp();
+      }
       float lse = ok ? fmaf(m, sl * kLn2, logf(l)) : NAN;
       float fo = ok ? 1.0f / l : NAN, fp = 0.0f;
-      if (p.prior_lse != nullptr) {
-        const float before = p.prior_lse[at];
-        if (before != -INFINITY) {
-          const float top = fmaxf(lse, before);
-          const float a = expf(lse - top), b = expf(before - top);
-          fp = b / (a + b);
-          fo *= a / (a + b);
-          lse = top + logf(a + b);
-        }
+      if (before != -INFINITY) {
+        const float top = fmaxf(lse, before);
+        const float a = expf(lse - top), b = expf(before - top);
+        fp = b / (a + b);
+        fo *= a / (a + b);
+        lse = top + logf(a + b);
       }
 #pragma unroll 1
-      for (int c = 0; c < kHeadDim; c += 32) {
+      for (int c4 = 0; c4 < 16; c4 += 4) {
         uint32_t o[32];
         if (ok) {
-          tld32(tO + c, o);
+          tld32(tO + 8 * c4, o);
           tld_wait();
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0x7fc00000u;
         }
-        if (live) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            float x[8];
+        for (int e = 0; e < 4; ++e) {
+          uint4* mine = reinterpret_cast<uint4*>(rows + tile_off(32 * (warp & 3) + lane, c4 + e));
+          float x[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(o[e + k]) * fo;
-            if (fp != 0.0f) {     // (also NaN)
-              const uint4 u = *reinterpret_cast<const uint4*>(p.prior_out + at * kHeadDim + c + e);
-              x[0] = fmaf(bf16_lo(u.x), fp, x[0]);
-              x[1] = fmaf(bf16_hi(u.x), fp, x[1]);
-              x[2] = fmaf(bf16_lo(u.y), fp, x[2]);
-              x[3] = fmaf(bf16_hi(u.y), fp, x[3]);
-              x[4] = fmaf(bf16_lo(u.z), fp, x[4]);
-              x[5] = fmaf(bf16_hi(u.z), fp, x[5]);
-              x[6] = fmaf(bf16_lo(u.w), fp, x[6]);
-              x[7] = fmaf(bf16_hi(u.w), fp, x[7]);
-            }
-            *reinterpret_cast<uint4*>(p.out + at * kHeadDim + c + e) =
-                make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                           pack_bf16x2(x[6], x[7]));
+          for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(o[8 * e + k]) * fo;
+          if (fp != 0.0f) {     // (also NaN)
+            const uint4 b = *mine;
+            x[0] = fmaf(bf16_lo(b.x), fp, x[0]);
+            x[1] = fmaf(bf16_hi(b.x), fp, x[1]);
+            x[2] = fmaf(bf16_lo(b.y), fp, x[2]);
+            x[3] = fmaf(bf16_hi(b.y), fp, x[3]);
+            x[4] = fmaf(bf16_lo(b.z), fp, x[4]);
+            x[5] = fmaf(bf16_hi(b.z), fp, x[5]);
+            x[6] = fmaf(bf16_lo(b.w), fp, x[6]);
+            x[7] = fmaf(bf16_hi(b.w), fp, x[7]);
           }
+          *mine = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                             pack_bf16x2(x[6], x[7]));
         }
       }
+      __syncwarp();
+#pragma unroll
+      for (int x = 0; x < 16; ++x)
+        if (w0 + r0 + 2 * x < T.rows)
+          *reinterpret_cast<uint4*>(p.out + place(r0 + 2 * x)) =
+              *reinterpret_cast<const uint4*>(rows + tile_off(32 * (warp & 3) + r0 + 2 * x, c));
       if (live && p.lse != nullptr) p.lse[at] = lse;
     }
   }
