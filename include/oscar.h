@@ -587,7 +587,7 @@ typedef struct oscar_score_rule {
                               by cap 2^-21 at most                            */
   int32_t reserved;        /* 0                                               */
   const float* slopes;     /* NULL, or float32 [num_q_heads], device or
-                              page-locked host memory                         */
+                              page-locked host memory; magnitudes below 2^60  */
 } oscar_score_rule;
 
 /* Rows of a tensor [tokens, heads, 128] that is read: strides in elements,
@@ -625,7 +625,7 @@ typedef struct oscar_rows {
  *   lse           float32 [rows, num_q_heads] or NULL: natural log-sum-exp of the
  *                 merged row
  *   prior_out, prior_lse, out and lse: device or page-locked host memory
- *   softmax_scale 0 means 1 / sqrt(128)
+ *   softmax_scale 0 means 1 / sqrt(128); with slopes at least 2^-60
  * Keys and values that a token does not see have no part in its row, whatever
  * they hold.  Softmax weights are rounded to bf16 for the product with the
  * values (row sums are not); the rest is float32.  Should a bounded wait within

@@ -5,31 +5,41 @@
 //   o = sum exp(x_t) v_t / sum exp(x_t),  t < max(i + 1, prefix),
 // and is merged with the row that it got over what precedes the chunk.
 //
-// A CTA takes up to two tiles of 128 (token, query head) rows of one document
-// and KV head (row = token * gqa + head: the heads of a group share every key
-// tile, and a causal tile's diagonal is 128 / gqa tokens wide), and walks over
-// the document's keys 128 at a time.  12 warps:
+// A piece of work is up to two tiles of 128 (token, query head) rows of one
+// document and KV head (row = token * gqa + head: the heads of a group share every
+// key tile, and a causal tile's diagonal is 128 / gqa tokens wide) against the
+// document's keys, 128 at a time.  A CTA an SM takes pieces from the list of all,
+// the longest first, in rounds of alternating direction (piece k of CTA b of G: k G
+// + b, or (k + 1) G - 1 - b): set-up is paid once, and the loads of the next piece
+// run during the end of this one.  12 warps:
 //   * warps 0-3 and 4-7: softmax of the two row tiles, thread = row.  Scores
 //     are read from TMEM once, kept in registers, and P (bf16) is written back
 //     over them as the A operand of P.V.  The output accumulator stays in TMEM
 //     and is rescaled only when a row's maximum grows by more than 8 (log2
 //     units); by then its last P.V is done, since the scores of a step are
 //     issued behind the P.V of the step before;
-//   * warp 8: one thread issues every tcgen05.mma.  S = Q K^T and O += P V of
-//     the two tiles alternate, so that one tile's products run while the other
-//     tile's softmax does;
-//   * warp 9: one thread loads key and value tiles by TMA (128-byte swizzle)
-//     into a ring of five 32 KB slots;
+//   * warp 8 issues every tcgen05.mma.  S = Q K^T and O += P V of the two tiles
+//     alternate, so that one tile's products run while the other tile's softmax does;
+//   * warp 9: one thread loads key and value tiles by TMA (128-byte swizzle) into a
+//     ring of four 32 KB slots, and describes the pieces of work to the others;
 //   * warps 10, 11: look through the value rows of tiles with hidden keys.  A
 //     hidden key has p = 0, but 0 times an infinite or NaN value would still
 //     spoil every row of the tile: such value rows are cleared in shared
 //     memory, and rows that do see them add them on the CUDA cores.
 // Bound: 4 * 128 flops per visible (row, key) on the tensor cores for long
-// documents; launch and pipeline latency for short ones.
+// documents; launch and pipeline latency for short ones.  A step of 128 keys takes
+// 2,980 cycles for two tiles, 2,048 of them products: a tile's chain is 1,500 cycles
+// of softmax, then the second half of its P.V and the next scores (768), and the way
+// from one to the other and back (700).  Tried and slower: a second warpgroup a tile
+// for half of the keys (533 against 374 us, 8,192 tokens of 32 heads: 104 registers a
+// thread do not hold a half), pieces handed out by cluster launch control (407 us),
+// a piece a CTA (379 us, and 78 against 57 for 64 documents of 128 tokens).
 // P is rounded to bf16 (the type of V: the tensor cores take both operands of a
-// product in one type), relative 2^-9 a weight; row sums are of the float32
+// product in one type), relative 2^-8 a weight; row sums are of the float32
 // weights, scores and outputs accumulate in float32.
+#include <algorithm>
 #include <cstddef>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -42,28 +52,70 @@ namespace {
 constexpr int kChRows = 128;                  // rows of a tile (M)
 constexpr int kChKeys = 128;                  // keys of a step (N)
 constexpr int kChThreads = 12 * 32;
-constexpr int kChSlots = 5;
+constexpr int kChSlots = 4;
+constexpr int kWorkReaders = 11;              // warps that read a piece: issuer, two that look through values, softmax
+constexpr int kStageRow = 32;                // bytes of a row that pass through shared memory at a time
 constexpr int kBox = 64 * 2 * 128;            // 128 rows of 64 channels
 constexpr int kTileBytes = 2 * kBox;
 // TMEM columns of tile i: scores (then P in the first 64), output accumulator
 __host__ __device__ constexpr uint32_t col_s(int i) { return 128u * i; }
 __host__ __device__ constexpr uint32_t col_o(int i) { return 256u + 128u * i; }
 constexpr uint32_t kTmemCols = 512;
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 80;   // registers of a thread: warps 0-7, warps 8-11
+constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;   // registers of a thread: warps 0-7, warps 8-11
 constexpr float kGrowth = 8.0f;               // see above
 constexpr float kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// cap tanh(x / cap) of a raw score, in log2 units: cap - 2 cap / (1 + exp(2 x /
+// cap)), off by cap 2^-22 at most.
+template <typename P>
+__device__ __forceinline__ float cap_far(float s, const P& p) {
+  return fmaf(p.cap_out, rcp_approx(1.0f + tc_exp2(s * p.cap_in)), p.cap_log2);
+}
+
+// The same within 0.4 of the cap, two scores: tanh(x) = x (1 + c1 x^2 + c2 x^4 +
+// c3 x^6), the smallest largest relative error over that range (2^-23), with the
+// scale and the cap in the coefficients.
+template <typename P>
+__device__ __forceinline__ float2 cap_near(float2 s, const P& p) {
+  const float2 y = __fmul2_rn(s, s);
+  auto two = [](float v) { return make_float2(v, v); };
+  float2 t = __ffma2_rn(two(p.cap_c[3]), y, two(p.cap_c[2]));
+  t = __ffma2_rn(t, y, two(p.cap_c[1]));
+  return __fmul2_rn(s, __ffma2_rn(t, y, two(p.cap_c[0])));
+}
+
+// A piece of work.
+struct ChunkTile {
+  int row0, len, prefix;     // the document: first token, tokens, prefix
+  int head;                  // KV head
+  int first_row;             // of the piece, within the document's rows
+  int rows;                  // of the document
+  int steps[2];              // key steps of each tile (0: no rows)
+  int plain[2];              // leading steps in which its rows see every key
+  int there;                 // 0: no more work
+};
 
 struct ChunkSmem {
   alignas(1024) uint8_t q[2][kTileBytes];
   alignas(1024) uint8_t ring[kChSlots][kTileBytes];
+  alignas(128) uint8_t stage[8][32 * kStageRow];   // of a softmax warp: channels of its rows on their way
   alignas(8) uint64_t full[kChSlots];
   uint64_t empty[kChSlots];
   uint64_t s_full[2];         // scores of a tile's step are done (and the P.V before them)
   uint64_t p_ready[2][2];     // P of the step's first and second 64 keys is in TMEM
   uint64_t o_done[2];
   uint64_t v_clean[4];        // value rows of a step with hidden keys have been looked through
+  uint64_t q_ready[2];        // queries of a tile are in place
+  uint64_t w_full[2], w_empty[2];   // pieces of work: described, read by every role
   uint64_t drained;           // everything issued is done (only where a wait gave up)
   uint32_t bad[4][4];         // value rows cleared there, a bit each
+  ChunkTile work[2];
   uint32_t issued[kChSlots];  // uses of each slot requested so far
   uint32_t tmem_base;
   int abort_flag;
@@ -104,31 +156,21 @@ __device__ __forceinline__ uint32_t tile_off(int r, int c) {
 __device__ __forceinline__ int key_pos(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int value_pos(int j, int steps) { return j == steps - 1 ? 2 * steps - 1 : 2 * j + 2; }
 
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// What a CTA works on.
-struct ChunkTile {
-  int row0, len, prefix;     // the document: first token, tokens, prefix
-  int head;                  // KV head
-  int first_row;             // of the CTA, within the document's rows
-  int rows;                  // of the document
-  int steps[2];              // key steps of each tile (0: no rows)
-  int plain[2];              // leading steps in which its rows see every key
-};
-
 template <int MAXS>
-__device__ __forceinline__ ChunkTile locate(const ChunkParams<MAXS>& p) {
+__device__ __forceinline__ ChunkTile locate(const ChunkParams<MAXS>& p, int work) {
   ChunkTile t;
-  const int u = (int)(blockIdx.x / (unsigned)p.hkv);
-  t.head = (int)(blockIdx.x - (unsigned)u * (unsigned)p.hkv);
-  int lo = 0, hi = p.n_seqs - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (p.seq[mid].tbase <= u) lo = mid; else hi = mid - 1;
+  t.there = 1;
+  const int u = (int)((unsigned)work / (unsigned)p.hkv);
+  t.head = work - u * p.hkv;
+  int lo = 0, hi = p.n_seqs - 1, tile = -1;
+  if (p.sorted) {
+    lo = (int)(p.order[u] >> 22);
+    tile = (int)(p.order[u] & 0x3fffffu);
+  } else {
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.seq[mid].tbase <= u) lo = mid; else hi = mid - 1;
+    }
   }
   const ChunkSeq s = p.seq[lo];
   t.row0 = s.row0;
@@ -136,7 +178,8 @@ __device__ __forceinline__ ChunkTile locate(const ChunkParams<MAXS>& p) {
   t.prefix = s.prefix;
   t.rows = s.len * p.gqa;
   const int tiles = (t.rows + p.cta_rows - 1) / p.cta_rows;
-  t.first_row = (tiles - 1 - (u - s.tbase)) * p.cta_rows;     // the longest ones first
+  if (tile < 0) tile = tiles - 1 - (u - s.tbase);     // the longest ones first
+  t.first_row = tile * p.cta_rows;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r0 = t.first_row + i * kChRows;
@@ -181,6 +224,11 @@ __device__ __noinline__ void add_cleared(uint32_t t_p, uint32_t t_o, const uint3
   }
 }
 
+// 16 bytes from global to shared memory, without a register in between.
+__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
 template <int MAXS, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kChThreads, 1)
     chunk_kernel(const __grid_constant__ ChunkParams<MAXS> p, const __grid_constant__ CUtensorMap tmk,
@@ -188,23 +236,33 @@ __global__ void __launch_bounds__(kChThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   ChunkSmem& S = *reinterpret_cast<ChunkSmem*>(smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023));
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-  const ChunkTile T = locate(p);
-  const int steps = max(T.steps[0], T.steps[1]);
-  const int plain = min(T.plain[0], T.plain[1]);      // steps before this one hide no key from any row
 
-  // the n-th load of the ring: K0, K1, V0, K2, V1, ...
-  auto load = [&](int n) {
-    const int s = n % kChSlots;
+  // the n-th load of a piece of work, K0, K1, V0, K2, V1, ..., into ring use `use`
+  auto load = [&](const ChunkTile& T, int steps, int n, uint32_t use) {
+    const int s = (int)(use % kChSlots);
     const bool val = n == 2 * steps - 1 || (n > 0 && (n & 1) == 0);
     const int j = n == 2 * steps - 1 ? steps - 1 : val ? (n - 2) / 2 : (n + 1) / 2;
     const CUtensorMap* m = val ? &tmv : &tmk;
     mbar_arrive_expect_tx(&S.full[s], kTileBytes);
     tma_load_3d(S.ring[s], m, 0, T.head, T.row0 + j * kChKeys, &S.full[s]);
     tma_load_3d(S.ring[s] + kBox, m, 64, T.head, T.row0 + j * kChKeys, &S.full[s]);
-    reinterpret_cast<volatile uint32_t*>(S.issued)[s] = (uint32_t)(n / kChSlots) + 1;
+    reinterpret_cast<volatile uint32_t*>(S.issued)[s] = use / kChSlots + 1;
   };
-  const int early = min(kChSlots, 2 * steps);     // loads that no slot has to be waited for
 
+  // ---- a softmax warp's place: tile i, rows 32 (warp & 3) .. of it
+  const int i = warp >> 2, wr = 32 * (warp & 3);
+  const int c16 = lane & 15, r16 = lane >> 4;        // 16 lanes a query row in global memory
+  // The warp's 32 query rows of a piece (rows behind the last one repeat it): a
+  // lane works out where its own row is, 16 lanes copy a row.
+  auto load_queries = [&](const ChunkTile& T) {
+    const int row = min(T.first_row + i * kChRows + wr + lane, T.rows - 1), tok = row / p.gqa;
+    const int64_t off = (int64_t)(T.row0 + tok) * p.q_token + (int64_t)(T.head * p.gqa + row - tok * p.gqa) * p.q_head;
+#pragma unroll 2
+    for (int x = 0; x < 16; ++x)
+      copy16_async(S.q[i] + tile_off(wr + r16 + 2 * x, c16), p.q + __shfl_sync(0xffffffffu, off, r16 + 2 * x) + 8 * c16);
+  };
+
+  uint32_t loaded = 0;     // ring uses issued so far (warp 9, lane 0)
   if (warp == 9 && lane == 0) {
     for (int i = 0; i < kChSlots; ++i) {
       mbar_init(&S.full[i], 1);
@@ -216,13 +274,21 @@ __global__ void __launch_bounds__(kChThreads, 1)
       mbar_init(&S.p_ready[i][0], 4);
       mbar_init(&S.p_ready[i][1], 4);
       mbar_init(&S.o_done[i], 1);
+      mbar_init(&S.q_ready[i], 4);
+      mbar_init(&S.w_full[i], 1);
+      mbar_init(&S.w_empty[i], kWorkReaders);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&S.v_clean[i], 2);
     mbar_init(&S.drained, 1);
     S.abort_flag = 0;
     fence_mbar_init();
+    // the first loads, for which no slot has to be waited
     grid_dependency_wait();
-    for (int n = 0; n < early; ++n) load(n);
+    const ChunkTile T = locate(p, (int)blockIdx.x);
+    const int steps = max(T.steps[0], T.steps[1]);
+    S.work[0] = T;
+    mbar_arrive(&S.w_full[0]);
+    for (; (int)loaded < min(kChSlots, 2 * steps); ++loaded) load(T, steps, (int)loaded, loaded);
   }
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem_base)),
@@ -233,39 +299,37 @@ __global__ void __launch_bounds__(kChThreads, 1)
   grid_dependency_wait();
   allow_dependents();
   if (warp < 8) {
-    // the queries of the rows, 16 lanes a row (rows behind the last one repeat
-    // it), all of a thread's loads in flight at once
-    const int i = warp >> 2;
-    if (T.steps[i] > 0) {
-      const int first = T.first_row + i * kChRows, t0 = first / p.gqa, rest = first - t0 * p.gqa;
-      const int c = tid & 15, r0 = (tid & 127) >> 4;
-      const float inv = 1.0f / (float)p.gqa;
-      const uint16_t* base = p.q + (int64_t)(T.row0 + t0) * p.q_token + (int64_t)(T.head * p.gqa) * p.q_head + 8 * c;
-      uint4 u[16];
-#pragma unroll
-      for (int x = 0; x < 16; ++x) {
-        const int at = rest + min(r0 + 8 * x, T.rows - 1 - first);
-        // at / gqa: below 2^17, where the half keeps the product off whole numbers
-        const int tok = (int)(((float)at + 0.5f) * inv), h = at - tok * p.gqa;
-        u[x] = *reinterpret_cast<const uint4*>(base + (int64_t)tok * p.q_token + (int64_t)h * p.q_head);
-      }
-#pragma unroll
-      for (int x = 0; x < 16; ++x) *reinterpret_cast<uint4*>(S.q[i] + tile_off(r0 + 8 * x, c)) = u[x];
-      async_fence();
-    }
+    const ChunkTile T = locate(p, (int)blockIdx.x);
+    if ((i ? T.steps[1] : T.steps[0]) > 0) load_queries(T);
   }
   tfence_before();
   __syncthreads();
   tfence_after();
   const uint32_t tmem = S.tmem_base;
 
+  // The CTA's k-th piece (its `there` is 0 behind the last one, or when a wait
+  // gave up); every reading warp takes and releases each piece once.
+  auto take = [&](int k) {
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.w_full[k & 1], (k >> 1) & 1, &S.abort_flag, nullptr));
+    ChunkTile T = S.work[k & 1];
+    if (!ok) T.there = 0;
+    return T;
+  };
+  auto release = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.w_empty[k & 1]);
+  };
+
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == 8) {
       // ---------------------------------------------------------- MMA issuer
       const uint64_t dq[2] = {desc128(smem_u32(S.q[0]), 16, 1024), desc128(smem_u32(S.q[1]), 16, 1024)};
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, &S.abort_flag, nullptr));
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, &S.abort_flag, nullptr); };
+      auto slot_full = [&](uint32_t use) { return wait(&S.full[use % kChSlots], (use / kChSlots) & 1); };
+      // after the waits for what the next products read: the warp goes on together
+      auto go_on = [&](bool ok) {
+        ok = __all_sync(0xffffffffu, ok);
         tfence_after();
         return ok;
       };
@@ -283,49 +347,72 @@ __global__ void __launch_bounds__(kChThreads, 1)
         }
         __syncwarp();
       };
-      bool ok = wait(&S.full[0], 0);
-      if (ok) {
-        if (T.steps[0] > 0) scores(0, 0, T.steps[1] == 0);
-        if (T.steps[1] > 0) scores(1, 0, true);
-      }
-      for (int j = 0; ok && j < steps; ++j) {
-        const int kn = key_pos(j + 1), vn = value_pos(j, steps);
-        const int vs = vn % kChSlots, ksl = kn % kChSlots;
-        const bool more = j + 1 < steps;
-        const bool hidden = j >= plain;
-        ok = wait(&S.full[vs], (vn / kChSlots) & 1);
-        if (ok && more) ok = wait(&S.full[ksl], (kn / kChSlots) & 1);
-        bool keep = j > 0;
-        if (ok && hidden) {
-          ok = wait(&S.v_clean[j & 3], ((j - plain) >> 2) & 1);
-          keep = keep || (S.bad[j & 3][0] | S.bad[j & 3][1] | S.bad[j & 3][2] | S.bad[j & 3][3]) != 0u;
+      bool ok = true;
+      uint32_t base = 0, hid = 0, step[2] = {0, 0}, tiles[2] = {0, 0};   // ring uses, steps with hidden keys, of each tile place
+      for (int k = 0;; ++k) {
+        int my[2], plain;
+        {
+          const ChunkTile T = take(k);
+          release(k);
+          // (reductions: values that the compiler knows to be the whole warp's)
+          if (!__reduce_or_sync(0xffffffffu, (unsigned)T.there)) break;
+          my[0] = __reduce_max_sync(0xffffffffu, T.steps[0]);
+          my[1] = __reduce_max_sync(0xffffffffu, T.steps[1]);
+          plain = __reduce_max_sync(0xffffffffu, min(T.plain[0], T.plain[1]));
         }
-        // values are N-major: 64 channels a box, 16 keys a k-step
-        const uint64_t dv = desc128(smem_u32(S.ring[vs]), kBox, 1024);
+        const int steps = max(my[0], my[1]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (!ok || j >= T.steps[i]) continue;
-          const bool last = i == 1 || j >= T.steps[1];       // the step's last tile
+          if (!ok || my[i] == 0) continue;
+          ok = go_on(slot_full(base) && wait(&S.q_ready[i], tiles[i] & 1));
+          ++tiles[i];
+          if (ok) scores(i, base % kChSlots, i == 1 || my[1] == 0);
+        }
+        for (int j = 0; ok && j < steps; ++j) {
+          const uint32_t kn = base + key_pos(j + 1), vn = base + value_pos(j, steps);
+          const int vs = vn % kChSlots, ksl = kn % kChSlots;
+          bool keep = j > 0;
+          // values are N-major: 64 channels a box, 16 keys a k-step
+          const uint64_t dv = desc128(smem_u32(S.ring[vs]), kBox, 1024);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            ok = ok && wait(&S.p_ready[i][half], j & 1);
+          for (int i = 0; i < 2; ++i) {
+            if (!ok || j >= my[i]) continue;
+            const bool last = i == 1 || my[1] == 0;       // the step's last tile (the second one has no fewer steps)
+            const uint32_t turn = step[i] & 1;
+            ++step[i];
+            ok = wait(&S.p_ready[i][0], turn);
+            if (i == 0 || my[0] <= j) {       // the step's first tile: its values, and the next keys
+              ok = ok && slot_full(vn) && (j + 1 >= steps || slot_full(kn));
+              if (j >= plain) ok = ok && wait(&S.v_clean[hid & 3], (hid >> 2) & 1);
+            }
+            ok = go_on(ok);
+            if (!ok) continue;
+            if (j == 0 && j >= plain)
+              keep = (S.bad[hid & 3][0] | S.bad[hid & 3][1] | S.bad[hid & 3][2] | S.bad[hid & 3][3]) != 0u;
+            if (elect_one()) {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma_ts(tmem + col_o(i), tmem + col_s(i) + 8 * ks, dv + (uint64_t)((ks * 2048) >> 4), kIdescPV, keep || ks > 0);
+            }
+            __syncwarp();
+            ok = go_on(wait(&S.p_ready[i][1], turn));
             if (!ok) continue;
             if (elect_one()) {
 #pragma unroll
-              for (int ks = 4 * half; ks < 4 * half + 4; ++ks)
-                mma_ts(tmem + col_o(i), tmem + col_s(i) + 8 * ks, dv + (uint64_t)((ks * 2048) >> 4), kIdescPV, keep || ks > 0);
-              if (half == 1) {
-                if (last) mma_commit(&S.empty[vs]);
-                if (j + 1 >= T.steps[i]) mma_commit(&S.o_done[i]);
-              }
+              for (int ks = 4; ks < 8; ++ks)
+                mma_ts(tmem + col_o(i), tmem + col_s(i) + 8 * ks, dv + (uint64_t)((ks * 2048) >> 4), kIdescPV, true);
+              if (last) mma_commit(&S.empty[vs]);
+              if (j + 1 >= my[i]) mma_commit(&S.o_done[i]);
             }
             __syncwarp();
+            if (j + 1 < my[i]) scores(i, ksl, last);
           }
-          if (ok && j + 1 < T.steps[i]) scores(i, ksl, last);
+          if (j >= plain) ++hid;
         }
-        // (a tile that ends before the other: the other one's scores free the keys)
+        if (!ok) break;
+        base += 2 * steps;
       }
-      if (!ok) {
+      if (S.abort_flag) {
         // gave up: what has been issued completes before TMEM is freed (bounded)
         if (elect_one()) mma_commit(&S.drained);
         for (uint32_t n = 0; n < kSpinLimit; ++n)
@@ -333,253 +420,361 @@ __global__ void __launch_bounds__(kChThreads, 1)
       }
     } else if (warp == 9 && lane == 0) {
       // -------------------------------------------------------------- loads
-      int n = early;
-      for (; n < 2 * steps; ++n) {
-        if (!mbar_wait_bounded(&S.empty[n % kChSlots], ((n / kChSlots) - 1) & 1, &S.abort_flag, nullptr)) break;
-        load(n);
+      int n = (int)loaded;      // (of the first piece, requested above)
+      bool ok = true;
+      ChunkTile T = S.work[0];
+      for (int k = 1;; ++k) {
+        const int steps = max(T.steps[0], T.steps[1]);
+        for (; n < 2 * steps; ++n, ++loaded) {
+          ok = loaded < kChSlots ||
+               mbar_wait_bounded(&S.empty[loaded % kChSlots], ((loaded / kChSlots) - 1) & 1, &S.abort_flag, nullptr);
+          if (!ok) break;
+          load(T, steps, n, loaded);
+        }
+        n = 0;
+        if (!ok || !T.there) break;
+        const unsigned G = gridDim.x, b = blockIdx.x;
+        const unsigned w = (unsigned)k * G + ((k & 1) ? G - 1 - b : b);
+        if (w < (unsigned)p.pieces) {
+          T = locate(p, (int)w);
+        } else {
+          T.there = T.steps[0] = T.steps[1] = 0;
+        }
+        if (k >= 2) ok = mbar_wait_bounded(&S.w_empty[k & 1], ((k >> 1) - 1) & 1, &S.abort_flag, nullptr);
+        if (!ok) break;
+        S.work[k & 1] = T;
+        mbar_arrive(&S.w_full[k & 1]);
       }
       if (S.abort_flag) {
         // gave up: the copies in flight get their time (bounded)
-        for (int x = max(0, n - kChSlots); x < n; ++x)
+        for (uint32_t x = loaded > kChSlots ? loaded - kChSlots : 0; x < loaded; ++x)
           for (uint32_t i = 0; i < kSpinLimit; ++i)
             if (mbar_try_wait(&S.full[x % kChSlots], (x / kChSlots) & 1)) break;
       }
     } else if (warp >= 10) {
       // ----------------------------------------- value rows of partial steps
-      const int w = warp - 10;
-      for (int j = plain; j < steps; ++j) {
-        const int vn = value_pos(j, steps), vs = vn % kChSlots;
-        // (these warps do not follow a slot's earlier uses: its phase is waited for once it exists)
-        const bool ok = wait_issued(&S.issued[vs], (uint32_t)(vn / kChSlots), &S.abort_flag, nullptr) &&
-                        mbar_wait_bounded(&S.full[vs], (vn / kChSlots) & 1, &S.abort_flag, nullptr);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        bool cleared = false;
+      const int half = warp - 10;
+      uint32_t base = 0, hid = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        const ChunkTile T = take(k);
+        release(k);
+        if (!T.there) break;
+        const int steps = max(T.steps[0], T.steps[1]), plain = min(T.plain[0], T.plain[1]);
+        for (int j = plain; j < steps; ++j, ++hid) {
+          const uint32_t vn = base + value_pos(j, steps);
+          const int vs = vn % kChSlots;
+          // (these warps do not follow a slot's earlier uses: its phase is waited for once it exists)
+          ok = wait_issued(&S.issued[vs], vn / kChSlots, &S.abort_flag, nullptr) &&
+               mbar_wait_bounded(&S.full[vs], (vn / kChSlots) & 1, &S.abort_flag, nullptr);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          bool cleared = false;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = 64 * w + 32 * i + lane;
-          uint32_t any = 0u;
+          for (int i = 0; i < 2; ++i) {
+            const int r = 64 * half + 32 * i + lane;
+            uint32_t any = 0u;
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const uint4 u = *reinterpret_cast<const uint4*>(S.ring[vs] + tile_off(r, c));
-            // an exponent of all ones carries into bit 15 of its half
-            any |= (((u.x & 0x7f807f80u) + 0x00800080u) | ((u.y & 0x7f807f80u) + 0x00800080u) |
-                    ((u.z & 0x7f807f80u) + 0x00800080u) | ((u.w & 0x7f807f80u) + 0x00800080u)) &
-                   0x80008000u;
-          }
-          const uint32_t bits = __ballot_sync(0xffffffffu, any != 0u);
-          if (lane == 0) S.bad[j & 3][2 * w + i] = bits;
-          if (any != 0u) {
+            for (int c = 0; c < 16; ++c) {
+              const uint4 u = *reinterpret_cast<const uint4*>(S.ring[vs] + tile_off(r, c));
+              // an exponent of all ones carries into bit 15 of its half
+              any |= (((u.x & 0x7f807f80u) + 0x00800080u) | ((u.y & 0x7f807f80u) + 0x00800080u) |
+                      ((u.z & 0x7f807f80u) + 0x00800080u) | ((u.w & 0x7f807f80u) + 0x00800080u)) &
+                     0x80008000u;
+            }
+            const uint32_t bits = __ballot_sync(0xffffffffu, any != 0u);
+            if (lane == 0) S.bad[hid & 3][2 * half + i] = bits;
+            if (any != 0u) {
 #pragma unroll 1
-            for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4*>(S.ring[vs] + tile_off(r, c)) = make_uint4(0, 0, 0, 0);
+              for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4*>(S.ring[vs] + tile_off(r, c)) = make_uint4(0, 0, 0, 0);
+            }
+            cleared = cleared || bits != 0u;
           }
-          cleared = cleared || bits != 0u;
+          if (cleared) async_fence();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.v_clean[hid & 3]);
         }
-        if (cleared) async_fence();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.v_clean[j & 3]);
+        base += 2 * steps;
       }
     }
     __syncwarp();
   } else {
     // -------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-    const int i = warp >> 2;
-    const int my_steps = i ? T.steps[1] : T.steps[0], my_plain = i ? T.plain[1] : T.plain[0];
-    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t lanes = (uint32_t)wr << 16;
     const uint32_t tS = tmem + col_s(i) + lanes, tO = tmem + col_o(i) + lanes;
-    const int r = T.first_row + i * kChRows + 32 * (warp & 3) + lane;
-    const bool live = r < T.rows;
-    const int row = min(r, T.rows - 1);
-    const int tok = row / p.gqa, h = T.head * p.gqa + row - tok * p.gqa;
-    const int limit = min(max(tok + 1, T.prefix), T.len);     // visible keys: [0, limit)
-    const float slope2 = BIAS ? p.slopes[h] * 1.4426950408889634f : 0.0f;
-    // scores to log2 units: a factor here, the rule's arithmetic otherwise
-    const float sl = CAP || BIAS ? 1.0f : p.scale_log2;
-    float m = -INFINITY, l = 0.0f;     // running maximum (before sl) and sum
+    uint8_t* stage = S.stage[warp];
+    // scores to log2 units: a factor here (slopes are divided by it), the cap's arithmetic otherwise
+    const float sl = CAP ? 1.0f : p.scale_log2;
+
+    auto queries_loaded = [&] {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      async_fence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.q_ready[i]);
+    };
+
     bool ok = true;
-    for (int j = 0; j < my_steps; ++j) {
-      ok = mbar_wait_bounded(&S.s_full[i], j & 1, &S.abort_flag, nullptr);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tfence_after();
-      float s[kChKeys];
-#pragma unroll
-      for (int c = 0; c < kChKeys; c += 32) tld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&s[c]));
-      tld_wait();
-      if constexpr (CAP) {
-        // cap tanh(x / cap) = cap - 2 cap / (1 + exp(2 x / cap)), in log2 units
-#pragma unroll
-        for (int c = 0; c < kChKeys; ++c)
-          s[c] = fmaf(p.cap_out, rcp_approx(1.0f + tc_exp2(s[c] * p.cap_in)), p.cap_log2);
+    uint32_t step = 0, hid = 0, done = 0;     // steps of this tile place, steps with hidden keys, tiles
+    {
+      const ChunkTile T = S.work[0];
+      if ((i ? T.steps[1] : T.steps[0]) > 0) queries_loaded();
+    }
+    for (int k = 0;; ++k) {
+      // (the piece is read anew where it is needed: its registers would be missed in the steps)
+      int limit, my_steps, my_plain, plain, tok0;
+      uint32_t orow;                       // the lane's row of the outputs
+      float slope2 = 0.0f;
+      {
+        const ChunkTile T = take(k);
+        my_steps = i ? T.steps[1] : T.steps[0];
+        my_plain = i ? T.plain[1] : T.plain[0];
+        plain = min(T.plain[0], T.plain[1]);      // steps before this one hide no key from any row
+        const int row = min(T.first_row + i * kChRows + wr + lane, T.rows - 1);
+        tok0 = row / p.gqa;
+        limit = min(max(tok0 + 1, T.prefix), T.len);     // visible keys: [0, limit)
+        orow = (uint32_t)(T.row0 + tok0) * p.hq + T.head * p.gqa + row - tok0 * p.gqa;
+        if constexpr (BIAS) slope2 = p.slopes[T.head * p.gqa + row - tok0 * p.gqa] * p.slope_unit;
       }
-      if constexpr (BIAS) {
-        const float d0 = (float)(j * kChKeys - tok);
+      float m = -INFINITY, l = 0.0f;     // running maximum (before sl) and sum
+      uint32_t hj = hid;
+      for (int j = 0; j < my_steps; ++j, ++step) {
+        ok = ok && mbar_wait_bounded(&S.s_full[i], step & 1, &S.abort_flag, nullptr);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tfence_after();
+        float s[kChKeys];
+        float top = -INFINITY;
+        {
 #pragma unroll
-        for (int c = 0; c < kChKeys; ++c)
-          s[c] = fmaf(-slope2, fabsf(d0 + (float)c), CAP ? s[c] : s[c] * p.scale_log2);
-      }
-      if (j >= my_plain) {
-        const int vis = limit - j * kChKeys;
-#pragma unroll
-        for (int c = 0; c < kChKeys; ++c) s[c] = c < vis ? s[c] : -INFINITY;
-      }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-      for (int c = 4; c < kChKeys; c += 8) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (c + 4 + e < kChKeys)
-            asm("max.f32 %0, %0, %1, %2;" : "+f"(mx[e]) : "f"(s[c + e]), "f"(s[c + 4 + e]));
-          else
-            mx[e] = fmaxf(mx[e], s[c + e]);
-        }
-      }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      // a larger maximum takes effect where it is far above the one in use
-      const bool grow = (top - m) * sl > kGrowth || m == -INFINITY;
-      const float m_new = grow ? fmaxf(m, top) : m;
-      if (__any_sync(0xffffffffu, grow && j > 0)) {
-        const float f = m_new == -INFINITY ? 1.0f : tc_exp2((m - m_new) * sl);
-        l *= f;
-#pragma unroll 1
-        for (int c = 0; c < kHeadDim; c += 16) {
-          uint32_t o[16];
-          tld16(tO + c, o);
+          for (int c = 0; c < kChKeys; c += 32) tld32(tS + c, *reinterpret_cast<uint32_t(*)[32]>(&s[c]));
           tld_wait();
+          if constexpr (CAP) {
+            float hi = fmaxf(s[0], s[1]), lo = fminf(s[0], s[1]);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-          tst16(tO + c, o);
+            for (int c = 2; c < kChKeys; c += 2) {
+              asm("max.f32 %0, %0, %1, %2;" : "+f"(hi) : "f"(s[c]), "f"(s[c + 1]));
+              asm("min.f32 %0, %0, %1, %2;" : "+f"(lo) : "f"(s[c]), "f"(s[c + 1]));
+            }
+            // (uniform; the scores of a model with a cap mostly stay well within it)
+            if (__all_sync(0xffffffffu, fmaxf(hi, -lo) * p.cap_near <= 1.0f)) {
+#pragma unroll
+              for (int c = 0; c < kChKeys; c += 2) {
+                const float2 y = cap_near(make_float2(s[c], s[c + 1]), p);
+                s[c] = y.x;
+                s[c + 1] = y.y;
+              }
+              top = cap_near(make_float2(hi, hi), p).x;
+            } else {
+#pragma unroll
+              for (int c = 0; c < kChKeys; ++c) s[c] = cap_far(s[c], p);
+              top = cap_far(hi, p);
+            }
+          }
+          if constexpr (BIAS) {
+            const float2 slope = make_float2(-slope2, -slope2);
+            float2 d[4];     // distances, tok0 - key
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float d0 = (float)(tok0 - j * kChKeys - 2 * e);
+              d[e] = make_float2(d0, d0 - 1.0f);
+            }
+            auto lower = [&](auto both_ways) {
+#pragma unroll
+              for (int c = 0; c < kChKeys; c += 8) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  float2 y = make_float2(s[c + 2 * e], s[c + 2 * e + 1]);
+                  y = __ffma2_rn(slope, decltype(both_ways)::value ? make_float2(fabsf(d[e].x), fabsf(d[e].y)) : d[e], y);
+                  s[c + 2 * e] = y.x;
+                  s[c + 2 * e + 1] = y.y;
+                  d[e] = __fadd2_rn(d[e], make_float2(-8.0f, -8.0f));
+                }
+              }
+            };
+            if (__any_sync(0xffffffffu, tok0 < (j + 1) * kChKeys - 1)) lower(std::true_type{});   // keys behind the query's token
+            else lower(std::false_type{});
+          }
+          if (j >= my_plain) {
+            const int vis = limit - j * kChKeys;
+#pragma unroll
+            for (int c = 0; c < kChKeys; ++c) s[c] = c < vis ? s[c] : -INFINITY;
+          }
+          if (BIAS || !CAP || j >= my_plain) {
+            float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int c = 4; c < kChKeys; c += 8) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if (c + 4 + e < kChKeys)
+                  asm("max.f32 %0, %0, %1, %2;" : "+f"(mx[e]) : "f"(s[c + e]), "f"(s[c + 4 + e]));
+                else
+                  mx[e] = fmaxf(mx[e], s[c + e]);
+              }
+            }
+            top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          }
         }
-        tst_wait();
-      }
-      m = m_new;
-      const float base = m == -INFINITY ? 0.0f : -m * sl;
-      const float2 sl2 = make_float2(sl, sl), base2 = make_float2(base, base);
-      float2 sum0 = make_float2(0.0f, 0.0f), sum1 = make_float2(0.0f, 0.0f);
+        // a larger maximum takes effect where it is far above the one in use
+        const bool grow = (top - m) * sl > kGrowth || m == -INFINITY;
+        const float m_new = grow ? fmaxf(m, top) : m;
+        if (__any_sync(0xffffffffu, grow && j > 0)) {
+          const float f = m_new == -INFINITY ? 1.0f : tc_exp2((m - m_new) * sl);
+          l *= f;
+#pragma unroll 1
+          for (int c = 0; c < kHeadDim; c += 16) {
+            uint32_t o[16];
+            tld16(tO + c, o);
+            tld_wait();
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const int c = 64 * half + 2 * e;
-          const float2 a = __ffma2_rn(make_float2(s[c], s[c + 1]), sl2, base2);
-          const float2 b = __ffma2_rn(make_float2(s[c + 2], s[c + 3]), sl2, base2);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tst16(tO + c, o);
+          }
+          tst_wait();
+        }
+        m = m_new;
+        const float base = m == -INFINITY ? 0.0f : -m * sl;
+        const float2 sl2 = make_float2(sl, sl), base2 = make_float2(base, base);
+        float2 sum0 = make_float2(0.0f, 0.0f), sum1 = make_float2(0.0f, 0.0f);
+        auto weights = [&](const float* x, uint32_t* pk) {     // of 4 scores
+          const float2 a = __ffma2_rn(make_float2(x[0], x[1]), sl2, base2), b = __ffma2_rn(make_float2(x[2], x[3]), sl2, base2);
           const float2 pa = make_float2(tc_exp2(a.x), tc_exp2(a.y)), pb = make_float2(tc_exp2(b.x), tc_exp2(b.y));
           sum0 = __fadd2_rn(sum0, pa);
           sum1 = __fadd2_rn(sum1, pb);
-          pk[e] = pack_bf16x2(pa.x, pa.y);
-          pk[e + 1] = pack_bf16x2(pb.x, pb.y);
-        }
-        tst32(tS + 32 * half, pk);
-        if (half == 0 && j < plain) {
-          tst_wait();
-          tfence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&S.p_ready[i][0]);
-        }
-      }
-      tst_wait();
-      if (j >= plain) {
-        // hidden keys in this step: values that had to be cleared are added here
-        ok = mbar_wait_bounded(&S.v_clean[j & 3], ((j - plain) >> 2) & 1, &S.abort_flag, nullptr);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint32_t* bad = S.bad[j & 3];
-        if ((bad[0] | bad[1] | bad[2] | bad[3]) != 0u)
-          add_cleared(tS, tO, bad, limit - j * kChKeys, j == 0,
-                      p.v + (int64_t)(T.row0 + j * kChKeys) * p.v_token + (int64_t)T.head * p.v_head, p.v_token);
-        tfence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.p_ready[i][0]);
-      } else {
-        tfence_before();
-        __syncwarp();
-      }
-      if (lane == 0) mbar_arrive(&S.p_ready[i][1]);
-      l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-    }
-    if (my_steps > 0) {
-      // o / l, merged with the row over what precedes the chunk.  Rows pass
-      // through the tile's query memory (free by now), a warp's 32 rows by itself:
-      // 16 lanes a row in global memory, a thread a row in between.
-      uint8_t* rows = S.q[i];
-      const int w0 = T.first_row + i * kChRows + 32 * (warp & 3);     // the warp's first row
-      const int t0 = w0 / p.gqa, rest = w0 - t0 * p.gqa, c = lane & 15, r0 = lane >> 4;
-      const float inv = 1.0f / (float)p.gqa;
-      const int64_t base = ((int64_t)(T.row0 + t0) * p.hq + T.head * p.gqa) * kHeadDim + 8 * c;
-      // element of row w0 + r, chunk c
-      auto place = [&](int r) {
-        const int at = rest + r, tk = (int)(((float)at + 0.5f) * inv);
-        return base + ((int64_t)tk * p.hq + (at - tk * p.gqa)) * kHeadDim;
-      };
-      const int64_t at = (int64_t)(T.row0 + tok) * p.hq + h;
-      float before = -INFINITY;
-      uint4 u[16];
-      if (p.prior_lse != nullptr) {
-        before = p.prior_lse[at];
+          pk[0] = pack_bf16x2(pa.x, pa.y);
+          pk[1] = pack_bf16x2(pb.x, pb.y);
+        };
 #pragma unroll
-        for (int x = 0; x < 16; ++x)
-          u[x] = w0 + r0 + 2 * x < T.rows ? *reinterpret_cast<const uint4*>(p.prior_out + place(r0 + 2 * x))
-                                          : make_uint4(0, 0, 0, 0);
-      }
-      if (ok) {
-        ok = mbar_wait_bounded(&S.o_done[i], 0, &S.abort_flag, nullptr);
-        ok = __all_sync(0xffffffffu, ok);
-        tfence_after();
-      }
-      if (p.prior_lse != nullptr) {
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
 #pragma unroll
-        for (int x = 0; x < 16; ++x) *reinterpret_cast<uint4*>(rows + tile_off(32 * (warp & 3) + r0 + 2 * x, c)) = u[x];
-        __syncwarp();
-      }
-      float lse = ok ? fmaf(m, sl * kLn2, logf(l)) : NAN;
-      float fo = ok ? 1.0f / l : NAN, fp = 0.0f;
-      if (before != -INFINITY) {
-        const float top = fmaxf(lse, before);
-        const float a = expf(lse - top), b = expf(before - top);
-        fp = b / (a + b);
-        fo *= a / (a + b);
-        lse = top + logf(a + b);
-      }
-#pragma unroll 1
-      for (int c4 = 0; c4 < 16; c4 += 4) {
-        uint32_t o[32];
-        if (ok) {
-          tld32(tO + 8 * c4, o);
-          tld_wait();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0x7fc00000u;
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint4* mine = reinterpret_cast<uint4*>(rows + tile_off(32 * (warp & 3) + lane, c4 + e));
-          float x[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(o[8 * e + k]) * fo;
-          if (fp != 0.0f) {     // (also NaN)
-            const uint4 b = *mine;
-            x[0] = fmaf(bf16_lo(b.x), fp, x[0]);
-            x[1] = fmaf(bf16_hi(b.x), fp, x[1]);
-            x[2] = fmaf(bf16_lo(b.y), fp, x[2]);
-            x[3] = fmaf(bf16_hi(b.y), fp, x[3]);
-            x[4] = fmaf(bf16_lo(b.z), fp, x[4]);
-            x[5] = fmaf(bf16_hi(b.z), fp, x[5]);
-            x[6] = fmaf(bf16_lo(b.w), fp, x[6]);
-            x[7] = fmaf(bf16_hi(b.w), fp, x[7]);
+          for (int e = 0; e < 32; e += 2) weights(&s[64 * half + 2 * e], &pk[e]);
+          tst32(tS + 32 * half, pk);
+          if (half == 0 && j < plain) {
+            tst_wait();
+            tfence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.p_ready[i][0]);
           }
-          *mine = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                             pack_bf16x2(x[6], x[7]));
         }
+        tst_wait();
+        if (j >= plain) {
+          // hidden keys in this step: values that had to be cleared are added here
+          ok = mbar_wait_bounded(&S.v_clean[hj & 3], (hj >> 2) & 1, &S.abort_flag, nullptr);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          const uint32_t* bad = S.bad[hj & 3];
+          ++hj;
+          if ((bad[0] | bad[1] | bad[2] | bad[3]) != 0u) {
+            const ChunkTile T = S.work[k & 1];
+            add_cleared(tS, tO, bad, limit - j * kChKeys, j == 0,
+                        p.v + (int64_t)(T.row0 + j * kChKeys) * p.v_token + (int64_t)T.head * p.v_head, p.v_token);
+          }
+        }
+        tfence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (j >= plain) mbar_arrive(&S.p_ready[i][0]);
+          mbar_arrive(&S.p_ready[i][1]);
+        }
+        l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
       }
-      __syncwarp();
+      const ChunkTile T = S.work[k & 1];
+      release(k);
+      hid += max(T.steps[0], T.steps[1]) - plain;
+
+      // every product with this piece's queries is done (its last scores were):
+      // the next piece's take their place meanwhile
+      bool more, queries;
+      {
+        const ChunkTile N = take(k + 1);
+        more = N.there != 0;
+        queries = more && (i ? N.steps[1] : N.steps[0]) > 0;
+        if (queries && ok) load_queries(N);
+      }
+      if (my_steps > 0) {
+        // o / l, merged with the row over what precedes the chunk.  A warp's rows pass
+        // through its part of shared memory, 16 channels at a time (a loop of few
+        // instructions: they are fetched anew for every piece): 2 lanes a row (a sector)
+        // in global memory, a thread a row in between.
+        const int rows = T.rows - (T.first_row + i * kChRows + wr);     // rows of the warp that exist
+        const int c2 = lane & 1, r2 = lane >> 1;
+        // element of the warp's row x, 16-byte chunk c2
+        auto place = [&](int x) { return (int64_t)__shfl_sync(0xffffffffu, orow, x) * kHeadDim + 8 * c2; };
+        const int64_t at0 = place(r2), at1 = place(r2 + 16);
+        auto staged = [&](int x, int c) { return reinterpret_cast<uint4*>(stage + x * kStageRow + ((c ^ ((x >> 2) & 1)) << 4)); };
+        const bool merge = p.prior_lse != nullptr;
+        const float before = merge ? p.prior_lse[orow] : -INFINITY;
+        // rows r2 and r2 + 16 to merge with (rows behind the last one repeat it), requested early
+        uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
+        auto load_prior = [&](int c) {
+          u0 = *reinterpret_cast<const uint4*>(p.prior_out + at0 + c);
+          u1 = *reinterpret_cast<const uint4*>(p.prior_out + at1 + c);
+        };
+        if (merge) load_prior(0);
+        if (ok) {
+          ok = mbar_wait_bounded(&S.o_done[i], done & 1, &S.abort_flag, nullptr);
+          ok = __all_sync(0xffffffffu, ok);
+          tfence_after();
+        }
+        ++done;
+        float lse = ok ? fmaf(m, sl * kLn2, logf(l)) : NAN;
+        float fo = ok ? 1.0f / l : NAN, fp = 0.0f;
+        if (before != -INFINITY) {
+          const float top = fmaxf(lse, before);
+          const float a = expf(lse - top), b = expf(before - top);
+          fp = b / (a + b);
+          fo *= a / (a + b);
+          lse = top + logf(a + b);
+        }
+#pragma unroll 1
+        for (int c = 0; c < kHeadDim; c += 16) {
+          if (merge) {
+            *staged(r2, c2) = u0;
+            *staged(r2 + 16, c2) = u1;
+            __syncwarp();
+            if (c + 16 < kHeadDim) load_prior(c + 16);
+          }
+          uint32_t o[16];
+          if (ok) {
+            tld16(tO + c, o);
+            tld_wait();
+          } else {
 #pragma unroll
-      for (int x = 0; x < 16; ++x)
-        if (w0 + r0 + 2 * x < T.rows)
-          *reinterpret_cast<uint4*>(p.out + place(r0 + 2 * x)) =
-              *reinterpret_cast<const uint4*>(rows + tile_off(32 * (warp & 3) + r0 + 2 * x, c));
-      if (live && p.lse != nullptr) p.lse[at] = lse;
+            for (int q = 0; q < 16; ++q) o[q] = 0x7fc00000u;
+          }
+#pragma unroll
+          for (int d = 0; d < 2; ++d) {
+            uint4* mine = staged(lane, d);
+            float x[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) x[q] = __uint_as_float(o[8 * d + q]) * fo;
+            if (fp != 0.0f) {     // (also NaN)
+              const uint4 b = *mine;
+              x[0] = fmaf(bf16_lo(b.x), fp, x[0]);
+              x[1] = fmaf(bf16_hi(b.x), fp, x[1]);
+              x[2] = fmaf(bf16_lo(b.y), fp, x[2]);
+              x[3] = fmaf(bf16_hi(b.y), fp, x[3]);
+              x[4] = fmaf(bf16_lo(b.z), fp, x[4]);
+              x[5] = fmaf(bf16_hi(b.z), fp, x[5]);
+              x[6] = fmaf(bf16_lo(b.w), fp, x[6]);
+              x[7] = fmaf(bf16_hi(b.w), fp, x[7]);
+            }
+            *mine = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                               pack_bf16x2(x[6], x[7]));
+          }
+          __syncwarp();
+          if (r2 < rows) *reinterpret_cast<uint4*>(p.out + at0 + c) = *staged(r2, c2);
+          if (r2 + 16 < rows) *reinterpret_cast<uint4*>(p.out + at1 + c) = *staged(r2 + 16, c2);
+          __syncwarp();
+        }
+        tfence_before();
+        if (lane < rows && p.lse != nullptr) p.lse[orow] = lse;
+      }
+      if (!more || !ok) break;
+      if (queries) queries_loaded();
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
 
   tfence_before();
@@ -639,7 +834,31 @@ cudaError_t launch_chunk(ChunkParams<MAXS>& p, const uint16_t* k, int64_t k_toke
     }
     if (p.cta_rows == kChRows || tiles * p.hkv >= sms) break;
   }
-  const unsigned grid = (unsigned)(tiles * p.hkv);
+  p.pieces = (int32_t)(tiles * p.hkv);
+  // several rounds over documents of different lengths: pieces in descending order
+  // of their steps (without the table, document by document: 24 documents of 60 to
+  // 1,531 tokens took 1.3 times as long)
+  p.sorted = p.pieces > sms && p.n_seqs > 1 && tiles <= ChunkParams<MAXS>::kOrder;
+  if (p.sorted) {
+    struct Entry {
+      int32_t steps;
+      uint32_t what;
+    } list[ChunkParams<MAXS>::kOrder];
+    int n = 0;
+    for (int i = 0; i < p.n_seqs; ++i) {
+      const int64_t rows = (int64_t)p.seq[i].len * p.gqa;
+      for (int64_t r = 0; r < rows; r += p.cta_rows) {
+        const int last = (int)((std::min<int64_t>(r + p.cta_rows, rows) - 1) / p.gqa);
+        const int lim = std::min(std::max(last + 1, p.seq[i].prefix), p.seq[i].len);
+        list[n++] = Entry{(lim + kChKeys - 1) / kChKeys, (uint32_t)i << 22 | (uint32_t)(r / p.cta_rows)};
+      }
+    }
+    std::sort(list, list + n, [](const Entry& a, const Entry& b) {
+      return a.steps != b.steps ? a.steps > b.steps : a.what < b.what;
+    });
+    for (int i = 0; i < n; ++i) p.order[i] = list[i].what;
+  }
+  const unsigned grid = (unsigned)std::min<int64_t>(p.pieces, sms);
   const bool cap = p.cap_log2 != 0.0f, bias = p.slopes != nullptr;
   if (cap) return bias ? launch_chunk_t<MAXS, true, true>(p, tmk, tmv, grid, stream)
                        : launch_chunk_t<MAXS, true, false>(p, tmk, tmv, grid, stream);

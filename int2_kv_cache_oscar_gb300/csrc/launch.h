@@ -384,12 +384,16 @@ struct ChunkParams {
   int32_t hkv;
   int32_t gqa;
   int32_t hq;
-  int32_t cta_rows;    // (token, head) rows of a CTA, 128 or 256; set by the launch
+  int32_t cta_rows;    // (token, head) rows of a piece of work, 128 or 256, and
+  int32_t pieces;      // how many pieces; set by the launch
   float scale_log2;    // softmax_scale * log2(e)
   float cap_in;        // 2 softmax_scale log2(e) / cap
   float cap_out;       // -2 cap log2(e)
   float cap_log2;      // cap log2(e); 0: no cap
+  float cap_near;      // softmax_scale / (0.4 cap): |raw score| times it up to 1 takes the polynomial
+  float cap_c[4];      // of the raw score (x times a polynomial of x^2)
   const float* slopes; // [hq], or NULL
+  float slope_unit;    // log2(e) with a cap (scores in log2 units), 1 / softmax_scale without (raw scores)
   const uint16_t* q;
   const uint16_t* v;
   int64_t q_token, q_head, v_token, v_head;   // strides in elements
@@ -398,6 +402,11 @@ struct ChunkParams {
   uint16_t* out;               // [tokens, hq, 128]
   float* lse;                  // [tokens, hq], or NULL
   ChunkSeq seq[MAXS];
+  // row tiles in the order in which they are taken (document << 22 | tile), set by
+  // the launch where there is one
+  static constexpr int kOrder = MAXS <= kDecodeSeqsSmall ? 496 : 2000;
+  int32_t sorted;
+  uint32_t order[kOrder];
 };
 
 template <int MAXS>

@@ -1605,6 +1605,8 @@ oscar_status oscar_chunk_attention(int32_t n_seqs, const int32_t* cu, const int3
     if (n_seqs == 0) return ok();
     if (!cu) return fail(OSCAR_ERR_INVALID_ARG, "cu_seqlens is NULL");
     if (cu[0] != 0) return fail(OSCAR_ERR_INVALID_ARG, "cu_seqlens[0] must be 0");
+    if (rule && rule->slopes && scale_of(softmax_scale) < 0x1p-60f)
+      return fail(OSCAR_ERR_INVALID_ARG, "with slopes softmax_scale must be at least 2^-60");
     const int32_t gqa = hq / hkv;
     std::vector<ChunkSeq> seqs;
     for (int32_t i = 0; i < n_seqs; ++i) {
@@ -1654,8 +1656,18 @@ oscar_status oscar_chunk_attention(int32_t n_seqs, const int32_t* cu, const int3
       P.cap_in = 2.0f * scale * kLog2e / cap;
       P.cap_log2 = cap * kLog2e;
       P.cap_out = -2.0f * P.cap_log2;
+      // x = k s: the polynomial's coefficients in powers of k, where these are far
+      // from the ends of float32 (else the polynomial is not used)
+      const double r = (double)scale / cap, y = r * r, first = (double)P.scale_log2;
+      const bool fits = r >= 0x1p-15 && r <= 0x1p15;
+      P.cap_near = fits ? (float)(r / 0.4) : INFINITY;
+      P.cap_c[0] = (float)first;
+      P.cap_c[1] = fits ? (float)(first * y * -0.33331882259987955) : 0.0f;
+      P.cap_c[2] = fits ? (float)(first * y * y * 0.13277628990878212) : 0.0f;
+      P.cap_c[3] = fits ? (float)(first * y * y * y * -0.04779421895253378) : 0.0f;
     }
     P.slopes = slopes;
+    P.slope_unit = cap != 0.0f ? kLog2e : 1.0f / scale;
     P.q = static_cast<const uint16_t*>(rq.data);
     P.v = static_cast<const uint16_t*>(rv.data);
     P.q_token = rq.token_stride;
