@@ -78,14 +78,15 @@ __device__ __forceinline__ float cap_far(float s, const P& p) {
   return fmaf(p.cap_out, rcp_approx(1.0f + tc_exp2(s * p.cap_in)), p.cap_log2);
 }
 
-// The same within 0.4 of the cap, two scores: tanh(x) = x (1 + c1 x^2 + c2 x^4 +
-// c3 x^6), the smallest largest relative error over that range (2^-23), with the
-// scale and the cap in the coefficients.
+// The same within 0.6 of the cap, two scores: tanh(x) = x (1 + c1 x^2 + .. + c4 x^8),
+// the smallest largest relative error over that range (2^-23.5), with the scale and
+// the cap in the coefficients.
 template <typename P>
 __device__ __forceinline__ float2 cap_near(float2 s, const P& p) {
   const float2 y = __fmul2_rn(s, s);
   auto two = [](float v) { return make_float2(v, v); };
-  float2 t = __ffma2_rn(two(p.cap_c[3]), y, two(p.cap_c[2]));
+  float2 t = __ffma2_rn(two(p.cap_c[4]), y, two(p.cap_c[3]));
+  t = __ffma2_rn(t, y, two(p.cap_c[2]));
   t = __ffma2_rn(t, y, two(p.cap_c[1]));
   return __fmul2_rn(s, __ffma2_rn(t, y, two(p.cap_c[0])));
 }

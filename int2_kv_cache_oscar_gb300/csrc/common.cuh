@@ -284,23 +284,22 @@ __device__ __forceinline__ uint32_t f32_to_bf16_bits(float x) {
   return u >> 16;
 }
 
-// cap tanh(s / cap), all in log2 units: s, cap, and inv = 1 / cap.  Within 0.4
-// of zero the odd series of tanh (to x^13: the next term is 2^-25 of the sum
-// there), elsewhere 1 - 2 / (1 + e^2x) with the hardware's exponential and
-// reciprocal: tanh is off by 2^-23 at most there, by 2^-23 of itself within.
-// `all_small`: every |s| of the warp is within 0.4 cap (uniform); the series
-// alone is then worked out, in packed pairs.
-__device__ __forceinline__ float2 tanh_series(float2 x) {
-  const float2 y = __fmul2_rn(x, x);
-  auto c = [](float v) { return make_float2(v, v); };
-  float2 t = c(21844.0f / 6081075.0f);
-  t = __ffma2_rn(t, y, c(-1382.0f / 155925.0f));
-  t = __ffma2_rn(t, y, c(62.0f / 2835.0f));
-  t = __ffma2_rn(t, y, c(-17.0f / 315.0f));
-  t = __ffma2_rn(t, y, c(2.0f / 15.0f));
-  t = __ffma2_rn(t, y, c(-1.0f / 3.0f));
-  return __ffma2_rn(__fmul2_rn(t, y), x, x);
-}
+// The score rule (include/oscar.h) as the cache's kernels use it, in log2 units.
+struct ScoreRule {
+  float cap;             // cap log2(e); 0: none
+  float inv_cap;
+  float c[6];            // coefficients of tanh's polynomial over powers of the cap (see capped)
+  float b[4];            // of a shorter one (see capped_bf16)
+  const float* slopes;   // [query heads], natural units, or NULL
+  __host__ __device__ bool any() const { return cap != 0.0f || slopes != nullptr; }
+};
+
+// cap tanh(s / cap) of two scores.  Up to the cap tanh(x) = x (1 + c0 x^2 + .. + c5
+// x^12), the smallest largest relative error over that range (2^-24); beyond, 1 - 2 /
+// (1 + e^2x) with the hardware's exponential and reciprocal, off by 2^-23 at most.
+// `all_near`: every score of the warp is within the cap (uniform); only the
+// polynomial is worked out then.
+constexpr float kTanhNear = 1.0f;
 
 __device__ __forceinline__ float tanh_far(float x) {
   float e, r;
@@ -309,16 +308,38 @@ __device__ __forceinline__ float tanh_far(float x) {
   return fmaf(-2.0f, r, 1.0f);
 }
 
-constexpr float kTanhNear = 0.4f;
-
-__device__ __forceinline__ float2 capped(float2 s, float cap, float inv, bool all_small) {
-  const float2 x = __fmul2_rn(s, make_float2(inv, inv));
-  float2 t = tanh_series(x);
-  if (!all_small) {
-    if (!(fabsf(x.x) <= kTanhNear)) t.x = tanh_far(x.x);   // (NaN too)
-    if (!(fabsf(x.y) <= kTanhNear)) t.y = tanh_far(x.y);
+__device__ __forceinline__ float2 capped(float2 s, const ScoreRule& r, bool all_near) {
+  const float2 y = __fmul2_rn(s, s);
+  auto two = [](float v) { return make_float2(v, v); };
+  float2 t = __ffma2_rn(two(r.c[5]), y, two(r.c[4]));
+  t = __ffma2_rn(t, y, two(r.c[3]));
+  t = __ffma2_rn(t, y, two(r.c[2]));
+  t = __ffma2_rn(t, y, two(r.c[1]));
+  t = __ffma2_rn(t, y, two(r.c[0]));
+  t = __fmul2_rn(s, __ffma2_rn(t, y, two(1.0f)));
+  if (!all_near) {
+    const float2 x = __fmul2_rn(s, two(r.inv_cap));
+    if (!(fabsf(x.x) <= kTanhNear)) t.x = r.cap * tanh_far(x.x);   // (NaN too)
+    if (!(fabsf(x.y) <= kTanhNear)) t.y = r.cap * tanh_far(x.y);
   }
-  return __fmul2_rn(t, make_float2(cap, cap));
+  return t;
+}
+
+// The same where outputs are bf16, off by cap 2^-22 at most: within 0.6 of the cap a
+// polynomial of two terms less (relative error 2^-23.5), and where a score of the
+// warp is outside the other form for all of them.
+constexpr float kTanhNearBf16 = 0.6f;
+
+__device__ __forceinline__ float2 capped_bf16(float2 s, const ScoreRule& r, bool all_near) {
+  auto two = [](float v) { return make_float2(v, v); };
+  if (all_near) {
+    const float2 y = __fmul2_rn(s, s);
+    float2 t = __ffma2_rn(two(r.b[3]), y, two(r.b[2]));
+    t = __ffma2_rn(t, y, two(r.b[1]));
+    t = __ffma2_rn(t, y, two(r.b[0]));
+    return __fmul2_rn(s, __ffma2_rn(t, y, two(1.0f)));
+  }
+  return make_float2(r.cap * tanh_far(s.x * r.inv_cap), r.cap * tanh_far(s.y * r.inv_cap));
 }
 
 // Bit position exponent p of fragment slot i = 2*kk + hf: codes at bits

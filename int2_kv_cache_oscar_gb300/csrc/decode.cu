@@ -599,9 +599,9 @@ __global__ void __launch_bounds__(kDecThreads, kCtasPerSm)
           float top = 0.0f;
 #pragma unroll
           for (int mt = 0; mt < 8; ++mt) top = fmaxf(top, fmaxf(fabsf(sc[mt].x), fabsf(sc[mt].y)));
-          const bool small = __all_sync(0xffffffffu, top * p.h.rule.inv_cap <= kTanhNear);
+          const bool near = __all_sync(0xffffffffu, top * p.h.rule.inv_cap <= kTanhNear);
 #pragma unroll
-          for (int mt = 0; mt < 8; ++mt) sc[mt] = capped(sc[mt], p.h.rule.cap, p.h.rule.inv_cap, small);
+          for (int mt = 0; mt < 8; ++mt) sc[mt] = capped(sc[mt], p.h.rule, near);
         }
         // distance: tokens from 128 group + 16 mt + g (.x), + 8 (.y) to the newest
         const float far = (float)(p.seq[b].len - 1 - kGroup * (g0 + (int)(kk - k_begin)) - g);
@@ -903,7 +903,7 @@ __global__ void __launch_bounds__(kCombineThreads)
         a0 = fmaf(qb.z, bf16_lo(kv4.w), a0); a1 = fmaf(qb.w, bf16_hi(kv4.w), a1);
       }
       scw = (a0 + a1) * p.h.scale_log2;
-      if (p.h.rule.cap != 0.0f) scw = capped(make_float2(scw, 0.0f), p.h.rule.cap, p.h.rule.inv_cap, false).x;
+      if (p.h.rule.cap != 0.0f) scw = capped(make_float2(scw, 0.0f), p.h.rule, false).x;
       if (p.h.rule.slopes != nullptr)
         scw = fmaf(-1.4426950408889634f * p.h.rule.slopes[j * p.h.q_group + p.h.q_head0 + h], (float)(wlen - 1 - t), scw);
     }

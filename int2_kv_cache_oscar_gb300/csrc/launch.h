@@ -79,14 +79,6 @@ cudaError_t launch_quantize_small(const QuantPlan<kQuantPlanSmall>& plan, uint8_
 cudaError_t launch_quantize_large(const QuantPlan<kQuantPlanLarge>& plan, uint8_t* arena, const uint16_t* k,
                                   const uint16_t* v, bool meta16, cudaStream_t stream);
 
-// The score rule (include/oscar.h) as the cache's kernels use it, in log2 units.
-struct ScoreRule {
-  float cap;             // cap log2(e); 0: none
-  float inv_cap;
-  const float* slopes;   // [query heads], natural units, or NULL
-  __host__ __device__ bool any() const { return cap != 0.0f || slopes != nullptr; }
-};
-
 // ------------------------------------------------------------------ decode
 
 // Per-sequence data of one decode launch.  Work units are (sequence, KV head,
@@ -390,8 +382,8 @@ struct ChunkParams {
   float cap_in;        // 2 softmax_scale log2(e) / cap
   float cap_out;       // -2 cap log2(e)
   float cap_log2;      // cap log2(e); 0: no cap
-  float cap_near;      // softmax_scale / (0.4 cap): |raw score| times it up to 1 takes the polynomial
-  float cap_c[4];      // of the raw score (x times a polynomial of x^2)
+  float cap_near;      // softmax_scale / (0.6 cap): |raw score| times it up to 1 takes the polynomial
+  float cap_c[5];      // of the raw score (x times a polynomial of x^2)
   const float* slopes; // [hq], or NULL
   float slope_unit;    // log2(e) with a cap (scores in log2 units), 1 / softmax_scale without (raw scores)
   const uint16_t* q;

@@ -180,11 +180,20 @@ oscar_status check_rule(const oscar_score_rule* r) {
 
 // The rule for the cache's kernels; with the cache's device current.
 oscar_status cache_rule(const oscar_score_rule* r, int device, ScoreRule* out) {
-  *out = ScoreRule{0.0f, 0.0f, nullptr};
+  *out = ScoreRule{};
   if (r == nullptr) return OSCAR_OK;
   if (r->cap != 0.0f) {
     out->cap = r->cap * kLog2e;
     out->inv_cap = 1.0f / out->cap;
+    const double c[6] = {-0.3333298680917359, 0.13326408458826144,  -0.05349867504186163,
+                         0.020359682485341188, -0.006259264284882422, 0.0010582383503523435};
+    double power = 1.0;
+    const double b[4] = {-0.33332597509867323, 0.1331311669852155, -0.05221180873069635, 0.015612635835695849};
+    for (int i = 0; i < 6; ++i) {
+      power /= (double)out->cap * out->cap;
+      out->c[i] = (float)(c[i] * power);
+      if (i < 4) out->b[i] = (float)(b[i] * power);
+    }
   }
   out->slopes = r->slopes;
   return out->slopes ? device_view_as(out->slopes, "slopes", device, &out->slopes) : OSCAR_OK;
@@ -1659,12 +1668,12 @@ oscar_status oscar_chunk_attention(int32_t n_seqs, const int32_t* cu, const int3
       // x = k s: the polynomial's coefficients in powers of k, where these are far
       // from the ends of float32 (else the polynomial is not used)
       const double r = (double)scale / cap, y = r * r, first = (double)P.scale_log2;
-      const bool fits = r >= 0x1p-15 && r <= 0x1p15;
-      P.cap_near = fits ? (float)(r / 0.4) : INFINITY;
+      const bool fits = r >= 0x1p-12 && r <= 0x1p12;
+      P.cap_near = fits ? (float)(r / 0.6) : INFINITY;
       P.cap_c[0] = (float)first;
-      P.cap_c[1] = fits ? (float)(first * y * -0.33331882259987955) : 0.0f;
-      P.cap_c[2] = fits ? (float)(first * y * y * 0.13277628990878212) : 0.0f;
-      P.cap_c[3] = fits ? (float)(first * y * y * y * -0.04779421895253378) : 0.0f;
+      const double c[4] = {-0.33332597509867323, 0.1331311669852155, -0.05221180873069635, 0.015612635835695849};
+      double power = first;
+      for (int i = 0; i < 4; ++i) P.cap_c[i + 1] = fits ? (float)(c[i] * (power *= y)) : 0.0f;
     }
     P.slopes = slopes;
     P.slope_unit = cap != 0.0f ? kLog2e : 1.0f / scale;

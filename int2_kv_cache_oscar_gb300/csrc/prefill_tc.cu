@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // 1024-byte alignment of the dynamic window (descriptors address 16-byte units)
   TcSmem& S = *reinterpret_cast<TcSmem*>(smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023));
   const int tid = threadIdx.x;
-  const int warp = tid >> 5, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int j = blockIdx.y;                 // KV head
   const int part = blockIdx.z;
   const int g_begin = (int)(((int64_t)part * p.ng) / p.n_parts);
@@ -345,11 +345,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp == 12) {
     // ============================================================ MMA issuer
-    // One thread issues every tcgen05.mma: the scores of half-step j + 1 as
+    // One lane issues every tcgen05.mma (see elect_one): the scores of half-step j + 1 as
     // soon as the rows have read those of j (one score buffer), the P.V of j
     // once they have written its P.  An issue blocks while the MMA queue is
-    // full, so this thread does nothing else.
-    if (lane == 0) {
+    // full, so this warp does nothing else.
+    {
       // every operand address is fixed: descriptors and TMEM columns are set
       // up once, and each half-step's MMAs are one unrolled sequence (an MMA
       // issue stalls this thread for its own latency, so nothing else sits
@@ -366,16 +366,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // window's B1 + B2 are H k_t 2^fw as fp16 hi + lo
       auto issue_scores = [&](int jj) {
         const int h = jj & 1;
-        if (!tc_wait_count(&S.kready, (uint32_t)jj, &S.abort_flag, p.err_word)) return false;
+        if (!__all_sync(0xffffffffu, tc_wait_count(&S.kready, (uint32_t)jj, &S.abort_flag, p.err_word))) return false;
         tfence_after();
         const uint64_t dk = h ? dK1 : dK0;
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          mma_ts(tS, tQ + 8 * ks, dk + (uint64_t)((2 * ks * kLboK) >> 4), idK, ks > 0);
-          mma_ss(tS, dQ + (uint64_t)((2 * ks * (kTcRows / 8) * 128) >> 4), dk + (uint64_t)((2 * ks * kLboK) >> 4), idK1,
-                 true);
+          for (int ks = 0; ks < 8; ++ks) {
+            mma_ts(tS, tQ + 8 * ks, dk + (uint64_t)((2 * ks * kLboK) >> 4), idK, ks > 0);
+            mma_ss(tS, dQ + (uint64_t)((2 * ks * (kTcRows / 8) * 128) >> 4), dk + (uint64_t)((2 * ks * kLboK) >> 4), idK1,
+                   true);
+          }
+          mma_commit(&S.sdone[h]);
         }
-        mma_commit(&S.sdone[h]);
+        __syncwarp();
         ++n_sd[h];
         return true;
       };
@@ -384,43 +387,47 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // (window: O += (Phi + Plo) V, bf16, N = 128)
       auto issue_pv = [&](int jj) {
         const int h = jj & 1;
-        if (!tc_wait_count(&S.vready, (uint32_t)jj, &S.abort_flag, p.err_word)) return false;
+        if (!__all_sync(0xffffffffu, tc_wait_count(&S.vready, (uint32_t)jj, &S.abort_flag, p.err_word))) return false;
         tfence_after();
         const uint32_t tP = tmem + p_col(jj & 1, 0, false);
         const uint64_t v1 = dV1 + (uint64_t)((8 * h * kLboV1) >> 4), v2 = dV2 + (uint64_t)((8 * h * kLboV) >> 4);
         const bool first = jj == 0;
-        if ((jj >> 1) == ng) {
+        const bool win = (jj >> 1) == ng;
+        if (elect_one()) {
+          if (win) {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            const uint32_t ah = tP + 32 * (ks >> 1) + 8 * (ks & 1);
-            const uint64_t ko = (uint64_t)((2 * ks * kLboV1) >> 4);
-            mma_ts(tO, ah, v1 + ko, idOW, !first || ks > 0);
-            mma_ts(tO, ah + 16, v1 + ko, idOW, true);
-          }
-        } else {
+            for (int ks = 0; ks < 4; ++ks) {
+              const uint32_t ah = tP + 32 * (ks >> 1) + 8 * (ks & 1);
+              const uint64_t ko = (uint64_t)((2 * ks * kLboV1) >> 4);
+              mma_ts(tO, ah, v1 + ko, idOW, !first || ks > 0);
+              mma_ts(tO, ah + 16, v1 + ko, idOW, true);
+            }
+          } else {
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            const uint32_t ah = tP + 32 * (ks >> 1) + 8 * (ks & 1);
-            const uint64_t ko1 = (uint64_t)((2 * ks * kLboV1) >> 4), ko2 = (uint64_t)((2 * ks * kLboV) >> 4);
-            mma_ts(tO, ah, v1 + ko1, idOZ, !first || ks > 0);
-            mma_ts(tO, ah + 16, v1 + ko1, idOZ, true);
-            mma_ts(tO, ah, v2 + ko2, idO, true);
+            for (int ks = 0; ks < 4; ++ks) {
+              const uint32_t ah = tP + 32 * (ks >> 1) + 8 * (ks & 1);
+              const uint64_t ko1 = (uint64_t)((2 * ks * kLboV1) >> 4), ko2 = (uint64_t)((2 * ks * kLboV) >> 4);
+              mma_ts(tO, ah, v1 + ko1, idOZ, !first || ks > 0);
+              mma_ts(tO, ah + 16, v1 + ko1, idOZ, true);
+              mma_ts(tO, ah, v2 + ko2, idO, true);
+            }
           }
+          mma_commit(&S.odone[h]);
         }
-        mma_commit(&S.odone[h]);
+        __syncwarp();
         ++n_od[h];
         return true;
       };
       bool ok = nh == 0 || issue_scores(0);
       for (int jj = 0; jj < nh && ok; ++jj) {
         if (jj + 1 < nh) {
-          ok = tc_wait_count(&S.sread, (uint32_t)(8 * jj + 7), &S.abort_flag, p.err_word);   // all 8 row warps
+          ok = __all_sync(0xffffffffu, tc_wait_count(&S.sread, (uint32_t)(8 * jj + 7), &S.abort_flag, p.err_word));   // all 8 row warps
           if (!ok) break;
           tfence_after();
           ok = issue_scores(jj + 1);
           if (!ok) break;
         }
-        ok = tc_wait_count(&S.pcount, (uint32_t)(8 * jj + 7), &S.abort_flag, p.err_word);
+        ok = __all_sync(0xffffffffu, tc_wait_count(&S.pcount, (uint32_t)(8 * jj + 7), &S.abort_flag, p.err_word));
         if (!ok) break;
         tfence_after();
         ok = issue_pv(jj);
@@ -762,21 +769,41 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if constexpr (RULE) {
         if (ok) {
           if (p.rule.cap != 0.0f) {
-            // (tokens past the window are -inf: they take no part in the choice)
-            float top = 0.0f;
+            float hi = fmaxf(w[0], w[1]), lo = fminf(w[0], w[1]);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) top = fmaxf(top, w[i] == -INFINITY ? 0.0f : fabsf(w[i]));
-            const bool small = __all_sync(0xffffffffu, top * p.rule.inv_cap <= kTanhNear);
+            for (int i = 2; i < 32; i += 2) {
+              asm("max.f32 %0, %0, %1, %2;" : "+f"(hi) : "f"(w[i]), "f"(w[i + 1]));
+              asm("min.f32 %0, %0, %1, %2;" : "+f"(lo) : "f"(w[i]), "f"(w[i + 1]));
+            }
+            // (tokens past the window are -inf: the long way then)
+            const bool near = __all_sync(0xffffffffu, fmaxf(hi, -lo) * p.rule.inv_cap <= kTanhNearBf16);
+            if (near) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 y = capped(make_float2(w[i], w[i + 1]), p.rule.cap, p.rule.inv_cap, small);
-              w[i] = y.x;
-              w[i + 1] = y.y;
+              for (int i = 0; i < 32; i += 2) {
+                const float2 y = capped_bf16(make_float2(w[i], w[i + 1]), p.rule, true);
+                w[i] = y.x;
+                w[i + 1] = y.y;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 y = capped_bf16(make_float2(w[i], w[i + 1]), p.rule, false);
+                w[i] = y.x;
+                w[i + 1] = y.y;
+              }
             }
           }
-          const float far = (float)(q_pos - (win ? p.ng : g_begin + k) * kGroup - c0);
+          if (p.rule.slopes != nullptr) {
+            const float far = (float)(q_pos - (win ? p.ng : g_begin + k) * kGroup - c0);
+            float2 d = make_float2(far, far - 1.0f);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) w[i] = fmaf(-slope2, far - (float)i, w[i]);
+            for (int i = 0; i < 32; i += 2) {
+              const float2 y = __ffma2_rn(make_float2(-slope2, -slope2), d, make_float2(w[i], w[i + 1]));
+              w[i] = y.x;
+              w[i + 1] = y.y;
+              d = __fadd2_rn(d, make_float2(-2.0f, -2.0f));
+            }
+          }
           if (win) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) w[i] = c0 + i < wlen ? w[i] : -INFINITY;
