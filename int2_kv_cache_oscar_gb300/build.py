@@ -22,7 +22,7 @@ CALLS = os.path.join(PKG, "_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]
 SOURCES = ["quantize.cu", "decode.cu", "prefill.cu", "prefill_tc.cu", "bf16_decode.cu", "rotary.cu", "read.cu",
-           "select.cu", "chunk.cu", "move.cu", "oscar_api.cu"]
+           "select.cu", "chunk.cu", "chunk_short.cu", "move.cu", "oscar_api.cu"]
 
 
 def _nvcc() -> str:

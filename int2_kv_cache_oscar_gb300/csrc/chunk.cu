@@ -819,10 +819,9 @@ cudaError_t launch_chunk_t(const ChunkParams<MAXS>& p, const CUtensorMap& tmk, c
 }  // namespace
 
 template <int MAXS>
-cudaError_t launch_chunk(ChunkParams<MAXS>& p, const uint16_t* k, int64_t k_token, int64_t k_head, int64_t tokens,
-                         int sms, cudaStream_t stream) {
+cudaError_t launch_chunk(ChunkParams<MAXS>& p, int64_t tokens, int sms, cudaStream_t stream) {
   CUtensorMap tmk, tmv;
-  if (!encode_chunk_map(&tmk, k, tokens, p.hkv, 2 * k_token, 2 * k_head) ||
+  if (!encode_chunk_map(&tmk, p.k, tokens, p.hkv, 2 * p.k_token, 2 * p.k_head) ||
       !encode_chunk_map(&tmv, p.v, tokens, p.hkv, 2 * p.v_token, 2 * p.v_head))
     return cudaErrorInvalidValue;
   // two row tiles a CTA share its key tiles; one each while that leaves SMs without work
@@ -867,9 +866,7 @@ cudaError_t launch_chunk(ChunkParams<MAXS>& p, const uint16_t* k, int64_t k_toke
               : launch_chunk_t<MAXS, false, false>(p, tmk, tmv, grid, stream);
 }
 
-template cudaError_t launch_chunk<kDecodeSeqsSmall>(ChunkParams<kDecodeSeqsSmall>&, const uint16_t*, int64_t, int64_t,
-                                                    int64_t, int, cudaStream_t);
-template cudaError_t launch_chunk<kDecodeSeqsLarge>(ChunkParams<kDecodeSeqsLarge>&, const uint16_t*, int64_t, int64_t,
-                                                    int64_t, int, cudaStream_t);
+template cudaError_t launch_chunk<kDecodeSeqsSmall>(ChunkParams<kDecodeSeqsSmall>&, int64_t, int, cudaStream_t);
+template cudaError_t launch_chunk<kDecodeSeqsLarge>(ChunkParams<kDecodeSeqsLarge>&, int64_t, int, cudaStream_t);
 
 }  // namespace oscar

@@ -205,6 +205,9 @@ struct ReadParams {
   int64_t n_tiles;
   void* k_out;         // rows of 128 channels, or NULL
   void* v_out;
+  int32_t late;        // 1: nothing of the kernel before this one is read or written over; it is
+                       // waited for at the end only (that kernel has waited for those before it)
+  int32_t reserved;
   int64_t row_pitch;   // elements from one row of an output to the next, and from
   int64_t head_pitch;  // one KV head to the next
   uint32_t spin_limit; // polls of a bounded wait; the test hook's `fault` (1) leaves
@@ -340,7 +343,7 @@ struct MoveParams {
   int32_t hkv;
   int32_t max_groups;
   int32_t block_bytes;
-  int32_t reserved;
+  int32_t passing;       // a copy writes more than the L2 cache keeps
   int64_t n_units;
   int64_t blocks_off;
   int64_t windows_off;
@@ -387,8 +390,10 @@ struct ChunkParams {
   const float* slopes; // [hq], or NULL
   float slope_unit;    // log2(e) with a cap (scores in log2 units), 1 / softmax_scale without (raw scores)
   const uint16_t* q;
+  const uint16_t* k;
   const uint16_t* v;
-  int64_t q_token, q_head, v_token, v_head;   // strides in elements
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;   // strides in elements
+  ScoreRule rule;              // as the kernel of short documents takes it
   const uint16_t* prior_out;   // [tokens, hq, 128], with prior_lse or both NULL
   const float* prior_lse;      // [tokens, hq]
   uint16_t* out;               // [tokens, hq, 128]
@@ -401,9 +406,12 @@ struct ChunkParams {
   uint32_t order[kOrder];
 };
 
+constexpr int kChunkShort = 32;    // tokens of a document that chunk_short.cu takes
+
 template <int MAXS>
-cudaError_t launch_chunk(ChunkParams<MAXS>& p, const uint16_t* k, int64_t k_token, int64_t k_head, int64_t tokens,
-                         int sms, cudaStream_t stream);
+cudaError_t launch_chunk(ChunkParams<MAXS>& p, int64_t tokens, int sms, cudaStream_t stream);
+template <int MAXS>
+cudaError_t launch_chunk_short(ChunkParams<MAXS>& p, cudaStream_t stream);
 
 int num_sms(int device);
 int decode_int2_ctas_per_sm();

@@ -132,8 +132,10 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
     fence_mbar_init();
   }
   __syncthreads();
-  grid_dependency_wait();
-  allow_dependents();
+  if (!p.late) {
+    grid_dependency_wait();
+    allow_dependents();
+  }
   uint32_t* err = reinterpret_cast<uint32_t*>(const_cast<uint8_t*>(arena));
 
   // requests the block of tile u (window tiles need none)
@@ -306,6 +308,10 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
     }
   }
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");   // the last rows are written
+  if (p.late) {
+    grid_dependency_wait();
+    allow_dependents();
+  }
 }
 
 template <int MAXS, bool M16, bool F32>

@@ -302,3 +302,75 @@ def test_refusals_on_the_device():
     O.oscar_chunk_attention([0, 20], q, k, v, ok)
     torch.cuda.synchronize()
     assert torch.equal(ok.cuda(), call(O, [20], q, k, v)[0])
+
+
+# ---- documents of at most 32 tokens have a kernel of their own
+
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (30.0, True), (1.0, False)])
+@pytest.mark.parametrize("gqa", [1, 4, 5, 16, 33])
+@pytest.mark.parametrize("prior", [False, True])
+def test_short_documents(gqa, cap, bias, prior):
+    O = U.lib()
+    lens = [5, 32, 1, 0, 17, 8, 9, 16, 31, 24]
+    prefix = [0, 32, 1, 0, 16, 3, 9, 15, 0, 20]
+    q, k, v, p = inputs(lens, 3, gqa, seed=40 + gqa, extra=2, layout="fused", prior=prior)
+    slopes = slopes_of(3 * gqa) if bias else None
+    compare(lens, q, k, v, *call(O, lens, q, k, v, p, cap=cap, slopes=slopes), prior=p, cap=cap, slopes=slopes)
+    compare(lens, q, k, v, *call(O, lens, q, k, v, p, prefix=prefix, cap=cap, slopes=slopes), prior=p, prefix=prefix,
+            cap=cap, slopes=slopes)
+
+
+def test_short_documents_beside_a_longer_one():
+    """The longest document chooses the kernel: the same rows either way, within both bounds."""
+    O = U.lib()
+    lens = [5, 20, 32]
+    q, k, v, _ = inputs(lens + [40], 2, 4, seed=60)
+    compare(lens, q[:57], k[:57], v[:57], *call(O, lens, q[:57], k[:57], v[:57]))
+    compare(lens + [40], q, k, v, *call(O, lens + [40], q, k, v))
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf"), 3.0e38])
+def test_short_hidden_tokens_have_no_part(value):
+    O = U.lib()
+    lens = [11, 6, 32]
+    q, k, v, _ = inputs(lens, 2, 4, seed=61, extra=9)
+    clean = call(O, lens, q, k, v)
+    for rows in (slice(49, 58), slice(11, 17), slice(5, 11), slice(30, 49)):
+        k2, v2 = k.clone(), v.clone()
+        k2[rows] = value
+        v2[rows] = value
+        out, lse = call(O, lens, q, k2, v2)
+        keep = torch.ones(49, dtype=torch.bool)
+        keep[rows] = False
+        # (the rows of a document with such a token are summed in another order)
+        assert (out[:49][keep].float() - clean[0][:49][keep].float()).abs().max() <= 2.0 ** -7 * 4
+        assert torch.equal(lse[:49][keep], clean[1][:49][keep])
+
+
+@pytest.mark.parametrize("where", [0, 7, 8, 31])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_short_visible_values_that_are_not_finite(where, value):
+    O = U.lib()
+    lens = [32, 3]
+    q, k, v, _ = inputs(lens, 2, 3, seed=62)
+    v[where, 1, 7] = value
+    out, lse = call(O, lens, q, k, v)
+    compare(lens, q, k, v, out, lse)
+    assert torch.isfinite(out[:, :3].float()).all() and torch.isfinite(out[:where].float()).all()
+
+
+def test_short_merge_in_place_captured():
+    O = U.lib()
+    lens = [5] * 8
+    q, k, v, p = inputs(lens, 2, 4, seed=63, prior=True)
+    want = call(O, lens, q, k, v, p)
+    keep = p[0].clone(), p[1].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        O.oscar_chunk_attention(cumulative(lens), q, k, v, p[0], p[1], prior_out=p[0], prior_lse=p[1])
+    for _ in range(2):
+        p[0].copy_(keep[0])
+        p[1].copy_(keep[1])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(p[0], want[0]) and torch.equal(p[1], want[1])
