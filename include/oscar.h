@@ -683,7 +683,9 @@ oscar_status oscar_cache_window_offset(const oscar_cache* cache, int32_t seq, in
  * oscar_scored_decode_attention, oscar_append_decode, oscar_sparse_decode_attention, oscar_cache_read,
  * oscar_select_groups) has one bulk copy of its first CTA left unissued, and its bounded waits give up after 2^14 polls
  * instead of 2^24.  (A listed decode of sequences without a group: the window
- * copies of its combine, where it has any.)  The consumer waiting for that copy then
+ * copies of its combine, where it has any.  oscar_chunk_attention, documents of
+ * more than 32 tokens: one tile copy of its first CTA; it has no arena to set a
+ * flag in, the rows of that CTA are NaN.)  The consumer waiting for that copy then
  * gives up, the kernel sets the arena's error flag, skips its remaining work
  * and returns (no fault, no hang; the results of that call are undefined),
  * and oscar_cache_check reports OSCAR_ERR_DEVICE_TIMEOUT.  Later calls are

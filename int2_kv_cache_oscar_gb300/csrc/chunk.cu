@@ -120,6 +120,7 @@ struct ChunkSmem {
   uint32_t issued[kChSlots];  // uses of each slot requested so far
   uint32_t tmem_base;
   int abort_flag;
+  int stopped;                // first piece of the CTA that a wait which gave up left out
 };
 static_assert(sizeof(ChunkSmem) + 1024 <= 232448, "one CTA per SM");
 
@@ -244,6 +245,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
     const bool val = n == 2 * steps - 1 || (n > 0 && (n & 1) == 0);
     const int j = n == 2 * steps - 1 ? steps - 1 : val ? (n - 2) / 2 : (n + 1) / 2;
     const CUtensorMap* m = val ? &tmv : &tmk;
+    if (p.fault && blockIdx.x == 0 && use == 1) return;     // (failure-path test)
     mbar_arrive_expect_tx(&S.full[s], kTileBytes);
     tma_load_3d(S.ring[s], m, 0, T.head, T.row0 + j * kChKeys, &S.full[s]);
     tma_load_3d(S.ring[s] + kBox, m, 64, T.head, T.row0 + j * kChKeys, &S.full[s]);
@@ -282,6 +284,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
     for (int i = 0; i < 4; ++i) mbar_init(&S.v_clean[i], 2);
     mbar_init(&S.drained, 1);
     S.abort_flag = 0;
+    S.stopped = INT32_MAX;
     fence_mbar_init();
     // the first loads, for which no slot has to be waited
     grid_dependency_wait();
@@ -308,10 +311,15 @@ __global__ void __launch_bounds__(kChThreads, 1)
   tfence_after();
   const uint32_t tmem = S.tmem_base;
 
+  // the number of the CTA's k-th piece (-1: no more)
+  auto piece_of = [&](int k) {
+    const unsigned G = gridDim.x, b = blockIdx.x, w = (unsigned)k * G + ((k & 1) ? G - 1 - b : b);
+    return w < (unsigned)p.pieces ? (int)w : -1;
+  };
   // The CTA's k-th piece (its `there` is 0 behind the last one, or when a wait
   // gave up); every reading warp takes and releases each piece once.
   auto take = [&](int k) {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.w_full[k & 1], (k >> 1) & 1, &S.abort_flag, nullptr));
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.w_full[k & 1], (k >> 1) & 1, &S.abort_flag, nullptr, p.spin_limit));
     ChunkTile T = S.work[k & 1];
     if (!ok) T.there = 0;
     return T;
@@ -326,7 +334,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
     if (warp == 8) {
       // ---------------------------------------------------------- MMA issuer
       const uint64_t dq[2] = {desc128(smem_u32(S.q[0]), 16, 1024), desc128(smem_u32(S.q[1]), 16, 1024)};
-      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, &S.abort_flag, nullptr); };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait_bounded(bar, parity, &S.abort_flag, nullptr, p.spin_limit); };
       auto slot_full = [&](uint32_t use) { return wait(&S.full[use % kChSlots], (use / kChSlots) & 1); };
       // after the waits for what the next products read: the warp goes on together
       auto go_on = [&](bool ok) {
@@ -416,7 +424,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       if (S.abort_flag) {
         // gave up: what has been issued completes before TMEM is freed (bounded)
         if (elect_one()) mma_commit(&S.drained);
-        for (uint32_t n = 0; n < kSpinLimit; ++n)
+        for (uint32_t n = 0; n < p.spin_limit; ++n)
           if (mbar_try_wait(&S.drained, 0)) break;
       }
     } else if (warp == 9 && lane == 0) {
@@ -428,20 +436,19 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const int steps = max(T.steps[0], T.steps[1]);
         for (; n < 2 * steps; ++n, ++loaded) {
           ok = loaded < kChSlots ||
-               mbar_wait_bounded(&S.empty[loaded % kChSlots], ((loaded / kChSlots) - 1) & 1, &S.abort_flag, nullptr);
+               mbar_wait_bounded(&S.empty[loaded % kChSlots], ((loaded / kChSlots) - 1) & 1, &S.abort_flag, nullptr, p.spin_limit);
           if (!ok) break;
           load(T, steps, n, loaded);
         }
         n = 0;
         if (!ok || !T.there) break;
-        const unsigned G = gridDim.x, b = blockIdx.x;
-        const unsigned w = (unsigned)k * G + ((k & 1) ? G - 1 - b : b);
-        if (w < (unsigned)p.pieces) {
-          T = locate(p, (int)w);
+        const int w = piece_of(k);
+        if (w >= 0) {
+          T = locate(p, w);
         } else {
           T.there = T.steps[0] = T.steps[1] = 0;
         }
-        if (k >= 2) ok = mbar_wait_bounded(&S.w_empty[k & 1], ((k >> 1) - 1) & 1, &S.abort_flag, nullptr);
+        if (k >= 2) ok = mbar_wait_bounded(&S.w_empty[k & 1], ((k >> 1) - 1) & 1, &S.abort_flag, nullptr, p.spin_limit);
         if (!ok) break;
         S.work[k & 1] = T;
         mbar_arrive(&S.w_full[k & 1]);
@@ -449,7 +456,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       if (S.abort_flag) {
         // gave up: the copies in flight get their time (bounded)
         for (uint32_t x = loaded > kChSlots ? loaded - kChSlots : 0; x < loaded; ++x)
-          for (uint32_t i = 0; i < kSpinLimit; ++i)
+          for (uint32_t i = 0; i < p.spin_limit; ++i)
             if (mbar_try_wait(&S.full[x % kChSlots], (x / kChSlots) & 1)) break;
       }
     } else if (warp >= 10) {
@@ -466,8 +473,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
           const uint32_t vn = base + value_pos(j, steps);
           const int vs = vn % kChSlots;
           // (these warps do not follow a slot's earlier uses: its phase is waited for once it exists)
-          ok = wait_issued(&S.issued[vs], vn / kChSlots, &S.abort_flag, nullptr) &&
-               mbar_wait_bounded(&S.full[vs], (vn / kChSlots) & 1, &S.abort_flag, nullptr);
+          ok = wait_issued(&S.issued[vs], vn / kChSlots, &S.abort_flag, nullptr, p.spin_limit) &&
+               mbar_wait_bounded(&S.full[vs], (vn / kChSlots) & 1, &S.abort_flag, nullptr, p.spin_limit);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           bool cleared = false;
@@ -540,7 +547,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       float m = -INFINITY, l = 0.0f;     // running maximum (before sl) and sum
       uint32_t hj = hid;
       for (int j = 0; j < my_steps; ++j, ++step) {
-        ok = ok && mbar_wait_bounded(&S.s_full[i], step & 1, &S.abort_flag, nullptr);
+        ok = ok && mbar_wait_bounded(&S.s_full[i], step & 1, &S.abort_flag, nullptr, p.spin_limit);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tfence_after();
@@ -661,7 +668,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         tst_wait();
         if (j >= plain) {
           // hidden keys in this step: values that had to be cleared are added here
-          ok = mbar_wait_bounded(&S.v_clean[hj & 3], (hj >> 2) & 1, &S.abort_flag, nullptr);
+          ok = mbar_wait_bounded(&S.v_clean[hj & 3], (hj >> 2) & 1, &S.abort_flag, nullptr, p.spin_limit);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const uint32_t* bad = S.bad[hj & 3];
@@ -714,7 +721,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
         };
         if (merge) load_prior(0);
         if (ok) {
-          ok = mbar_wait_bounded(&S.o_done[i], done & 1, &S.abort_flag, nullptr);
+          ok = mbar_wait_bounded(&S.o_done[i], done & 1, &S.abort_flag, nullptr, p.spin_limit);
           ok = __all_sync(0xffffffffu, ok);
           tfence_after();
         }
@@ -772,10 +779,28 @@ __global__ void __launch_bounds__(kChThreads, 1)
         tfence_before();
         if (lane < rows && p.lse != nullptr) p.lse[orow] = lse;
       }
-      if (!more || !ok) break;
+      if (!more || !ok) {
+        if (S.abort_flag && lane == 0) atomicMin(&S.stopped, k + 1);
+        break;
+      }
       if (queries) queries_loaded();
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    named_bar_sync(1, 256);
+    if (S.abort_flag) {
+      // gave up: the rows of the pieces that were not begun (the others' are written)
+      for (int k = S.stopped; k < INT32_MAX && piece_of(k) >= 0; ++k) {
+        const ChunkTile T = locate(p, piece_of(k));
+        const int rows = min(p.cta_rows, T.rows - T.first_row);
+        for (int x = tid; x < 16 * rows; x += 256) {
+          const int row = T.first_row + x / 16, tok = row / p.gqa;
+          const int64_t at = (int64_t)(T.row0 + tok) * p.hq + T.head * p.gqa + row - tok * p.gqa;
+          const uint32_t nan2 = 0x7fc07fc0u;
+          *reinterpret_cast<uint4*>(p.out + at * kHeadDim + 8 * (x % 16)) = make_uint4(nan2, nan2, nan2, nan2);
+          if (x % 16 == 0 && p.lse != nullptr) p.lse[at] = NAN;
+        }
+      }
+    }
   }
 
   tfence_before();
@@ -799,6 +824,8 @@ bool encode_chunk_map(CUtensorMap* map, const void* base, uint64_t tokens, uint6
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+static_assert(sizeof(ChunkParams<kDecodeSeqsLarge>) + 2 * sizeof(CUtensorMap) + 64 <= 32764, "kernel parameter limit");
 
 template <int MAXS, bool CAP, bool BIAS>
 cudaError_t launch_chunk_t(const ChunkParams<MAXS>& p, const CUtensorMap& tmk, const CUtensorMap& tmv, unsigned grid,

@@ -1661,6 +1661,9 @@ oscar_status oscar_chunk_attention(int32_t n_seqs, const int32_t* cu, const int3
     P.hkv = hkv;
     P.gqa = gqa;
     P.hq = hq;
+    // (the kernel of short documents waits for nothing)
+    P.fault = seqs[0].len > kChunkShort && take_armed_timeout() ? 1 : 0;
+    P.spin_limit = P.fault ? kArmedSpinLimit : kSpinLimit;
     const float scale = scale_of(softmax_scale), cap = rule ? rule->cap : 0.0f;
     P.scale_log2 = scale * kLog2e;
     if (cap != 0.0f) {

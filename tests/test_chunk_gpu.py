@@ -374,3 +374,20 @@ def test_short_merge_in_place_captured():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(p[0], want[0]) and torch.equal(p[1], want[1])
+
+
+@pytest.mark.parametrize("lens", [[33], [700, 300], [5000], [64] * 500])
+def test_a_wait_that_gives_up(lens):
+    """One copy of the first CTA left out: the call ends, rows that were not computed are NaN, the others are right,
+    and the next call is unaffected."""
+    O = U.lib()
+    q, k, v, _ = inputs(lens, 2, 4, seed=70)
+    want = call(O, lens, q, k, v)
+    O.oscar_test_arm_wait_timeout()
+    out, lse = call(O, lens, q, k, v)
+    gone = torch.isnan(lse)
+    assert gone.any() and torch.equal(gone, torch.isnan(out.float()).all(-1))
+    assert torch.equal(gone, torch.isnan(out.float()).any(-1))
+    assert torch.equal(out[~gone], want[0][~gone]) and torch.equal(lse[~gone], want[1][~gone])
+    again = call(O, lens, q, k, v)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
