@@ -16,6 +16,8 @@ constexpr int kPfMergeWarps = 8;
 
 __global__ void __launch_bounds__(kPfMergeWarps * 32)
     prefill_merge_kernel(const __grid_constant__ PrefillParams p) {
+  grid_dependency_wait();
+  allow_dependents();
   const int lane = threadIdx.x & 31;
   const int64_t gw = (int64_t)blockIdx.x * kPfMergeWarps + (threadIdx.x >> 5);   // KV head * rows + row
   if (gw >= (int64_t)p.hkv * p.rows) return;
@@ -54,8 +56,8 @@ cudaError_t launch_prefill_t(const PrefillParams& p, const uint8_t* arena, cudaS
   cudaError_t e = launch_prefill_tc(p, arena, M16, stream);
   if (e != cudaSuccess || p.n_parts <= 1) return e;
   const int64_t warps = (int64_t)p.hkv * p.rows;
-  prefill_merge_kernel<<<(unsigned)((warps + kPfMergeWarps - 1) / kPfMergeWarps), kPfMergeWarps * 32, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(prefill_merge_kernel, dim3((unsigned)((warps + kPfMergeWarps - 1) / kPfMergeWarps)),
+                          dim3(kPfMergeWarps * 32), 0, stream, 1, p);
 }
 }  // namespace
 

@@ -71,6 +71,10 @@ constexpr uint32_t kTO = 336;      // output accumulator [336, 464), then the va
 constexpr uint32_t kTZ = kTO + kHeadDim;
 constexpr uint32_t kTCols = 512;
 constexpr float kRescaleLog2 = 8.0f;
+// Floats of a staged query row: a thread reads its row 16 bytes at a time, and
+// rows 16 bytes apart in the banks keep a quarter warp's reads apart (512
+// queries over 32K tokens 872 -> 861 us, 77 over 9,999 67.0 -> 64).
+constexpr int kQPitch = kHeadDim + 4;
 
 // TMEM column of the P pairs of k-step ks of a half (tokens 16 ks .. + 15)
 // in P buffer pb, hi or lo: each 32-token chunk c becomes [hi of its two
@@ -107,7 +111,7 @@ struct TcSmem {
 };
 static_assert(sizeof(TcSmem) + 1024 <= 232448, "one CTA per SM");
 static_assert(offsetof(TcSmem, stage) % 128 == 0 && offsetof(TcSmem, full) % 8 == 0, "alignment");
-static_assert(offsetof(TcSmem, v2) == offsetof(TcSmem, v1) + kV1Bytes && kV1Bytes + kVBytes >= kTcRows * kHeadDim * 4,
+static_assert(offsetof(TcSmem, v2) == offsetof(TcSmem, v1) + kV1Bytes && kV1Bytes + kVBytes >= kTcRows * kQPitch * 4,
               "q staging fits in the value buffers");
 
 __device__ __forceinline__ float tc_pow2(int e) {
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   // ---- q rows: rotate (warp-cooperative FWHT, lanes = 4 channels) into the
   // staging area, then each row thread stores its row into TMEM
-  float* qst = reinterpret_cast<float*>(S.v1);                    // [128][128] rotated q * 2^F (v1, v2)
+  float* qst = reinterpret_cast<float*>(S.v1);                    // [128][kQPitch] rotated q * 2^F (v1, v2)
   for (int r = warp; r < kTcRows; r += kTcThreads / 32) {
     const int row = blockIdx.x * kTcRows + r;
     uint2 raw = make_uint2(0u, 0u);
@@ -309,7 +313,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       F = 15 - e;
     }
     const float f = tc_pow2(F);
-    *reinterpret_cast<float4*>(qst + r * kHeadDim + 4 * lane) = make_float4(qv[0] * f, qv[1] * f, qv[2] * f, qv[3] * f);
+    *reinterpret_cast<float4*>(qst + r * kQPitch + 4 * lane) = make_float4(qv[0] * f, qv[1] * f, qv[2] * f, qv[3] * f);
     if (lane == 0) S.fexp[r] = tc_pow2(-(F + 2)) * p.scale_log2;
   }
   tfence_before();
@@ -328,9 +332,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int i = 0; i < 32; i += 4) {
         uint32_t lo[4];   // channels 2 (c0 + i) .. + 7: one 16-byte row of a core matrix
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x0 = qst[r * kHeadDim + 2 * (c0 + i + e)], x1 = qst[r * kHeadDim + 2 * (c0 + i + e) + 1];
-          split2(x0, x1, false, hi[i + e], lo[e]);
+        for (int e = 0; e < 4; e += 2) {
+          const float4 x = *reinterpret_cast<const float4*>(qst + r * kQPitch + 2 * (c0 + i + e));
+          split2(x.x, x.y, false, hi[i + e], lo[e]);
+          split2(x.z, x.w, false, hi[i + e + 1], lo[e + 1]);
         }
         *reinterpret_cast<uint4*>(S.qlo + canon(r, 2 * (c0 + i), kTcRows)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
