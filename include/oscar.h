@@ -623,7 +623,7 @@ typedef struct oscar_rows {
  *   out           bf16 [rows, num_q_heads, 128], 16-byte aligned; must not overlap
  *                 q, k or v
  *   lse           float32 [rows, num_q_heads] or NULL: natural log-sum-exp of the
- *                 merged row
+ *                 merged row; overlaps nothing but an equal prior_lse
  *   prior_out, prior_lse, out and lse: device or page-locked host memory
  *   softmax_scale 0 means 1 / sqrt(128); with slopes at least 2^-60
  * Keys and values that a token does not see have no part in its row, whatever

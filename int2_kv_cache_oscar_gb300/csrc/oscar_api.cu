@@ -1644,9 +1644,16 @@ oscar_status oscar_chunk_attention(int32_t n_seqs, const int32_t* cu, const int3
     const int64_t bytes = tokens * hq * kHeadDim * 2;
     if (overlap(out, bytes, q->data, eq) || overlap(out, bytes, k->data, ek) || overlap(out, bytes, v->data, ev))
       return fail(OSCAR_ERR_INVALID_ARG, "out overlaps q, k or v");
+    const int64_t lse_bytes = tokens * hq * 4;
+    if (lse && (overlap(lse, lse_bytes, q->data, eq) || overlap(lse, lse_bytes, k->data, ek) ||
+                overlap(lse, lse_bytes, v->data, ev) || overlap(lse, lse_bytes, out, bytes) ||
+                (prior_out && overlap(lse, lse_bytes, prior_out, bytes))))
+      return fail(OSCAR_ERR_INVALID_ARG, "lse overlaps q, k, v, out or prior_out");
+    if (prior_lse && overlap(out, bytes, prior_lse, lse_bytes))
+      return fail(OSCAR_ERR_INVALID_ARG, "out overlaps prior_lse");
     if (prior_out && prior_out != out && overlap(out, bytes, prior_out, bytes))
       return fail(OSCAR_ERR_INVALID_ARG, "out and prior_out overlap without being the same");
-    if (prior_lse && lse && prior_lse != lse && overlap(lse, tokens * hq * 4, prior_lse, tokens * hq * 4))
+    if (prior_lse && lse && prior_lse != lse && overlap(lse, lse_bytes, prior_lse, lse_bytes))
       return fail(OSCAR_ERR_INVALID_ARG, "lse and prior_lse overlap without being the same");
     ScoreRule how;
     if ((s = cache_rule(rule, dev, &how)) != OSCAR_OK) return s;

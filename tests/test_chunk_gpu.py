@@ -304,6 +304,27 @@ def test_refusals_on_the_device():
     assert torch.equal(ok.cuda(), call(O, [20], q, k, v)[0])
 
 
+@pytest.mark.parametrize("n", [20, 40])
+def test_overlapping_buffers_are_refused(n):
+    O = U.lib()
+    q, k, v, p = inputs([n], 2, 4, seed=18, prior=True)
+    out = torch.full_like(q, 7.0)
+
+    def refused(**kw):
+        with pytest.raises(O.OscarError, match="overlap"):
+            O.oscar_chunk_attention(**{**dict(cu_seqlens=[0, n], q=q, k=k, v=v, out=out), **kw})
+
+    inside = lambda t: t.view(-1).view(torch.float32)[:n * 8].view(n, 8)  # noqa: E731
+    for t in (q, k, v, out):
+        refused(lse=inside(t))
+    refused(prior_out=p[0], prior_lse=p[1], lse=inside(p[0]))
+    refused(prior_out=p[0], prior_lse=inside(out))
+    both = torch.empty((n + 1, 8), device="cuda")
+    refused(prior_out=p[0], prior_lse=both[1:], lse=both[:n])
+    torch.cuda.synchronize()
+    assert torch.all(out == 7.0)
+
+
 # ---- documents of at most 32 tokens have a kernel of their own
 
 @pytest.mark.parametrize("cap,bias", [(0.0, False), (30.0, True), (1.0, False)])
