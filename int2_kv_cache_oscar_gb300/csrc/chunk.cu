@@ -10,8 +10,8 @@
 // key tile, and a causal tile's diagonal is 128 / gqa tokens wide) against the
 // document's keys, 128 at a time.  A CTA an SM takes pieces from the list of all,
 // the longest first, in rounds of alternating direction (piece k of CTA b of G: k G
-// + b, or (k + 1) G - 1 - b): set-up is paid once, and the loads of the next piece
-// run during the end of this one.  12 warps:
+// + b, or (k + 1) G - 1 - b): set-up is paid once, and the loads and first scores
+// of the next piece run while this one's rows are written.  12 warps:
 //   * warps 0-3 and 4-7: softmax of the two row tiles, thread = row.  Scores
 //     are read from TMEM once, kept in registers, and P (bf16) is written back
 //     over them as the A operand of P.V.  The output accumulator stays in TMEM
@@ -21,7 +21,10 @@
 //   * warp 8 issues every tcgen05.mma.  S = Q K^T and O += P V of the two tiles
 //     alternate, so that one tile's products run while the other tile's softmax does;
 //   * warp 9: one thread loads key and value tiles by TMA (128-byte swizzle) into a
-//     ring of four 32 KB slots, and describes the pieces of work to the others;
+//     ring of four 32 KB slots, and describes the pieces of work to the others.
+//     Queries come by TMA too where 128 rows are whole tokens (gqa divides 128),
+//     requested by the softmax warps once the last scores of a piece are there,
+//     else by 16-byte copies (64 documents of 128 tokens 42 against 47 us);
 //   * warps 10, 11: look through the value rows of tiles with hidden keys.  A
 //     hidden key has p = 0, but 0 times an infinite or NaN value would still
 //     spoil every row of the tile: such value rows are cleared in shared
@@ -30,10 +33,13 @@
 // documents; launch and pipeline latency for short ones.  A step of 128 keys takes
 // 2,980 cycles for two tiles, 2,048 of them products: a tile's chain is 1,500 cycles
 // of softmax, then the second half of its P.V and the next scores (768), and the way
-// from one to the other and back (700).  Tried and slower: a second warpgroup a tile
-// for half of the keys (533 against 374 us, 8,192 tokens of 32 heads: 104 registers a
-// thread do not hold a half), pieces handed out by cluster launch control (407 us),
-// a piece a CTA (379 us, and 78 against 57 for 64 documents of 128 tokens).
+// from one to the other and back (700): 8,192 tokens of 32 heads take 366 us, 1,500
+// TFLOP/s.  A piece of a single step takes 9,000 cycles, most of them the softmax
+// warps' own: 3,000 of softmax with a mask, 4,000 of output rows on their way out
+// (64 bytes of a row at a time: 32 or 128 of them 2 to 6 % slower).  Tried when the
+// former took 374 us, and slower: a second warpgroup a tile for half of the keys (533
+// us: 104 registers a thread do not hold a half), pieces handed out by cluster launch
+// control (407 us), a piece a CTA (379 us, and 78 against 57 for the 64 documents).
 // P is rounded to bf16 (the type of V: the tensor cores take both operands of a
 // product in one type), relative 2^-8 a weight; row sums are of the float32
 // weights, scores and outputs accumulate in float32.
@@ -54,7 +60,7 @@ constexpr int kChKeys = 128;                  // keys of a step (N)
 constexpr int kChThreads = 12 * 32;
 constexpr int kChSlots = 4;
 constexpr int kWorkReaders = 11;              // warps that read a piece: issuer, two that look through values, softmax
-constexpr int kStageRow = 32;                // bytes of a row that pass through shared memory at a time
+constexpr int kStageRow = 64;                // bytes of a row that pass through shared memory at a time
 constexpr int kBox = 64 * 2 * 128;            // 128 rows of 64 channels
 constexpr int kTileBytes = 2 * kBox;
 // TMEM columns of tile i: scores (then P in the first 64), output accumulator
@@ -234,7 +240,7 @@ __device__ __forceinline__ void copy16_async(void* dst, const void* src) {
 template <int MAXS, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kChThreads, 1)
     chunk_kernel(const __grid_constant__ ChunkParams<MAXS> p, const __grid_constant__ CUtensorMap tmk,
-                 const __grid_constant__ CUtensorMap tmv) {
+                 const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmq) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   ChunkSmem& S = *reinterpret_cast<ChunkSmem*>(smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023));
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
@@ -265,6 +271,15 @@ __global__ void __launch_bounds__(kChThreads, 1)
       copy16_async(S.q[i] + tile_off(wr + r16 + 2 * x, c16), p.q + __shfl_sync(0xffffffffu, off, r16 + 2 * x) + 8 * c16);
   };
 
+  // The same of a whole tile by one thread, where a tile is whole tokens (rows of
+  // tokens behind the document's are loaded as they are, or as 0 behind the last).
+  auto load_tile = [&](const ChunkTile& T, int i) {
+    const int tok = T.row0 + (T.first_row + i * kChRows) / p.gqa;
+    mbar_arrive_expect_tx(&S.q_ready[i], kTileBytes);
+    tma_load_3d(S.q[i], &tmq, 0, T.head * p.gqa, tok, &S.q_ready[i]);
+    tma_load_3d(S.q[i] + kBox, &tmq, 64, T.head * p.gqa, tok, &S.q_ready[i]);
+  };
+
   uint32_t loaded = 0;     // ring uses issued so far (warp 9, lane 0)
   if (warp == 9 && lane == 0) {
     for (int i = 0; i < kChSlots; ++i) {
@@ -277,7 +292,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
       mbar_init(&S.p_ready[i][0], 4);
       mbar_init(&S.p_ready[i][1], 4);
       mbar_init(&S.o_done[i], 1);
-      mbar_init(&S.q_ready[i], 4);
+      mbar_init(&S.q_ready[i], p.whole_tokens ? 1 : 4);
       mbar_init(&S.w_full[i], 1);
       mbar_init(&S.w_empty[i], kWorkReaders);
     }
@@ -292,6 +307,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
     const int steps = max(T.steps[0], T.steps[1]);
     S.work[0] = T;
     mbar_arrive(&S.w_full[0]);
+    for (int i = 0; i < 2; ++i)
+      if (p.whole_tokens && T.steps[i] > 0) load_tile(T, i);
     for (; (int)loaded < min(kChSlots, 2 * steps); ++loaded) load(T, steps, (int)loaded, loaded);
   }
   if (warp == 8) {
@@ -302,7 +319,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
   }
   grid_dependency_wait();
   allow_dependents();
-  if (warp < 8) {
+  if (warp < 8 && !p.whole_tokens) {
     const ChunkTile T = locate(p, (int)blockIdx.x);
     if ((i ? T.steps[1] : T.steps[0]) > 0) load_queries(T);
   }
@@ -524,26 +541,41 @@ __global__ void __launch_bounds__(kChThreads, 1)
 
     bool ok = true;
     uint32_t step = 0, hid = 0, done = 0;     // steps of this tile place, steps with hidden keys, tiles
+    uint32_t tiles = 0;                       // whose queries have been requested
     {
       const ChunkTile T = S.work[0];
-      if ((i ? T.steps[1] : T.steps[0]) > 0) queries_loaded();
+      tiles = (i ? T.steps[1] : T.steps[0]) > 0;
+      if (tiles > 0 && !p.whole_tokens) queries_loaded();
+    }
+    // what the lane's row needs of a piece
+    struct Row {
+      int steps, plain_steps, plain;       // of this tile; steps before `plain` hide no key from any row of the piece
+      int tok, limit;                      // visible keys: [0, limit)
+      uint32_t at;                         // the row in the outputs
+      float slope;
+    };
+    auto row_of = [&](const ChunkTile& T) {
+      Row r;
+      r.steps = i ? T.steps[1] : T.steps[0];
+      r.plain_steps = i ? T.plain[1] : T.plain[0];
+      r.plain = min(T.plain[0], T.plain[1]);
+      const int row = min(T.first_row + i * kChRows + wr + lane, T.rows - 1);
+      r.tok = row / p.gqa;
+      r.limit = min(max(r.tok + 1, T.prefix), T.len);
+      r.at = (uint32_t)(T.row0 + r.tok) * p.hq + T.head * p.gqa + row - r.tok * p.gqa;
+      r.slope = 0.0f;
+      if constexpr (BIAS) r.slope = p.slopes[T.head * p.gqa + row - r.tok * p.gqa] * p.slope_unit;
+      return r;
+    };
+    Row next;
+    {
+      const ChunkTile T = take(0);
+      next = row_of(T);
     }
     for (int k = 0;; ++k) {
-      // (the piece is read anew where it is needed: its registers would be missed in the steps)
-      int limit, my_steps, my_plain, plain, tok0;
-      uint32_t orow;                       // the lane's row of the outputs
-      float slope2 = 0.0f;
-      {
-        const ChunkTile T = take(k);
-        my_steps = i ? T.steps[1] : T.steps[0];
-        my_plain = i ? T.plain[1] : T.plain[0];
-        plain = min(T.plain[0], T.plain[1]);      // steps before this one hide no key from any row
-        const int row = min(T.first_row + i * kChRows + wr + lane, T.rows - 1);
-        tok0 = row / p.gqa;
-        limit = min(max(tok0 + 1, T.prefix), T.len);     // visible keys: [0, limit)
-        orow = (uint32_t)(T.row0 + tok0) * p.hq + T.head * p.gqa + row - tok0 * p.gqa;
-        if constexpr (BIAS) slope2 = p.slopes[T.head * p.gqa + row - tok0 * p.gqa] * p.slope_unit;
-      }
+      const int my_steps = next.steps, my_plain = next.plain_steps, plain = next.plain, tok0 = next.tok, limit = next.limit;
+      const uint32_t orow = next.at;
+      const float slope2 = next.slope;
       float m = -INFINITY, l = 0.0f;     // running maximum (before sl) and sum
       uint32_t hj = hid;
       for (int j = 0; j < my_steps; ++j, ++step) {
@@ -605,8 +637,13 @@ __global__ void __launch_bounds__(kChThreads, 1)
           }
           if (j >= my_plain) {
             const int vis = limit - j * kChKeys;
+            // (a bit a key: tested in fewer instructions than a comparison each)
 #pragma unroll
-            for (int c = 0; c < kChKeys; ++c) s[c] = c < vis ? s[c] : -INFINITY;
+            for (int c = 0; c < kChKeys; c += 32) {
+              const uint32_t seen = vis >= c + 32 ? 0xffffffffu : vis <= c ? 0u : (1u << (vis - c)) - 1u;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) s[c + e] = (seen >> e) & 1u ? s[c + e] : -INFINITY;
+            }
           }
           if (BIAS || !CAP || j >= my_plain) {
             float mx[4] = {s[0], s[1], s[2], s[3]};
@@ -698,26 +735,36 @@ __global__ void __launch_bounds__(kChThreads, 1)
         const ChunkTile N = take(k + 1);
         more = N.there != 0;
         queries = more && (i ? N.steps[1] : N.steps[0]) > 0;
-        if (queries && ok) load_queries(N);
+        if (more) next = row_of(N);
+        if (queries && ok) {
+          ++tiles;
+          if (!p.whole_tokens) load_queries(N);
+          else if ((warp & 3) == 0 && lane == 0) load_tile(N, i);
+        }
       }
       if (my_steps > 0) {
         // o / l, merged with the row over what precedes the chunk.  A warp's rows pass
-        // through its part of shared memory, 16 channels at a time (a loop of few
-        // instructions: they are fetched anew for every piece): 2 lanes a row (a sector)
-        // in global memory, a thread a row in between.
+        // through its part of shared memory, kStageRow bytes at a time (a loop of few
+        // instructions: they are fetched anew for every piece): kLanes lanes a row in
+        // global memory, a thread a row in between.
         const int rows = T.rows - (T.first_row + i * kChRows + wr);     // rows of the warp that exist
-        const int c2 = lane & 1, r2 = lane >> 1;
-        // element of the warp's row x, 16-byte chunk c2
-        auto place = [&](int x) { return (int64_t)__shfl_sync(0xffffffffu, orow, x) * kHeadDim + 8 * c2; };
-        const int64_t at0 = place(r2), at1 = place(r2 + 16);
-        auto staged = [&](int x, int c) { return reinterpret_cast<uint4*>(stage + x * kStageRow + ((c ^ ((x >> 2) & 1)) << 4)); };
+        constexpr int kLanes = kStageRow / 16, kTogether = 32 / kLanes;
+        const int cx = lane % kLanes, rx = lane / kLanes;
+        uint32_t from[kLanes];     // rows rx, rx + kTogether, ... of the outputs (rows behind the last one repeat it)
+#pragma unroll
+        for (int x = 0; x < kLanes; ++x) from[x] = __shfl_sync(0xffffffffu, orow, rx + kTogether * x);
+        // 16-byte chunk c of row x in shared memory: 8 lanes of either order touch every bank once
+        auto staged = [&](int x, int c) {
+          return reinterpret_cast<uint4*>(stage + x * kStageRow + ((c ^ ((x * kLanes / 8) & (kLanes - 1))) << 4));
+        };
         const bool merge = p.prior_lse != nullptr;
         const float before = merge ? p.prior_lse[orow] : -INFINITY;
-        // rows r2 and r2 + 16 to merge with (rows behind the last one repeat it), requested early
-        uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
+        // rows to merge with, requested early
+        uint4 u[kLanes];
         auto load_prior = [&](int c) {
-          u0 = *reinterpret_cast<const uint4*>(p.prior_out + at0 + c);
-          u1 = *reinterpret_cast<const uint4*>(p.prior_out + at1 + c);
+#pragma unroll
+          for (int x = 0; x < kLanes; ++x)
+            u[x] = *reinterpret_cast<const uint4*>(p.prior_out + (int64_t)from[x] * kHeadDim + c + 8 * cx);
         };
         if (merge) load_prior(0);
         if (ok) {
@@ -736,23 +783,24 @@ __global__ void __launch_bounds__(kChThreads, 1)
           lse = top + logf(a + b);
         }
 #pragma unroll 1
-        for (int c = 0; c < kHeadDim; c += 16) {
+        for (int c = 0; c < kHeadDim; c += kStageRow / 2) {
           if (merge) {
-            *staged(r2, c2) = u0;
-            *staged(r2 + 16, c2) = u1;
+#pragma unroll
+            for (int x = 0; x < kLanes; ++x) *staged(rx + kTogether * x, cx) = u[x];
             __syncwarp();
-            if (c + 16 < kHeadDim) load_prior(c + 16);
+            if (c + kStageRow / 2 < kHeadDim) load_prior(c + kStageRow / 2);
           }
-          uint32_t o[16];
+          uint32_t o[kStageRow / 2];
           if (ok) {
-            tld16(tO + c, o);
+#pragma unroll
+            for (int d = 0; d < kStageRow / 2; d += 32) tld32(tO + c + d, *reinterpret_cast<uint32_t(*)[32]>(&o[d]));
             tld_wait();
           } else {
 #pragma unroll
-            for (int q = 0; q < 16; ++q) o[q] = 0x7fc00000u;
+            for (int q = 0; q < kStageRow / 2; ++q) o[q] = 0x7fc00000u;
           }
 #pragma unroll
-          for (int d = 0; d < 2; ++d) {
+          for (int d = 0; d < kLanes; ++d) {
             uint4* mine = staged(lane, d);
             float x[8];
 #pragma unroll
@@ -772,8 +820,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
                                pack_bf16x2(x[6], x[7]));
           }
           __syncwarp();
-          if (r2 < rows) *reinterpret_cast<uint4*>(p.out + at0 + c) = *staged(r2, c2);
-          if (r2 + 16 < rows) *reinterpret_cast<uint4*>(p.out + at1 + c) = *staged(r2 + 16, c2);
+#pragma unroll
+          for (int x = 0; x < kLanes; ++x)
+            if (rx + kTogether * x < rows)
+              *reinterpret_cast<uint4*>(p.out + (int64_t)from[x] * kHeadDim + c + 8 * cx) = *staged(rx + kTogether * x, cx);
           __syncwarp();
         }
         tfence_before();
@@ -783,9 +833,12 @@ __global__ void __launch_bounds__(kChThreads, 1)
         if (S.abort_flag && lane == 0) atomicMin(&S.stopped, k + 1);
         break;
       }
-      if (queries) queries_loaded();
+      if (queries && !p.whole_tokens) queries_loaded();
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (S.abort_flag && p.whole_tokens && tiles > 0)     // (bounded: the last queries' copy gets its time)
+      for (uint32_t n = 0; n < p.spin_limit; ++n)
+        if (mbar_try_wait(&S.q_ready[i], (tiles - 1) & 1)) break;
     named_bar_sync(1, 256);
     if (S.abort_flag) {
       // gave up: the rows of the pieces that were not begun (the others' are written)
@@ -811,24 +864,24 @@ __global__ void __launch_bounds__(kChThreads, 1)
   }
 }
 
-// Rows [token][head][128 channels] of bf16: box = 64 channels of one head, 128 tokens.
+// Rows [token][head][128 channels] of bf16: box = 64 channels of 128 rows, box_heads heads a token.
 bool encode_chunk_map(CUtensorMap* map, const void* base, uint64_t tokens, uint64_t heads, uint64_t token_bytes,
-                      uint64_t head_bytes) {
+                      uint64_t head_bytes, uint32_t box_heads = 1) {
   const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
   if (encode == nullptr) return false;
   const cuuint64_t dims[3] = {kHeadDim, heads, tokens};
   const cuuint64_t strides[2] = {head_bytes, token_bytes};
-  const cuuint32_t box[3] = {64, 1, kChKeys};
+  const cuuint32_t box[3] = {64, box_heads, kChRows / box_heads};
   const cuuint32_t estr[3] = {1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-static_assert(sizeof(ChunkParams<kDecodeSeqsLarge>) + 2 * sizeof(CUtensorMap) + 64 <= 32764, "kernel parameter limit");
+static_assert(sizeof(ChunkParams<kDecodeSeqsLarge>) + 3 * sizeof(CUtensorMap) + 64 <= 32764, "kernel parameter limit");
 
 template <int MAXS, bool CAP, bool BIAS>
-cudaError_t launch_chunk_t(const ChunkParams<MAXS>& p, const CUtensorMap& tmk, const CUtensorMap& tmv, unsigned grid,
+cudaError_t launch_chunk_t(const ChunkParams<MAXS>& p, const CUtensorMap& tmk, const CUtensorMap& tmv, const CUtensorMap& tmq, unsigned grid,
                            cudaStream_t stream) {
   static bool attr_done[64] = {};
   const int smem = (int)sizeof(ChunkSmem) + 1024;
@@ -840,16 +893,19 @@ cudaError_t launch_chunk_t(const ChunkParams<MAXS>& p, const CUtensorMap& tmk, c
     return cudaFuncGetAttributes(&a, chunk_kernel<MAXS, CAP, BIAS>) == cudaSuccess ? a.numRegs : 0;
   }();
   if (regs * kChThreads < 256 * kSoftmaxRegs + 128 * kOtherRegs) return cudaErrorInvalidConfiguration;
-  return launch_dependent(chunk_kernel<MAXS, CAP, BIAS>, dim3(grid), dim3(kChThreads), (size_t)smem, stream, 1, p, tmk, tmv);
+  return launch_dependent(chunk_kernel<MAXS, CAP, BIAS>, dim3(grid), dim3(kChThreads), (size_t)smem, stream, 1, p, tmk, tmv, tmq);
 }
 
 }  // namespace
 
 template <int MAXS>
 cudaError_t launch_chunk(ChunkParams<MAXS>& p, int64_t tokens, int sms, cudaStream_t stream) {
-  CUtensorMap tmk, tmv;
+  CUtensorMap tmk, tmv, tmq{};
   if (!encode_chunk_map(&tmk, p.k, tokens, p.hkv, 2 * p.k_token, 2 * p.k_head) ||
       !encode_chunk_map(&tmv, p.v, tokens, p.hkv, 2 * p.v_token, 2 * p.v_head))
+    return cudaErrorInvalidValue;
+  p.whole_tokens = kChRows % p.gqa == 0;
+  if (p.whole_tokens && !encode_chunk_map(&tmq, p.q, tokens, p.hq, 2 * p.q_token, 2 * p.q_head, p.gqa))
     return cudaErrorInvalidValue;
   // two row tiles a CTA share its key tiles; one each while that leaves SMs without work
   int64_t tiles = 0;
@@ -887,10 +943,10 @@ cudaError_t launch_chunk(ChunkParams<MAXS>& p, int64_t tokens, int sms, cudaStre
   }
   const unsigned grid = (unsigned)std::min<int64_t>(p.pieces, sms);
   const bool cap = p.cap_log2 != 0.0f, bias = p.slopes != nullptr;
-  if (cap) return bias ? launch_chunk_t<MAXS, true, true>(p, tmk, tmv, grid, stream)
-                       : launch_chunk_t<MAXS, true, false>(p, tmk, tmv, grid, stream);
-  return bias ? launch_chunk_t<MAXS, false, true>(p, tmk, tmv, grid, stream)
-              : launch_chunk_t<MAXS, false, false>(p, tmk, tmv, grid, stream);
+  if (cap) return bias ? launch_chunk_t<MAXS, true, true>(p, tmk, tmv, tmq, grid, stream)
+                       : launch_chunk_t<MAXS, true, false>(p, tmk, tmv, tmq, grid, stream);
+  return bias ? launch_chunk_t<MAXS, false, true>(p, tmk, tmv, tmq, grid, stream)
+              : launch_chunk_t<MAXS, false, false>(p, tmk, tmv, tmq, grid, stream);
 }
 
 template cudaError_t launch_chunk<kDecodeSeqsSmall>(ChunkParams<kDecodeSeqsSmall>&, int64_t, int, cudaStream_t);

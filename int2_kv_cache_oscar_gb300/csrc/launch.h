@@ -381,6 +381,7 @@ struct ChunkParams {
   int32_t hq;
   int32_t cta_rows;    // (token, head) rows of a piece of work, 128 or 256, and
   int32_t pieces;      // how many pieces; set by the launch
+  int32_t whole_tokens;   // 128 rows are whole tokens: queries come by TMA; set by the launch
   uint32_t spin_limit; // polls of a bounded wait; the test hook's `fault` (1) leaves
   int32_t fault;       // the second copy of CTA 0 unissued, with a small limit
   float scale_log2;    // softmax_scale * log2(e)
