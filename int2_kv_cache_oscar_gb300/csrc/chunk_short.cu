@@ -10,12 +10,16 @@
 //   scores: A = queries, B = keys, straight from 16-byte loads (the channels in any
 //           order, the same for both);
 //   values: A = the weights where the scores were accumulated, in two bf16 terms (16
-//           bits), B = values through shared memory (ldmatrix.trans).
+//           bits), B = values through shared memory (ldmatrix.trans), copied there
+//           without registers in between: 162 a thread instead of 220, 12 warps an SM
+//           instead of 8 (1,000 documents of 32 tokens 371 -> 263 us; 16 warps, with
+//           spills, 285).
 // Rows leave through shared memory, 16 lanes a row.  Values that are not finite and
 // that some row does not see would spoil it through 0 times infinity: a warp that
 // finds one sums its values on the CUDA cores, visible keys only.
 // 8 documents of 5 tokens, 32 heads, merged: 7.9 us in the tiled kernel, 4.3 here; 64
-// documents of 32 tokens 25.6 us (of 40, tiled: 35.9).
+// documents of 32 tokens 22 us (of 40, tiled: 28).  Bound by latency: a warp's loads,
+// scores, weights and rows follow one another.
 #include "common.cuh"
 #include "launch.h"
 
@@ -37,8 +41,13 @@ struct ShortSmem {
 };
 static_assert(kShortWarps * sizeof(ShortSmem<kChunkShort>) <= 48 * 1024, "static shared memory");
 
+// 16 bytes from global to shared memory, or 0 there.
+__device__ __forceinline__ void copy16_or_zero(void* dst, const void* src, bool copy) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(copy ? 16 : 0) : "memory");
+}
+
 template <int MAXS, int KEYS>
-__global__ void __launch_bounds__(32 * kShortWarps)
+__global__ void __launch_bounds__(32 * kShortWarps, KEYS == 32 ? 3 : 4)
     chunk_short_kernel(const __grid_constant__ ChunkParams<MAXS> p) {
   __shared__ ShortSmem<KEYS> smem[kShortWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -47,14 +56,17 @@ __global__ void __launch_bounds__(32 * kShortWarps)
   ShortSmem<KEYS>& S = smem[warp];
   constexpr int kTiles = KEYS / 8;
   // the piece: document, KV head, rows
-  const int u = piece / p.hkv, j = piece - u * p.hkv;
+  const int u = piece / p.hkv;
   int lo = 0, hi = p.n_seqs - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (p.seq[mid].tbase <= u) lo = mid; else hi = mid - 1;
   }
   const ChunkSeq d = p.seq[lo];
-  const int first = (u - d.tbase) * kShortRows, rows = d.len * p.gqa;
+  const int rows = d.len * p.gqa, tiles = (rows + kShortRows - 1) / kShortRows;
+  // (the pieces of a head side by side: they share keys and values)
+  const int at_doc = piece - d.tbase * p.hkv, j = at_doc / tiles;
+  const int first = (at_doc - j * tiles) * kShortRows;
   const int last_tok = (min(first + kShortRows, rows) - 1) / p.gqa;
   const int keys = min(max(last_tok + 1, d.prefix), d.len);
   const int g = lane >> 2, tig = lane & 3;
@@ -78,7 +90,7 @@ __global__ void __launch_bounds__(32 * kShortWarps)
 
   // ---- everything that is read
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  uint4 qa[4], qb[4], kf[kTiles][4], vf[KEYS / 2];
+  uint4 qa[4], qb[4], kf[kTiles][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     qa[i] = *reinterpret_cast<const uint4*>(q[0] + 32 * i);
@@ -95,7 +107,8 @@ __global__ void __launch_bounds__(32 * kShortWarps)
   const uint16_t* vbase = p.v + (int64_t)d.row0 * p.v_token + (int64_t)j * p.v_head + 8 * c16;
 #pragma unroll
   for (int x = 0; x < KEYS / 2; ++x)
-    vf[x] = 2 * x + r16 < keys ? *reinterpret_cast<const uint4*>(vbase + (2 * x + r16) * p.v_token) : zero;
+    copy16_or_zero(S.v + (2 * x + r16) * kVPitch + 16 * c16, vbase + min(2 * x + r16, keys - 1) * p.v_token,
+                   2 * x + r16 < keys);
   if (p.rule.slopes != nullptr) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -139,12 +152,12 @@ __global__ void __launch_bounds__(32 * kShortWarps)
       m[x] = fmaxf(m[x], fmaxf(s[nt][2 * x], s[nt][2 * x + 1]));
     }
   }
-  // ---- values into shared memory, looked through on the way
+  // ---- the values are in shared memory: a lane looks through what it copied
   bool odd = false;
+  asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
   for (int x = 0; x < KEYS / 2; ++x) {
-    const uint4 w = vf[x];
-    *reinterpret_cast<uint4*>(S.v + (2 * x + r16) * kVPitch + 16 * c16) = w;
+    const uint4 w = *reinterpret_cast<const uint4*>(S.v + (2 * x + r16) * kVPitch + 16 * c16);
     // an exponent of all ones carries into bit 15 of its half
     odd = odd || ((((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
                    ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u)) &
