@@ -116,6 +116,24 @@ def test_many_documents():
     compare(lens, q, k, v, *call(O, lens, q, k, v))
 
 
+@pytest.mark.parametrize("gqa", [1, 3, 4, 5, 8])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+def test_several_pieces_a_block(gqa, cap):
+    """More pieces of work than SMs, of all lengths: each one's queries replace the last one's."""
+    O = U.lib()
+    lens = [33 + (37 * i) % 290 for i in range(40)]
+    q, k, v, p = inputs(lens, 4, gqa, seed=20 + gqa, layout="fused", prior=True, extra=2)
+    compare(lens, q, k, v, *call(O, lens, q, k, v, p, cap=cap), prior=p, cap=cap)
+
+
+@pytest.mark.parametrize("gqa", [32, 64, 127, 128])
+def test_many_heads_a_group(gqa):
+    O = U.lib()
+    lens = [40, 3, 71]
+    q, k, v, _ = inputs(lens, 2, gqa, seed=gqa, layout="heads", extra=1)
+    compare(lens, q, k, v, *call(O, lens, q, k, v))
+
+
 def test_long_document():
     O = U.lib()
     lens = [5001]
@@ -398,11 +416,12 @@ def test_short_merge_in_place_captured():
 
 
 @pytest.mark.parametrize("lens", [[33], [700, 300], [5000], [64] * 500])
-def test_a_wait_that_gives_up(lens):
+@pytest.mark.parametrize("gqa", [3, 4])
+def test_a_wait_that_gives_up(lens, gqa):
     """One copy of the first CTA left out: the call ends, rows that were not computed are NaN, the others are right,
     and the next call is unaffected."""
     O = U.lib()
-    q, k, v, _ = inputs(lens, 2, 4, seed=70)
+    q, k, v, _ = inputs(lens, 2, gqa, seed=70)
     want = call(O, lens, q, k, v)
     O.oscar_test_arm_wait_timeout()
     out, lse = call(O, lens, q, k, v)
