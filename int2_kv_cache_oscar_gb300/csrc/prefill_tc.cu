@@ -20,7 +20,7 @@
 //     keys are rotated like the query (H k_t) and split into fp16 hi + lo in
 //     the places of the two pieces.  The first builder also streams the group
 //     blocks through a ring of bulk copies;
-//   * MMA issuer (warp 12): one thread issues every tcgen05.mma;
+//   * MMA issuer (warp 12): stays converged, an elected lane issues every tcgen05.mma;
 //   * rows (warps 0-7; warps w and w + 4 share TMEM lanes 32 (w & 3) ..,
 //     thread = row, each warp group a 32-token chunk of every half): online
 //     softmax over the scores read from TMEM; P (hi + lo) goes to TMEM (two
@@ -38,7 +38,10 @@
 // have written its P, so the tensor cores work while the rows do.  The window
 // comes last; its P.V is on bf16 operands (V exact; P as bf16 hi + lo).  With
 // a workspace the history is split into parts (grid.z), each writing per-row
-// records (o unnormalised, m, l) that the merge kernel combines.
+// records (o unnormalised, m, l) that the merge kernel combines.  A CTA's start
+// (queries turned, first blocks, first scores) and end (rows out) take 18,000 and
+// 4,000 cycles of 290,000 at 37 groups a part: 512 queries of 32 heads over 32K
+// tokens 849 us, capped 927, 77 of 20 heads over 9,999 60.
 #include <cstddef>
 
 #include <cuda_fp16.h>
@@ -99,7 +102,6 @@ struct TcSmem {
   int gz;                                             // the value-zero rows carry 2^gz
   float fexp[kTcRows];                                // 2^-(F_row + 2) * scale_log2
   float pmax[2][2][kTcRows];                          // row maxima of the two token chunks (by half-step parity)
-  float lpart[kTcRows];                               // the second warp group's sum of p
   alignas(8) uint64_t full[kTcStages];
   uint64_t sdone[2], odone[2];   // scores / P.V of token half h done (one phase per step)
   // counts, monotonic (a waiter may fall a phase behind): key / value halves
@@ -218,23 +220,32 @@ __device__ __forceinline__ void split_p16(float x0, float x1, uint32_t& hi, uint
 
 // Normalised Walsh-Hadamard transform of a 128-vector held by one warp (lane
 // = elements 4 lane .. + 3): two stages in registers, five across lanes.
-__device__ __forceinline__ void fwht128_warp(float (&v)[4], int lane) {
-  const float a = v[0] + v[1], bq = v[0] - v[1], c = v[2] + v[3], d = v[2] - v[3];
-  v[0] = a + c;
-  v[2] = a - c;
-  v[1] = bq + d;
-  v[3] = bq - d;
+template <int N>
+__device__ __forceinline__ void fwht128_warp(float (&v)[N][4], int lane) {
+#pragma unroll
+  for (int x = 0; x < N; ++x) {
+    const float a = v[x][0] + v[x][1], bq = v[x][0] - v[x][1], c = v[x][2] + v[x][3], d = v[x][2] - v[x][3];
+    v[x][0] = a + c;
+    v[x][2] = a - c;
+    v[x][1] = bq + d;
+    v[x][3] = bq - d;
+  }
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const bool upper = (lane & o) != 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float other = __shfl_xor_sync(0xffffffffu, v[i], o);
-      v[i] = upper ? other - v[i] : v[i] + other;
+    for (int x = 0; x < N; ++x) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float other = __shfl_xor_sync(0xffffffffu, v[x][i], o);
+        v[x][i] = upper ? other - v[x][i] : v[x][i] + other;
+      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] *= 0.088388347648318440550f;   // 1/sqrt(128)
+  for (int x = 0; x < N; ++x)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[x][i] *= 0.088388347648318440550f;   // 1/sqrt(128)
 }
 
 // RULE: scores under the rule of `p` (each row's query is the chunk's token row
@@ -283,6 +294,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     S.pcount = 0;
     S.abort_flag = 0;
     fence_mbar_init();
+    // the first blocks, on their way while the queries are turned
+    for (int k = 0; k < ng && k < kTcStages; ++k) {
+      mbar_arrive_expect_tx(&S.full[k], B::kBytes);
+      bulk_g2s(S.stage[k], blocks + (int64_t)k * B::kBytes, B::kBytes, &S.full[k]);
+      S.nissued[k] = 1;
+    }
   }
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(&S.tmem_base)),
@@ -292,29 +309,54 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   // ---- q rows: rotate (warp-cooperative FWHT, lanes = 4 channels) into the
   // staging area, then each row thread stores its row into TMEM
   float* qst = reinterpret_cast<float*>(S.v1);                    // [128][kQPitch] rotated q * 2^F (v1, v2)
-  for (int r = warp; r < kTcRows; r += kTcThreads / 32) {
-    const int row = blockIdx.x * kTcRows + r;
-    uint2 raw = make_uint2(0u, 0u);
-    if (row < p.rows) {
+  // A warp's rows are all requested first and turned in batches, stage by stage (each
+  // alone waits for its own shuffles).
+  constexpr int kWarps = kTcThreads / 32, kBatch = 5, kWarpRows = (kTcRows + kWarps - 1) / kWarps;
+  static_assert(kWarpRows % kBatch == 0, "whole batches");
+  uint2 raw[kWarpRows];
+#pragma unroll
+  for (int x = 0; x < kWarpRows; ++x) {
+    const int row = blockIdx.x * kTcRows + warp + x * kWarps;
+    raw[x] = make_uint2(0u, 0u);
+    if (warp + x * kWarps < kTcRows && row < p.rows) {
       const int qi = row / p.gqa, h = j * p.gqa + row % p.gqa;
-      raw = *reinterpret_cast<const uint2*>(p.q + ((int64_t)qi * p.hq + h) * kHeadDim + 4 * lane);
+      raw[x] = *reinterpret_cast<const uint2*>(p.q + ((int64_t)qi * p.hq + h) * kHeadDim + 4 * lane);
     }
-    float qv[4] = {bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y)};
+  }
+#pragma unroll
+  for (int x0 = 0; x0 < kWarpRows; x0 += kBatch) {
+    float qv[kBatch][4], mx[kBatch];
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const uint2 u = raw[x0 + x];
+      qv[x][0] = bf16_lo(u.x);
+      qv[x][1] = bf16_hi(u.x);
+      qv[x][2] = bf16_lo(u.y);
+      qv[x][3] = bf16_hi(u.y);
+    }
     fwht128_warp(qv, lane);
-    float mx = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fabsf(qv[i]));
+    for (int x = 0; x < kBatch; ++x) {
+      mx[x] = 0.0f;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    int F = 0;
-    if (mx > 0.0f) {
-      int e;
-      frexpf(mx, &e);   // mx < 2^e
-      F = 15 - e;
+      for (int i = 0; i < 4; ++i) mx[x] = fmaxf(mx[x], fabsf(qv[x][i]));
+      mx[x] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx[x])));   // (not negative: ordered as integers)
     }
-    const float f = tc_pow2(F);
-    *reinterpret_cast<float4*>(qst + r * kQPitch + 4 * lane) = make_float4(qv[0] * f, qv[1] * f, qv[2] * f, qv[3] * f);
-    if (lane == 0) S.fexp[r] = tc_pow2(-(F + 2)) * p.scale_log2;
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const int r = warp + (x0 + x) * kWarps;
+      int F = 0;
+      if (mx[x] > 0.0f) {
+        int e;
+        frexpf(mx[x], &e);   // mx < 2^e
+        F = 15 - e;
+      }
+      if (r >= kTcRows) continue;
+      const float f = tc_pow2(F);
+      *reinterpret_cast<float4*>(qst + r * kQPitch + 4 * lane) =
+          make_float4(qv[x][0] * f, qv[x][1] * f, qv[x][2] * f, qv[x][3] * f);
+      if (lane == 0) S.fexp[r] = tc_pow2(-(F + 2)) * p.scale_log2;
+    }
   }
   tfence_before();
   __syncthreads();
@@ -459,7 +501,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int bt = b & 63, bh = b >> 6;   // token of a half, channel half (key codes, the window)
     const int bw = warp - 8;
     const float gv = tc_pow2(Gv);
-    const bool lead = b == 0;    // also streams the group blocks
+    const bool lead = b == 0;    // also streams the group blocks (behind the first ones)
     const uint8_t* wsrc = arena + p.windows_off + ((int64_t)p.slot * p.hkv + j) * kWindowBytes;
     bool ok = true;
     // rows no build writes: key rows 66..79 of each half (64 and 65 carry the
@@ -469,13 +511,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       *reinterpret_cast<uint4*>(S.kb[h] + canon(rr, 8 * kb, kNK)) = make_uint4(0u, 0u, 0u, 0u);
     }
     *reinterpret_cast<uint4*>(S.v1 + canon(136 + (b >> 4), 8 * (b & 15), kNV1)) = make_uint4(0u, 0u, 0u, 0u);
-    if (lead) {
-      for (int k = 0; k < ng && k < kTcStages; ++k) {
-        mbar_arrive_expect_tx(&S.full[k], B::kBytes);
-        bulk_g2s(S.stage[k], blocks + (int64_t)k * B::kBytes, B::kBytes, &S.full[k]);
-        S.nissued[k] = 1;
-      }
-    }
     // 2^gz with max |z^V| 2^gz < 2^14 over the sequence's groups (the
     // quantiser records each (slot, head)'s largest |value zero|): the zero
     // sums accumulate across groups in these units
@@ -543,8 +578,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int tl = 16 * bw + i, tt = 64 * h + tl;
             const uint2 raw = tt < wlen ? *reinterpret_cast<const uint2*>(wsrc + tt * kHeadDim * 2 + 8 * lane)
                                         : make_uint2(0u, 0u);
-            float kv[4] = {bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y)};
-            fwht128_warp(kv, lane);
+            float rot[1][4] = {{bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y)}};
+            fwht128_warp(rot, lane);
+            const float* kv = rot[0];
             uint32_t h01, l01, h23, l23;
             split2(kv[0] * f, kv[1] * f, false, h01, l01);
             split2(kv[2] * f, kv[3] * f, false, h23, l23);
@@ -771,6 +807,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
       }
+      count(&S.sread);   // the score buffer is free for the next half-step's scores
       if constexpr (RULE) {
         if (ok) {
           if (p.rule.cap != 0.0f) {
@@ -815,7 +852,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         }
       }
-      count(&S.sread);   // the score buffer is free for the next half-step's scores
       // pass 1: this warp group's maximum over its 32 tokens
       float mx = -INFINITY;
       if (ok) {
@@ -899,13 +935,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // ---- the last P.V, then the rows out (group 0): o = (O 2^-Gv + Z
     // 2^-gz) / l, lse = (m + log2 l) ln 2 (the TMEM loads for the whole warp,
     // the stores for rows that exist)
-    if (grp == 1) S.lpart[r] = l;
+    S.pmax[nh & 1][grp][r] = l;           // (this buffer's last readers have passed a barrier)
     ok = ok && (nh == 0 || pv_done(nh - 1));
     ok = __all_sync(0xffffffffu, ok);
     named_bar_sync(3, 256);
-    if (grp == 0 && ok) {
+    if (ok) {
       tfence_after();
-      l += S.lpart[r];
+      l += S.pmax[nh & 1][grp ^ 1][r];
       float zs[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // sum p z^V per value group (no groups: none)
       {
         uint32_t zr[16];
@@ -920,36 +956,38 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool live_row = row < p.rows;
       const float iv = tc_pow2(-Gv);
       const int qi = row / p.gqa, hq = j * p.gqa + row % p.gqa;
-      float* rec = p.n_parts > 1 ? p.parts + (((int64_t)part * p.hkv + j) * p.rows + row) * kPrefillRecFloats : nullptr;
-      const float inv = 1.0f / l;
+      float* const part_rows = p.parts + ((int64_t)part * p.hkv + j) * p.rows * kPrefillRecFloats;
+      float* rec = p.n_parts > 1 ? part_rows + (int64_t)row * kPrefillRecFloats : nullptr;
+      const float inv = rec ? 1.0f : 1.0f / l;
+      // each warp group half of the channels, through the staging area (its products
+      // are done) so that a row leaves side by side
 #pragma unroll 1
-      for (int o0 = 0; o0 < kHeadDim; o0 += 32) {
+      for (int o0 = 64 * grp; o0 < 64 * grp + 64; o0 += 32) {
         uint32_t orr[32];
         tld32(lane_base + kTO + o0, orr);
         tld_wait();
-        const float z = zs[o0 >> 5];
-        if (live_row && rec) {
+        const float z = o0 < 64 ? (o0 < 32 ? zs[0] : zs[1]) : (o0 < 96 ? zs[2] : zs[3]);
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(rec + o0 + i) =
-                make_float4(fmaf(__uint_as_float(orr[i]), iv, z), fmaf(__uint_as_float(orr[i + 1]), iv, z),
-                            fmaf(__uint_as_float(orr[i + 2]), iv, z), fmaf(__uint_as_float(orr[i + 3]), iv, z));
-        } else if (live_row) {
-          uint32_t* orow = reinterpret_cast<uint32_t*>(p.out + ((int64_t)qi * p.hq + hq) * kHeadDim + o0);
-#pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            uint32_t u[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float o_0 = fmaf(__uint_as_float(orr[i + 2 * e]), iv, z) * inv;
-              const float o_1 = fmaf(__uint_as_float(orr[i + 2 * e + 1]), iv, z) * inv;
-              u[e] = f32_to_bf16_bits(o_0) | (f32_to_bf16_bits(o_1) << 16);
-            }
-            *reinterpret_cast<uint4*>(orow + i / 2) = make_uint4(u[0], u[1], u[2], u[3]);
-          }
-        }
+        for (int i = 0; i < 32; i += 4)
+          *reinterpret_cast<float4*>(qst + r * kQPitch + o0 + i) =
+              make_float4(fmaf(__uint_as_float(orr[i]), iv, z) * inv, fmaf(__uint_as_float(orr[i + 1]), iv, z) * inv,
+                          fmaf(__uint_as_float(orr[i + 2]), iv, z) * inv, fmaf(__uint_as_float(orr[i + 3]), iv, z) * inv);
       }
-      if (!live_row) {
+      __syncwarp();
+#pragma unroll 4
+      for (int x = 0; x < 32; x += 2) {
+        const int rr = 32 * (warp & 3) + x + (lane >> 4), c = 64 * grp + 4 * (lane & 15);
+        const int to = blockIdx.x * kTcRows + rr;
+        if (to >= p.rows) continue;
+        const float4 o4 = *reinterpret_cast<const float4*>(qst + rr * kQPitch + c);
+        if (rec)
+          *reinterpret_cast<float4*>(part_rows + (int64_t)to * kPrefillRecFloats + c) = o4;
+        else
+          *reinterpret_cast<uint2*>(p.out + ((int64_t)(to / p.gqa) * p.hq + j * p.gqa + to % p.gqa) * kHeadDim + c) =
+              make_uint2(f32_to_bf16_bits(o4.x) | (f32_to_bf16_bits(o4.y) << 16),
+                         f32_to_bf16_bits(o4.z) | (f32_to_bf16_bits(o4.w) << 16));
+      }
+      if (!live_row || grp == 1) {
       } else if (rec) {
         *reinterpret_cast<float2*>(rec + kHeadDim) = make_float2(m_used, l);
       } else if (p.lse != nullptr) {
