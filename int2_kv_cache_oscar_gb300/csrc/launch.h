@@ -390,6 +390,7 @@ struct ChunkParams {
   float cap_log2;      // cap log2(e); 0: no cap
   float cap_near;      // softmax_scale / (0.6 cap): |raw score| times it up to 1 takes the polynomial
   float cap_c[5];      // of the raw score (x times a polynomial of x^2)
+  float cap_d[3];      // the same of a shorter one, up to a quarter of the cap
   const float* slopes; // [hq], or NULL
   float slope_unit;    // log2(e) with a cap (scores in log2 units), 1 / softmax_scale without (raw scores)
   const uint16_t* q;

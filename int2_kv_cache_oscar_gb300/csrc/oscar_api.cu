@@ -1686,6 +1686,9 @@ oscar_status oscar_chunk_attention(int32_t n_seqs, const int32_t* cu, const int3
       const double c[4] = {-0.33332597509867323, 0.1331311669852155, -0.05221180873069635, 0.015612635835695849};
       double power = first;
       for (int i = 0; i < 4; ++i) P.cap_c[i + 1] = fits ? (float)(c[i] * (power *= y)) : 0.0f;
+      const double d[2] = {-0.3332457141137327, 0.1287642123823267};
+      P.cap_d[0] = (float)first;
+      for (int i = 0; i < 2; ++i) P.cap_d[i + 1] = fits ? (float)(d[i] * first * (i ? y * y : y)) : 0.0f;
     }
     P.slopes = how.slopes;
     P.rule = how;
