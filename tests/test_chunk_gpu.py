@@ -116,6 +116,17 @@ def test_many_documents():
     compare(lens, q, k, v, *call(O, lens, q, k, v))
 
 
+@pytest.mark.parametrize("cap", [2.0, 5.0, 8.0, 12.0, 18.0, 30.0, 60.0, 1000.0])
+@pytest.mark.parametrize("lens", [[21], [333]])
+def test_caps_near_and_far(cap, lens):
+    """Scores of a few units under caps that they reach, come near and stay far from."""
+    O = U.lib()
+    q, k, v, _ = inputs(lens, 2, 4, seed=int(cap))
+    compare(lens, q, k, v, *call(O, lens, q, k, v, cap=cap), cap=cap)
+    q[::7] = (q[::7].float() * 4.0).bfloat16()          # rows of a warp in different ranges
+    compare(lens, q, k, v, *call(O, lens, q, k, v, cap=cap), cap=cap)
+
+
 @pytest.mark.parametrize("gqa", [1, 3, 4, 5, 8])
 @pytest.mark.parametrize("cap", [0.0, 30.0])
 def test_several_pieces_a_block(gqa, cap):
