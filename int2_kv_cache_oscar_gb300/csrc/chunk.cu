@@ -69,32 +69,29 @@ __host__ __device__ constexpr uint32_t col_o(int i) { return 256u + 128u * i; }
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;   // registers of a thread: warps 0-7, warps 8-11
 constexpr float kGrowth = 8.0f;               // see above
+constexpr float kCapSmall = 0.25f / 0.6f;     // a quarter of the cap, in units of 0.6 of it (see cap_small)
 constexpr float kLn2 = 0.69314718055994530942f;
 
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // cap tanh(x / cap) of a raw score, in log2 units: cap - 2 cap / (1 + exp(2 x /
-// cap)), off by cap 2^-22 at most.
-template <typename P>
-__device__ __forceinline__ float cap_far(float s, const P& p) {
-  return fmaf(p.cap_out, rcp_approx(1.0f + tc_exp2(s * p.cap_in)), p.cap_log2);
+// cap)), off by cap 2^-22 at most (`in` = 2 x / cap of a raw score of 1 in log2 units,
+// `out` = -2 cap).
+__device__ __forceinline__ float cap_far(float s, float in, float out, float cap) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(s * in));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return fmaf(out, r, cap);
 }
 
 // The same within 0.6 of the cap, two scores: tanh(x) = x (1 + c1 x^2 + .. + c4 x^8),
 // the smallest largest relative error over that range (2^-23.5), with the scale and
 // the cap in the coefficients.
-template <typename P>
-__device__ __forceinline__ float2 cap_near(float2 s, const P& p) {
+__device__ __forceinline__ float2 cap_near(float2 s, const float (&c)[5]) {
   const float2 y = __fmul2_rn(s, s);
   auto two = [](float v) { return make_float2(v, v); };
-  float2 t = __ffma2_rn(two(p.cap_c[4]), y, two(p.cap_c[3]));
-  t = __ffma2_rn(t, y, two(p.cap_c[2]));
-  t = __ffma2_rn(t, y, two(p.cap_c[1]));
-  return __fmul2_rn(s, __ffma2_rn(t, y, two(p.cap_c[0])));
+  float2 t = __ffma2_rn(two(c[4]), y, two(c[3]));
+  t = __ffma2_rn(t, y, two(c[2]));
+  t = __ffma2_rn(t, y, two(c[1]));
+  return __fmul2_rn(s, __ffma2_rn(t, y, two(c[0])));
 }
 
 // The same within a quarter of the cap: two terms less, relative error 2^-21 (cap
@@ -240,6 +237,12 @@ __device__ __noinline__ void add_cleared(uint32_t t_p, uint32_t t_o, const uint3
     tst32(t_o + c0, o);
     tst_wait();
   }
+}
+
+// Which of the step's keys c .. c + 31 a row sees, of which the first `visible` are
+// visible: a bit a key (tested in fewer instructions than a comparison each).
+__device__ __forceinline__ uint32_t seen_of(int visible, int c) {
+  return visible >= c + 32 ? 0xffffffffu : visible <= c ? 0u : (1u << (visible - c)) - 1u;
 }
 
 // 16 bytes from global to shared memory, without a register in between.
@@ -606,9 +609,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
               asm("max.f32 %0, %0, %1, %2;" : "+f"(hi) : "f"(s[c]), "f"(s[c + 1]));
               asm("min.f32 %0, %0, %1, %2;" : "+f"(lo) : "f"(s[c]), "f"(s[c + 1]));
             }
-            // (uniform; the scores of a model with a cap mostly stay well within it)
+            // (the scores of a model with a cap mostly stay well within it, hidden ones too)
             const float reach = fmaxf(hi, -lo) * p.cap_near;
-            if (__all_sync(0xffffffffu, reach <= 0.25f / 0.6f)) {
+            if (__all_sync(0xffffffffu, reach <= kCapSmall)) {
 #pragma unroll
               for (int c = 0; c < kChKeys; c += 2) {
                 const float2 y = cap_small(make_float2(s[c], s[c + 1]), p);
@@ -616,18 +619,51 @@ __global__ void __launch_bounds__(kChThreads, 1)
                 s[c + 1] = y.y;
               }
               top = cap_small(make_float2(hi, hi), p).x;
-            } else if (__all_sync(0xffffffffu, reach <= 1.0f)) {
-#pragma unroll
-              for (int c = 0; c < kChKeys; c += 2) {
-                const float2 y = cap_near(make_float2(s[c], s[c + 1]), p);
-                s[c] = y.x;
-                s[c + 1] = y.y;
-              }
-              top = cap_near(make_float2(hi, hi), p).x;
             } else {
+              // A row takes the form that the scores which it sees ask for, by itself:
+              // neither hidden keys nor the warp's other rows have a part in its bits
+              // (the short polynomial is the long one with zeros for its last terms).
+              // Branches by row cost what each takes (8,192 capped tokens: 450 us where
+              // all scores are small, 553 within 0.6 of the cap, 822 all beyond, 1,000 to
+              // 1,160 with rows of every kind in a warp; with one form a warp, chosen by
+              // what its rows do not see as well, 448, 515, 750 and 777 to 856).
+              float own = reach;
+              if (j >= my_plain) {
+                const int vis = limit - j * kChKeys;
+                own = 0.0f;
 #pragma unroll
-              for (int c = 0; c < kChKeys; ++c) s[c] = cap_far(s[c], p);
-              top = cap_far(hi, p);
+                for (int c = 0; c < kChKeys; c += 32) {
+                  const uint32_t seen = seen_of(vis, c);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) own = (seen >> e) & 1u ? fmaxf(own, fabsf(s[c + e])) : own;
+                }
+                own *= p.cap_near;
+              }
+              float c[5];
+#pragma unroll
+              for (int e = 0; e < 5; ++e) c[e] = !(own <= kCapSmall) ? p.cap_c[e] : e < 3 ? p.cap_d[e] : 0.0f;
+              if (__all_sync(0xffffffffu, own <= 1.0f)) {
+#pragma unroll
+                for (int k = 0; k < kChKeys; k += 2) {
+                  const float2 y = cap_near(make_float2(s[k], s[k + 1]), c);
+                  s[k] = y.x;
+                  s[k + 1] = y.y;
+                }
+                top = cap_near(make_float2(hi, hi), c).x;
+              } else if (own <= 1.0f) {
+#pragma unroll
+                for (int k = 0; k < kChKeys; k += 2) {
+                  const float2 y = cap_near(make_float2(s[k], s[k + 1]), c);
+                  s[k] = y.x;
+                  s[k + 1] = y.y;
+                }
+                top = cap_near(make_float2(hi, hi), c).x;
+              } else {
+#pragma unroll
+                for (int k = 0; k < kChKeys; ++k) s[k] = cap_far(s[k], p.cap_in, p.cap_out, p.cap_log2);
+                top = cap_far(hi, p.cap_in, p.cap_out, p.cap_log2);
+              }
+              __syncwarp();
             }
           }
           if constexpr (BIAS) {
@@ -656,10 +692,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
           }
           if (j >= my_plain) {
             const int vis = limit - j * kChKeys;
-            // (a bit a key: tested in fewer instructions than a comparison each)
 #pragma unroll
             for (int c = 0; c < kChKeys; c += 32) {
-              const uint32_t seen = vis >= c + 32 ? 0xffffffffu : vis <= c ? 0u : (1u << (vis - c)) - 1u;
+              const uint32_t seen = seen_of(vis, c);
 #pragma unroll
               for (int e = 0; e < 32; ++e) s[c + e] = (seen >> e) & 1u ? s[c + e] : -INFINITY;
             }
