@@ -11,12 +11,13 @@
 //           order, the same for both);
 //   values: A = the weights where the scores were accumulated, in two bf16 terms (16
 //           bits), B = values through shared memory (ldmatrix.trans), copied there
-//           without registers in between: 162 a thread instead of 220, 12 warps an SM
-//           instead of 8 (1,000 documents of 32 tokens 371 -> 263 us; 16 warps, with
+//           without registers in between: 168 a thread instead of 220, 12 warps an SM
+//           instead of 8 (1,000 documents of 32 tokens 371 -> 255 us; 16 warps, with
 //           spills, 285).
 // Rows leave through shared memory, 16 lanes a row.  Values that are not finite and
 // that some row does not see would spoil it through 0 times infinity: a warp that
-// finds one sums its values on the CUDA cores, visible keys only.
+// finds one clears the token's values there, and rows that do see it add them on the
+// CUDA cores.
 // 8 documents of 5 tokens, 32 heads, merged: 7.9 us in the tiled kernel, 4.3 here; 64
 // documents of 32 tokens 22 us (of 40, tiled: 28).  Bound by latency: a warp's loads,
 // scores, weights and rows follow one another.
@@ -36,7 +37,7 @@ template <int KEYS>
 struct ShortSmem {
   static constexpr int kValues = KEYS * kVPitch, kOut = kShortRows * kOPitch * 4;
   alignas(16) uint8_t v[kValues > kOut ? kValues : kOut];   // values, then the rows' outputs in float32
-  float p[kShortRows][KEYS];                      // weights (of a warp that sums on the CUDA cores)
+  float p[kShortRows][KEYS];                      // weights (of a warp that has cleared values)
   float prior[kShortRows];                        // factor of the row to merge with
 };
 static_assert(kShortWarps * sizeof(ShortSmem<kChunkShort>) <= 48 * 1024, "static shared memory");
@@ -153,17 +154,27 @@ __global__ void __launch_bounds__(32 * kShortWarps, KEYS == 32 ? 3 : 4)
     }
   }
   // ---- the values are in shared memory: a lane looks through what it copied
+  auto mine_of = [&](int x) { return reinterpret_cast<uint4*>(S.v + (2 * x + r16) * kVPitch + 16 * c16); };
+  auto not_finite = [](uint4 w) {
+    // an exponent of all ones carries into bit 15 of its half
+    return ((((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
+             ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u)) &
+            0x80008000u) != 0u;
+  };
   bool odd = false;
   asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
-  for (int x = 0; x < KEYS / 2; ++x) {
-    const uint4 w = *reinterpret_cast<const uint4*>(S.v + (2 * x + r16) * kVPitch + 16 * c16);
-    // an exponent of all ones carries into bit 15 of its half
-    odd = odd || ((((w.x & 0x7f807f80u) + 0x00800080u) | ((w.y & 0x7f807f80u) + 0x00800080u) |
-                   ((w.z & 0x7f807f80u) + 0x00800080u) | ((w.w & 0x7f807f80u) + 0x00800080u)) &
-                  0x80008000u) != 0u;
-  }
+  for (int x = 0; x < KEYS / 2; ++x) odd = odd || not_finite(*mine_of(x));
   odd = __any_sync(0xffffffffu, odd);
+  uint32_t bad = 0u;                       // tokens whose values are not finite, cleared there
+  if (odd) {
+#pragma unroll 1
+    for (int x = 0; x < KEYS / 2; ++x) {
+      const uint32_t lanes = __ballot_sync(0xffffffffu, not_finite(*mine_of(x)));
+      bad |= ((lanes & 0xffffu) != 0u ? 1u : 0u) << (2 * x) | ((lanes >> 16) != 0u ? 1u : 0u) << (2 * x + 1);
+      if ((bad >> (2 * x + r16)) & 1u) *mine_of(x) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     m[x] = fmaxf(m[x], __shfl_xor_sync(0xffffffffu, m[x], 1));
@@ -201,73 +212,65 @@ __global__ void __launch_bounds__(32 * kShortWarps, KEYS == 32 ? 3 : 4)
   }
   __syncwarp();
   float* out = reinterpret_cast<float*>(S.v);
-  if (!odd) {
-    float o[16][4];
+  float o[16][4];
 #pragma unroll
-    for (int t = 0; t < 16; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.0f;
+  for (int t = 0; t < 16; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.0f;
 #pragma unroll
-    for (int kk = 0; kk < KEYS / 16; ++kk) {
-      if (16 * kk >= keys) break;
-      uint32_t ph[4], pl[4];
+  for (int kk = 0; kk < KEYS / 16; ++kk) {
+    if (16 * kk >= keys) break;
+    uint32_t ph[4], pl[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {       // rows g, g + 8 of keys 2 tig .., then of keys 2 tig + 8 ..
-        const float* x = &s[2 * kk + (e >> 1)][2 * (e & 1)];
-        ph[e] = pack_bf16x2(x[0], x[1]);
-        pl[e] = pack_bf16x2(x[0] - bf16_lo(ph[e]), x[1] - bf16_hi(ph[e]));
-      }
-      const uint32_t at = smem_u32(S.v) + (16 * kk + (lane & 15)) * kVPitch + 16 * (lane >> 4);
-#pragma unroll
-      for (int t = 0; t < 16; t += 2) {
-        uint32_t b0, b1, b2, b3;
-        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3)
-                     : "r"(at + 16 * t));
-        mma_bf16_16816(o[t], ph[0], ph[1], ph[2], ph[3], b0, b1);
-        mma_bf16_16816(o[t + 1], ph[0], ph[1], ph[2], ph[3], b2, b3);
-        mma_bf16_16816(o[t], pl[0], pl[1], pl[2], pl[3], b0, b1);
-        mma_bf16_16816(o[t + 1], pl[0], pl[1], pl[2], pl[3], b2, b3);
-      }
+    for (int e = 0; e < 4; ++e) {       // rows g, g + 8 of keys 2 tig .., then of keys 2 tig + 8 ..
+      const float* x = &s[2 * kk + (e >> 1)][2 * (e & 1)];
+      ph[e] = pack_bf16x2(x[0], x[1]);
+      pl[e] = pack_bf16x2(x[0] - bf16_lo(ph[e]), x[1] - bf16_hi(ph[e]));
     }
-    __syncwarp();                          // the values have been read
+    const uint32_t at = smem_u32(S.v) + (16 * kk + (lane & 15)) * kVPitch + 16 * (lane >> 4);
 #pragma unroll
-    for (int t = 0; t < 16; ++t) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x)
-        *reinterpret_cast<float2*>(out + (g + 8 * x) * kOPitch + 8 * t + 2 * tig) =
-            make_float2(o[t][2 * x] * fo[x], o[t][2 * x + 1] * fo[x]);
+    for (int t = 0; t < 16; t += 2) {
+      uint32_t b0, b1, b2, b3;
+      asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(b0), "=r"(b1), "=r"(b2), "=r"(b3)
+                   : "r"(at + 16 * t));
+      mma_bf16_16816(o[t], ph[0], ph[1], ph[2], ph[3], b0, b1);
+      mma_bf16_16816(o[t + 1], ph[0], ph[1], ph[2], ph[3], b2, b3);
+      mma_bf16_16816(o[t], pl[0], pl[1], pl[2], pl[3], b0, b1);
+      mma_bf16_16816(o[t + 1], pl[0], pl[1], pl[2], pl[3], b2, b3);
     }
-  } else {
+  }
+  __syncwarp();                          // the values have been read
+#pragma unroll
+  for (int t = 0; t < 16; ++t) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      *reinterpret_cast<float2*>(out + (g + 8 * x) * kOPitch + 8 * t + 2 * tig) =
+          make_float2(o[t][2 * x] * fo[x], o[t][2 * x + 1] * fo[x]);
+  }
+  if (odd) {
+    // rows that see a cleared token add its values by their weights; the others keep
+    // the bits that they have whatever it holds
 #pragma unroll
     for (int nt = 0; nt < kTiles; ++nt)
 #pragma unroll
       for (int x = 0; x < 4; ++x) S.p[g + 8 * (x >> 1)][8 * nt + 2 * tig + (x & 1)] = s[nt][x] * fo[x >> 1];
     __syncwarp();
-    float acc[kShortRows][4];
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-#pragma unroll
-      for (int r = 0; r < kShortRows / 2; ++r) {
-        const int row = r + kShortRows / 2 * half;
-        const int see = min(max(min(first + row, rows - 1) / p.gqa + 1, d.prefix), d.len);
-        float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int t = 0; t < see; ++t) {
-          const uint2 w = *reinterpret_cast<const uint2*>(S.v + t * kVPitch + 8 * lane);
-          a[0] = fmaf(S.p[row][t], bf16_lo(w.x), a[0]);
-          a[1] = fmaf(S.p[row][t], bf16_hi(w.x), a[1]);
-          a[2] = fmaf(S.p[row][t], bf16_lo(w.y), a[2]);
-          a[3] = fmaf(S.p[row][t], bf16_hi(w.y), a[3]);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (half == 0) acc[r][e] = a[e];
-          else acc[r + kShortRows / 2][e] = a[e];
-        }
+    for (int r = 0; r < kShortRows; ++r) {
+      const int see = min(max(min(first + r, rows - 1) / p.gqa + 1, d.prefix), d.len);
+      uint32_t left = see >= 32 ? bad : bad & ((1u << see) - 1u);
+      if (left == 0u) continue;
+      float4 a = *reinterpret_cast<const float4*>(out + r * kOPitch + 4 * lane);
+      for (; left != 0u; left &= left - 1u) {
+        const int t = __ffs((int)left) - 1;
+        const uint2 w = *reinterpret_cast<const uint2*>(p.v + (int64_t)(d.row0 + t) * p.v_token + (int64_t)j * p.v_head + 4 * lane);
+        const float f = S.p[r][t];
+        a.x = fmaf(f, bf16_lo(w.x), a.x);
+        a.y = fmaf(f, bf16_hi(w.x), a.y);
+        a.z = fmaf(f, bf16_lo(w.y), a.z);
+        a.w = fmaf(f, bf16_hi(w.y), a.w);
       }
+      *reinterpret_cast<float4*>(out + r * kOPitch + 4 * lane) = a;
     }
-    __syncwarp();
-#pragma unroll
-    for (int r = 0; r < kShortRows; ++r)
-      *reinterpret_cast<float4*>(out + r * kOPitch + 4 * lane) = make_float4(acc[r][0], acc[r][1], acc[r][2], acc[r][3]);
   }
   __syncwarp();
   // ---- rows out, merged

@@ -33,3 +33,38 @@ def test_hidden_tokens_under_a_cap(cap, bias, gqa, loud):
         keep[rows] = False
         assert torch.equal(out[:353][keep], clean[0][:353][keep]), name
         assert torch.equal(lse[:353][keep], clean[1][:353][keep]), name
+
+
+@pytest.mark.parametrize("loud", [40.0, 3.0e38, float("inf"), float("nan")])
+@pytest.mark.parametrize("gqa", [1, 3, 4])
+@pytest.mark.parametrize("cap,prior", [(0.0, False), (0.0, True), (30.0, False)])
+def test_hidden_tokens_of_short_documents(cap, prior, gqa, loud):
+    """The same of documents of up to 32 tokens, 16 rows of which share their keys and values."""
+    O = U.lib()
+    lens = [11, 6, 32, 16]
+    q, k, v, p = inputs(lens, 2, gqa, seed=81, extra=9, prior=prior)
+    clean = call(O, lens, q, k, v, p, cap=cap)
+    compare(lens, q, k, v, *clean, prior=p, cap=cap)
+    for rows in (slice(65, 74), slice(11, 17), slice(9, 10), slice(5, 11), slice(20, 21), slice(30, 49), slice(56, 57)):
+        k2, v2 = k.clone(), v.clone()
+        k2[rows] = (k2[rows].float() * loud).bfloat16()
+        v2[rows] = loud
+        out, lse = call(O, lens, q, k2, v2, p, cap=cap)
+        seen = torch.zeros(65, dtype=torch.bool)         # rows at or behind one of these tokens, in its document
+        for a, n in ((0, 11), (11, 6), (17, 32), (49, 16)):
+            first = max(a, rows.start)
+            if first < min(a + n, rows.stop):
+                seen[first:a + n] = True
+        assert torch.equal(out[:65][~seen], clean[0][:65][~seen])
+        assert torch.equal(lse[:65][~seen], clean[1][:65][~seen])
+
+
+@pytest.mark.parametrize("n", [9, 16, 32])
+def test_values_that_are_not_finite_in_several_tokens_of_a_short_document(n):
+    """Rows that see some of them, in one channel each: the other channels keep their sums."""
+    O = U.lib()
+    q, k, v, _ = inputs([n, n], 2, 3, seed=82)
+    for t in range(2, n, 3):
+        v[t, t % 2, 5 * t % 128] = float("inf") if t % 2 else float("nan")
+    out, lse = call(O, [n, n], q, k, v)
+    compare([n, n], q, k, v, out, lse)
