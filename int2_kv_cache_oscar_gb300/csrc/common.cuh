@@ -289,7 +289,6 @@ struct ScoreRule {
   float cap;             // cap log2(e); 0: none
   float inv_cap;
   float c[6];            // coefficients of tanh's polynomial over powers of the cap (see capped)
-  float b[4];            // of a shorter one (see capped_bf16)
   const float* slopes;   // [query heads], natural units, or NULL
   __host__ __device__ bool any() const { return cap != 0.0f || slopes != nullptr; }
 };
@@ -325,20 +324,9 @@ __device__ __forceinline__ float2 capped(float2 s, const ScoreRule& r, bool all_
   return t;
 }
 
-// The same where outputs are bf16, off by cap 2^-22 at most: within 0.6 of the cap a
-// polynomial of two terms less (relative error 2^-23.5), and where a score of the
-// warp is outside the other form for all of them.
-constexpr float kTanhNearBf16 = 0.6f;
-
-__device__ __forceinline__ float2 capped_bf16(float2 s, const ScoreRule& r, bool all_near) {
-  auto two = [](float v) { return make_float2(v, v); };
-  if (all_near) {
-    const float2 y = __fmul2_rn(s, s);
-    float2 t = __ffma2_rn(two(r.b[3]), y, two(r.b[2]));
-    t = __ffma2_rn(t, y, two(r.b[1]));
-    t = __ffma2_rn(t, y, two(r.b[0]));
-    return __fmul2_rn(s, __ffma2_rn(t, y, two(1.0f)));
-  }
+// The same by the exponential alone, off by cap 2^-22 at most: no choice of a form, so
+// none that other scores of the warp could make.
+__device__ __forceinline__ float2 capped_by_exp(float2 s, const ScoreRule& r) {
   return make_float2(r.cap * tanh_far(s.x * r.inv_cap), r.cap * tanh_far(s.y * r.inv_cap));
 }
 

@@ -188,11 +188,9 @@ oscar_status cache_rule(const oscar_score_rule* r, int device, ScoreRule* out) {
     const double c[6] = {-0.3333298680917359, 0.13326408458826144,  -0.05349867504186163,
                          0.020359682485341188, -0.006259264284882422, 0.0010582383503523435};
     double power = 1.0;
-    const double b[4] = {-0.33332597509867323, 0.1331311669852155, -0.05221180873069635, 0.015612635835695849};
     for (int i = 0; i < 6; ++i) {
       power /= (double)out->cap * out->cap;
       out->c[i] = (float)(c[i] * power);
-      if (i < 4) out->b[i] = (float)(b[i] * power);
     }
   }
   out->slopes = r->slopes;

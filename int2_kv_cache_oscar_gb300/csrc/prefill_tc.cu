@@ -41,7 +41,7 @@
 // records (o unnormalised, m, l) that the merge kernel combines.  A CTA's start
 // (queries turned, first blocks, first scores) and end (rows out) take 18,000 and
 // 4,000 cycles of 290,000 at 37 groups a part: 512 queries of 32 heads over 32K
-// tokens 849 us, capped 927, 77 of 20 heads over 9,999 60.
+// tokens 849 us, capped 913, 77 of 20 heads over 9,999 60.
 #include <cstddef>
 
 #include <cuda_fp16.h>
@@ -811,28 +811,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if constexpr (RULE) {
         if (ok) {
           if (p.rule.cap != 0.0f) {
-            float hi = fmaxf(w[0], w[1]), lo = fminf(w[0], w[1]);
+            // (a polynomial where every score of the warp is near zero hides behind the
+            // products no better, 909 against 908 us, costs the vote where some are not,
+            // 931 against 912, and lets the rows beside a row choose its form)
 #pragma unroll
-            for (int i = 2; i < 32; i += 2) {
-              asm("max.f32 %0, %0, %1, %2;" : "+f"(hi) : "f"(w[i]), "f"(w[i + 1]));
-              asm("min.f32 %0, %0, %1, %2;" : "+f"(lo) : "f"(w[i]), "f"(w[i + 1]));
-            }
-            // (tokens past the window are -inf: the long way then)
-            const bool near = __all_sync(0xffffffffu, fmaxf(hi, -lo) * p.rule.inv_cap <= kTanhNearBf16);
-            if (near) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 y = capped_bf16(make_float2(w[i], w[i + 1]), p.rule, true);
-                w[i] = y.x;
-                w[i + 1] = y.y;
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 y = capped_bf16(make_float2(w[i], w[i + 1]), p.rule, false);
-                w[i] = y.x;
-                w[i + 1] = y.y;
-              }
+            for (int i = 0; i < 32; i += 2) {
+              const float2 y = capped_by_exp(make_float2(w[i], w[i + 1]), p.rule);
+              w[i] = y.x;
+              w[i + 1] = y.y;
             }
           }
           if (p.rule.slopes != nullptr) {
