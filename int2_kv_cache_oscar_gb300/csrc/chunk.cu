@@ -69,6 +69,7 @@ __host__ __device__ constexpr uint32_t col_o(int i) { return 256u + 128u * i; }
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSoftmaxRegs = 216, kOtherRegs = 72;   // registers of a thread: warps 0-7, warps 8-11
 constexpr float kGrowth = 8.0f;               // see above
+constexpr float kFarBase = 0x1p20f;           // log2 units: a base beyond is not exact to 2^-4
 constexpr float kCapSmall = 0.25f / 0.6f;     // a quarter of the cap, in units of 0.6 of it (see cap_small)
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -732,7 +733,18 @@ __global__ void __launch_bounds__(kChThreads, 1)
           tst_wait();
         }
         m = m_new;
-        const float base = m == -INFINITY ? 0.0f : -m * sl;
+        float base = m == -INFINITY ? 0.0f : -m * sl;
+        if constexpr (BIAS || !CAP) {
+          // scores far from zero: -m sl is rounded by more than an exponent bears (the same
+          // for all of a row's weights, so it does not matter before); the maximum is taken off first
+          const bool far = fabsf(base) > kFarBase;
+          if (__any_sync(0xffffffffu, far)) {
+            const float off = far ? -m : 0.0f;
+#pragma unroll
+            for (int c = 0; c < kChKeys; ++c) s[c] += off;
+            if (far) base = 0.0f;
+          }
+        }
         const float2 sl2 = make_float2(sl, sl), base2 = make_float2(base, base);
         float2 sum0 = make_float2(0.0f, 0.0f), sum1 = make_float2(0.0f, 0.0f);
         auto weights = [&](const float* x, uint32_t* pk) {     // of 4 scores
