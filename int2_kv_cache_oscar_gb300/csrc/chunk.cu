@@ -251,7 +251,8 @@ __device__ __forceinline__ void copy16_async(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-template <int MAXS, bool CAP, bool BIAS>
+// UNIT: raw scores are taken times a power of two before the slopes (see ChunkParams)
+template <int MAXS, bool CAP, bool BIAS, bool UNIT>
 __global__ void __launch_bounds__(kChThreads, 1)
     chunk_kernel(const __grid_constant__ ChunkParams<MAXS> p, const __grid_constant__ CUtensorMap tmk,
                  const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmq) {
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__(kChThreads, 1)
     const uint32_t tS = tmem + col_s(i) + lanes, tO = tmem + col_o(i) + lanes;
     uint8_t* stage = S.stage[warp];
     // scores to log2 units: a factor here (slopes are divided by it), the cap's arithmetic otherwise
-    const float sl = CAP ? 1.0f : p.scale_log2;
+    const float sl = CAP ? 1.0f : UNIT ? p.unit_log2 : p.scale_log2;
 
     auto queries_loaded = [&] {
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -666,6 +667,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
               }
               __syncwarp();
             }
+          }
+          if constexpr (UNIT) {
+#pragma unroll
+            for (int c = 0; c < kChKeys; ++c) s[c] *= p.score_unit;
           }
           if constexpr (BIAS) {
             const float2 slope = make_float2(-slope2, -slope2);
@@ -946,20 +951,20 @@ bool encode_chunk_map(CUtensorMap* map, const void* base, uint64_t tokens, uint6
 
 static_assert(sizeof(ChunkParams<kDecodeSeqsLarge>) + 3 * sizeof(CUtensorMap) + 64 <= 32764, "kernel parameter limit");
 
-template <int MAXS, bool CAP, bool BIAS>
+template <int MAXS, bool CAP, bool BIAS, bool UNIT = false>
 cudaError_t launch_chunk_t(const ChunkParams<MAXS>& p, const CUtensorMap& tmk, const CUtensorMap& tmv, const CUtensorMap& tmq, unsigned grid,
                            cudaStream_t stream) {
   static bool attr_done[64] = {};
   const int smem = (int)sizeof(ChunkSmem) + 1024;
-  cudaError_t e = ensure_smem_attr(chunk_kernel<MAXS, CAP, BIAS>, smem, attr_done);
+  cudaError_t e = ensure_smem_attr(chunk_kernel<MAXS, CAP, BIAS, UNIT>, smem, attr_done);
   if (e != cudaSuccess) return e;
   // the warps' shares of the registers must fit in what the block is launched with
   static const int regs = [] {
     cudaFuncAttributes a;
-    return cudaFuncGetAttributes(&a, chunk_kernel<MAXS, CAP, BIAS>) == cudaSuccess ? a.numRegs : 0;
+    return cudaFuncGetAttributes(&a, chunk_kernel<MAXS, CAP, BIAS, UNIT>) == cudaSuccess ? a.numRegs : 0;
   }();
   if (regs * kChThreads < 256 * kSoftmaxRegs + 128 * kOtherRegs) return cudaErrorInvalidConfiguration;
-  return launch_dependent(chunk_kernel<MAXS, CAP, BIAS>, dim3(grid), dim3(kChThreads), (size_t)smem, stream, 1, p, tmk, tmv, tmq);
+  return launch_dependent(chunk_kernel<MAXS, CAP, BIAS, UNIT>, dim3(grid), dim3(kChThreads), (size_t)smem, stream, 1, p, tmk, tmv, tmq);
 }
 
 }  // namespace
@@ -1011,6 +1016,8 @@ cudaError_t launch_chunk(ChunkParams<MAXS>& p, int64_t tokens, int sms, cudaStre
   const bool cap = p.cap_log2 != 0.0f, bias = p.slopes != nullptr;
   if (cap) return bias ? launch_chunk_t<MAXS, true, true>(p, tmk, tmv, tmq, grid, stream)
                        : launch_chunk_t<MAXS, true, false>(p, tmk, tmv, tmq, grid, stream);
+  if constexpr (MAXS == kDecodeSeqsLarge)
+    if (bias && p.score_unit != 1.0f) return launch_chunk_t<MAXS, false, true, true>(p, tmk, tmv, tmq, grid, stream);
   return bias ? launch_chunk_t<MAXS, false, true>(p, tmk, tmv, tmq, grid, stream)
               : launch_chunk_t<MAXS, false, false>(p, tmk, tmv, tmq, grid, stream);
 }

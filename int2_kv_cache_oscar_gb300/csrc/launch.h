@@ -392,7 +392,9 @@ struct ChunkParams {
   float cap_c[5];      // of the raw score (x times a polynomial of x^2)
   float cap_d[3];      // the same of a shorter one, up to a quarter of the cap
   const float* slopes; // [hq], or NULL
-  float slope_unit;    // log2(e) with a cap (scores in log2 units), 1 / softmax_scale without (raw scores)
+  float slope_unit;    // log2(e) with a cap (scores in log2 units), score_unit / softmax_scale without
+  float score_unit;    // what raw scores are taken times before the slopes: 1, under a scale so small that a slope
+  float unit_log2;     // over it might overflow its power of two (the large block only); scale_log2 / score_unit
   const uint16_t* q;
   const uint16_t* k;
   const uint16_t* v;

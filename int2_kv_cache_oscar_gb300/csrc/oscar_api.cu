@@ -1690,7 +1690,10 @@ oscar_status oscar_chunk_attention(int32_t n_seqs, const int32_t* cu, const int3
     }
     P.slopes = how.slopes;
     P.rule = how;
-    P.slope_unit = cap != 0.0f ? kLog2e : 1.0f / scale;
+    // (slopes are below 2^60, distances below 2^31: over a scale of 2^-30 they stay in range)
+    P.score_unit = how.slopes != nullptr && cap == 0.0f && scale < 0x1p-30f ? std::exp2(std::floor(std::log2(scale))) : 1.0f;
+    P.unit_log2 = P.scale_log2 / P.score_unit;
+    P.slope_unit = cap != 0.0f ? kLog2e : P.score_unit / scale;
     P.q = static_cast<const uint16_t*>(rq.data);
     P.k = static_cast<const uint16_t*>(rk.data);
     P.v = static_cast<const uint16_t*>(rv.data);
@@ -1706,8 +1709,9 @@ oscar_status oscar_chunk_attention(int32_t n_seqs, const int32_t* cu, const int3
     P.lse = lse;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int sms = num_sms(dev);
-    e = seqs.size() <= (size_t)kDecodeSeqsSmall ? run_chunk<kDecodeSeqsSmall>(P, seqs, tokens, sms, st)
-                                                : run_chunk<kDecodeSeqsLarge>(P, seqs, tokens, sms, st);
+    const bool small = seqs.size() <= (size_t)kDecodeSeqsSmall && P.score_unit == 1.0f;
+    e = small ? run_chunk<kDecodeSeqsSmall>(P, seqs, tokens, sms, st)
+              : run_chunk<kDecodeSeqsLarge>(P, seqs, tokens, sms, st);
     if (e != cudaSuccess) return cuda_fail(e, "chunk launch");
     return ok();
   } catch (const std::exception& ex) {

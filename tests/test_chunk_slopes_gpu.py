@@ -61,3 +61,24 @@ def test_steep_slopes(lens, scale, sign):
         # the score itself (below 2^15.7 times the scale: 128 products of at most 8 x 50) beside the distance's, in float32
         assert ((lse[at:at + n] - top).abs() <= 2.0 ** 15.7 * (scale or 128 ** -0.5) + 2.0 ** -21 * top).all()
         at += n
+
+
+@pytest.mark.parametrize("lens", [[20], [300, 33], [700]])
+@pytest.mark.parametrize("scale", [2.0 ** -60, 1.3 * 2.0 ** -45, 2.0 ** -31])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_steep_slopes_and_small_scales(lens, scale, sign):
+    """The same where a slope over the scale leaves float32's range at a distance of a few hundred tokens."""
+    test_steep_slopes(lens, scale, sign)
+
+
+@pytest.mark.parametrize("scale", [1.7 * 2.0 ** -40, 2.0 ** -31])
+@pytest.mark.parametrize("prior", [False, True])
+def test_ordinary_slopes_and_small_scales(scale, prior):
+    """Scores that hardly differ: distances alone weigh the values."""
+    O = U.lib()
+    lens = [130, 40, 257]
+    q, k, v, p = inputs(lens, 2, 4, seed=91, prior=prior)
+    slopes = slopes_of(8)
+    slopes[::2] *= -0.1
+    compare(lens, q, k, v, *call(O, lens, q, k, v, p, slopes=slopes, softmax_scale=scale), prior=p, slopes=slopes,
+            softmax_scale=scale)
