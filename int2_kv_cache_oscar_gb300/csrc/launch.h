@@ -382,6 +382,8 @@ struct ChunkParams {
   int32_t cta_rows;    // (token, head) rows of a piece of work, 128 or 256, and
   int32_t pieces;      // how many pieces; set by the launch
   int32_t whole_tokens;   // 128 rows are whole tokens: queries come by TMA; set by the launch
+  int32_t late;        // short documents beside the tiled kernel of the same call, just before: nothing of its
+                       // is read or written over, so it is waited for at the end only (it has waited for those before)
   uint32_t spin_limit; // polls of a bounded wait; the test hook's `fault` (1) leaves
   int32_t fault;       // the second copy of CTA 0 unissued, with a small limit
   float scale_log2;    // softmax_scale * log2(e)
@@ -412,7 +414,7 @@ struct ChunkParams {
   uint32_t order[kOrder];
 };
 
-constexpr int kChunkShort = 32;    // tokens of a document that chunk_short.cu takes
+constexpr int kChunkShort = 32;    // documents of up to so many tokens are chunk_short.cu's
 
 template <int MAXS>
 cudaError_t launch_chunk(ChunkParams<MAXS>& p, int64_t tokens, int sms, cudaStream_t stream);

@@ -1579,15 +1579,15 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   return x < y + nb && y < x + na;
 }
 
+// Documents first .. first + n - 1 of a call, all short or none.
 template <int CAP>
-cudaError_t run_chunk(const ChunkParams<1>& head, const std::vector<ChunkSeq>& seqs, int64_t tokens, int sms,
+cudaError_t run_chunk(const ChunkParams<1>& head, const ChunkSeq* seqs, size_t n, int64_t tokens, int sms,
                       cudaStream_t st) {
   ChunkParams<CAP> P;
   std::memcpy(&P, &head, offsetof(ChunkParams<1>, seq));
   static_assert(offsetof(ChunkParams<1>, seq) == offsetof(ChunkParams<CAP>, seq), "the same header");
-  P.n_seqs = (int32_t)seqs.size();
-  std::copy(seqs.begin(), seqs.end(), P.seq);
-  // (the longest document is the first)
+  P.n_seqs = (int32_t)n;
+  std::copy(seqs, seqs + n, P.seq);
   return seqs[0].len <= kChunkShort ? launch_chunk_short(P, st) : launch_chunk(P, tokens, sms, st);
 }
 
@@ -1709,9 +1709,21 @@ oscar_status oscar_chunk_attention(int32_t n_seqs, const int32_t* cu, const int3
     P.lse = lse;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int sms = num_sms(dev);
-    const bool small = seqs.size() <= (size_t)kDecodeSeqsSmall && P.score_unit == 1.0f;
-    e = small ? run_chunk<kDecodeSeqsSmall>(P, seqs, tokens, sms, st)
-              : run_chunk<kDecodeSeqsLarge>(P, seqs, tokens, sms, st);
+    // Each document goes to the kernel of its length, whatever else is in the call: the
+    // longest ones are the first.
+    const size_t tiled = std::find_if(seqs.begin(), seqs.end(), [](const ChunkSeq& d) { return d.len <= kChunkShort; }) -
+                         seqs.begin();
+    auto run = [&](size_t first, size_t n) {
+      const ChunkSeq* d = seqs.data() + first;
+      const bool small = n <= (size_t)kDecodeSeqsSmall && (P.score_unit == 1.0f || first >= tiled);
+      return small ? run_chunk<kDecodeSeqsSmall>(P, d, n, tokens, sms, st)
+                   : run_chunk<kDecodeSeqsLarge>(P, d, n, tokens, sms, st);
+    };
+    if (tiled > 0) e = run(0, tiled);
+    if (e == cudaSuccess && tiled < seqs.size()) {
+      P.late = tiled > 0 ? 1 : 0;
+      e = run(tiled, seqs.size() - tiled);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "chunk launch");
     return ok();
   } catch (const std::exception& ex) {
