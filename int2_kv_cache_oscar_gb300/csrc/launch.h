@@ -382,8 +382,6 @@ struct ChunkParams {
   int32_t cta_rows;    // (token, head) rows of a piece of work, 128 or 256, and
   int32_t pieces;      // how many pieces; set by the launch
   int32_t whole_tokens;   // 128 rows are whole tokens: queries come by TMA; set by the launch
-  int32_t late;        // short documents beside the tiled kernel of the same call, just before: nothing of its
-                       // is read or written over, so it is waited for at the end only (it has waited for those before)
   uint32_t spin_limit; // polls of a bounded wait; the test hook's `fault` (1) leaves
   int32_t fault;       // the second copy of CTA 0 unissued, with a small limit
   float scale_log2;    // softmax_scale * log2(e)
@@ -397,6 +395,10 @@ struct ChunkParams {
   float slope_unit;    // log2(e) with a cap (scores in log2 units), score_unit / softmax_scale without
   float score_unit;    // what raw scores are taken times before the slopes: 1, under a scale so small that a slope
   float unit_log2;     // over it might overflow its power of two (the large block only); scale_log2 / score_unit
+  int32_t late;        // short documents beside the tiled kernel of the same call, just before: nothing of its
+                       // is read or written over, so it is waited for at the end only (it has waited for those
+                       // before).  Here, where it moves no pair of the values above off 8 bytes: further up it
+                       // made the capped kernel spill (8,192 capped tokens 453 -> 470 us)
   const uint16_t* q;
   const uint16_t* k;
   const uint16_t* v;
