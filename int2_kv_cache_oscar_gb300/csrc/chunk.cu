@@ -168,6 +168,25 @@ __device__ __forceinline__ uint32_t tile_off(int r, int c) {
   return (uint32_t)((c >> 3) * kBox + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
+// A wait that may take as long as the other roles need for a whole piece, whose length
+// is the document's: bounded like the others, but by polls during which no tile was
+// requested into the slot that `issued` counts.
+template <typename Ready>
+__device__ __forceinline__ bool wait_for_piece(Ready ready, const volatile uint32_t* issued, volatile int* abort_flag,
+                                               uint32_t limit) {
+  uint32_t seen = 0;
+  for (uint32_t i = 0; i < limit; ++i) {
+    if (ready()) return true;
+    if (*abort_flag) return false;
+    if (i % 64 == 63 && *issued != seen) {
+      seen = *issued;
+      i = 0;
+    }
+  }
+  *abort_flag = 1;
+  return false;
+}
+
 // Ring position of key and value tiles: K0, K1, V0, K2, V1, ...
 __device__ __forceinline__ int key_pos(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int value_pos(int j, int steps) { return j == steps - 1 ? 2 * steps - 1 : 2 * j + 2; }
@@ -351,7 +370,9 @@ __global__ void __launch_bounds__(kChThreads, 1)
   // The CTA's k-th piece (its `there` is 0 behind the last one, or when a wait
   // gave up); every reading warp takes and releases each piece once.
   auto take = [&](int k) {
-    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(&S.w_full[k & 1], (k >> 1) & 1, &S.abort_flag, nullptr, p.spin_limit));
+    bool ok = wait_for_piece([&] { return mbar_try_wait(&S.w_full[k & 1], (k >> 1) & 1); }, &S.issued[0], &S.abort_flag,
+                             p.spin_limit);
+    ok = __all_sync(0xffffffffu, ok);
     ChunkTile T = S.work[k & 1];
     if (!ok) T.there = 0;
     return T;
@@ -505,7 +526,8 @@ __global__ void __launch_bounds__(kChThreads, 1)
           const uint32_t vn = base + value_pos(j, steps);
           const int vs = vn % kChSlots;
           // (these warps do not follow a slot's earlier uses: its phase is waited for once it exists)
-          ok = wait_issued(&S.issued[vs], vn / kChSlots, &S.abort_flag, nullptr, p.spin_limit) &&
+          const volatile uint32_t* uses = &S.issued[vs];
+          ok = wait_for_piece([&] { return *uses > vn / kChSlots; }, uses, &S.abort_flag, p.spin_limit) &&
                mbar_wait_bounded(&S.full[vs], (vn / kChSlots) & 1, &S.abort_flag, nullptr, p.spin_limit);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
