@@ -991,6 +991,15 @@ cudaError_t launch_chunk_t(const ChunkParams<MAXS>& p, const CUtensorMap& tmk, c
 
 }  // namespace
 
+int64_t chunk_tiles(const ChunkSeq* docs, int n, int gqa, int hkv, int sms, int32_t* cta_rows) {
+  // two row tiles a CTA share its key tiles; one each while that leaves SMs without work
+  for (*cta_rows = 2 * kChRows;; *cta_rows = kChRows) {
+    int64_t tiles = 0;
+    for (int i = 0; i < n; ++i) tiles += ((int64_t)docs[i].len * gqa + *cta_rows - 1) / *cta_rows;
+    if (*cta_rows == kChRows || tiles * hkv >= sms) return tiles;
+  }
+}
+
 template <int MAXS>
 cudaError_t launch_chunk(ChunkParams<MAXS>& p, int64_t tokens, int sms, cudaStream_t stream) {
   CUtensorMap tmk, tmv, tmq{};
@@ -1000,17 +1009,13 @@ cudaError_t launch_chunk(ChunkParams<MAXS>& p, int64_t tokens, int sms, cudaStre
   p.whole_tokens = kChRows % p.gqa == 0;
   if (p.whole_tokens && !encode_chunk_map(&tmq, p.q, tokens, p.hq, 2 * p.q_token, 2 * p.q_head, p.gqa))
     return cudaErrorInvalidValue;
-  // two row tiles a CTA share its key tiles; one each while that leaves SMs without work
-  int64_t tiles = 0;
-  for (p.cta_rows = 2 * kChRows;; p.cta_rows = kChRows) {
-    tiles = 0;
-    for (int i = 0; i < p.n_seqs; ++i) {
-      p.seq[i].tbase = (int32_t)tiles;
-      tiles += ((int64_t)p.seq[i].len * p.gqa + p.cta_rows - 1) / p.cta_rows;
-    }
-    if (p.cta_rows == kChRows || tiles * p.hkv >= sms) break;
-  }
+  int64_t tiles = chunk_tiles(p.seq, p.n_seqs, p.gqa, p.hkv, sms, &p.cta_rows);
   p.pieces = (int32_t)(tiles * p.hkv);
+  tiles = 0;
+  for (int i = 0; i < p.n_seqs; ++i) {
+    p.seq[i].tbase = (int32_t)tiles;
+    tiles += ((int64_t)p.seq[i].len * p.gqa + p.cta_rows - 1) / p.cta_rows;
+  }
   // several rounds over documents of different lengths: pieces in descending order
   // of their steps (without the table, document by document: 24 documents of 60 to
   // 1,531 tokens took 1.3 times as long)

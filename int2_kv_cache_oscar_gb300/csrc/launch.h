@@ -418,6 +418,8 @@ struct ChunkParams {
 
 constexpr int kChunkShort = 32;    // documents of up to so many tokens are chunk_short.cu's
 
+// Row tiles of a KV head in the tiled kernel's launch, and their rows.
+int64_t chunk_tiles(const ChunkSeq* docs, int n, int gqa, int hkv, int sms, int32_t* cta_rows);
 template <int MAXS>
 cudaError_t launch_chunk(ChunkParams<MAXS>& p, int64_t tokens, int sms, cudaStream_t stream);
 template <int MAXS>
