@@ -680,10 +680,12 @@ oscar_status oscar_cache_window_offset(const oscar_cache* cache, int32_t seq, in
 /*
  * Test hook of the failure path: the next INT2 decode, read-back or selection
  * launch made on the calling thread (oscar_decode_attention, _f32,
- * oscar_scored_decode_attention, oscar_append_decode, oscar_sparse_decode_attention, oscar_cache_read,
- * oscar_select_groups) has one bulk copy of its first CTA left unissued, and its bounded waits give up after 2^14 polls
- * instead of 2^24.  (A listed decode of sequences without a group: the window
- * copies of its combine, where it has any.  oscar_chunk_attention, documents of
+ * oscar_scored_decode_attention, oscar_append_decode,
+ * oscar_sparse_decode_attention, oscar_cache_read, oscar_select_groups, a cut
+ * inside a group by oscar_cache_fork) has one bulk copy of its first CTA left
+ * unissued, and its bounded waits give up after 2^14 polls instead of 2^24.  (A
+ * listed decode of sequences without a group: the window copies of its combine,
+ * where it has any.  oscar_chunk_attention, documents of
  * more than 32 tokens: one tile copy of its first CTA; it has no arena to set a
  * flag in, the rows of that CTA are NaN.)  The consumer waiting for that copy then
  * gives up, the kernel sets the arena's error flag, skips its remaining work

@@ -50,8 +50,9 @@ namespace {
 thread_local std::string g_err;
 thread_local cudaEvent_t g_ev_start = nullptr;
 thread_local cudaEvent_t g_ev_stop = nullptr;
-// armed by oscar_test_arm_wait_timeout: the next INT2 decode, read-back or
-// selection launch on this thread leaves one copy unissued and gives up its waits early
+// armed by oscar_test_arm_wait_timeout: the next INT2 decode, read-back, cut inside a
+// group, selection or tiled chunk launch on this thread leaves one copy unissued and
+// gives up its waits early
 thread_local bool g_arm_timeout = false;
 constexpr uint32_t kArmedSpinLimit = 1u << 14;
 
@@ -1178,7 +1179,7 @@ oscar_status run_read(oscar_cache* c, const std::vector<ReadSeq>& seqs, size_t f
   P.late = late ? 1 : 0;
   P.row_pitch = to_windows ? kHeadDim : (int64_t)P.hkv * kHeadDim;
   P.head_pitch = to_windows ? kWindowBytes / 2 : kHeadDim;
-  P.fault = !to_windows && take_armed_timeout() ? 1 : 0;
+  P.fault = take_armed_timeout() ? 1 : 0;
   P.spin_limit = P.fault ? kArmedSpinLimit : kSpinLimit;
   int64_t ubase = 0;
   for (size_t i = 0; i < n; ++i) {

@@ -612,8 +612,9 @@ def oscar_bf16_decode_attention(seq_ids: Sequence[int], seq_lens: Sequence[int],
 
 
 def oscar_test_arm_wait_timeout() -> None:
-    """Test hook: the next INT2 decode, read-back or selection on this thread
-    leaves one copy unissued so that a bounded device wait runs out (see include/oscar.h)."""
+    """Test hook: the next INT2 decode, read-back, cut inside a group, selection or tiled chunk
+    attention on this thread leaves one copy unissued so that a bounded device wait runs out
+    (see include/oscar.h)."""
     _check(_lib.oscar_test_arm_wait_timeout())
 
 
