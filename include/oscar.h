@@ -626,10 +626,12 @@ typedef struct oscar_rows {
  *                 merged row; overlaps nothing but an equal prior_lse
  *   prior_out, prior_lse, out and lse: device or page-locked host memory
  *   softmax_scale 0 means 1 / sqrt(128); with slopes at least 2^-60
- * Keys and values that a token does not see have no part in its row, whatever
- * they hold.  Softmax weights are rounded to bf16 for the product with the
- * values (row sums are not); the rest is float32.  Should a bounded wait within
- * the kernel give up, the rows that it keeps from being computed are NaN.
+ * Keys and values that a token does not see, and the other rows' queries, have
+ * no part in its row, not in its last bits, whatever they hold.  Softmax weights
+ * are rounded to bf16 for the product with the values (to two bf16 terms in
+ * documents of up to 32 tokens; row sums are not); the rest is float32.  Should
+ * a bounded wait within the kernel give up, the rows that it keeps from being
+ * computed are NaN.
  */
 oscar_status oscar_chunk_attention(int32_t n_seqs, const int32_t* cu_seqlens, const int32_t* prefix,
                                    const oscar_rows* q, const oscar_rows* k, const oscar_rows* v,

@@ -730,8 +730,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // A step (a group, or the window) is taken in two half-steps, one per
     // 64-token half; half-step j = 2 k + h.  Warps w and w + 4 share rows
     // 32 (w & 3) .. + 31 (their TMEM lanes) and split each half's tokens:
-    // warp group 0 takes the first 32 and owns O and the output, group 1 the
-    // other 32.  Each warp counts, for the issuer, when it has read the scores
+    // warp group 0 takes the first 32 and rescales O, group 1 the other 32; each
+    // writes half of the output's channels.  Each warp counts, for the issuer, when it has read the scores
     // of a half-step and when it has written its P.  As for the builders: the
     // same barriers in every half-step, work skipped after an abort.
     const int grp = warp >> 2;
@@ -918,9 +918,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tst_wait();
       count(&S.pcount);
     }
-    // ---- the last P.V, then the rows out (group 0): o = (O 2^-Gv + Z
-    // 2^-gz) / l, lse = (m + log2 l) ln 2 (the TMEM loads for the whole warp,
-    // the stores for rows that exist)
+    // ---- the last P.V, then the rows out (half of the channels each; m, l and lse
+    // by group 0): o = (O 2^-Gv + Z 2^-gz) / l, lse = (m + log2 l) ln 2 (the TMEM
+    // loads for the whole warp, the stores for rows that exist)
     S.pmax[nh & 1][grp][r] = l;           // (this buffer's last readers have passed a barrier)
     ok = ok && (nh == 0 || pv_done(nh - 1));
     ok = __all_sync(0xffffffffu, ok);
