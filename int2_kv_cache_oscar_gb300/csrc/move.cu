@@ -13,8 +13,9 @@
 //     barrier writes them.  A read of group g_k, k > i, is never of place i <
 //     g_k, so the reads of the next groups are requested before the writes.
 // Bound by HBM: every moved byte is read and written once.  Four forks of 128K tokens
-// (8 KV heads, 113 MB read, 453 written) 95 us, 99 without stores that leave the L2
-// first; half of 128K kept 17.3 us (57 MB); blocks an SM: 4 as 6, 8 slower (120 us).
+// (8 KV heads, 113 MB read, 453 written) 95 us a call, 99 without stores that leave the
+// L2 first; half of 128K kept 21 us (57 MB; the kernel alone, caches cold, 19); blocks
+// an SM: 4 as 6, 8 slower (120 us).
 #include <algorithm>
 
 #include "common.cuh"
