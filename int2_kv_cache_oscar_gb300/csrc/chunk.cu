@@ -647,10 +647,10 @@ __global__ void __launch_bounds__(kChThreads, 1)
               // A row takes the form that the scores which it sees ask for, by itself:
               // neither hidden keys nor the warp's other rows have a part in its bits
               // (the short polynomial is the long one with zeros for its last terms).
-              // Branches by row cost what each takes (8,192 capped tokens: 450 us where
-              // all scores are small, 553 within 0.6 of the cap, 822 all beyond, 1,000 to
-              // 1,160 with rows of every kind in a warp; with one form a warp, chosen by
-              // what its rows do not see as well, 448, 515, 750 and 777 to 856).
+              // Branches by row cost what each takes (8,192 capped tokens: 454 us where
+              // all scores are small, 556 within 0.6 of the cap, 826 all beyond, 990 to
+              // 1,180 with rows of every kind in a warp; with one form a warp, chosen by
+              // what its rows do not see as well, 449, 515, 751 and 777 to 856).
               float own = reach;
               if (j >= my_plain) {
                 const int vis = limit - j * kChKeys;
