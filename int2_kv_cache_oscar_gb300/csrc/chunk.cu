@@ -31,9 +31,9 @@
 //     memory, and rows that do see them add them on the CUDA cores.
 // Bound: 4 * 128 flops per visible (row, key) on the tensor cores for long
 // documents; launch and pipeline latency for short ones.  A step of 128 keys takes
-// 2,980 cycles for two tiles, 2,048 of them products: a tile's chain is 1,500 cycles
+// some 2,900 cycles for two tiles, 2,048 of them products: a tile's chain is 1,500 cycles
 // of softmax, then the second half of its P.V and the next scores (768), and the way
-// from one to the other and back (700): 8,192 tokens of 32 heads take 366 us, 1,500
+// from one to the other and back (700): 8,192 tokens of 32 heads take 358 us, 1,530
 // TFLOP/s.  A piece of a single step takes 9,000 cycles, most of them the softmax
 // warps' own: 3,000 of softmax with a mask, 4,000 of output rows on their way out
 // (64 bytes of a row at a time: 32 or 128 of them 2 to 6 % slower).  Tried when the
@@ -1017,7 +1017,7 @@ cudaError_t launch_chunk(ChunkParams<MAXS>& p, int64_t tokens, int sms, cudaStre
     tiles += ((int64_t)p.seq[i].len * p.gqa + p.cta_rows - 1) / p.cta_rows;
   }
   // several rounds over documents of different lengths: pieces in descending order
-  // of their steps (without the table, document by document: 24 documents of 60 to
+  // of their steps (without the table, document by document: 24 documents of 1 to
   // 1,531 tokens took 1.3 times as long)
   p.sorted = p.pieces > sms && p.n_seqs > 1 && tiles <= ChunkParams<MAXS>::kOrder;
   if (p.sorted) {
